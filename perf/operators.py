@@ -174,7 +174,11 @@ def _cache(case, g):
         pages = -(-n[b] // S)
         table[b, :pages] = free[at:at + pages]
         at += pages
-    return {"k": k, "v": v, "table": table, "lengths": torch.tensor(n, dtype=torch.int32, device=DEV)}
+    s = {"k": k, "v": v, "table": table, "lengths": torch.tensor(n, dtype=torch.int32, device=DEV)}
+    if own:  # a serving program describes its pools once; table and lengths change in place
+        import sparse_weight_matmul_amd as swm
+        s["cache"] = swm.PagedCache(k, v, table, s["lengths"])
+    return s
 
 
 def prepare(case, seed):
@@ -246,13 +250,11 @@ def _run_own(s):
     case = s["case"]
     op = case["op"]
     if op == "attention":
-        out = swm.paged_attention(s["q"], s["k"], s["v"], s["table"], s["lengths"], mask=s["mask"],
-                                  weights=s["weights"])
+        out = swm.paged_attention(s["cache"], s["q"], mask=s["mask"], weights=s["weights"])
         return [out] if s["weights"] is None else [out, s["weights"]]
     if op == "evict":
-        n, kept = swm.kv_evict(s["k"], s["v"], s["weights"], s["positions"], s["table"], s["lengths"],
-                               case["budget"], case["recent"], weights_out=s["weights_out"],
-                               positions_out=s["positions_out"])
+        n, kept = swm.kv_evict(s["cache"], s["weights"], s["positions"], case["budget"], case["recent"],
+                               weights_out=s["weights_out"], positions_out=s["positions_out"])
         return [n, kept, s["weights_out"], s["positions_out"], s["k"], s["v"]]
     if op == "product":
         return [swm.spmm_epilogue(s["fmt"], s["X"], bias=s["bias"], act=case["act"], residual=s["residual"],
