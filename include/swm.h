@@ -456,6 +456,73 @@ swm_status swm_dense_gemm(const void* W, int64_t ldw, const void* X, int64_t ldx
 swm_status swm_hbm_stream(const void* buf, size_t bytes, int32_t unroll, int32_t blocks,
                           uint32_t* out, void* stream);
 
+/* ------------------------------------------------------------------ serving
+ * What a pruned model's decode step needs between its products. */
+
+/* A paged key-value cache.  The pools hold `pages` pages of `page_size` slots
+ * of `heads` rows of `dim` fp16 elements; row (page, slot, head) starts at
+ * page * k_page + slot * k_slot + head * k_head elements (v_*: values), so
+ * token-major and head-major pools are the same call.  Token t of sequence b
+ * is slot t % page_size of page table[b * table_ld + t / page_size], for
+ * t < lengths[b]; lengths beyond the capacity pages_per_seq * page_size count
+ * as the capacity, negative ones as 0.  A table entry outside [0, pages)
+ * names no page: its tokens are not there (the entries past a length may hold
+ * anything).  All pointers are DEVICE memory; table and lengths are read by
+ * the kernels, so a captured graph follows what is written into them.
+ *  Limits: 1 <= dim <= 256 and dim % 8 == 0, page_size >= 1, pages >= 1,
+ *  heads >= 1, pages_per_seq >= 0, a capacity below 2^31 - 65536, batch
+ *  at most 65535 (SWM_ERR_UNSUPPORTED beyond, SWM_ERR_INVALID_ARG for
+ *  negative sizes or strides and null pointers); k and v 16-byte aligned and
+ *  every stride of theirs a multiple of 8 elements (SWM_ERR_ALIGN). */
+typedef struct swm_kv_cache {
+  void* k;
+  void* v;
+  const int32_t* table;
+  const int32_t* lengths;
+  int64_t k_page, k_slot, k_head;
+  int64_t v_page, v_slot, v_head;
+  int64_t table_ld;
+  int64_t pages, page_size, heads, dim;
+  int64_t batch, pages_per_seq;
+} swm_kv_cache;
+
+/* paged_attention: attention of one new token per sequence over the cache,
+ *   x_t = scale * q . k_t,  p = softmax of x over the live tokens,
+ *   out = sum_t p_t v_t,
+ * for q_heads query heads, a multiple of cache->heads: query head h reads
+ * key-value head h / (q_heads / heads).  A token is live if it is below its
+ * sequence's length, on a page of the pool and not masked; a row without live
+ * tokens gives zeros.  Rows that are not live may hold anything, infinities
+ * and NaN included.
+ *  q, out: DEVICE fp16, element (b, h, d) at b * q_batch + h * q_head + d
+ *  (out likewise; out must not alias q).  q 16-byte aligned with strides that
+ *  are multiples of 8.
+ *  mask: DEVICE bytes or NULL, mask[b * mask_ld + t] == 0 drops token t
+ *  (mask_ld >= the capacity).
+ *  weights: DEVICE fp32 or NULL, the accumulator of the attention weights of
+ *  each cached row: weights[page * w_page + head * w_head + slot] grows by
+ *  the sum of p_t over the head's group of query heads.  The adds are atomic:
+ *  where sequences share a page their order, and with it the last bit, is not
+ *  fixed; everything else of this call is bitwise reproducible.
+ *  workspace: DEVICE memory of at least swm_paged_attention_workspace_bytes
+ *  bytes (0 for few splits and no weights: NULL is fine then), 16-byte
+ *  aligned; calls that share it must be ordered on one stream.
+ *  Scores, maxima, sums and outputs are fp32; out is rounded once.
+ *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
+ *  heads, a scale that is not finite, negative strides, mask_ld below the
+ *  capacity, a workspace too small.  SWM_ERR_ALIGN: q or the workspace.
+ *  SWM_ERR_UNSUPPORTED: q_heads above 65535 or a grid beyond the device's.
+ *  One or two launches, asynchronous on stream. */
+swm_status swm_paged_attention(const swm_kv_cache* cache, const void* q, int64_t q_batch, int64_t q_head,
+                               int64_t q_heads, float scale, const uint8_t* mask, int64_t mask_ld, float* weights,
+                               int64_t w_page, int64_t w_head, void* out, int64_t out_batch, int64_t out_head,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace swm_paged_attention uses for this cache's sizes
+ * (its pointers are not looked at) on the current device; weights: nonzero if
+ * the call will pass an accumulator.  0 for sizes that call refuses. */
+size_t swm_paged_attention_workspace_bytes(const swm_kv_cache* cache, int64_t q_heads, int32_t weights);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static string for a status code (never NULL). */

@@ -47,6 +47,14 @@ class FormatInfo(ctypes.Structure):
         return {f[0]: getattr(self, f[0]) for f in self._fields_ if f[0] != "reserved"}
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("table", _vp), ("lengths", _vp),
+                ("k_page", _i64), ("k_slot", _i64), ("k_head", _i64),
+                ("v_page", _i64), ("v_slot", _i64), ("v_head", _i64),
+                ("table_ld", _i64), ("pages", _i64), ("page_size", _i64), ("heads", _i64), ("dim", _i64),
+                ("batch", _i64), ("pages_per_seq", _i64)]
+
+
 _PP = ctypes.POINTER(_vp)
 SIGNATURES = {
     "swm_sparse_compress": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, ctypes.POINTER(TileCfg), _vp, _PP]),
@@ -74,6 +82,9 @@ SIGNATURES = {
     "swm_colruns_encode_blob": (_i32, [_vp, _sz, _vp, _sz, ctypes.POINTER(_sz)]),
     "swm_dense_gemm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp]),
     "swm_hbm_stream": (_i32, [_vp, _sz, _i32, _i32, _vp, _vp]),
+    "swm_paged_attention_workspace_bytes": (_sz, [_vp, _i64, _i32]),
+    "swm_paged_attention": (_i32, [_vp, _vp, _i64, _i64, _i64, ctypes.c_float, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                   _i64, _vp, _sz, _vp]),
     "swm_status_str": (ctypes.c_char_p, [_i32]),
     "swm_last_hip_error": (_i32, []),
     "swm_version": (_i32, []),
@@ -457,6 +468,151 @@ def hbm_stream(buf, unroll: int, blocks: int, out=None, stream=None):
     nbytes = buf.numel() * buf.element_size()
     _check(lib.swm_hbm_stream(ctypes.c_void_p(buf.data_ptr()), nbytes, unroll, blocks,
                               ctypes.c_void_p(out.data_ptr()), _stream_ptr(stream)), "swm_hbm_stream")
+    return out
+
+
+def _raw_stream(stream, device) -> int:
+    """Handle of `stream`, or of the device's current stream; the device must be the current one."""
+    import torch
+    index = torch.cuda.current_device()
+    if device.index != index:
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{index}")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor, kept from reuse until `stream` is done with it where that is not the current stream."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _workspace(workspace, need, device, stream):
+    """(tensor to keep alive, pointer, bytes) of a caller's workspace, or of a new one if there is none."""
+    import torch
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = _empty((need,), torch.uint8, device, stream)
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+class PagedCache:
+    """A paged key-value cache: pools of key and value rows, the page table
+    and the lengths of a batch of sequences.
+
+    k, v: (pages, page_size, heads, dim) fp16 CUDA tensors with unit stride
+    along dim, and any other strides that are multiples of 8 (a head-major
+    pool is passed as its transpose(1, 2)); dim is a multiple of 8 up to 256.
+    table: (batch, pages_per_seq) int32, the page of each run of page_size
+    tokens (entries outside the pool name no page); lengths: (batch,) int32.
+    The object keeps the tensors and their addresses: their contents may
+    change at any time, in place."""
+
+    def __init__(self, k, v, table, lengths):
+        import torch
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float16 or t.dim() != 4:
+                raise TypeError(f"{name} must be a 4-D float16 CUDA tensor")
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{name} must have unit stride along its last dimension")
+        if k.shape != v.shape:
+            raise ValueError("k and v must have the same shape")
+        for name, t, dim in (("table", table, 2), ("lengths", lengths, 1)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32 or t.dim() != dim:
+                raise TypeError(f"{name} must be a {dim}-D int32 CUDA tensor")
+        if lengths.shape[0] != table.shape[0]:
+            raise ValueError("table and lengths must have one row per sequence")
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table must have unit stride along its last dimension")
+        if lengths.shape[0] > 1 and lengths.stride(0) != 1:
+            raise ValueError("lengths must be contiguous")
+        if not (k.device == v.device == table.device == lengths.device):
+            raise ValueError("all tensors of a cache must be on one device")
+        self.k, self.v, self.table, self.lengths = k, v, table, lengths
+        self.device = k.device
+        self.pages, self.page_size, self.heads, self.dim = k.shape
+        self.batch, self.pages_per_seq = table.shape
+        self.capacity = self.pages_per_seq * self.page_size
+        # strides of dimensions of one element are arbitrary and never used
+        ks = [s if n > 1 else 0 for s, n in zip(k.stride()[:3], k.shape)]
+        vs = [s if n > 1 else 0 for s, n in zip(v.stride()[:3], v.shape)]
+        self._c = KvCache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lengths.data_ptr(), *ks, *vs,
+                          table.stride(0), *k.shape, *table.shape)
+        self._p = ctypes.addressof(self._c)
+        self._attn_bytes = {}
+
+    def attention_workspace_bytes(self, q_heads: int, weights: bool = False) -> int:
+        """Device workspace bytes paged_attention uses (0: none)."""
+        key = (int(q_heads), bool(weights))
+        if key not in self._attn_bytes:
+            self._attn_bytes[key] = int(load().swm_paged_attention_workspace_bytes(self._p, *key))
+        return self._attn_bytes[key]
+
+    def _per_slot(self, t, name, dtype):
+        """Check an array with one entry per cached row, (pages, heads, page_size)."""
+        if not t.is_cuda or t.device != self.device or t.dtype != dtype:
+            raise TypeError(f"{name} must be a {dtype} tensor on {self.device}")
+        if t.shape != (self.pages, self.heads, self.page_size):
+            raise ValueError(f"{name} must be (pages, heads, page_size)")
+        if self.page_size > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name} must have unit stride along its last dimension")
+
+
+def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=None, weights=None, out=None,
+                    workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache: out (B, Hq,
+    D) = softmax(scale * q . k) v over each sequence's live tokens (zeros where
+    there are none); scale defaults to D ** -0.5.  q: (B, Hq, D) fp16, Hq a
+    multiple of the cache's heads.  mask: (B, >= capacity) bool or uint8,
+    false drops a token.  weights: (pages, heads, page_size) fp32, grows by
+    each row's attention weight summed over the query heads that share it.
+    workspace: a CUDA tensor of cache.attention_workspace_bytes(Hq, weights is
+    not None) bytes; None allocates it."""
+    import torch
+    lib = load()
+    if not q.is_cuda or q.dtype != torch.float16 or q.dim() != 3:
+        raise TypeError("q must be a 3-D float16 CUDA tensor")
+    B, Hq, D = q.shape
+    if B != cache.batch or D != cache.dim or q.device != cache.device:
+        raise ValueError(f"q must be ({cache.batch}, heads, {cache.dim}) on {cache.device}")
+    q_b, q_h, q_d = q.stride()
+    if D > 1 and q_d != 1:
+        raise ValueError("q must have unit stride along its last dimension")
+    if out is None:
+        out = _empty((B, Hq, D), torch.float16, cache.device, stream)
+    elif not out.is_cuda or out.dtype != torch.float16 or out.shape != q.shape or out.device != q.device:
+        raise TypeError("out must be a float16 CUDA tensor of q's shape")
+    elif out.stride(2) != 1:
+        raise ValueError("out must have unit stride along its last dimension")
+    mp, mask_ld = None, 0
+    if mask is not None:
+        if not mask.is_cuda or mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 2:
+            raise TypeError("mask must be a 2-D bool or uint8 CUDA tensor")
+        if mask.shape[0] != B or mask.shape[1] < cache.capacity or mask.device != q.device:
+            raise ValueError(f"mask must be ({B}, >= {cache.capacity}) on {cache.device}")
+        if mask.shape[1] > 1 and mask.stride(1) != 1:
+            raise ValueError("mask must have unit stride along its last dimension")
+        # of one sequence only the first row is read, whatever its stride says
+        mp, mask_ld = mask.data_ptr(), mask.stride(0) if B > 1 else max(mask.shape[1], 1)
+        if B > 1 and mask_ld < cache.capacity:
+            raise ValueError("mask rows must not overlap")
+    wp, w_page, w_head = None, 0, 0
+    if weights is not None:
+        cache._per_slot(weights, "weights", torch.float32)
+        wp, w_page, w_head = weights.data_ptr(), weights.stride(0), weights.stride(1)
+    s = _raw_stream(stream, cache.device)
+    keep, ws, ws_bytes = _workspace(workspace, cache.attention_workspace_bytes(Hq, weights is not None),
+                                    cache.device, stream)
+    # a stride along one sequence or one head is never used: pass 0 for it
+    _check(lib.swm_paged_attention(cache._p, q.data_ptr(), q_b if B > 1 else 0, q_h if Hq > 1 else 0, Hq,
+                                   D ** -0.5 if scale is None else scale, mp, mask_ld, wp, w_page, w_head,
+                                   out.data_ptr(), out.stride(0), out.stride(1), ws, ws_bytes, s),
+           "swm_paged_attention")
     return out
 
 

@@ -13,6 +13,7 @@
 #include <new>
 #include <vector>
 
+#include "host_util.h"
 #include "kernels.h"
 #include "swm.h"
 #include "swm_internal.h"
@@ -47,7 +48,11 @@ bool log_on() {
   return v;
 }
 
-__attribute__((format(printf, 1, 2))) void swm_log(const char* fmt, ...) {
+}  // namespace
+
+namespace swm {
+
+void swm_log(const char* fmt, ...) {
   if (!log_on()) return;
   char line[256];
   va_list ap;
@@ -56,6 +61,33 @@ __attribute__((format(printf, 1, 2))) void swm_log(const char* fmt, ...) {
   va_end(ap);
   fprintf(stderr, "[swm] %s\n", line);
 }
+
+swm_status hip_fail(hipError_t e) {
+  g_last_hip.store(int32_t(e));
+  return SWM_ERR_HIP;
+}
+
+int num_cus(int dev) {
+  static std::mutex mu;
+  static std::vector<int> cache;
+  std::lock_guard<std::mutex> g(mu);
+  if (dev >= int(cache.size())) cache.resize(dev + 1, 0);
+  if (cache[dev] == 0) {
+    int v = 0;
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0)
+      v = 256;
+    cache[dev] = v;
+  }
+  return cache[dev];
+}
+
+}  // namespace swm
+
+namespace {
+
+using swm::hip_fail;
+using swm::num_cus;
+using swm::swm_log;
 
 // SWM_SKIP (read once): "off" never takes the column-run kernel, "on" takes
 // it for every token count it serves (n <= 4), anything else (default) up to
@@ -71,32 +103,7 @@ int skip_mode() {
   return v;
 }
 
-swm_status hip_fail(hipError_t e) {
-  g_last_hip.store(int32_t(e));
-  return SWM_ERR_HIP;
-}
-
-#define SWM_HIP(expr)                              \
-  do {                                             \
-    hipError_t e_ = (expr);                        \
-    if (e_ != hipSuccess) return hip_fail(e_);     \
-  } while (0)
-
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-int num_cus(int dev) {
-  static std::mutex mu;
-  static std::vector<int> cache;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev >= int(cache.size())) cache.resize(dev + 1, 0);
-  if (cache[dev] == 0) {
-    int v = 0;
-    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0)
-      v = 256;
-    cache[dev] = v;
-  }
-  return cache[dev];
-}
 
 swm_status upload(std::vector<uint8_t>&& blob, const swm::Header& h, hipStream_t s, swm_format** out) {
   swm_format* f = new (std::nothrow) swm_format;

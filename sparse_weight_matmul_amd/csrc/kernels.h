@@ -123,4 +123,31 @@ hipError_t launch_smf(const Header& h, const Sparse24Layout& L, bool residual, c
 // The SMFMAC kernel addresses the compacted layers and X with 32-bit byte offsets.
 bool smf_fits(const Header& h, int64_t N, int64_t ldx);
 
+// A paged key-value cache: row (page, slot, head) of a pool starts at
+// page * _p + slot * _s + head * _h elements; token t of sequence b is slot
+// t % S of page table[b * table_b + t / S].
+struct KvView {
+  uint16_t *k = nullptr, *v = nullptr;
+  const int32_t *table = nullptr, *lengths = nullptr;
+  int64_t k_p = 0, k_s = 0, k_h = 0, v_p = 0, v_s = 0, v_h = 0, table_b = 0;
+  int64_t pages = 0, S = 0, Hkv = 0, D = 0, B = 0, per_seq = 0;
+};
+
+// Attention of one new token per sequence over the cache.
+struct AttnCall {
+  const uint16_t* q = nullptr;
+  uint16_t* out = nullptr;
+  const uint8_t* mask = nullptr;  // [B][>= capacity], nonzero = attended
+  float* weights = nullptr;       // page * w_p + head * w_h + slot
+  int64_t q_b = 0, q_h = 0, o_b = 0, o_h = 0, mask_b = 0, w_p = 0, w_h = 0;
+  int64_t Hq = 0;
+  float scale = 1.f;
+};
+struct AttnPlan {
+  int splits = 1, split_len = 0;
+  size_t off_part = 0, off_logits = 0, bytes = 0;  // workspace
+};
+AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, bool weights, int num_cus);
+hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& p, void* ws, hipStream_t s);
+
 }  // namespace swm
