@@ -523,6 +523,65 @@ swm_status swm_paged_attention(const swm_kv_cache* cache, const void* q, int64_t
  * the call will pass an accumulator.  0 for sizes that call refuses. */
 size_t swm_paged_attention_workspace_bytes(const swm_kv_cache* cache, int64_t q_heads, int32_t weights);
 
+/* kv_evict: cut every sequence of the cache back to `budget` tokens per head,
+ * keeping those that the attention looked at most (the accumulator that
+ * swm_paged_attention fills) and a window of recent ones.  Per sequence longer
+ * than the budget and per key-value head, the budget tokens with the largest
+ * keys stay, ties going to the lower slot.  The key of a token is
+ *   "first", before all numbers, if its position > newest - recent (newest =
+ *   the largest position of the sequence and head), or its weight is NaN or
+ *   +inf;  its weight otherwise.
+ * The j-th (in slot order) of the tokens that stay in slots >= budget moves
+ * into the j-th freed slot < budget, with its key and value rows, weight and
+ * position; nothing else moves, and the slots from the budget on keep their
+ * old contents.  Sequences within the budget stay as they are.  The order of
+ * slots is no longer the order of positions afterwards, which the attention
+ * does not need.  A head's slot then holds another token than the next
+ * head's: positions and weights are kept per head.
+ *  weights, positions: DEVICE fp32 / int32, one entry per cached row, at
+ *  page * w_page + head * w_head + slot (p_*: positions).
+ *  weights_out, positions_out: where the slots below the new length get their
+ *  values, with strides of their own; the inputs themselves (same address and
+ *  strides) or memory that does not overlap them.
+ *  lengths_out: DEVICE int32, one per sequence: min(length, budget); not the
+ *  cache's own lengths.
+ *  kept: DEVICE int32, batch x heads x budget, contiguous: the slot each slot's
+ *  token came from, -1 from the new length on.
+ *  No page may be shared by two sequences, or appear twice in one.  A token
+ *  whose table entry names no page has the lowest key and is not copied.
+ *  budget >= 0, recent >= 0, both below 2^31.
+ *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, lengths_out
+ *  == lengths, an output at its input's address with other strides.  Cache
+ *  errors as above.  No workspace; two launches, asynchronous on stream; whole
+ *  numbers and copies, so bitwise reproducible. */
+swm_status swm_kv_evict(const swm_kv_cache* cache, const float* weights, int64_t w_page, int64_t w_head,
+                        const int32_t* positions, int64_t p_page, int64_t p_head, int64_t budget, int64_t recent,
+                        float* weights_out, int64_t wo_page, int64_t wo_head, int32_t* positions_out,
+                        int64_t po_page, int64_t po_head, int32_t* lengths_out, int32_t* kept, void* stream);
+
+/* token_logprobs: for each of N rows of V logits, log p of the row's target
+ * token, the entropy of the row's distribution and its `top` most likely
+ * tokens, p = softmax(row): what a pruned model's perplexity and a caller's
+ * alternatives come from.  Natural logarithms, fp32 throughout.
+ *  logits: DEVICE, fp16 (fp32 == 0) or fp32 (fp32 != 0), N rows of V, leading
+ *  dimension ld >= V.  A logit of -inf rules its token out (log p = -inf); a
+ *  row with nothing but -inf has log probabilities of -inf and entropy 0; a
+ *  row with a NaN or +inf gives NaN.
+ *  targets: DEVICE int32 (wide == 0) or int64 (wide != 0), one per row, or
+ *  NULL (then logp is not written and may be NULL).  A negative target means
+ *  "none": log p = 0.  A target >= V gives NaN.
+ *  logp, entropy: DEVICE fp32, one per row; entropy may be NULL.
+ *  top: 0..64; top_ids (DEVICE int64) and top_logp (DEVICE fp32): N x top,
+ *  contiguous, most likely first, equal logits by the lower index; past V
+ *  entries -1 and -inf.  NULL if top == 0.
+ *  SWM_ERR_INVALID_ARG: null pointers, N < 0, V < 1, ld < V, top < 0, targets
+ *  without logp.  SWM_ERR_ALIGN: logits not aligned to their type.
+ *  SWM_ERR_UNSUPPORTED: top > 64, V >= 2^31 - 65536, N >= 2^22.  One launch,
+ *  no workspace, asynchronous on stream, bitwise reproducible. */
+swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64_t V, int64_t ld,
+                              const void* targets, int32_t wide, float* logp, float* entropy, int32_t top,
+                              int64_t* top_ids, float* top_logp, void* stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static string for a status code (never NULL). */

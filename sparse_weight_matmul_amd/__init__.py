@@ -85,6 +85,9 @@ SIGNATURES = {
     "swm_paged_attention_workspace_bytes": (_sz, [_vp, _i64, _i32]),
     "swm_paged_attention": (_i32, [_vp, _vp, _i64, _i64, _i64, ctypes.c_float, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
                                    _i64, _vp, _sz, _vp]),
+    "swm_kv_evict": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                            _vp, _vp]),
+    "swm_token_logprobs": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp]),
     "swm_status_str": (ctypes.c_char_p, [_i32]),
     "swm_last_hip_error": (_i32, []),
     "swm_version": (_i32, []),
@@ -614,6 +617,91 @@ def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=No
                                    out.data_ptr(), out.stride(0), out.stride(1), ws, ws_bytes, s),
            "swm_paged_attention")
     return out
+
+
+def kv_evict(cache: PagedCache, weights, positions, budget: int, recent: int = 0, weights_out=None,
+             positions_out=None, lengths_out=None, kept=None, stream=None):
+    """Cut every sequence of a paged cache back to `budget` tokens per head:
+    those within `recent` of the newest position and those with the largest
+    accumulated attention weight stay, ties going to the lower slot; the ones
+    that stay above the budget move into the slots freed below it.
+    weights (fp32) and positions (int32): (pages, heads, page_size), one entry
+    per cached row, updated in place unless outputs are given.  Returns the
+    new lengths (B,) (the cache's own tensor is left alone: copy them into it)
+    and kept (B, heads, budget), the slot each slot's token came from (-1
+    where there is none).  No page may belong to two sequences."""
+    import torch
+    lib = load()
+    cache._per_slot(weights, "weights", torch.float32)
+    cache._per_slot(positions, "positions", torch.int32)
+    if weights_out is None:
+        weights_out = weights
+    else:
+        cache._per_slot(weights_out, "weights_out", torch.float32)
+    if positions_out is None:
+        positions_out = positions
+    else:
+        cache._per_slot(positions_out, "positions_out", torch.int32)
+    budget = int(budget)
+    if budget < 0:
+        raise ValueError("budget must not be negative")
+    if lengths_out is None:
+        lengths_out = _empty((cache.batch,), torch.int32, cache.device, stream)
+    elif (not lengths_out.is_cuda or lengths_out.dtype != torch.int32 or lengths_out.shape != (cache.batch,)
+          or not lengths_out.is_contiguous()):
+        raise TypeError("lengths_out must be a contiguous int32 CUDA tensor, one entry per sequence")
+    shape = (cache.batch, cache.heads, budget)
+    if kept is None:
+        kept = _empty(shape, torch.int32, cache.device, stream)
+    elif not kept.is_cuda or kept.dtype != torch.int32 or kept.shape != shape or not kept.is_contiguous():
+        raise TypeError(f"kept must be a contiguous {shape} int32 CUDA tensor")
+    s = _raw_stream(stream, cache.device)
+    _check(lib.swm_kv_evict(cache._p, weights.data_ptr(), weights.stride(0), weights.stride(1), positions.data_ptr(),
+                            positions.stride(0), positions.stride(1), budget, int(recent), weights_out.data_ptr(),
+                            weights_out.stride(0), weights_out.stride(1), positions_out.data_ptr(),
+                            positions_out.stride(0), positions_out.stride(1), lengths_out.data_ptr(),
+                            kept.data_ptr(), s), "swm_kv_evict")
+    return lengths_out, kept
+
+
+def token_logprobs(logits, targets=None, top: int = 0, stream=None):
+    """(logprobs, entropy, top_ids, top_logprobs) of rows of logits (N, V),
+    fp16 or fp32: log p of each row's target token ((N,) int32 or int64; a
+    negative one means none and gives 0), the entropy of each row, and its
+    `top` <= 64 most likely tokens, equal logits by the lower index.  fp32 and
+    int64; logprobs is None without targets, top_ids and top_logprobs are None
+    for top = 0."""
+    import torch
+    lib = load()
+    if not logits.is_cuda or logits.dtype not in (torch.float16, torch.float32) or logits.dim() != 2:
+        raise TypeError("logits must be a 2-D float16 or float32 CUDA tensor")
+    N, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit stride along the last dimension")
+    device = logits.device
+    ld = logits.stride(0) if N > 1 else V
+    if ld < V:
+        raise ValueError("rows of logits must not overlap")
+    s = _raw_stream(stream, device)
+    tp, wide, logp = None, 0, None
+    if targets is not None:
+        if targets.dtype not in (torch.int32, torch.int64) or targets.device != device:
+            raise TypeError(f"targets must be an int32 or int64 tensor on {device}")
+        if targets.shape != (N,) or (N > 1 and targets.stride(0) != 1):
+            raise ValueError(f"targets must be contiguous, ({N},)")
+        tp, wide = targets.data_ptr(), int(targets.dtype == torch.int64)
+        logp = _empty((N,), torch.float32, device, stream)
+    entropy = _empty((N,), torch.float32, device, stream)
+    top = int(top)
+    ids = lps = None
+    if top > 0:
+        ids = _empty((N, top), torch.int64, device, stream)
+        lps = _empty((N, top), torch.float32, device, stream)
+    _check(lib.swm_token_logprobs(logits.data_ptr(), int(logits.dtype == torch.float32), N, V, ld, tp, wide,
+                                  None if logp is None else logp.data_ptr(), entropy.data_ptr(), top,
+                                  None if ids is None else ids.data_ptr(), None if lps is None else lps.data_ptr(),
+                                  s), "swm_token_logprobs")
+    return logp, entropy, ids, lps
 
 
 def status_str(code: int) -> str:

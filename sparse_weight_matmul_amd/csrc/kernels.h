@@ -148,6 +148,30 @@ struct AttnPlan {
   size_t off_part = 0, off_logits = 0, bytes = 0;  // workspace
 };
 AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, bool weights, int num_cus);
+// Eviction down to `budget` tokens per sequence and head.
+struct EvictCall {
+  const float* weights = nullptr;      // page * w_p + head * w_h + slot
+  const int32_t* positions = nullptr;  // page * p_p + head * p_h + slot
+  float* weights_out = nullptr;        // may be weights, with the same strides
+  int32_t* positions_out = nullptr;
+  int32_t *lengths_out = nullptr, *kept = nullptr;
+  int64_t w_p = 0, w_h = 0, p_p = 0, p_h = 0, wo_p = 0, wo_h = 0, po_p = 0, po_h = 0;
+  int64_t budget = 0, recent = 0;
+};
+hipError_t launch_evict(const KvView& c, const EvictCall& r, hipStream_t s);
+
+// Log probabilities, entropy and top tokens of N rows of V logits.
+constexpr int kLogprobMaxTop = 64;
+struct LogprobCall {
+  const void *logits = nullptr, *targets = nullptr;
+  float *logp = nullptr, *entropy = nullptr, *top_logp = nullptr;
+  int64_t* top_ids = nullptr;
+  int64_t N = 0, V = 0, ld = 0;
+  int32_t top = 0;
+  bool fp32 = false, wide = false;  // 32-bit logits, 64-bit targets
+};
+hipError_t launch_logprobs(const LogprobCall& r, hipStream_t s);
+
 hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& p, void* ws, hipStream_t s);
 
 }  // namespace swm

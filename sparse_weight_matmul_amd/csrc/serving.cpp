@@ -122,4 +122,73 @@ swm_status swm_paged_attention(const swm_kv_cache* c, const void* q, int64_t q_b
   return SWM_OK;
 }
 
+swm_status swm_kv_evict(const swm_kv_cache* c, const float* weights, int64_t w_page, int64_t w_head,
+                        const int32_t* positions, int64_t p_page, int64_t p_head, int64_t budget, int64_t recent,
+                        float* weights_out, int64_t wo_page, int64_t wo_head, int32_t* positions_out,
+                        int64_t po_page, int64_t po_head, int32_t* lengths_out, int32_t* kept, void* stream) {
+  swm::KvView v;
+  swm_status st = check_cache(c, &v);
+  if (st != SWM_OK) return st;
+  if (budget < 0 || recent < 0 || budget >= (int64_t(1) << 31) || recent >= (int64_t(1) << 31))
+    return SWM_ERR_INVALID_ARG;
+  if (w_page < 0 || w_head < 0 || p_page < 0 || p_head < 0 || wo_page < 0 || wo_head < 0 || po_page < 0 ||
+      po_head < 0)
+    return SWM_ERR_INVALID_ARG;
+  if (c->batch == 0) return SWM_OK;
+  if (!weights || !positions || !weights_out || !positions_out || !lengths_out || (!kept && budget > 0))
+    return SWM_ERR_INVALID_ARG;
+  if (lengths_out == c->lengths || (weights_out == weights && (wo_page != w_page || wo_head != w_head)) ||
+      (positions_out == positions && (po_page != p_page || po_head != p_head)))
+    return SWM_ERR_INVALID_ARG;
+  swm_log("kv_evict B=%lld heads=%lld D=%lld capacity=%lld: budget %lld, recent %lld", (long long)c->batch,
+          (long long)c->heads, (long long)c->dim, (long long)(c->pages_per_seq * c->page_size), (long long)budget,
+          (long long)recent);
+  swm::EvictCall r;
+  r.weights = weights;
+  r.positions = positions;
+  r.weights_out = weights_out;
+  r.positions_out = positions_out;
+  r.lengths_out = lengths_out;
+  r.kept = kept;
+  r.w_p = w_page;
+  r.w_h = w_head;
+  r.p_p = p_page;
+  r.p_h = p_head;
+  r.wo_p = wo_page;
+  r.wo_h = wo_head;
+  r.po_p = po_page;
+  r.po_h = po_head;
+  r.budget = budget;
+  r.recent = recent;
+  SWM_HIP(swm::launch_evict(v, r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
+swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64_t V, int64_t ld,
+                              const void* targets, int32_t wide, float* logp, float* entropy, int32_t top,
+                              int64_t* top_ids, float* top_logp, void* stream) {
+  if (N < 0 || V < 1 || ld < V || top < 0 || (targets && !logp)) return SWM_ERR_INVALID_ARG;
+  if (top > swm::kLogprobMaxTop || V >= (int64_t(1) << 31) - 65536 || N >= (int64_t(1) << 22))
+    return SWM_ERR_UNSUPPORTED;
+  if (N == 0) return SWM_OK;
+  if (!logits || (top > 0 && (!top_ids || !top_logp))) return SWM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % (fp32 ? 4 : 2)) return SWM_ERR_ALIGN;
+  swm::LogprobCall r;
+  r.logits = logits;
+  r.targets = targets;
+  r.logp = logp;
+  r.entropy = entropy;
+  r.top_logp = top_logp;
+  r.top_ids = top_ids;
+  r.N = N;
+  r.V = V;
+  r.ld = ld;
+  r.top = top;
+  r.fp32 = fp32 != 0;
+  r.wide = wide != 0;
+  swm_log("token_logprobs N=%lld V=%lld top=%d: a workgroup per row", (long long)N, (long long)V, top);
+  SWM_HIP(swm::launch_logprobs(r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
 }  // extern "C"

@@ -1,0 +1,194 @@
+"""token_logprobs against log softmax in 64 bits.
+
+Tolerances: log p = (x - m) - log l.  The exponent x log2(e) - m log2(e) is one
+fused multiply-add of fp32 numbers: off by 2^-24 of itself and, in common with
+every other logit of the row, by the rounding of the base (2^-24 |m|, which
+cancels between the two terms) and of log2(e) (2^-25 of x - m).  An exponential
+is off by 2^-22 of itself and l, whose rounding grows with the running sum, by
+2^-18 at most for the lengths here.  With d the larger of 1 and |log p|, an
+error of 2^-18 + 2^-21 d (the entropy, a sum of p log p, the same with d = 1 +
+its own log range).
+"""
+import numpy as np
+import pytest
+
+import sparse_weight_matmul_amd as swm
+
+gpu = pytest.mark.gpu
+
+
+def reference(x, top):
+    x = x.astype(np.float64)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        m = x.max(-1, keepdims=True)
+        m0 = np.where(np.isfinite(m), m, 0)
+        z = np.exp(x - m0).sum(-1, keepdims=True)
+        lp = np.where(z > 0, x - m0 - np.log(np.where(z > 0, z, 1)), -np.inf)
+        p = np.exp(lp)
+        h = -np.where(p > 0, p * lp, 0).sum(-1)
+    ids = np.argsort(-x, axis=-1, kind="stable")[:, :top]
+    return lp, h, ids
+
+
+def rows(kind, N, V, dtype, seed=0):
+    r = np.random.default_rng([seed, N, V])
+    x = 2.5 * r.standard_normal((N, V))
+    if kind == "masked":
+        x[r.random((N, V)) < 0.6] = -np.inf
+        x[::3] = -np.inf                      # nothing left
+        x[1::3, : V - 1] = -np.inf            # one token left, the last
+    elif kind == "ties":
+        x = r.integers(-2, 3, (N, V)).astype(float)
+        x[x == 0] *= r.choice([-1.0, 1.0], int((x == 0).sum()))  # zeros of both signs are equal
+    elif kind == "constant":
+        x[:] = 1.5
+        x[::2] = -3.0
+    elif kind == "large":
+        x = x * 4000
+    elif kind == "descending":
+        x = np.tile(np.linspace(30, -30, V), (N, 1))
+    elif kind == "stripes":                   # one place of each 8192 holds all the large ones: one thread's
+        x[:, ::8192] = 20 + r.random((N, len(range(0, V, 8192))))
+    return x.astype(dtype)
+
+
+CASES = [
+    (1, 1, 1, "plain"), (3, 7, 64, "plain"), (5, 100, 20, "plain"), (1, 32000, 5, "plain"), (4, 32001, 0, "plain"),
+    (7, 1029, 64, "plain"), (2, 131071, 32, "plain"), (33, 4099, 1, "plain"), (300, 517, 3, "plain"),
+    (6, 50021, 20, "masked"), (6, 300, 64, "masked"), (4, 20000, 64, "ties"), (4, 900, 40, "ties"),
+    (4, 50000, 33, "constant"), (4, 1500, 64, "constant"), (3, 9999, 10, "large"), (3, 40000, 64, "descending"),
+    (2, 131072, 17, "stripes"), (2, 1100, 64, "constant"), (2, 1030, 64, "plain"),
+]
+
+
+@gpu
+@pytest.mark.parametrize("N,V,top,kind", CASES)
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_against_64_bits(gpu_lib, N, V, top, kind, dtype):
+    import torch
+    x = rows(kind, N, V, dtype)
+    t = np.random.default_rng(1).integers(0, V, N)
+    X, T = torch.from_numpy(x).cuda(), torch.from_numpy(t).cuda()
+    logp, ent, ids, lps = swm.token_logprobs(X, T, top=top)
+    lp, h, want_ids = reference(x, top)
+    want = lp[np.arange(N), t]
+    close(logp.cpu().numpy(), want, np.maximum(1, np.abs(want)))
+    spread = 1 + np.log(V) + np.where(np.isfinite(lp), np.exp(lp) * np.abs(np.where(np.isfinite(lp), lp, 0)), 0).sum(-1)
+    close(ent.cpu().numpy(), h, spread)
+    if top:
+        k = min(top, V)
+        assert np.array_equal(ids.cpu().numpy()[:, :k], want_ids)
+        want = np.take_along_axis(lp, want_ids, -1)
+        close(lps.cpu().numpy()[:, :k], want, np.maximum(1, np.abs(want)))
+        assert bool((ids[:, k:] == -1).all()) and bool((lps[:, k:] == -float("inf")).all())
+    else:
+        assert ids is None and lps is None
+    again = swm.token_logprobs(X, T.int(), top=top)  # the same bits, whatever the targets' type
+    for a, b in zip((logp, ent, ids, lps), again):
+        assert a is None or torch.equal(a, b)
+
+
+def close(got, want, d):
+    fin = np.isfinite(want)
+    assert np.array_equal(got[~fin], want[~fin].astype(np.float32), equal_nan=True)
+    with np.errstate(invalid="ignore"):
+        bad = (np.abs(got - want) > 2.0**-18 + 2.0**-21 * d) & fin
+    assert not bad.any(), (int(bad.sum()), float(np.abs(got - want)[fin].max()))
+
+
+@gpu
+def test_strides_alignment_and_targets(gpu_lib):
+    import torch
+    x = rows("plain", 6, 1000, np.float16)
+    lp, h, ids = reference(x, 9)
+    wide = torch.full((6, 1017), float("nan"), dtype=torch.float16, device="cuda")
+    t = torch.tensor([0, 999, -1, -100, 1000, 5], device="cuda")
+    for off in range(9):  # every alignment of a row's start
+        wide.fill_(float("nan"))
+        wide[:, off:off + 1000] = torch.from_numpy(x).cuda()
+        logp, ent, got, _ = swm.token_logprobs(wide[:, off:off + 1000], t, top=9)
+        assert np.array_equal(got.cpu().numpy(), ids)
+        logp = logp.cpu().numpy()
+        assert np.all(logp[2:4] == 0) and np.isnan(logp[4])
+        close(logp[[0, 1, 5]], lp[[0, 1, 5], [0, 999, 5]], 8.0)
+        close(ent.cpu().numpy(), h, 8.0)
+    none, ent, _, _ = swm.token_logprobs(wide[:, 8:1008])
+    assert none is None
+    close(ent.cpu().numpy(), h, 8.0)
+    a = swm.token_logprobs(wide[:0, :1000], t[:0], top=2)
+    assert a[0].shape == (0,) and a[2].shape == (0, 2)
+
+
+@gpu
+def test_infinities_and_nan(gpu_lib):
+    import torch
+    x = np.zeros((4, 3000), np.float32)
+    x[0, 77], x[1, 2999] = np.nan, np.inf
+    x[2, 5] = -np.nan
+    x[3] = np.linspace(-1, 1, 3000)
+    logp, ent, ids, lps = swm.token_logprobs(torch.from_numpy(x).cuda(), torch.tensor([3, 3, 3, 3]).cuda(), top=3)
+    assert bool(torch.isnan(logp[:3]).logical_or(logp[:3] == -float("inf")).all())
+    assert bool(torch.isnan(ent[:3]).all())
+    assert bool(((ids >= 0) & (ids < 3000)).all())
+    lp, h, want = reference(x[3:], 3)
+    assert np.array_equal(ids[3:].cpu().numpy(), want)
+    close(ent[3:].cpu().numpy(), h, 8.0)
+
+
+@gpu
+def test_graph_and_stream(gpu_lib):
+    import torch
+    X, T = torch.from_numpy(rows("plain", 9, 3333, np.float16)).cuda(), torch.arange(9, device="cuda")
+    swm.token_logprobs(X, T, top=4)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = swm.token_logprobs(X, T, top=4)
+    for seed in (1, 2, 3):
+        X.copy_(torch.from_numpy(rows("plain", 9, 3333, np.float16, seed)))
+        eager = swm.token_logprobs(X, T, top=4)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = swm.token_logprobs(X, T, top=4, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(out, other))
+
+
+@gpu
+def test_binding_refuses(gpu_lib):
+    import torch
+    X = torch.zeros((4, 100), dtype=torch.float16, device="cuda")
+    T = torch.zeros(4, dtype=torch.int64, device="cuda")
+    with pytest.raises(TypeError):
+        swm.token_logprobs(X.double(), T)
+    with pytest.raises(TypeError):
+        swm.token_logprobs(X, T.float())
+    with pytest.raises(ValueError):
+        swm.token_logprobs(X, T[:3])
+    with pytest.raises(ValueError):
+        swm.token_logprobs(X.t(), torch.zeros(100, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):  # rows that overlap
+        swm.token_logprobs(X.view(-1).as_strided((4, 100), (50, 1)), T)
+    with pytest.raises(swm.SwmError):
+        swm.token_logprobs(X, T, top=65)
+    with pytest.raises(swm.SwmError):
+        swm.token_logprobs(X, T, top=-1)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(logits=None), 1), (dict(N=-1), 1), (dict(V=0), 1), (dict(ld=99), 1), (dict(top=-1), 1),
+    (dict(logp=None), 1), (dict(top_ids=None), 1), (dict(top_logp=None), 1), (dict(logits=4097), 3),
+    (dict(fp32=1, logits=4098), 3), (dict(top=65), 8), (dict(V=1 << 31, ld=1 << 31), 8), (dict(N=1 << 22), 8),
+])
+def test_call_refusals(change, code):
+    a = dict(logits=4096, fp32=0, N=4, V=100, ld=100, targets=8192, wide=1, logp=12288, entropy=16384, top=5,
+             top_ids=20480, top_logp=24576, stream=None)
+    a.update(change)
+    assert swm.load().swm_token_logprobs(*a.values()) == code
+
+
+def test_nothing_to_do():
+    assert swm.load().swm_token_logprobs(None, 0, 0, 100, 100, None, 0, None, None, 0, None, None, None) == 0
