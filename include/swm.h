@@ -456,6 +456,31 @@ swm_status swm_dense_gemm(const void* W, int64_t ldw, const void* X, int64_t ldx
 swm_status swm_hbm_stream(const void* buf, size_t bytes, int32_t unroll, int32_t blocks,
                           uint32_t* out, void* stream);
 
+/* Activations of swm_spmm_epilogue: x, max(x, 0), x / (1 + e^-x), and x Phi(x)
+ * with the normal distribution function Phi (GELU by the error function). */
+#define SWM_ACT_NONE 0
+#define SWM_ACT_RELU 1
+#define SWM_ACT_SILU 2
+#define SWM_ACT_GELU 3
+
+/* spmm_epilogue: swm_spmm_ws with what follows the product done on its fp32
+ * sums,
+ *   Y[n][m] = act(sum_k (W (.) mask)[m][k] X[n][k] + bias[m]) + residual[n][m],
+ * rounded once to fp16, by every route of that call and in the same launches:
+ * the output projections of a block with the residual stream, or a
+ * feed-forward projection with its bias and activation.
+ *  bias: DEVICE fp16, M entries, or NULL.  act: SWM_ACT_*.  residual: DEVICE
+ *  fp16 token-major N x M (ldr >= M), or NULL; it may be Y itself (same
+ *  address and ldr == ldy: an update in place), and must not overlap it
+ *  otherwise.  The other arguments, the workspace
+ *  (swm_spmm_workspace_bytes) and the errors are swm_spmm_ws's; with no bias,
+ *  no residual and SWM_ACT_NONE the result is the same bits.
+ *  SWM_ERR_INVALID_ARG also: an unknown act, ldr < M, residual == Y with
+ *  ldr != ldy. */
+swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
+                             const void* bias, int32_t act, const void* residual, int64_t ldr, void* workspace,
+                             size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ serving
  * What a pruned model's decode step needs between its products. */
 

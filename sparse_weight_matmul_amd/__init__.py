@@ -70,6 +70,7 @@ SIGNATURES = {
     "swm_spmm": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp]),
     "swm_spmm_workspace_bytes": (_sz, [_vp, _i64]),
     "swm_spmm_ws": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "swm_spmm_epilogue": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _vp, _i64, _vp, _sz, _vp]),
     "swm_spmspv": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp]),
     "swm_spmspv_noalloc": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp]),
     "swm_spmspv_threshold": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, ctypes.c_float, _vp]),
@@ -342,6 +343,43 @@ def spmm_ws(fmt: Format, X, workspace, Y=None, stream=None):
             raise ValueError("workspace must be a contiguous CUDA tensor")
         wp, wb = ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
     _check(lib.swm_spmm_ws(fmt._h, xp, ldx, yp, ldy, N, wp, wb, _stream_ptr(stream)), "swm_spmm_ws")
+    return Y
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, workspace=None, Y=None, stream=None):
+    """Y (N, M) = act(X @ (W * mask).T + bias) + residual, rounded once: spmm_ws
+    with its epilogue in the same launches.  bias: (M,) fp16 or None; act:
+    "none", "relu", "silu" or "gelu"; residual: (N, M) fp16 or None, which may
+    be Y itself; workspace: as for spmm_ws (spmm_workspace_bytes)."""
+    import torch
+    lib = load()
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    N = X.shape[0]
+    xp, ldx = _dev2d(X, "X", cols=fmt.K)
+    Y = _out(Y, N, fmt.M, X)
+    yp, ldy = _dev2d(Y, "Y", rows=N, cols=fmt.M)
+    bp = rp = None
+    ldr = 0
+    if bias is not None:
+        if not bias.is_cuda or bias.dtype != torch.float16 or bias.shape != (fmt.M,):
+            raise TypeError(f"bias must be a float16 CUDA tensor, ({fmt.M},)")
+        if fmt.M > 1 and bias.stride(0) != 1:
+            raise ValueError("bias must be contiguous")
+        bp = bias.data_ptr()
+    if residual is not None:
+        rp, ldr = _dev2d(residual, "residual", rows=N, cols=fmt.M)
+    if workspace is None:
+        wp, wb = None, 0
+    else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.swm_spmm_epilogue(fmt._h, xp, ldx, yp, ldy, N, bp, ACTIVATIONS[act], rp, ldr, wp, wb,
+                                 _stream_ptr(stream)), "swm_spmm_epilogue")
     return Y
 
 

@@ -428,10 +428,10 @@ static const swm::DecodePlan& decode_plan(const swm_format* f, int64_t n) {
 }
 
 static bool run_smf(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
-                    hipStream_t s, swm_status* st);
+                    const swm::Epilogue& epi, hipStream_t s, swm_status* st);
 
 static swm_status run_products(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy,
-                               int64_t N, bool skip, hipStream_t s) {
+                               int64_t N, bool skip, hipStream_t s, const swm::Epilogue& epi = {}) {
   if (!f || !X || !Y) return SWM_ERR_INVALID_ARG;
   if (N <= 0 || ldx < f->h.k || ldy < f->h.m || ldx <= 0 || ldy <= 0) return SWM_ERR_INVALID_ARG;
   swm_status st = check_tile_supported(f->h);
@@ -446,16 +446,19 @@ static swm_status run_products(const swm_format* f, const void* X, int64_t ldx, 
     swm_log("%s M=%lld K=%lld N=%lld: decode (%s, %d tiles x %d waves per slab)", skip ? "spmspv" : "spmm",
             (long long)f->h.m, (long long)f->h.k, (long long)N, p.seq_segs > 0 && N <= 16 ? "straight-line" : "looped",
             p.tiles_per_wave, p.waves);
-    SWM_HIP(swm::launch_decode(f->d, p, x, ldx, y, ldy, int(N), skip, s));
+    if (epi.on)
+      SWM_HIP(swm::launch_decode_fused(f->d, p, x, ldx, y, ldy, int(N), epi, s));
+    else
+      SWM_HIP(swm::launch_decode(f->d, p, x, ldx, y, ldy, int(N), skip, s));
     return SWM_OK;
   }
   swm_status sst = SWM_OK;
-  if (!skip && run_smf(f, X, ldx, Y, ldy, N, s, &sst)) return sst;
+  if (!skip && run_smf(f, X, ldx, Y, ldy, N, epi, s, &sst)) return sst;
   if (!skip && swm::prefill_supported(f->h.k, ldx, X) && swm::prefill_sparse_lds(f->h) <= 160 * 1024 &&
       swm::prefill_sparse_fits(f->h, N, ldx)) {
     swm_log("spmm M=%lld K=%lld N=%lld: on-chip prefill (128x256 blocks)", (long long)f->h.m, (long long)f->h.k,
             (long long)N);
-    SWM_HIP(swm::launch_prefill_sparse(f->d, x, ldx, y, ldy, N, s));
+    SWM_HIP(swm::launch_prefill_sparse(f->d, x, ldx, y, ldy, N, s, epi));
     return SWM_OK;
   }
   swm_log("%s M=%lld K=%lld N=%lld: decode in %d-token slices", skip ? "spmspv" : "spmm", (long long)f->h.m,
@@ -465,7 +468,14 @@ static swm_status run_products(const swm_format* f, const void* X, int64_t ldx, 
   const int64_t slice = skip ? 16 : 32;
   for (int64_t n0 = 0; n0 < N; n0 += slice) {
     const int nn = int(std::min<int64_t>(slice, N - n0));
-    SWM_HIP(swm::launch_decode(f->d, decode_plan(f, nn), x + n0 * ldx, ldx, y + n0 * ldy, ldy, nn, skip, s));
+    swm::Epilogue part = epi;
+    if (part.residual) part.residual += n0 * part.ldr;
+    const uint16_t* xn = x + n0 * ldx;
+    uint16_t* yn = y + n0 * ldy;
+    if (epi.on)
+      SWM_HIP(swm::launch_decode_fused(f->d, decode_plan(f, nn), xn, ldx, yn, ldy, nn, part, s));
+    else
+      SWM_HIP(swm::launch_decode(f->d, decode_plan(f, nn), xn, ldx, yn, ldy, nn, skip, s));
   }
   return SWM_OK;
 }
@@ -531,7 +541,7 @@ static bool smf_route(const swm_format* f, int64_t N) {
 // The cached layers through v_smfmac; false when the operands do not fit the
 // kernel's 32-bit offsets or alignment (then the caller takes another route).
 static bool run_smf(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
-                    hipStream_t s, swm_status* st) {
+                    const swm::Epilogue& epi, hipStream_t s, swm_status* st) {
   if (!smf_route(f, N) || !swm::prefill_supported(f->h.k, ldx, X) || !swm::smf_fits(f->h, N, ldx)) return false;
   swm_log("spmm M=%lld K=%lld N=%lld: resident 2:4 layers + SMFMAC (%s)", (long long)f->h.m, (long long)f->h.k,
           (long long)N, f->res24 ? "with residual layer" : "no residual");
@@ -539,7 +549,7 @@ static bool run_smf(const swm_format* f, const void* X, int64_t ldx, void* Y, in
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess)
     e = swm::launch_smf(f->h, f->smf_layout, f->res24, f->smf_mem, static_cast<const uint16_t*>(X), ldx,
-                        static_cast<uint16_t*>(Y), ldy, N, num_cus(dev), s);
+                        static_cast<uint16_t*>(Y), ldy, N, num_cus(dev), s, epi);
   *st = e == hipSuccess ? SWM_OK : hip_fail(e);
   return true;
 }
@@ -549,15 +559,15 @@ size_t swm_spmm_workspace_bytes(const swm_format* f, int64_t N) {
   return align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
 }
 
-swm_status swm_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
-                       void* workspace, size_t ws_bytes, void* stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
+static swm_status run_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
+                              void* workspace, size_t ws_bytes, hipStream_t s, const swm::Epilogue& epi) {
   if (!f || !X || !Y) return SWM_ERR_INVALID_ARG;
-  if (!workspace && ws_bytes == 0) return run_products(f, X, ldx, Y, ldy, N, false, s);
+  if (!workspace && ws_bytes == 0) return run_products(f, X, ldx, Y, ldy, N, false, s, epi);
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return SWM_ERR_ALIGN;
   if (!workspace) return SWM_ERR_INVALID_ARG;
   const size_t need = swm_spmm_workspace_bytes(f, N);
-  if (need == 0 || !swm::prefill_supported(f->h.k, ldx, X)) return run_products(f, X, ldx, Y, ldy, N, false, s);
+  if (need == 0 || !swm::prefill_supported(f->h.k, ldx, X))
+    return run_products(f, X, ldx, Y, ldy, N, false, s, epi);
   if (ws_bytes < need) return SWM_ERR_INVALID_ARG;
   if (N <= 0 || ldx < f->h.k || ldy < f->h.m) return SWM_ERR_INVALID_ARG;
   swm_status st = check_tile_supported(f->h);
@@ -570,8 +580,27 @@ swm_status swm_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y,
   int dev = 0;
   SWM_HIP(hipGetDevice(&dev));
   SWM_HIP(swm::launch_prefill_dense(w, f->h.k, static_cast<const uint16_t*>(X), ldx, static_cast<uint16_t*>(Y),
-                                    ldy, f->h.m, f->h.k, N, num_cus(dev), s));
+                                    ldy, f->h.m, f->h.k, N, num_cus(dev), s, epi));
   return SWM_OK;
+}
+
+swm_status swm_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
+                       void* workspace, size_t ws_bytes, void* stream) {
+  return run_spmm_ws(f, X, ldx, Y, ldy, N, workspace, ws_bytes, static_cast<hipStream_t>(stream), {});
+}
+
+swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
+                             const void* bias, int32_t act, const void* residual, int64_t ldr, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (!f || act < SWM_ACT_NONE || act > SWM_ACT_GELU) return SWM_ERR_INVALID_ARG;
+  if (residual && (ldr < f->h.m || ldr <= 0 || (residual == Y && ldr != ldy))) return SWM_ERR_INVALID_ARG;
+  swm::Epilogue e;
+  e.bias = static_cast<const uint16_t*>(bias);
+  e.residual = static_cast<const uint16_t*>(residual);
+  e.ldr = residual ? ldr : 0;
+  e.act = act;
+  e.on = bias || residual || act != SWM_ACT_NONE;
+  return run_spmm_ws(f, X, ldx, Y, ldy, N, workspace, ws_bytes, static_cast<hipStream_t>(stream), e);
 }
 
 static swm_status run_colruns(const swm_format* f, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t n,

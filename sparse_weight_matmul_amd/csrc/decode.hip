@@ -26,6 +26,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "epilogue.h"
 #include "kernels.h"
 
 namespace swm {
@@ -194,6 +195,32 @@ __device__ __forceinline__ void slab_reduce_glu_store(float* red, int wpm, int w
   }
 }
 
+// As slab_reduce_store with an epilogue.  Its operands are requested before
+// the barrier, so that they arrive while the last waves finish; the threads
+// are a multiple of 16, so one thread's outputs are all of one row.
+__device__ __forceinline__ void slab_reduce_fused_store(float* red, int nwaves, int wave, int lane, const f32x4& acc,
+                                                        int slab, int M, int N, uint16_t* Y, int64_t ldy,
+                                                        const Epilogue& epi) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) red[wave * 256 + (lane & 15) * 16 + (lane >> 4) * 4 + v] = acc[v];
+  const int row = threadIdx.x & 15, m = min(slab * kSlab + row, M - 1);
+  int tok = threadIdx.x >> 4;
+  const float bias = epi.bias ? half_at(epi.bias + m) : 0.f;
+  float res = epi.residual && tok < N ? half_at(epi.residual + int64_t(tok) * epi.ldr + m) : 0.f;
+  __syncthreads();
+  for (int e = threadIdx.x; e < N * kSlab; e += blockDim.x, tok = e >> 4) {
+    float v[16];
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v[w] = red[min(w, nwaves - 1) * 256 + e];
+    float sum = bias;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum += w < nwaves ? v[w] : 0.f;
+    with_act(epi.act, [&](auto act) { sum = activate<act>(sum); });
+    if (epi.residual && e != int(threadIdx.x)) res = half_at(epi.residual + int64_t(tok) * epi.ldr + m);
+    if (slab * kSlab + row < M) Y[int64_t(tok) * ldy + m] = __builtin_bit_cast(uint16_t, _Float16(sum + res));
+  }
+}
+
 struct DecodeArgs {
   const uint32_t* tile_ptr;
   const uint64_t* bits;
@@ -217,13 +244,20 @@ struct GluArgs : DecodeArgs {
   int wpm;
   float tau;
 };
-template <bool kGlu>
+struct FusedArgs : DecodeArgs {
+  Epilogue epi;
+};
+template <int kEpi>
 struct SeqArgs {
   using type = DecodeArgs;
 };
 template <>
-struct SeqArgs<true> {
+struct SeqArgs<kGated> {
   using type = GluArgs;
+};
+template <>
+struct SeqArgs<kFused> {
+  using type = FusedArgs;
 };
 
 constexpr int kSegTiles = 4;  // tiles per streamed segment
@@ -241,8 +275,8 @@ constexpr int kSegTiles = 4;  // tiles per streamed segment
 // is still streamed).  kH = 2 serves 17 <= N <= 32 tokens: each decoded A
 // operand feeds two MFMAs, one per group of 16 tokens, so the weight stream is
 // read once for all of them.
-template <int kC, bool kSkip, bool kVec, int kH = 1>
-__global__ __launch_bounds__(1024) void decode_kernel(DecodeArgs a) {
+template <int kC, bool kSkip, bool kVec, int kH = 1, int kEpi = kPlain>
+__global__ __launch_bounds__(1024) void decode_kernel(typename SeqArgs<kEpi>::type a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -407,9 +441,19 @@ __global__ __launch_bounds__(1024) void decode_kernel(DecodeArgs a) {
   if (keep == 0x9E3779B9u && a.N < 0) a.Y[0] = 0;  // never true: keeps the prefetch loads
 
   __syncthreads();  // all segment buffers are free: reuse them as the reduction area
-  slab_reduce_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc[0], slab, a.M, min(a.N, 16),
-                    a.Y, a.ldy);
-  if constexpr (kH == 2) {
+  if constexpr (kEpi == kFused)
+    slab_reduce_fused_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc[0], slab, a.M,
+                            min(a.N, 16), a.Y, a.ldy, a.epi);
+  else
+    slab_reduce_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc[0], slab, a.M, min(a.N, 16),
+                      a.Y, a.ldy);
+  if constexpr (kH == 2 && kEpi == kFused) {
+    __syncthreads();  // every thread is done reading the first group's partials
+    Epilogue epi = a.epi;
+    if (epi.residual) epi.residual += 16 * epi.ldr;
+    slab_reduce_fused_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc[1], slab, a.M, a.N - 16,
+                            a.Y + 16 * a.ldy, a.ldy, epi);
+  } else if constexpr (kH == 2) {
     __syncthreads();  // every thread is done reading the first group's partials
     slab_reduce_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc[1], slab, a.M, a.N - 16,
                       a.Y + 16 * a.ldy, a.ldy);
@@ -469,8 +513,9 @@ constexpr int kXRow = 272;
 // none when the B operands are loaded straight into registers).
 constexpr int seq_x_bytes(int kxi, bool direct) { return direct ? 0 : 4 * kxi * kXRow; }
 
-template <int NS, int kC, int kXI, bool kGlu = false, bool kDB = false>
-__global__ __launch_bounds__(1024) void decode_seq_kernel(typename SeqArgs<kGlu>::type a) {
+template <int NS, int kC, int kXI, int kEpi = kPlain, bool kDB = false>
+__global__ __launch_bounds__(1024) void decode_seq_kernel(typename SeqArgs<kEpi>::type a) {
+  constexpr bool kGlu = kEpi == kGated;
   static_assert(!kDB || kXI == 4, "B operands straight from memory only with 16 staged token rows");
   constexpr int kT = 2 * NS;      // tile slots per wave
   constexpr int kSteps = 2 * kT;  // 32-column steps
@@ -703,6 +748,9 @@ __global__ __launch_bounds__(1024) void decode_seq_kernel(typename SeqArgs<kGlu>
   if constexpr (kGlu)
     slab_reduce_glu_store(reinterpret_cast<float*>(smem + 16), a.wpm, wave, lane, acc, slab, a.M, a.N, a.Y, a.ldy,
                           a.tau);
+  else if constexpr (kEpi == kFused)
+    slab_reduce_fused_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc, slab, a.M, a.N, a.Y, a.ldy,
+                            a.epi);
   else
     slab_reduce_store(reinterpret_cast<float*>(smem + 16), nwaves, wave, lane, acc, slab, a.M, a.N, a.Y, a.ldy);
 }
@@ -961,23 +1009,23 @@ __global__ __launch_bounds__(256) void decompress_kernel(DecompArgs a) {
   }
 }
 
-template <int NS, int kXI, bool kGlu, bool kDB = false>
-void launch_seq_x(int kc, dim3 grid, dim3 block, size_t lds, hipStream_t s, const typename SeqArgs<kGlu>::type& a) {
+template <int NS, int kXI, int kEpi, bool kDB = false>
+void launch_seq_x(int kc, dim3 grid, dim3 block, size_t lds, hipStream_t s, const typename SeqArgs<kEpi>::type& a) {
   switch (kc) {
-    case 1: hipLaunchKernelGGL((decode_seq_kernel<NS, 1, kXI, kGlu, kDB>), grid, block, lds, s, a); break;
-    case 2: hipLaunchKernelGGL((decode_seq_kernel<NS, 2, kXI, kGlu, kDB>), grid, block, lds, s, a); break;
-    case 3: hipLaunchKernelGGL((decode_seq_kernel<NS, 3, kXI, kGlu, kDB>), grid, block, lds, s, a); break;
-    default: hipLaunchKernelGGL((decode_seq_kernel<NS, 4, kXI, kGlu, kDB>), grid, block, lds, s, a); break;
+    case 1: hipLaunchKernelGGL((decode_seq_kernel<NS, 1, kXI, kEpi, kDB>), grid, block, lds, s, a); break;
+    case 2: hipLaunchKernelGGL((decode_seq_kernel<NS, 2, kXI, kEpi, kDB>), grid, block, lds, s, a); break;
+    case 3: hipLaunchKernelGGL((decode_seq_kernel<NS, 3, kXI, kEpi, kDB>), grid, block, lds, s, a); break;
+    default: hipLaunchKernelGGL((decode_seq_kernel<NS, 4, kXI, kEpi, kDB>), grid, block, lds, s, a); break;
   }
 }
 
-template <int NS, bool kGlu = false>
+template <int NS, int kEpi = kPlain>
 void launch_seq_ns(int kc, int kxi, bool direct, dim3 grid, dim3 block, size_t lds, hipStream_t s,
-                   const typename SeqArgs<kGlu>::type& a) {
-  if (kxi == 1) launch_seq_x<NS, 1, kGlu>(kc, grid, block, lds, s, a);
-  else if (kxi == 2) launch_seq_x<NS, 2, kGlu>(kc, grid, block, lds, s, a);
-  else if (direct) launch_seq_x<NS, 4, kGlu, true>(kc, grid, block, lds, s, a);
-  else launch_seq_x<NS, 4, kGlu>(kc, grid, block, lds, s, a);
+                   const typename SeqArgs<kEpi>::type& a) {
+  if (kxi == 1) launch_seq_x<NS, 1, kEpi>(kc, grid, block, lds, s, a);
+  else if (kxi == 2) launch_seq_x<NS, 2, kEpi>(kc, grid, block, lds, s, a);
+  else if (direct) launch_seq_x<NS, 4, kEpi, true>(kc, grid, block, lds, s, a);
+  else launch_seq_x<NS, 4, kEpi>(kc, grid, block, lds, s, a);
 }
 
 // Smallest instantiated segment count covering `segs` two-tile segments (0: none).
@@ -988,11 +1036,24 @@ int seq_instance(int segs) {
   return 0;
 }
 
-template <int kC>
-void launch_decode_c(bool skip, dim3 grid, dim3 block, size_t lds, hipStream_t s, const DecodeArgs& a) {
-  if (a.N > 16) hipLaunchKernelGGL((decode_kernel<kC, false, true, 2>), grid, block, lds, s, a);
-  else if (skip) hipLaunchKernelGGL((decode_kernel<kC, true, true>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((decode_kernel<kC, false, true>), grid, block, lds, s, a);
+// The skipping variants take no epilogue.
+template <int kC, bool kVec, int kEpi>
+void launch_looped(bool skip, dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                   const typename SeqArgs<kEpi>::type& a) {
+  if constexpr (kEpi == kPlain) {
+    if (skip) {
+      hipLaunchKernelGGL((decode_kernel<kC, true, kVec>), grid, block, lds, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((decode_kernel<kC, false, kVec, 1, kEpi>), grid, block, lds, s, a);
+}
+
+template <int kC, int kEpi>
+void launch_decode_c(bool skip, dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                     const typename SeqArgs<kEpi>::type& a) {
+  if (a.N > 16) hipLaunchKernelGGL((decode_kernel<kC, false, true, 2, kEpi>), grid, block, lds, s, a);
+  else launch_looped<kC, true, kEpi>(skip, grid, block, lds, s, a);
 }
 
 int env_int(const char* name, int dflt) {
@@ -1001,6 +1062,97 @@ int env_int(const char* name, int dflt) {
 }
 
 }  // namespace
+
+// The decode product with one of its epilogues (`epi` for kFused).
+template <int kEpi>
+static hipError_t launch_decode_as(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
+                                   uint16_t* Y, int64_t ldy, int n, bool skip, const Epilogue* epi, hipStream_t s) {
+  using Args = typename SeqArgs<kEpi>::type;
+  Args a;
+  if constexpr (kEpi == kFused) a.epi = *epi;
+  a.tile_ptr = f.tile_ptr;
+  a.bits = f.bits;
+  a.vals = f.vals;
+  a.zeros = f.zeros;
+  a.X = X;
+  a.Y = Y;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.M = int(f.h.m);
+  a.K = int(f.h.k);
+  a.N = n;
+  a.kt = int(f.h.kt);
+  a.tpw = p.tiles_per_wave;
+  if (f.h.tm != uint32_t(kSlab) || f.h.tk != uint32_t(kTK)) return hipErrorInvalidValue;
+  if (p.seg_chunks > 8) return hipErrorInvalidValue;  // 4 tiles hold at most 8 KiB
+  const bool vec = (f.h.k % 8 == 0) && (ldx % 8 == 0) && ((reinterpret_cast<uintptr_t>(X) & 15) == 0);
+  const int kC = vec ? p.seg_chunks : 8;
+  const size_t run_bytes = size_t(p.waves) * kC * 1024;
+  const size_t red_bytes = size_t(p.waves) * 256 * 4;
+  const size_t lds = 16 + (run_bytes > red_bytes ? run_bytes : red_bytes);
+  if (f.h.mt == 0) return hipSuccess;
+  const dim3 grid{unsigned(f.h.mt), 1, 1}, block{unsigned(p.waves * 64), 1, 1};
+  // The straight-line kernel addresses X with 32-bit byte offsets.
+  const bool x32 = 2 * ((int64_t(n) - 1) * ldx + f.h.k) < (int64_t(1) << 32);
+  // Activation skipping is not applied on this path: with 16-row tiles a
+  // bitmap word spans four columns (all inactive for only ~0.7^4 = 24% of
+  // words at 70% zero activations) and a column run is at most 32 bytes, so
+  // neither the decode nor the fetch of inactive columns can be dropped
+  // profitably; the product is computed in full (same result).
+  if (vec && p.seq_segs > 0 && a.K >= 8 && x32 && n <= 16) {
+    const int kxi = n <= 4 ? 1 : n <= 8 ? 2 : 4;
+    const bool direct = p.direct_b && kxi == 4;
+    const size_t per_wave = size_t(p.seq_chunks) * 1024 + size_t(seq_x_bytes(kxi, direct));
+    const size_t seq_lds = 16 + size_t(p.waves) * per_wave;
+    switch (p.seq_segs) {
+      case 1: launch_seq_ns<1, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+      case 2: launch_seq_ns<2, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+      case 3: launch_seq_ns<3, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+      case 4: launch_seq_ns<4, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+      case 6: launch_seq_ns<6, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+      default: launch_seq_ns<8, kEpi>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
+    }
+    return hipGetLastError();
+  }
+  if (!vec) {
+    if (n > 16) {
+      // unaligned activations: two passes of 16 and n - 16 tokens (a
+      // two-group instance of the unaligned kernel would spill registers)
+      Args a2 = a;
+      a2.N = 16;
+      launch_looped<8, false, kEpi>(false, grid, block, lds, s, a2);
+      a2.X = a.X + 16 * a.ldx;
+      a2.Y = a.Y + 16 * a.ldy;
+      if constexpr (kEpi == kFused)
+        if (a2.epi.residual) a2.epi.residual += 16 * a2.epi.ldr;
+      a2.N = n - 16;
+      launch_looped<8, false, kEpi>(false, grid, block, lds, s, a2);
+    } else launch_looped<8, false, kEpi>(skip, grid, block, lds, s, a);
+    return hipGetLastError();
+  }
+  switch (kC) {
+    case 1: launch_decode_c<1, kEpi>(skip, grid, block, lds, s, a); break;
+    case 2: launch_decode_c<2, kEpi>(skip, grid, block, lds, s, a); break;
+    case 3: launch_decode_c<3, kEpi>(skip, grid, block, lds, s, a); break;
+    case 4: launch_decode_c<4, kEpi>(skip, grid, block, lds, s, a); break;
+    case 5: launch_decode_c<5, kEpi>(skip, grid, block, lds, s, a); break;
+    case 6: launch_decode_c<6, kEpi>(skip, grid, block, lds, s, a); break;
+    case 7: launch_decode_c<7, kEpi>(skip, grid, block, lds, s, a); break;
+    default: launch_decode_c<8, kEpi>(skip, grid, block, lds, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+#ifdef SWM_DECODE_FUSED_UNIT
+hipError_t launch_decode_fused(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
+                               uint16_t* Y, int64_t ldy, int n, const Epilogue& epi, hipStream_t s) {
+  return launch_decode_as<kFused>(f, p, X, ldx, Y, ldy, n, false, &epi, s);
+}
+#else
+hipError_t launch_decode(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
+                         uint16_t* Y, int64_t ldy, int n, bool skip, hipStream_t s) {
+  return launch_decode_as<kPlain>(f, p, X, ldx, Y, ldy, n, skip, nullptr, s);
+}
 
 // ------------------------------------------------------------------ host launchers
 // Largest two-tile segment of ranges of `tpw` tiles, in 1 KiB loads.
@@ -1117,81 +1269,6 @@ DecodePlan plan_decode(const Header& h, const uint32_t* tp, int num_cus, int wav
   const char* path = getenv("SWM_DECODE_PATH");
   if (getenv("SWM_DECODE_LOOP") || (path && !strcmp(path, "loop"))) p.seq_segs = 0;
   return p;
-}
-
-hipError_t launch_decode(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
-                         uint16_t* Y, int64_t ldy, int n, bool skip, hipStream_t s) {
-  DecodeArgs a;
-  a.tile_ptr = f.tile_ptr;
-  a.bits = f.bits;
-  a.vals = f.vals;
-  a.zeros = f.zeros;
-  a.X = X;
-  a.Y = Y;
-  a.ldx = ldx;
-  a.ldy = ldy;
-  a.M = int(f.h.m);
-  a.K = int(f.h.k);
-  a.N = n;
-  a.kt = int(f.h.kt);
-  a.tpw = p.tiles_per_wave;
-  if (f.h.tm != uint32_t(kSlab) || f.h.tk != uint32_t(kTK)) return hipErrorInvalidValue;
-  if (p.seg_chunks > 8) return hipErrorInvalidValue;  // 4 tiles hold at most 8 KiB
-  const bool vec = (f.h.k % 8 == 0) && (ldx % 8 == 0) && ((reinterpret_cast<uintptr_t>(X) & 15) == 0);
-  const int kC = vec ? p.seg_chunks : 8;
-  const size_t run_bytes = size_t(p.waves) * kC * 1024;
-  const size_t red_bytes = size_t(p.waves) * 256 * 4;
-  const size_t lds = 16 + (run_bytes > red_bytes ? run_bytes : red_bytes);
-  if (f.h.mt == 0) return hipSuccess;
-  const dim3 grid{unsigned(f.h.mt), 1, 1}, block{unsigned(p.waves * 64), 1, 1};
-  // The straight-line kernel addresses X with 32-bit byte offsets.
-  const bool x32 = 2 * ((int64_t(n) - 1) * ldx + f.h.k) < (int64_t(1) << 32);
-  // Activation skipping is not applied on this path: with 16-row tiles a
-  // bitmap word spans four columns (all inactive for only ~0.7^4 = 24% of
-  // words at 70% zero activations) and a column run is at most 32 bytes, so
-  // neither the decode nor the fetch of inactive columns can be dropped
-  // profitably; the product is computed in full (same result).
-  if (vec && p.seq_segs > 0 && a.K >= 8 && x32 && n <= 16) {
-    const int kxi = n <= 4 ? 1 : n <= 8 ? 2 : 4;
-    const bool direct = p.direct_b && kxi == 4;
-    const size_t per_wave = size_t(p.seq_chunks) * 1024 + size_t(seq_x_bytes(kxi, direct));
-    const size_t seq_lds = 16 + size_t(p.waves) * per_wave;
-    switch (p.seq_segs) {
-      case 1: launch_seq_ns<1>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-      case 2: launch_seq_ns<2>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-      case 3: launch_seq_ns<3>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-      case 4: launch_seq_ns<4>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-      case 6: launch_seq_ns<6>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-      default: launch_seq_ns<8>(p.seq_chunks, kxi, direct, grid, block, seq_lds, s, a); break;
-    }
-    return hipGetLastError();
-  }
-  if (!vec) {
-    if (n > 16) {
-      // unaligned activations: two passes of 16 and n - 16 tokens (a
-      // two-group instance of the unaligned kernel would spill registers)
-      DecodeArgs a2 = a;
-      a2.N = 16;
-      hipLaunchKernelGGL((decode_kernel<8, false, false>), grid, block, lds, s, a2);
-      a2.X = a.X + 16 * a.ldx;
-      a2.Y = a.Y + 16 * a.ldy;
-      a2.N = n - 16;
-      hipLaunchKernelGGL((decode_kernel<8, false, false>), grid, block, lds, s, a2);
-    } else if (skip) hipLaunchKernelGGL((decode_kernel<8, true, false>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((decode_kernel<8, false, false>), grid, block, lds, s, a);
-    return hipGetLastError();
-  }
-  switch (kC) {
-    case 1: launch_decode_c<1>(skip, grid, block, lds, s, a); break;
-    case 2: launch_decode_c<2>(skip, grid, block, lds, s, a); break;
-    case 3: launch_decode_c<3>(skip, grid, block, lds, s, a); break;
-    case 4: launch_decode_c<4>(skip, grid, block, lds, s, a); break;
-    case 5: launch_decode_c<5>(skip, grid, block, lds, s, a); break;
-    case 6: launch_decode_c<6>(skip, grid, block, lds, s, a); break;
-    case 7: launch_decode_c<7>(skip, grid, block, lds, s, a); break;
-    default: launch_decode_c<8>(skip, grid, block, lds, s, a); break;
-  }
-  return hipGetLastError();
 }
 
 DensePlan plan_dense_small(int64_t M, int64_t K, int n, int num_cus) {
@@ -1383,5 +1460,7 @@ hipError_t launch_stream(const void* src, size_t bytes, int unroll, int blocks, 
   }
   return hipGetLastError();
 }
+
+#endif  // SWM_DECODE_FUSED_UNIT
 
 }  // namespace swm

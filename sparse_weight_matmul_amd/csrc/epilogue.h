@@ -1,0 +1,198 @@
+// What a product's epilogue does to an fp32 sum before its one rounding:
+// act(sum + bias[m]) + residual[n][m].
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace swm {
+
+// GELU by the error function, v Phi(v) = v erfc(-v / sqrt 2) / 2.  The tail is
+// taken as erfc(u) = t P(t) e^(-u^2), t = 1 / (1 + u/2), with P fitted to a
+// relative error of 1.6e-6 over u = 0..10 (beyond, e^(-u^2) is below fp32):
+// relative, so that small results of large negative v keep their bits where
+// 1 + erf would cancel.  About 16 instructions; erff() takes twice as many,
+// on 128 outputs a lane.
+__device__ __forceinline__ float gelu(float v) {
+  const float u = fabsf(v) * 0.70710678118654752440f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, u, 1.f));
+  float p = 0.0882040471f;
+  p = __builtin_fmaf(p, t, -0.3567372f);
+  p = __builtin_fmaf(p, t, 0.389223116f);
+  p = __builtin_fmaf(p, t, 0.0378916923f);
+  p = __builtin_fmaf(p, t, 0.281503372f);
+  p = __builtin_fmaf(p, t, 0.277582214f);
+  p = __builtin_fmaf(p, t, 0.282331407f);
+  const float q = 0.5f * t * p * __builtin_amdgcn_exp2f(u * u * -1.44269504088896340736f);
+  if (v >= 0.f) return v * (1.f - q);
+  return q == 0.f ? -0.f : v * q;  // -inf too
+}
+
+// The epilogues a product kernel is built with: none, the gated FFN step's, or
+// `Epilogue`.  Kernels without one keep their own instances: the epilogue's
+// operands and code would cost some of them registers and occupancy.
+enum { kPlain, kGated, kFused };
+
+template <int kAct>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (kAct == 1) return v < 0.f ? 0.f : v;
+  if constexpr (kAct == 2)
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
+  if constexpr (kAct == 3) return gelu(v);
+  return v;
+}
+
+// f(std::integral_constant<int, act>), for loops over many outputs: one
+// branch for all of them.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    default: f(std::integral_constant<int, 0>{}); break;
+  }
+}
+
+__device__ __forceinline__ float half_at(const uint16_t* p) { return float(__builtin_bit_cast(_Float16, *p)); }
+
+// The matrix products' outputs.  A wave holds kI x kJ accumulators of 32 x 32:
+// element v of lane l of accumulator (i, j) is row 32 i + 8 (v/4) + 4 (l/32) +
+// v%4 and token 32 j + l%32, from row m0 and token n0 on.
+typedef float epi_f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t epi_u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t epi_u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) epi_u32x2 epi_lds_u32x2;
+
+// Four consecutive halves from p[at]; those from p[end] on read p[end - 1].
+__device__ __forceinline__ epi_u32x2 halves4(const uint16_t* p, int at, int end, bool aligned8) {
+  if (aligned8 && at + 4 <= end) return *reinterpret_cast<const epi_u32x2*>(p + at);
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = p[min(at + e, end - 1)];
+  return epi_u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+}
+__device__ __forceinline__ float half_of(const epi_u32x2& w, int e) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(w[e / 2] >> (16 * (e % 2)))));
+}
+__device__ __forceinline__ bool aligned(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// The bias of a lane's rows, all requested at once.
+template <int kI>
+__device__ __forceinline__ void load_bias(const Epilogue& e, int m0, int M, int lane, epi_u32x2 (&bias)[kI][4]) {
+  const bool vec = aligned(e.bias, 8);  // m0 and the lane's rows are multiples of 4
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      bias[i][q] = e.bias ? halves4(e.bias, m0 + i * 32 + q * 8 + (lane >> 5) * 4, M, vec) : epi_u32x2{0, 0};
+}
+
+// One lane's four outputs of accumulator (i, j), rounded and packed.
+template <int kAct>
+__device__ __forceinline__ epi_u32x2 fuse4(const epi_f32x16& acc, int q, const epi_u32x2& bias,
+                                           const epi_u32x2& res) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = __builtin_bit_cast(
+        uint16_t, _Float16(activate<kAct>(acc[q * 4 + e] + half_of(bias, e)) + half_of(res, e)));
+  return epi_u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+}
+
+// Outputs into the wave's LDS region, a row of `stride` bytes per token, from
+// where the kernel stores them.  The residual comes in by the same way: whole
+// rows, 16 bytes a lane, and every lane finds the values of its outputs in
+// their places; read directly, a load would take 8 bytes from 32 rows.  The
+// barriers keep the scheduler from starting every output at once, which would
+// spill the accumulators.
+template <int kI, int kJ>
+__device__ __forceinline__ void fuse_to_lds(const Epilogue& e, const epi_f32x16 (&acc)[kI][kJ], uint32_t reg,
+                                            int stride, int m0, int n0, int M, int N, int lane) {
+  constexpr int kTM = 32 * kI, kTN = 32 * kJ, kLPR = kTM / 8, kRPI = 64 / kLPR;
+  epi_u32x2 bias[kI][4];
+  load_bias(e, m0, M, lane, bias);
+  if (e.residual) {
+    const int gm = m0 + (lane % kLPR) * 8;
+    const bool vec = e.ldr % 8 == 0 && aligned(e.residual, 16) && gm + 8 <= M;
+    for (int r = 0; r < kTN; r += 4 * kRPI) {
+      epi_u32x4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint16_t* src = e.residual + int64_t(min(n0 + r + u * kRPI + lane / kLPR, N - 1)) * e.ldr;
+        if (vec) {
+          v[u] = *reinterpret_cast<const epi_u32x4*>(src + gm);
+        } else {
+          const epi_u32x2 lo = halves4(src, gm, M, false), hi = halves4(src, gm + 4, M, false);
+          v[u] = epi_u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t at = reg + (r + u * kRPI + lane / kLPR) * stride + (lane % kLPR) * 16;  // a multiple of 8
+        *reinterpret_cast<epi_lds_u32x2*>(static_cast<uintptr_t>(at)) = epi_u32x2{v[u][0], v[u][1]};
+        *reinterpret_cast<epi_lds_u32x2*>(static_cast<uintptr_t>(at + 8)) = epi_u32x2{v[u][2], v[u][3]};
+      }
+    }
+  }
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const uint32_t at = reg + (j * 32 + (lane & 31)) * stride + 2 * (i * 32 + (lane >> 5) * 4);
+        epi_u32x2 res[4] = {};
+        if (e.residual) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            res[q] = *reinterpret_cast<const epi_lds_u32x2*>(static_cast<uintptr_t>(at + 16 * q));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<epi_lds_u32x2*>(static_cast<uintptr_t>(at + 16 * q)) =
+              fuse4<act>(acc[i][j], q, bias[i][q], res[q]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  });
+}
+
+// Outputs straight to Y, four rows of a token at a time.
+template <int kI, int kJ>
+__device__ __forceinline__ void fuse_and_store(const Epilogue& e, const epi_f32x16 (&acc)[kI][kJ], int m0, int n0,
+                                               int M, int N, uint16_t* Y, int64_t ldy, int lane) {
+  const bool rvec = e.ldr % 4 == 0 && aligned(e.residual, 8);
+  const bool yvec = ldy % 4 == 0 && aligned(Y, 8);
+  const bool bvec = aligned(e.bias, 8);
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int n = n0 + j * 32 + (lane & 31);
+        const uint16_t* src = e.residual + int64_t(min(n, N - 1)) * e.ldr;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = m0 + i * 32 + q * 8 + (lane >> 5) * 4;
+          const epi_u32x2 bias = e.bias ? halves4(e.bias, m, M, bvec) : epi_u32x2{0, 0};
+          const epi_u32x2 res = e.residual ? halves4(src, m, M, rvec) : epi_u32x2{0, 0};
+          const epi_u32x2 w = fuse4<act>(acc[i][j], q, bias, res);
+          uint16_t* dst = Y + int64_t(n) * ldy + m;
+          if (n < N && m + 4 <= M && yvec) {
+            *reinterpret_cast<epi_u32x2*>(dst) = w;
+          } else if (n < N) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (m + k < M) dst[k] = uint16_t(w[k / 2] >> (16 * (k % 2)));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+  });
+}
+
+}  // namespace swm

@@ -9,6 +9,16 @@
 
 namespace swm {
 
+// What a product does to its fp32 sums before they are rounded: act(sum +
+// bias[m]) + residual[n * ldr + m].
+struct Epilogue {
+  const uint16_t* bias = nullptr;
+  const uint16_t* residual = nullptr;
+  int64_t ldr = 0;
+  int32_t act = 0;  // 0 none, 1 ReLU, 2 SiLU, 3 GELU
+  int32_t on = 0;   // 0: the plain product
+};
+
 // Device memory of one SWM-TCB v2 handle (16-row tiles).
 struct DevFormat {
   Header h;
@@ -40,6 +50,9 @@ DecodePlan plan_decode(const Header& h, const uint32_t* tile_ptr, int num_cus, i
 
 hipError_t launch_decode(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
                          uint16_t* Y, int64_t ldy, int n, bool skip, hipStream_t s);
+// The same product with an epilogue (epi.on).
+hipError_t launch_decode_fused(const DevFormat& f, const DecodePlan& p, const uint16_t* X, int64_t ldx,
+                               uint16_t* Y, int64_t ldy, int n, const Epilogue& epi, hipStream_t s);
 
 // Activation-skipping decode over the SWM-CR v2 column-run encoding.
 constexpr int kCrMaxCols = 1024;  // input columns per workgroup (one per thread)
@@ -92,7 +105,7 @@ hipError_t launch_dense_small(const DensePlan& p, const uint16_t* W, int64_t ldw
 // Tiled MFMA GEMM for larger N: dense W, or W expanded from the format tile by tile.
 hipError_t launch_prefill_dense(const uint16_t* W, int64_t ldw, const uint16_t* X, int64_t ldx,
                                 uint16_t* Y, int64_t ldy, int64_t M, int64_t K, int64_t N, int num_cus,
-                                hipStream_t s);
+                                hipStream_t s, const Epilogue& epi = {});
 // The same kernel with the gated-FFN epilogue: W is M2 = 2 x channels rows
 // with gate and up rows interleaved (2c, 2c+1), H (N x M2/2) receives
 // SiLU(g) * u rounded to fp16, +0 where |h| < tau.  Needs the LDS-direct
@@ -102,7 +115,7 @@ hipError_t launch_prefill_dense_glu(const uint16_t* W, int64_t ldw, const uint16
                                     int num_cus, hipStream_t s);
 bool prefill_dense_dma_fits(int64_t M, int64_t ldw, int64_t K, int64_t N, int64_t ldx);
 hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t ldx, uint16_t* Y,
-                                 int64_t ldy, int64_t N, hipStream_t s);
+                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi = {});
 // The prefill kernels need K >= 8, K % 8 == 0, ldx % 8 == 0 and a 16-byte aligned X.
 bool prefill_supported(int64_t K, int64_t ldx, const void* X);
 size_t prefill_sparse_lds(const Header& h);
@@ -119,7 +132,8 @@ struct Sparse24Layout {
 Sparse24Layout sparse24_layout(const Header& h, bool residual);
 hipError_t launch_compact24(const DevFormat& f, const Sparse24Layout& L, bool residual, void* ws, hipStream_t s);
 hipError_t launch_smf(const Header& h, const Sparse24Layout& L, bool residual, const void* ws, const uint16_t* X,
-                      int64_t ldx, uint16_t* Y, int64_t ldy, int64_t N, int num_cus, hipStream_t s);
+                      int64_t ldx, uint16_t* Y, int64_t ldy, int64_t N, int num_cus, hipStream_t s,
+                      const Epilogue& epi = {});
 // The SMFMAC kernel addresses the compacted layers and X with 32-bit byte offsets.
 bool smf_fits(const Header& h, int64_t N, int64_t ldx);
 

@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <cstdlib>
 
+#include "epilogue.h"
 #include "kernels.h"
 
 namespace swm {
@@ -79,6 +80,17 @@ struct PrefillArgs {
   int run_chunks;  // 512-byte run chunks per tile (1..4), sparse variant
   float tau;       // gated epilogue: |h| below tau (after fp16 rounding) is stored as +0
 };
+struct PrefillFusedArgs : PrefillArgs {
+  Epilogue epi;
+};
+template <int kEpi>
+struct PrefillArgsOf {
+  using type = PrefillArgs;
+};
+template <>
+struct PrefillArgsOf<kFused> {
+  using type = PrefillFusedArgs;
+};
 
 // Map the workgroup id to an output tile: regroup ids so that each XCD (id % 8)
 // gets a contiguous range, then walk that range column-major inside bands of
@@ -101,8 +113,8 @@ __device__ __forceinline__ bool tile_of(const PrefillArgs& a, int& tm, int& tn) 
 // Dense block shapes: waves in a 2 x 2 layout, each owning kWI x kWJ 32 x 32
 // accumulators, so the block is 64 kWI (rows of W) x 64 kWJ (tokens).  The
 // host takes the largest block that still gives every CU work.
-template <int kWI, int kWJ>
-__global__ __launch_bounds__(256) void dense_kernel(PrefillArgs a) {
+template <int kWI, int kWJ, int kEpi = kPlain>
+__global__ __launch_bounds__(256) void dense_kernel(typename PrefillArgsOf<kEpi>::type a) {
   constexpr int kBM = 64 * kWI, kBN = 64 * kWJ;
   constexpr int kAT = kBM * BK * 2, kBT = kBN * BK * 2;  // stage bytes
   constexpr int kRA = kBM / 32, kRB = kBN / 32;         // 16-byte loads per thread
@@ -242,6 +254,10 @@ __global__ __launch_bounds__(256) void dense_kernel(PrefillArgs a) {
   }
 
   // Epilogue: fp16 round-to-nearest-even, 4 consecutive rows per 8-byte store.
+  if constexpr (kEpi == kFused) {
+    fuse_and_store(a.epi, acc, m0 + wm * kWI * 32, n0 + wn * kWJ * 32, a.M, a.N, a.Y, a.ldy, lane);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kWI; ++i)
 #pragma unroll
@@ -319,8 +335,9 @@ struct DmaShape {
 // H (N x M/2), h = SiLU(g) * u rounded once to fp16, +0 where |h| < tau.  A
 // lane's accumulator holds four consecutive rows of one token, so each
 // gate / up pair meets in the same lane's registers.
-template <int kWI, int kWJ, int kWM, int kWN, bool kGlu = false>
-__global__ __launch_bounds__(64 * kWM * kWN) void dense_dma_kernel(PrefillArgs a) {
+template <int kWI, int kWJ, int kWM, int kWN, int kEpi = kPlain>
+__global__ __launch_bounds__(64 * kWM * kWN) void dense_dma_kernel(typename PrefillArgsOf<kEpi>::type a) {
+  constexpr bool kGlu = kEpi == kGated;
   using S = DmaShape<kWI, kWJ, kWM, kWN>;
   constexpr int kAT = S::kAT, kStage = kAT + S::kBTB;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -462,8 +479,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_dma_kernel(PrefillArgs a
   // output rows per wave quadrant: 32 kWI, or half as many gated channels
   constexpr int kTM = kGlu ? 16 * kWI : 32 * kWI, kTN = 32 * kWJ, kRS = 2 * kTM + 8;
   const uint32_t reg = base + wave * (kTN * kRS);
+  if constexpr (kEpi == kFused)
+    fuse_to_lds(a.epi, acc, reg, kRS, m0 + wm * kTM, n0 + wn * kTN, a.M, a.N, lane);
 #pragma unroll
-  for (int i = 0; i < kWI; ++i)
+  for (int i = 0; i < (kEpi == kFused ? 0 : kWI); ++i)
 #pragma unroll
     for (int j = 0; j < kWJ; ++j)
 #pragma unroll
@@ -532,8 +551,8 @@ constexpr int WBM = 128, WBN = 256;
 constexpr int kWATile = WBM * BK * 2;  // 16 KiB
 constexpr int kWBTile = WBN * BK * 2;  // 32 KiB
 
-template <int kRC>
-__global__ __launch_bounds__(512, 1) void prefill_ws_kernel(PrefillArgs a) {
+template <int kRC, int kEpi = kPlain>
+__global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgsOf<kEpi>::type a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int tm, tn;
   if (!tile_of(a, tm, tn)) return;  // tiles_m / tiles_n count 128 x 256 blocks
@@ -721,6 +740,10 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(PrefillArgs a) {
     }
 
     // Epilogue: fp16 round-to-nearest-even, 4 consecutive rows per 8-byte store.
+    if constexpr (kEpi == kFused) {
+      fuse_and_store(a.epi, acc, m0, n0 + c * 64, a.M, a.N, a.Y, a.ldy, lane);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -791,8 +814,8 @@ bool prefill_sparse_fits(const Header& h, int64_t N, int64_t ldx) {
 }
 
 namespace {
-template <int kWI, int kWJ, bool kGlu = false>
-hipError_t launch_dense(PrefillArgs a, hipStream_t s) {
+template <int kWI, int kWJ, int kEpi = kPlain>
+hipError_t launch_dense(typename PrefillArgsOf<kEpi>::type a, hipStream_t s) {
   a.tiles_m = int((a.M + 64 * kWI - 1) / (64 * kWI));
   a.tiles_n = int((a.N + 64 * kWJ - 1) / (64 * kWJ));
   // The LDS-direct kernel where W and X fit 32-bit byte offsets; otherwise
@@ -803,27 +826,32 @@ hipError_t launch_dense(PrefillArgs a, hipStream_t s) {
   }();
   const bool fits = 2 * (int64_t(a.M - 1) * a.ldw + a.K) < (int64_t(1) << 32) &&
                     2 * (int64_t(a.N - 1) * a.ldx + a.K) < (int64_t(1) << 32);
-  if (kGlu && !fits) return hipErrorInvalidValue;  // the gated epilogue exists in this kernel only
-  if (kGlu || (dma && fits)) {
+  if (kEpi == kGated && !fits) return hipErrorInvalidValue;  // the gated epilogue exists in this kernel only
+  if (kEpi == kGated || (dma && fits)) {
     // 256 x 256 with eight waves (two per SIMD, 128 x 64 each); the smaller
     // blocks with four
     constexpr int kWN = kWI == 4 && kWJ == 4 ? 4 : 2;
     constexpr int kJ = kWI == 4 && kWJ == 4 ? 2 : kWJ;
     using S = DmaShape<kWI, kJ, 2, kWN>;
-    hipLaunchKernelGGL((dense_dma_kernel<kWI, kJ, 2, kWN, kGlu>), dim3(grid_size(a)), dim3(64 * S::kNW), S::kLds,
+    hipLaunchKernelGGL((dense_dma_kernel<kWI, kJ, 2, kWN, kEpi>), dim3(grid_size(a)), dim3(64 * S::kNW), S::kLds,
                        s, a);
     return hipGetLastError();
   }
-  const size_t lds = size_t(2) * (64 * kWI + 64 * kWJ) * BK * 2;
-  hipLaunchKernelGGL((dense_kernel<kWI, kWJ>), dim3(grid_size(a)), dim3(256), lds, s, a);
-  return hipGetLastError();
+  if constexpr (kEpi == kFused && kWI * kWJ > 4) {
+    // larger blocks' accumulators leave the epilogue no registers
+    return launch_dense<2, 2, kEpi>(a, s);
+  } else {
+    const size_t lds = size_t(2) * (64 * kWI + 64 * kWJ) * BK * 2;
+    hipLaunchKernelGGL((dense_kernel<kWI, kWJ, kEpi>), dim3(grid_size(a)), dim3(256), lds, s, a);
+    return hipGetLastError();
+  }
 }
 }  // namespace
 
 namespace {
 hipError_t launch_dense_any(const uint16_t* W, int64_t ldw, const uint16_t* X, int64_t ldx, uint16_t* Y,
                             int64_t ldy, int64_t M, int64_t K, int64_t N, int num_cus, bool glu, float tau,
-                            hipStream_t s) {
+                            const Epilogue& epi, hipStream_t s) {
   PrefillArgs a = make_args(M, N, K, X, ldx, Y, ldy);
   a.W = W;
   a.ldw = ldw;
@@ -854,9 +882,15 @@ hipError_t launch_dense_any(const uint16_t* W, int64_t ldw, const uint16_t* X, i
     if (*e >= '1' && *e <= '3') shape = *e - '0';
   }
   if (glu) {
-    if (shape == 1) return launch_dense<4, 4, true>(a, s);
-    if (shape == 2) return launch_dense<4, 2, true>(a, s);
-    return launch_dense<2, 2, true>(a, s);
+    if (shape == 1) return launch_dense<4, 4, kGated>(a, s);
+    if (shape == 2) return launch_dense<4, 2, kGated>(a, s);
+    return launch_dense<2, 2, kGated>(a, s);
+  }
+  if (epi.on) {
+    const PrefillFusedArgs fa{a, epi};
+    if (shape == 1) return launch_dense<4, 4, kFused>(fa, s);
+    if (shape == 2) return launch_dense<4, 2, kFused>(fa, s);
+    return launch_dense<2, 2, kFused>(fa, s);
   }
   if (shape == 1) return launch_dense<4, 4>(a, s);
   if (shape == 2) return launch_dense<4, 2>(a, s);
@@ -866,14 +900,14 @@ hipError_t launch_dense_any(const uint16_t* W, int64_t ldw, const uint16_t* X, i
 
 hipError_t launch_prefill_dense(const uint16_t* W, int64_t ldw, const uint16_t* X, int64_t ldx,
                                 uint16_t* Y, int64_t ldy, int64_t M, int64_t K, int64_t N, int num_cus,
-                                hipStream_t s) {
-  return launch_dense_any(W, ldw, X, ldx, Y, ldy, M, K, N, num_cus, false, 0.f, s);
+                                hipStream_t s, const Epilogue& epi) {
+  return launch_dense_any(W, ldw, X, ldx, Y, ldy, M, K, N, num_cus, false, 0.f, epi, s);
 }
 
 hipError_t launch_prefill_dense_glu(const uint16_t* W, int64_t ldw, const uint16_t* X, int64_t ldx,
                                     uint16_t* H, int64_t ldh, int64_t M2, int64_t K, int64_t N, float tau,
                                     int num_cus, hipStream_t s) {
-  return launch_dense_any(W, ldw, X, ldx, H, ldh, M2, K, N, num_cus, true, tau, s);
+  return launch_dense_any(W, ldw, X, ldx, H, ldh, M2, K, N, num_cus, true, tau, Epilogue{}, s);
 }
 
 bool prefill_dense_dma_fits(int64_t M, int64_t ldw, int64_t K, int64_t N, int64_t ldx) {
@@ -885,8 +919,19 @@ size_t prefill_sparse_lds(const Header& h) {
   return size_t(2) * kWATile + size_t(2) * kWBTile + 8 /*waves*/ * chunks * 512;
 }
 
+template <int kEpi>
+static void launch_ws(const typename PrefillArgsOf<kEpi>::type& a, dim3 grid, size_t lds, hipStream_t s) {
+  const dim3 block{512, 1, 1};
+  switch (a.run_chunks) {
+    case 1: hipLaunchKernelGGL((prefill_ws_kernel<1, kEpi>), grid, block, lds, s, a); break;
+    case 2: hipLaunchKernelGGL((prefill_ws_kernel<2, kEpi>), grid, block, lds, s, a); break;
+    case 3: hipLaunchKernelGGL((prefill_ws_kernel<3, kEpi>), grid, block, lds, s, a); break;
+    default: hipLaunchKernelGGL((prefill_ws_kernel<4, kEpi>), grid, block, lds, s, a); break;
+  }
+}
+
 hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t ldx, uint16_t* Y,
-                                 int64_t ldy, int64_t N, hipStream_t s) {
+                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi) {
   PrefillArgs a = make_args(f.h.m, N, f.h.k, X, ldx, Y, ldy);
   a.tile_ptr = f.tile_ptr;
   a.bits = f.bits;
@@ -903,13 +948,11 @@ hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t 
   if (!prefill_sparse_fits(f.h, N, ldx)) return hipErrorInvalidValue;
   a.tiles_m = int((f.h.m + WBM - 1) / WBM);
   a.tiles_n = int((N + WBN - 1) / WBN);
-  const dim3 grid{grid_size(a), 1, 1}, block{512, 1, 1};
-  switch (a.run_chunks) {
-    case 1: hipLaunchKernelGGL((prefill_ws_kernel<1>), grid, block, lds, s, a); break;
-    case 2: hipLaunchKernelGGL((prefill_ws_kernel<2>), grid, block, lds, s, a); break;
-    case 3: hipLaunchKernelGGL((prefill_ws_kernel<3>), grid, block, lds, s, a); break;
-    default: hipLaunchKernelGGL((prefill_ws_kernel<4>), grid, block, lds, s, a); break;
-  }
+  const dim3 grid{grid_size(a), 1, 1};
+  if (epi.on)
+    launch_ws<kFused>(PrefillFusedArgs{a, epi}, grid, lds, s);
+  else
+    launch_ws<kPlain>(a, grid, lds, s);
   return hipGetLastError();
 }
 

@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <cstdlib>
 
+#include "epilogue.h"
 #include "kernels.h"
 
 namespace swm {
@@ -184,6 +185,17 @@ struct SmfArgs {
   int M, N, K, Kp;
   int tiles_m, tiles_n, group_m;
 };
+struct SmfFusedArgs : SmfArgs {
+  Epilogue epi;
+};
+template <int kEpi>
+struct SmfArgsOf {
+  using type = SmfArgs;
+};
+template <>
+struct SmfArgsOf<kFused> {
+  using type = SmfFusedArgs;
+};
 
 __device__ __forceinline__ bool smf_tile_of(const SmfArgs& a, int& tm, int& tn) {
   const int total = a.tiles_m * a.tiles_n;
@@ -271,8 +283,8 @@ __device__ __forceinline__ void wait_vm_lgkm0() {
 // the wait before that barrier is explicit: at most the later steps' loads
 // may still be in flight.  kRes: the residual layer is staged and multiplied
 // too, into the same accumulators.
-template <bool kRes, int kWJ, int kWN = 2>
-__global__ __launch_bounds__(128 * kWN) void smf_kernel(SmfArgs a) {
+template <bool kRes, int kWJ, int kWN = 2, int kEpi = kPlain>
+__global__ __launch_bounds__(128 * kWN) void smf_kernel(typename SmfArgsOf<kEpi>::type a) {
   using S = SmfShape<kRes, kWJ, kWN>;
   constexpr int kJ = S::kJ, kIV = S::kIV, kII = S::kII;
   constexpr int kStage = S::kStage;
@@ -477,8 +489,10 @@ __global__ __launch_bounds__(128 * kWN) void smf_kernel(SmfArgs a) {
   __builtin_amdgcn_s_barrier();
   constexpr int kRS = 2 * 128 + 8, kTN = 32 * kJ;
   const uint32_t reg = base + wave * (kTN * kRS);
+  if constexpr (kEpi == kFused)
+    fuse_to_lds(a.epi, acc, reg, kRS, m0 + wm * 128, n0 + wn * kTN, a.M, a.N, lane);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < (kEpi == kFused ? 0 : 4); ++i)
 #pragma unroll
     for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -550,8 +564,32 @@ bool smf_fits(const Header& h, int64_t N, int64_t ldx) {
   return 2 * ((N - 1) * ldx + h.k) < (int64_t(1) << 32) && h.m * kp < (int64_t(1) << 32);
 }
 
+template <int kEpi>
+static void launch_shape(const typename SmfArgsOf<kEpi>::type& a, bool residual, bool wide, bool eight,
+                         unsigned grid, hipStream_t s) {
+  constexpr size_t kL04 = SmfShape<false, 4>::kLds, kL02 = SmfShape<false, 2>::kLds;
+  constexpr size_t kL14 = SmfShape<true, 4>::kLds, kL12 = SmfShape<true, 2>::kLds;
+  constexpr size_t kL04w = SmfShape<false, 4, 4>::kLds, kL02w = SmfShape<false, 2, 4>::kLds;
+  if (residual) {
+    if (wide)
+      hipLaunchKernelGGL((smf_kernel<true, 4, 2, kEpi>), dim3(grid), dim3(256), kL14, s, a);
+    else
+      hipLaunchKernelGGL((smf_kernel<true, 2, 2, kEpi>), dim3(grid), dim3(256), kL12, s, a);
+  } else {
+    if (wide && eight)
+      hipLaunchKernelGGL((smf_kernel<false, 4, 4, kEpi>), dim3(grid), dim3(512), kL04w, s, a);
+    else if (wide)
+      hipLaunchKernelGGL((smf_kernel<false, 4, 2, kEpi>), dim3(grid), dim3(256), kL04, s, a);
+    else if (eight)
+      hipLaunchKernelGGL((smf_kernel<false, 2, 4, kEpi>), dim3(grid), dim3(512), kL02w, s, a);
+    else
+      hipLaunchKernelGGL((smf_kernel<false, 2, 2, kEpi>), dim3(grid), dim3(256), kL02, s, a);
+  }
+}
+
 hipError_t launch_smf(const Header& h, const Sparse24Layout& L, bool residual, const void* ws, const uint16_t* X,
-                      int64_t ldx, uint16_t* Y, int64_t ldy, int64_t N, int num_cus, hipStream_t s) {
+                      int64_t ldx, uint16_t* Y, int64_t ldy, int64_t N, int num_cus, hipStream_t s,
+                      const Epilogue& epi) {
   if (h.k < 8 || h.k % 8 != 0 || N < 1 || !smf_fits(h, N, ldx)) return hipErrorInvalidValue;
   SmfArgs a;
   const uint8_t* w = static_cast<const uint8_t*>(ws);
@@ -578,9 +616,6 @@ hipError_t launch_smf(const Header& h, const Sparse24Layout& L, bool residual, c
   const bool wide = big >= num_cus;
   a.tiles_n = int(wide ? (N + 255) / 256 : (N + 127) / 128);
   const unsigned grid = unsigned((a.tiles_m * a.tiles_n + 7) / 8 * 8);
-  constexpr size_t kL04 = SmfShape<false, 4>::kLds, kL02 = SmfShape<false, 2>::kLds;
-  constexpr size_t kL14 = SmfShape<true, 4>::kLds, kL12 = SmfShape<true, 2>::kLds;
-  constexpr size_t kL04w = SmfShape<false, 4, 4>::kLds, kL02w = SmfShape<false, 2, 4>::kLds;
   // Blocks of a 2:4 mask with eight waves (two per SIMD) unless
   // SWM_SMF_WAVES=4 (read once).  Two A/B runs, us, q_proj 2:4: N = 4096
   // (256 x 256 blocks) 109.8 / 111.0 with four waves against 92.9 / 92.9
@@ -591,21 +626,10 @@ hipError_t launch_smf(const Header& h, const Sparse24Layout& L, bool residual, c
     const char* e = getenv("SWM_SMF_WAVES");
     return !(e && atoi(e) == 4);
   }();
-  if (residual) {
-    if (wide)
-      hipLaunchKernelGGL((smf_kernel<true, 4>), dim3(grid), dim3(256), kL14, s, a);
-    else
-      hipLaunchKernelGGL((smf_kernel<true, 2>), dim3(grid), dim3(256), kL12, s, a);
-  } else {
-    if (wide && eight)
-      hipLaunchKernelGGL((smf_kernel<false, 4, 4>), dim3(grid), dim3(512), kL04w, s, a);
-    else if (wide)
-      hipLaunchKernelGGL((smf_kernel<false, 4>), dim3(grid), dim3(256), kL04, s, a);
-    else if (eight)
-      hipLaunchKernelGGL((smf_kernel<false, 2, 4>), dim3(grid), dim3(512), kL02w, s, a);
-    else
-      hipLaunchKernelGGL((smf_kernel<false, 2>), dim3(grid), dim3(256), kL02, s, a);
-  }
+  if (epi.on)
+    launch_shape<kFused>(SmfFusedArgs{a, epi}, residual, wide, eight, grid, s);
+  else
+    launch_shape<kPlain>(a, residual, wide, eight, grid, s);
   return hipGetLastError();
 }
 
