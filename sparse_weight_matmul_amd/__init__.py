@@ -358,28 +358,29 @@ def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, w
     lib = load()
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
-    N = X.shape[0]
-    xp, ldx = _dev2d(X, "X", cols=fmt.K)
-    Y = _out(Y, N, fmt.M, X)
-    yp, ldy = _dev2d(Y, "Y", rows=N, cols=fmt.M)
+    N, M, K = X.shape[0], fmt.M, fmt.K
+    xp, ldx = _rows(X, "X", N, K)
     bp = rp = None
     ldr = 0
     if bias is not None:
-        if not bias.is_cuda or bias.dtype != torch.float16 or bias.shape != (fmt.M,):
-            raise TypeError(f"bias must be a float16 CUDA tensor, ({fmt.M},)")
-        if fmt.M > 1 and bias.stride(0) != 1:
+        if not bias.is_cuda or bias.dtype is not torch.float16 or bias.shape != (M,):
+            raise TypeError(f"bias must be a float16 CUDA tensor, ({M},)")
+        if M > 1 and bias.stride(0) != 1:
             raise ValueError("bias must be contiguous")
         bp = bias.data_ptr()
     if residual is not None:
-        rp, ldr = _dev2d(residual, "residual", rows=N, cols=fmt.M)
-    if workspace is None:
-        wp, wb = None, 0
-    else:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        rp, ldr = _rows(residual, "residual", N, M)
+    if Y is None:
+        if residual is not None and residual.is_contiguous():
+            Y = _empty_like(residual, stream)
+        else:
+            Y = _empty((N, M), X.dtype, X.device, stream)
+    yp, ldy = _rows(Y, "Y", N, M)
+    wp, wb = None, 0
+    if workspace is not None:
+        workspace, wp, wb = _workspace(workspace, 0, X.device, stream)
     _check(lib.swm_spmm_epilogue(fmt._h, xp, ldx, yp, ldy, N, bp, ACTIVATIONS[act], rp, ldr, wp, wb,
-                                 _stream_ptr(stream)), "swm_spmm_epilogue")
+                                 _raw_stream(stream, X.device.index)), "swm_spmm_epilogue")
     return Y
 
 
@@ -512,12 +513,16 @@ def hbm_stream(buf, unroll: int, blocks: int, out=None, stream=None):
     return out
 
 
-def _raw_stream(stream, device) -> int:
-    """Handle of `stream`, or of the device's current stream; the device must be the current one."""
+# The serving operators are a few microseconds of work: their wrappers look at
+# each tensor's properties once and allocate like a given tensor (the cheapest
+# way), so that the calls of a token do not wait for Python.
+
+def _raw_stream(stream, index: int) -> int:
+    """Handle of `stream`, or of the current stream of device `index`, which must be the current device."""
     import torch
-    index = torch.cuda.current_device()
-    if device.index != index:
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{index}")
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{current}")
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
@@ -528,6 +533,28 @@ def _empty(shape, dtype, device, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _empty_like(t, stream):
+    """As _empty, with the shape and type of a contiguous tensor."""
+    import torch
+    t = torch.empty_like(t)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _rows(t, name, rows, cols):
+    """(pointer, leading dimension) of a (rows, cols) fp16 CUDA tensor with unit column stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.float16 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D float16 CUDA tensor")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.data_ptr(), max(ld, cols, 1) if rows > 1 else max(cols, 1)
 
 
 def _workspace(workspace, need, device, stream):
@@ -579,6 +606,7 @@ class PagedCache:
         self.pages, self.page_size, self.heads, self.dim = k.shape
         self.batch, self.pages_per_seq = table.shape
         self.capacity = self.pages_per_seq * self.page_size
+        self._slots = torch.Size((self.pages, self.heads, self.page_size))
         # strides of dimensions of one element are arbitrary and never used
         ks = [s if n > 1 else 0 for s, n in zip(k.stride()[:3], k.shape)]
         vs = [s if n > 1 else 0 for s, n in zip(v.stride()[:3], v.shape)]
@@ -595,13 +623,15 @@ class PagedCache:
         return self._attn_bytes[key]
 
     def _per_slot(self, t, name, dtype):
-        """Check an array with one entry per cached row, (pages, heads, page_size)."""
-        if not t.is_cuda or t.device != self.device or t.dtype != dtype:
+        """(pointer, page stride, head stride) of an array with one entry per cached row, (pages, heads, page_size)."""
+        if not t.is_cuda or t.device != self.device or t.dtype is not dtype:
             raise TypeError(f"{name} must be a {dtype} tensor on {self.device}")
-        if t.shape != (self.pages, self.heads, self.page_size):
+        if t.shape != self._slots:
             raise ValueError(f"{name} must be (pages, heads, page_size)")
-        if self.page_size > 1 and t.stride(2) != 1:
+        page, head, slot = t.stride()
+        if self.page_size > 1 and slot != 1:
             raise ValueError(f"{name} must have unit stride along its last dimension")
+        return t.data_ptr(), page, head
 
 
 def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=None, weights=None, out=None,
@@ -616,7 +646,7 @@ def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=No
     not None) bytes; None allocates it."""
     import torch
     lib = load()
-    if not q.is_cuda or q.dtype != torch.float16 or q.dim() != 3:
+    if not q.is_cuda or q.dtype is not torch.float16 or q.dim() != 3:
         raise TypeError("q must be a 3-D float16 CUDA tensor")
     B, Hq, D = q.shape
     if B != cache.batch or D != cache.dim or q.device != cache.device:
@@ -625,7 +655,7 @@ def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=No
     if D > 1 and q_d != 1:
         raise ValueError("q must have unit stride along its last dimension")
     if out is None:
-        out = _empty((B, Hq, D), torch.float16, cache.device, stream)
+        out = _empty_like(q, stream) if q.is_contiguous() else _empty((B, Hq, D), q.dtype, cache.device, stream)
     elif not out.is_cuda or out.dtype != torch.float16 or out.shape != q.shape or out.device != q.device:
         raise TypeError("out must be a float16 CUDA tensor of q's shape")
     elif out.stride(2) != 1:
@@ -644,9 +674,8 @@ def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=No
             raise ValueError("mask rows must not overlap")
     wp, w_page, w_head = None, 0, 0
     if weights is not None:
-        cache._per_slot(weights, "weights", torch.float32)
-        wp, w_page, w_head = weights.data_ptr(), weights.stride(0), weights.stride(1)
-    s = _raw_stream(stream, cache.device)
+        wp, w_page, w_head = cache._per_slot(weights, "weights", torch.float32)
+    s = _raw_stream(stream, cache.device.index)
     keep, ws, ws_bytes = _workspace(workspace, cache.attention_workspace_bytes(Hq, weights is not None),
                                     cache.device, stream)
     # a stride along one sequence or one head is never used: pass 0 for it
@@ -670,21 +699,15 @@ def kv_evict(cache: PagedCache, weights, positions, budget: int, recent: int = 0
     where there is none).  No page may belong to two sequences."""
     import torch
     lib = load()
-    cache._per_slot(weights, "weights", torch.float32)
-    cache._per_slot(positions, "positions", torch.int32)
-    if weights_out is None:
-        weights_out = weights
-    else:
-        cache._per_slot(weights_out, "weights_out", torch.float32)
-    if positions_out is None:
-        positions_out = positions
-    else:
-        cache._per_slot(positions_out, "positions_out", torch.int32)
+    w = cache._per_slot(weights, "weights", torch.float32)
+    p = cache._per_slot(positions, "positions", torch.int32)
+    wo = w if weights_out is None else cache._per_slot(weights_out, "weights_out", torch.float32)
+    po = p if positions_out is None else cache._per_slot(positions_out, "positions_out", torch.int32)
     budget = int(budget)
     if budget < 0:
         raise ValueError("budget must not be negative")
     if lengths_out is None:
-        lengths_out = _empty((cache.batch,), torch.int32, cache.device, stream)
+        lengths_out = _empty_like(cache.lengths, stream)
     elif (not lengths_out.is_cuda or lengths_out.dtype != torch.int32 or lengths_out.shape != (cache.batch,)
           or not lengths_out.is_contiguous()):
         raise TypeError("lengths_out must be a contiguous int32 CUDA tensor, one entry per sequence")
@@ -693,11 +716,8 @@ def kv_evict(cache: PagedCache, weights, positions, budget: int, recent: int = 0
         kept = _empty(shape, torch.int32, cache.device, stream)
     elif not kept.is_cuda or kept.dtype != torch.int32 or kept.shape != shape or not kept.is_contiguous():
         raise TypeError(f"kept must be a contiguous {shape} int32 CUDA tensor")
-    s = _raw_stream(stream, cache.device)
-    _check(lib.swm_kv_evict(cache._p, weights.data_ptr(), weights.stride(0), weights.stride(1), positions.data_ptr(),
-                            positions.stride(0), positions.stride(1), budget, int(recent), weights_out.data_ptr(),
-                            weights_out.stride(0), weights_out.stride(1), positions_out.data_ptr(),
-                            positions_out.stride(0), positions_out.stride(1), lengths_out.data_ptr(),
+    s = _raw_stream(stream, cache.device.index)
+    _check(lib.swm_kv_evict(cache._p, *w, *p, budget, int(recent), *wo, *po, lengths_out.data_ptr(),
                             kept.data_ptr(), s), "swm_kv_evict")
     return lengths_out, kept
 
@@ -720,7 +740,7 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None):
     ld = logits.stride(0) if N > 1 else V
     if ld < V:
         raise ValueError("rows of logits must not overlap")
-    s = _raw_stream(stream, device)
+    s = _raw_stream(stream, device.index)
     tp, wide, logp = None, 0, None
     if targets is not None:
         if targets.dtype not in (torch.int32, torch.int64) or targets.device != device:
@@ -729,7 +749,7 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None):
             raise ValueError(f"targets must be contiguous, ({N},)")
         tp, wide = targets.data_ptr(), int(targets.dtype == torch.int64)
         logp = _empty((N,), torch.float32, device, stream)
-    entropy = _empty((N,), torch.float32, device, stream)
+    entropy = _empty((N,), torch.float32, device, stream) if logp is None else _empty_like(logp, stream)
     top = int(top)
     ids = lps = None
     if top > 0:

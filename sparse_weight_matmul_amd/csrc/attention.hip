@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "paging.h"
 
 namespace swm {
 namespace {
@@ -65,23 +66,16 @@ struct AttnArgs {
   float* weights;
   float* ml;      // [B][Hq][splits][2] maximum (in units of log2) and sum
   float* part;    // [B][Hq][splits][D] unnormalised outputs
-  float* logits;  // [B][Hq][cap] scores in units of log2
+  float* logits;  // [B][Hq][lrow] scores in units of log2
   int64_t q_b, q_h, o_b, o_h;
   int64_t k_p, k_s, k_h, v_p, v_s, v_h;
   int64_t table_b, mask_b, w_p, w_h;
   int32_t B, Hq, Hkv, G, D, S, pages, cap, per_seq;
-  int32_t splits, split_len;
+  int32_t splits, split_len, lrow;
+  int32_t own_weights;  // the only split adds the weights itself, its scores in LDS
   float scale;  // softmax scale * log2(e)
-  double inv_s;  // 1 / S
+  PageDiv div;  // by S
 };
-
-// Page and slot of token t (t < 2^31): t / S by one fp64 product; the half
-// keeps the quotient clear of rounding at whole numbers.
-__device__ __forceinline__ void page_of(const AttnArgs& a, int t, int* index, int* slot) {
-  const int i = int((double(t) + 0.5) * a.inv_s);
-  *index = i;
-  *slot = t - i * a.S;
-}
 
 // Where a token's rows are: its page, clamped into the pool, and whether the
 // table names a page of the pool for it.
@@ -92,27 +86,20 @@ struct Place {
 
 __device__ __forceinline__ Place place(const AttnArgs& a, const int32_t* row, int t) {
   Place p;
-  int i;
-  page_of(a, t, &i, &p.slot);
+  const int i = page_index(a.div, t);
+  p.slot = t - i * a.S;
   const int id = row[min(i, a.per_seq - 1)];
   p.ok = i < a.per_seq && id >= 0 && id < a.pages;
   p.page = p.ok ? id : 0;
   return p;
 }
 
-// Keys and values of one tile in registers.
-template <int DP>
-struct Tile {
-  u32x4 k[2][DP / 32];
-  u32x4 v[8][DP / 128 ? DP / 128 : 1];  // DP = 64: the first two words of each
-};
-
-// kSame8: a page holds a multiple of eight tokens, so eight aligned tokens
-// share one.
+// The lane's part of a tile's keys: of each of the two key tiles one row, 16
+// bytes of every 64.  kSame8: a page holds a multiple of eight tokens, so eight
+// aligned tokens share one.
 template <int DP, bool kFull, bool kSame8>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, const int32_t* row, const uint16_t* kh,
-                                          const uint16_t* vh, int t0, int lane, const Place& pk, const Place& pv,
-                                          Tile<DP>& t) {
+__device__ __forceinline__ void load_keys(const AttnArgs& a, const int32_t* row, const uint16_t* kh, int t0,
+                                          int lane, const Place& pk, u32x4 (&k)[2][DP / 32]) {
   const int g = lane >> 4, c = lane & 15;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -122,9 +109,17 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, const int32_t* row,
 #pragma unroll
     for (int s = 0; s < DP / 32; ++s) {
       const int d = 32 * s + 8 * g;
-      t.k[i][s] = *reinterpret_cast<const u32x4*>(src + (kFull || d < a.D ? d : 0));
+      k[i][s] = *reinterpret_cast<const u32x4*>(src + (kFull || d < a.D ? d : 0));
     }
   }
+}
+
+// The lane's part of a tile's values: its chunk of eight tokens' rows (DP =
+// 64: four halves, in the first two words).
+template <int DP, bool kFull, bool kSame8>
+__device__ __forceinline__ void load_values(const AttnArgs& a, const int32_t* row, const uint16_t* vh, int t0,
+                                            int lane, const Place& pv, u32x4 (&v)[8][DP / 128 ? DP / 128 : 1]) {
+  const int g = lane >> 4, c = lane & 15;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const Place p = kSame8 ? pv : place(a, row, t0 + 8 * g + e);
@@ -132,13 +127,13 @@ __device__ __forceinline__ void load_tile(const AttnArgs& a, const int32_t* row,
     if (DP == 64) {
       const int d = 4 * c;
       const u32x2 w = *reinterpret_cast<const u32x2*>(src + (kFull || d < a.D ? d : 0));
-      t.v[e][0][0] = w[0];
-      t.v[e][0][1] = w[1];
+      v[e][0][0] = w[0];
+      v[e][0][1] = w[1];
     } else {
 #pragma unroll
       for (int u = 0; u < DP / 128; ++u) {
         const int d = 128 * u + 8 * c;
-        t.v[e][u] = *reinterpret_cast<const u32x4*>(src + (kFull || d < a.D ? d : 0));
+        v[e][u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + (kFull || d < a.D ? d : 0)));
       }
     }
   }
@@ -165,19 +160,48 @@ __device__ __forceinline__ uint32_t live_bits(const AttnArgs& a, const int32_t* 
   return bits;
 }
 
-__device__ __forceinline__ float max_groups(float v) {  // over the four lane groups
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+// Maximum and sum over the four lane groups.  The swap instructions exchange
+// odd and even rows of 16 lanes (halves of 32) of two registers: given the
+// same value twice, the two results hold both partners' values.
+__device__ __forceinline__ void partners16(float v, float* a, float* b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *a = __uint_as_float(r[0]);
+  *b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void partners32(float v, float* a, float* b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *a = __uint_as_float(r[0]);
+  *b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_groups(float v) {
+  float a, b;
+  partners16(v, &a, &b);
+  partners32(fmaxf(a, b), &a, &b);
+  return fmaxf(a, b);
 }
 __device__ __forceinline__ float sum_groups(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  float a, b;
+  partners16(v, &a, &b);
+  partners32(a + b, &a, &b);
+  return a + b;
+}
+
+// Adds the weights of tokens t..t+3 (those below n) to the accumulator.
+// Atomic because sequences may share a page.
+__device__ __forceinline__ void add_weights(const AttnArgs& a, const int32_t* row, int hkv, int t, int n,
+                                            const f32x4& w) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (t + e >= n || w[e] == 0.f) continue;
+    const Place p = place(a, row, t + e);
+    if (p.ok) unsafeAtomicAdd(a.weights + int64_t(p.page) * a.w_p + int64_t(hkv) * a.w_h + p.slot, w[e]);
+  }
 }
 
 // One workgroup: one split of one sequence, up to 16 query heads of one
 // key-value head.
 template <int DP, bool kFull, bool kSame8>
-__global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(AttnArgs a) {
   constexpr int kJ = DP == 64 ? 4 : 8;             // halves of a value chunk
   constexpr int kU = DP / 128 ? DP / 128 : 1;      // value chunks of a lane
   extern __shared__ float smem[];
@@ -188,16 +212,17 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
   const int hkv = blockIdx.y / tiles_h, ht = blockIdx.y % tiles_h;
   const int gn = min(kHeads, a.G - ht * kHeads);  // query heads here
   const int h0 = hkv * a.G + ht * kHeads;
-  const int n = min(max(a.lengths[b], 0), a.cap);
-  const int begin = split * a.split_len, end = min(begin + a.split_len, n);
-  if (begin >= end && a.splits > 1) return;  // the join does not read splits past the length
-
+  const int begin = split * a.split_len;
+  const int first = begin + kTile * wave;
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   const uint8_t* mask = a.mask ? a.mask + int64_t(b) * a.mask_b : nullptr;
   const uint16_t* kh = a.k + int64_t(hkv) * a.k_h;
   const uint16_t* vh = a.v + int64_t(hkv) * a.v_h;
   const int g = lane >> 4, c = lane & 15;
 
+  // The length, the query and the first pages are requested together: each
+  // waited for in turn would add its latency to the shortest calls.
+  int n = a.lengths[b];
   half8 q[DP / 32];
   {
     const uint16_t* src = a.q + int64_t(b) * a.q_b + int64_t(h0 + min(c, gn - 1)) * a.q_h;
@@ -209,6 +234,15 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
       q[s] = __builtin_bit_cast(half8, w);
     }
   }
+  Place pk{}, pv{};
+  if (kSame8 && a.per_seq > 0) {
+    pk = place(a, row, first + 8 * (c >> 2));
+    pv = place(a, row, first + 8 * g);
+    asm volatile("" ::"v"(pk.page), "v"(pv.page), "v"(q[0]));  // not moved past the branch
+  }
+  n = min(max(n, 0), a.cap);
+  const int end = min(begin + a.split_len, n);
+  if (begin >= end && a.splits > 1) return;  // the join does not read splits past the length
 
   f32x4 o[kU][kJ];
 #pragma unroll
@@ -217,50 +251,34 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
     for (int j = 0; j < kJ; ++j) o[u][j] = f32x4{0, 0, 0, 0};
   float m = neg_inf(), l = 0.f;
 
-  float* logits = a.logits ? a.logits + (int64_t(b) * a.Hq + h0 + min(c, gn - 1)) * a.cap : nullptr;
+  float* sm_x = smem + 2 * kWaves * kHeads + kWaves * gn * (DP + 4);  // own_weights: scores [gn][lrow]
+  float* logits = a.logits ? a.logits + (int64_t(b) * a.Hq + h0 + min(c, gn - 1)) * a.lrow : nullptr;
 
   constexpr int kStep = kTile * kWaves;
-  const int first = begin + kTile * wave;
-  Tile<DP> cur;
-  Place pk{}, pv{}, pk2{}, pv2{};
+  u32x4 k[2][DP / 32], v[8][kU];
   uint32_t live = 0;
   if (first < end) {
-    if (kSame8) {
-      pk = place(a, row, first + 8 * (c >> 2));
-      pv = place(a, row, first + 8 * g);
-      pk2 = place(a, row, first + kStep + 8 * (c >> 2));
-      pv2 = place(a, row, first + kStep + 8 * g);
-    }
-    load_tile<DP, kFull, kSame8>(a, row, kh, vh, first, lane, pk, pv, cur);
+    load_keys<DP, kFull, kSame8>(a, row, kh, first, lane, pk, k);
+    load_values<DP, kFull, kSame8>(a, row, vh, first, lane, pv, v);
     live = live_bits<kSame8>(a, row, mask, first + 8 * g, end, pv);
+    if (kSame8) {
+      pk = place(a, row, first + kStep + 8 * (c >> 2));
+      pv = place(a, row, first + kStep + 8 * g);
+    }
   }
   for (int t0 = first; t0 < end; t0 += kStep) {
-    // request the next tile (its pages were looked up a tile ago) and look up
-    // the pages of the one after it
-    Tile<DP> nxt;
-    uint32_t live_n = 0;
     const bool more = t0 + kStep < end;
-    if (more) {
-      Place pk3{}, pv3{};
-      if (kSame8) {
-        pk3 = place(a, row, t0 + 2 * kStep + 8 * (c >> 2));
-        pv3 = place(a, row, t0 + 2 * kStep + 8 * g);
-      }
-      load_tile<DP, kFull, kSame8>(a, row, kh, vh, t0 + kStep, lane, pk2, pv2, nxt);
-      live_n = live_bits<kSame8>(a, row, mask, t0 + kStep + 8 * g, end, pv2);
-      pk2 = pk3;
-      pv2 = pv3;
-    }
-
     f32x4 s2[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
     for (int s = 0; s < DP / 32; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        u32x4 w = cur.k[i][s];
+        u32x4 w = k[i][s];
         if (!kFull && 32 * s + 8 * g >= a.D) w = u32x4{0, 0, 0, 0};
         s2[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w), q[s], s2[i], 0, 0, 0);
       }
+    // the keys' registers are free: the next tile's keys
+    if (more) load_keys<DP, kFull, kSame8>(a, row, kh, t0 + kStep, lane, pk, k);
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = s2[e >> 2][e & 3] * a.scale;
@@ -271,14 +289,17 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
         x[e] = on ? x[e] : neg_inf();
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          if (!on) cur.v[e][u] = u32x4{0, 0, 0, 0};
+          if (!on) v[e][u] = u32x4{0, 0, 0, 0};
       }
     }
-    if (logits && c < gn) {
-      const int t = t0 + 8 * g;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (t + e < end) logits[t + e] = x[e];
+    if (a.own_weights && c < gn) {
+      f32x4* dst = reinterpret_cast<f32x4*>(sm_x + c * a.lrow + t0 + 8 * g);
+      dst[0] = f32x4{x[0], x[1], x[2], x[3]};
+      dst[1] = f32x4{x[4], x[5], x[6], x[7]};
+    } else if (logits && c < gn) {  // rows are padded to whole tiles
+      f32x4* dst = reinterpret_cast<f32x4*>(logits + t0 + 8 * g);
+      dst[0] = f32x4{x[0], x[1], x[2], x[3]};
+      dst[1] = f32x4{x[4], x[5], x[6], x[7]};
     }
     float mx = x[0];
 #pragma unroll
@@ -309,19 +330,28 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          w[e] = __builtin_amdgcn_perm(cur.v[2 * e + 1][u][j / 2], cur.v[2 * e][u][j / 2],
+          w[e] = __builtin_amdgcn_perm(v[2 * e + 1][u][j / 2], v[2 * e][u][j / 2],
                                        j & 1 ? 0x07060302u : 0x05040100u);
         const half8 vt = __builtin_bit_cast(half8, w);
         o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, hi, o[u][j], 0, 0, 0);
         o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vt, lo, o[u][j], 0, 0, 0);
       }
-    cur = nxt;
-    live = live_n;
+    if (more) {  // the next tile's values, and the pages of the tile after it
+      const Place now = pv;
+      const uint32_t bits = live_bits<kSame8>(a, row, mask, t0 + kStep + 8 * g, end, now);
+      if (kSame8) {
+        pk = place(a, row, t0 + 2 * kStep + 8 * (c >> 2));
+        pv = place(a, row, t0 + 2 * kStep + 8 * g);
+      }
+      load_values<DP, kFull, kSame8>(a, row, vh, t0 + kStep, lane, now, v);
+      live = bits;
+    }
   }
   l = sum_groups(l);
 
   // Join the waves: maxima and sums, then the outputs (dimension 8(4g + r) + j
-  // of head c is element r of o[..][j]).
+  // of head c is element r of o[..][j]), four dimensions a thread.
+  constexpr int kRow = DP + 4;  // floats per row, off the bank stride
   float* sm_m = smem;
   float* sm_l = smem + kWaves * kHeads;
   float* sm_o = smem + 2 * kWaves * kHeads;
@@ -333,100 +363,139 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(AttnArgs a) {
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          sm_o[(wave * gn + c) * DP + 128 * u + kJ * (4 * g + r) + j] = o[u][j][r];
+        for (int j = 0; j < kJ; j += 4)
+          *reinterpret_cast<f32x4*>(&sm_o[(wave * gn + c) * kRow + 128 * u + kJ * (4 * g + r) + j]) =
+              f32x4{o[u][j][r], o[u][j + 1][r], o[u][j + 2][r], o[u][j + 3][r]};
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < gn * DP; i += 64 * kWaves) {
-    const int h = i / DP, d = i % DP;
+  for (int i = threadIdx.x; i < gn * (DP / 4); i += 64 * kWaves) {
+    const int h = i / (DP / 4), d = i % (DP / 4) * 4;
     float mm = neg_inf();
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sm_m[w * kHeads + h]);
     const float base = mm == neg_inf() ? 0.f : mm;
-    float sum = 0.f, acc = 0.f;
+    float sum = 0.f;
+    f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const float r = __builtin_amdgcn_exp2f(sm_m[w * kHeads + h] - base);
       sum += r * sm_l[w * kHeads + h];
-      acc += r * sm_o[(w * gn + h) * DP + d];
+      acc += r * *reinterpret_cast<const f32x4*>(&sm_o[(w * gn + h) * kRow + d]);
     }
     const int64_t bh = int64_t(b) * a.Hq + h0 + h;
     if (d == 0 && a.ml) {
       a.ml[(bh * a.splits + split) * 2] = mm;
       a.ml[(bh * a.splits + split) * 2 + 1] = sum;
     }
-    if (d >= a.D) continue;
-    if (a.splits > 1)
-      a.part[(bh * a.splits + split) * a.D + d] = acc;
-    else
-      a.out[int64_t(b) * a.o_b + int64_t(h0 + h) * a.o_h + d] =
-          __builtin_bit_cast(uint16_t, _Float16(sum == 0.f ? 0.f : acc / sum));
+    if (d >= a.D) continue;  // D is a multiple of 8
+    if (a.splits > 1) {
+      *reinterpret_cast<f32x4*>(&a.part[(bh * a.splits + split) * a.D + d]) = acc;
+    } else {
+      uint16_t* dst = a.out + int64_t(b) * a.o_b + int64_t(h0 + h) * a.o_h + d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[e] = __builtin_bit_cast(uint16_t, _Float16(sum == 0.f ? 0.f : acc[e] / sum));
+    }
+  }
+  if (!a.own_weights) return;
+  // Base and reciprocal sum of each head where its first wave's were, then
+  // four tokens a thread.
+  __syncthreads();
+  float base = 0.f, inv = 0.f;
+  if (threadIdx.x < gn) {
+    float mm = neg_inf(), sum = 0.f;
+    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sm_m[w * kHeads + threadIdx.x]);
+    base = mm == neg_inf() ? 0.f : mm;
+    for (int w = 0; w < kWaves; ++w)
+      sum += __builtin_amdgcn_exp2f(sm_m[w * kHeads + threadIdx.x] - base) * sm_l[w * kHeads + threadIdx.x];
+    inv = sum == 0.f ? 0.f : 1.f / sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < gn) {
+    sm_m[threadIdx.x] = base;
+    sm_l[threadIdx.x] = inv;
+  }
+  __syncthreads();
+  for (int t = 4 * threadIdx.x; t < n; t += 4 * 64 * kWaves) {
+    f32x4 w = {0, 0, 0, 0};
+    for (int h = 0; h < gn; ++h) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(sm_x + h * a.lrow + t);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(x[e] - sm_m[h]) * sm_l[h];
+    }
+    add_weights(a, row, hkv, t, n, w);
   }
 }
 
 constexpr int kJoinThreads = 256;
-constexpr int kWeightTokens = 1024;  // tokens whose weights one workgroup adds
+constexpr int kWeightTokens = 4 * kJoinThreads;  // tokens whose weights one workgroup adds
 constexpr int kMaxSplits = 1024;
+constexpr int kStatHeads = 128;  // heads whose maxima and sums a workgroup holds at a time
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) v = fmaxf(v, __shfl_xor(v, s));
+// Maximum and sum over groups of `width` lanes, a power of two.
+__device__ __forceinline__ float max_over(float v, int width) {
+  for (int s = 1; s < width; s *= 2) v = fmaxf(v, __shfl_xor(v, s));
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) v += __shfl_xor(v, s);
+__device__ __forceinline__ float sum_over(float v, int width) {
+  for (int s = 1; s < width; s *= 2) v += __shfl_xor(v, s);
   return v;
-}
-
-// Maximum and sum of one head over its splits (the whole wave gets both).
-__device__ __forceinline__ void head_ml(const float* ml, int valid, int lane, float* m, float* l) {
-  float mm = neg_inf();
-  for (int s = lane; s < valid; s += 64) mm = fmaxf(mm, ml[2 * s]);
-  mm = wave_max(mm);
-  const float base = mm == neg_inf() ? 0.f : mm;
-  float ll = 0.f;
-  for (int s = lane; s < valid; s += 64) ll += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1];
-  *m = mm;
-  *l = wave_sum(ll);
 }
 
 // After the splits: the first `joins` workgroups add up the splits of one
 // query head each; the others add the attention weights of kWeightTokens
-// tokens of a sequence and key-value head to the accumulator.  The adds are
-// atomic because sequences may share a page.
+// tokens of a sequence and key-value head to the accumulator.  Both are chains
+// of a few memory latencies, so every loop requests several rounds before it
+// uses one.
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int joins) {
   __shared__ float sc[kMaxSplits];
-  __shared__ float red[kJoinThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ f32x4 red[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (int(blockIdx.x) < joins) {
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
     const int n = min(max(a.lengths[b], 0), a.cap);
     const int valid = (n + a.split_len - 1) / a.split_len;
     const int64_t bh = int64_t(b) * a.Hq + h;
     const float* ml = a.ml + bh * a.splits * 2;
-    float m, l;
-    head_ml(ml, valid, lane, &m, &l);
+    // every wave finds the maximum and the sum; wave 0 leaves the factors
+    float m = neg_inf();
+    for (int s = lane; s < valid; s += 64) m = fmaxf(m, ml[2 * s]);
+    m = max_over(m, 64);
     const float base = m == neg_inf() ? 0.f : m;
-    for (int s = threadIdx.x; s < valid; s += kJoinThreads) sc[s] = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+    float l = 0.f;
+    for (int s = lane; s < valid; s += 64) {
+      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+      l += f * ml[2 * s + 1];
+      if (wave == 0) sc[s] = f;
+    }
+    l = sum_over(l, 64);
     __syncthreads();
-    // a power of two of threads per split row, the rest in parts over the splits
-    int dp = 64;
-    while (dp < a.D) dp *= 2;
-    const int parts = kJoinThreads / dp, part = threadIdx.x / dp, d = threadIdx.x % dp;
-    float acc = 0.f;
+    // four dimensions a thread, the splits dealt over the threads left
+    const int per = a.D <= 64 ? 16 : a.D <= 128 ? 32 : 64;
+    const int parts = kJoinThreads / per, part = tid / per, d = tid % per * 4;
+    f32x4 acc = {0, 0, 0, 0};
     if (d < a.D) {
       const float* src = a.part + bh * a.splits * a.D + d;
-      for (int s = part; s < valid; s += parts) acc += sc[s] * src[int64_t(s) * a.D];
+      constexpr int kUnroll = 8;
+      for (int s0 = part; s0 < valid; s0 += kUnroll * parts) {
+        f32x4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          v[u] = *reinterpret_cast<const f32x4*>(src + int64_t(min(s0 + u * parts, valid - 1)) * a.D);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (s0 + u * parts < valid) acc += sc[s0 + u * parts] * v[u];
+      }
     }
-    red[threadIdx.x] = acc;
+    red[tid] = acc;
     __syncthreads();
     if (part == 0 && d < a.D) {
-      for (int p = 1; p < parts; ++p) acc += red[p * dp + d];
-      a.out[int64_t(b) * a.o_b + int64_t(h) * a.o_h + d] =
-          __builtin_bit_cast(uint16_t, _Float16(l == 0.f ? 0.f : acc / l));
+      for (int p = 1; p < parts; ++p) acc += red[p * per + tid];
+      uint16_t* dst = a.out + int64_t(b) * a.o_b + int64_t(h) * a.o_h + d;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dst[e] = __builtin_bit_cast(uint16_t, _Float16(l == 0.f ? 0.f : acc[e] / l));
     }
     return;
   }
@@ -436,41 +505,51 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   i /= chunks;
   const int hkv = i % a.Hkv, b = i / a.Hkv;
   const int n = min(max(a.lengths[b], 0), a.cap);
-  const int t0 = chunk * kWeightTokens, t1 = min(t0 + kWeightTokens, n);
-  if (t0 >= t1) return;
+  const int t0 = chunk * kWeightTokens, t = t0 + 4 * tid;
+  if (t0 >= n) return;
   const int valid = (n + a.split_len - 1) / a.split_len;
-  float w[kWeightTokens / kJoinThreads] = {};
-  // kMaxSplits / 2 heads' maxima and reciprocal sums at a time
-  for (int g0 = 0; g0 < a.G; g0 += kMaxSplits / 2) {
-    const int gn = min(a.G - g0, kMaxSplits / 2);
-    for (int g = wave; g < gn; g += kJoinThreads / 64) {
-      const int64_t bh = int64_t(b) * a.Hq + hkv * a.G + g0 + g;
-      float m, l;
-      head_ml(a.ml + bh * a.splits * 2, valid, lane, &m, &l);
-      if (lane == 0) {
-        sc[2 * g] = m == neg_inf() ? 0.f : m;
+  // lanes per head for its maximum and sum over the splits
+  int width = 1;
+  while (width < valid && width < 64) width *= 2;
+  f32x4 w = {0, 0, 0, 0};
+  for (int g0 = 0; g0 < a.G; g0 += kStatHeads) {
+    const int gn = min(a.G - g0, kStatHeads);
+    const int64_t head = int64_t(b) * a.Hq + hkv * a.G + g0;
+    for (int g = tid / width; g < (gn + 63) / 64 * 64; g += kJoinThreads / width) {
+      const float* ml = a.ml + (head + min(g, gn - 1)) * a.splits * 2;
+      const int s0 = tid % width;
+      float m = neg_inf(), l = 0.f;
+      for (int s = s0; s < valid; s += width) m = fmaxf(m, ml[2 * s]);
+      m = max_over(m, width);
+      const float base = m == neg_inf() ? 0.f : m;
+      for (int s = s0; s < valid; s += width) l += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1];
+      l = sum_over(l, width);
+      if (s0 == 0 && g < gn) {
+        sc[2 * g] = base;
         sc[2 * g + 1] = l == 0.f ? 0.f : 1.f / l;
       }
     }
     __syncthreads();
-    for (int g = 0; g < gn; ++g) {
-      const float* x = a.logits + (int64_t(b) * a.Hq + hkv * a.G + g0 + g) * a.cap;
+    if (t < n) {
+      const float* x = a.logits + head * a.lrow + t;  // rows are padded: four tokens are always there
+      constexpr int kUnroll = 4;
+      for (int g = 0; g < gn; g += kUnroll) {
+        f32x4 v[kUnroll];
 #pragma unroll
-      for (int e = 0; e < kWeightTokens / kJoinThreads; ++e) {
-        const int t = t0 + e * kJoinThreads + threadIdx.x;
-        if (t < t1) w[e] += __builtin_amdgcn_exp2f(x[t] - sc[2 * g]) * sc[2 * g + 1];
+        for (int u = 0; u < kUnroll; ++u)
+          v[u] = *reinterpret_cast<const f32x4*>(x + int64_t(min(g + u, gn - 1)) * a.lrow);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (g + u < gn) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
+          }
       }
     }
     __syncthreads();
   }
-  const int32_t* row = a.table + int64_t(b) * a.table_b;
-#pragma unroll
-  for (int e = 0; e < kWeightTokens / kJoinThreads; ++e) {
-    const int t = t0 + e * kJoinThreads + threadIdx.x;
-    if (t >= t1 || w[e] == 0.f) continue;
-    const Place p = place(a, row, t);
-    if (p.ok) unsafeAtomicAdd(a.weights + int64_t(p.page) * a.w_p + int64_t(hkv) * a.w_h + p.slot, w[e]);
-  }
+  add_weights(a, a.table + int64_t(b) * a.table_b, hkv, t, n, w);
 }
 
 template <int DP, bool kFull>
@@ -489,8 +568,19 @@ hipError_t launch_dim(const AttnArgs& a, bool same8, dim3 grid, size_t lds, hipS
 
 }  // namespace
 
-// The split of the length.  A workgroup's four waves take 128 tokens at a
-// time.
+// The split of the length.  A workgroup's four waves take 128 tokens (a step)
+// at a time, at about 1.1 us; a second launch to join the splits costs 5 us
+// (kernel and gap).  So the length is split only where one workgroup per
+// sequence and group of heads leaves CUs idle and takes more than eight steps,
+// then into one workgroup per CU, of two steps or more.  Measured, us, at 1
+// split / this rule: 1 x 4096 tokens, 32 heads 51 / 17; 1 x 8192, 8 heads
+// 89 / 13; 1 x 1000, 32 heads 13 / 13; with two workgroups per CU 1 x 4096
+// takes 17, with four 2 x 131072 tokens of 8 heads 172 (this rule: 164); a
+// batch that fills the CUs loses 15-30% to any split.
+//
+// The weights: one workgroup that sees a whole sequence keeps its scores in
+// LDS and adds the weights itself, as long as three such workgroups fit on a
+// CU; otherwise the scores go through the workspace to the second launch.
 AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, bool weights, int num_cus) {
   AttnPlan p;
   const int64_t G = Hq / Hkv;
@@ -498,21 +588,24 @@ AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t c
   const int64_t step = int64_t(kTile) * kWaves;
   const int64_t steps = std::max<int64_t>(1, (cap + step - 1) / step);
   int64_t splits = 1;
-  const int64_t want = 4 * int64_t(num_cus);
-  if (units < want) splits = std::min<int64_t>({(want + units - 1) / units, (steps + 1) / 2, kMaxSplits});
-  splits = std::max<int64_t>(splits, 1);
+  if (units < num_cus && steps > 8)
+    splits = std::min<int64_t>({(num_cus + units - 1) / units, steps / 2, int64_t(kMaxSplits)});
   const int64_t per = (steps + splits - 1) / splits;
   p.split_len = int(std::min<int64_t>(per * step, (int64_t(1) << 31) - step));
-  p.splits = int((cap + p.split_len - 1) / p.split_len);
-  if (p.splits < 1) p.splits = 1;
+  p.splits = int(std::max<int64_t>(1, (cap + p.split_len - 1) / p.split_len));
+  p.lrow = int((cap + kTile - 1) / kTile * kTile);
+  const int64_t dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+  const int64_t join = 4 * (2 * kWaves * kHeads + kWaves * std::min<int64_t>(G, kHeads) * (dp + 4));
+  p.own_weights = weights && p.splits == 1 && G <= kHeads && join + 4 * G * p.lrow <= 52 * 1024;
+  p.lds = size_t(join + (p.own_weights ? 4 * G * p.lrow : 0));
   const size_t rows = size_t(B) * size_t(Hq);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.bytes = 0;
-  if (p.splits > 1 || weights) p.bytes += up(rows * p.splits * 2 * 4);
+  const bool scores = weights && !p.own_weights;
+  if (p.splits > 1 || scores) p.bytes += up(rows * p.splits * 2 * 4);
   p.off_part = p.bytes;
   if (p.splits > 1) p.bytes += up(rows * p.splits * size_t(D) * 4);
   p.off_logits = p.bytes;
-  if (weights) p.bytes += up(rows * size_t(cap) * 4);
+  if (scores) p.bytes += up(rows * size_t(p.lrow) * 4);
   return p;
 }
 
@@ -551,17 +644,20 @@ hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& 
   a.cap = int(c.per_seq * c.S);
   a.splits = p.splits;
   a.split_len = p.split_len;
+  a.lrow = p.lrow;
   a.scale = r.scale * 1.44269504088896340736f;
-  a.inv_s = 1.0 / double(c.S);
+  a.div = page_div(c.S);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const bool second = p.splits > 1 || r.weights;
+  const bool scores = r.weights && !p.own_weights;
+  const bool second = p.splits > 1 || scores;
+  a.own_weights = p.own_weights;
   if (second) a.ml = reinterpret_cast<float*>(w);
   if (p.splits > 1) a.part = reinterpret_cast<float*>(w + p.off_part);
-  if (r.weights) a.logits = reinterpret_cast<float*>(w + p.off_logits);
+  if (scores) a.logits = reinterpret_cast<float*>(w + p.off_logits);
 
-  const int tiles_h = (a.G + kHeads - 1) / kHeads, gn = std::min(a.G, kHeads);
+  const int tiles_h = (a.G + kHeads - 1) / kHeads;
   const int dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-  const size_t lds = 4 * (2 * kWaves * kHeads + size_t(kWaves) * gn * dp);
+  const size_t lds = p.lds;
   const dim3 grid(a.splits, a.Hkv * tiles_h, a.B);
   const bool same8 = a.S % 8 == 0;
   hipError_t e = dp == 64    ? launch_dim<64>(a, same8, grid, lds, s)
@@ -569,7 +665,7 @@ hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& 
                              : launch_dim<256>(a, same8, grid, lds, s);
   if (e != hipSuccess || !second) return e;
   const int64_t joins = p.splits > 1 ? int64_t(a.B) * a.Hq : 0;
-  const int64_t adds = r.weights ? int64_t(a.B) * a.Hkv * ((a.cap + kWeightTokens - 1) / kWeightTokens) : 0;
+  const int64_t adds = scores ? int64_t(a.B) * a.Hkv * ((a.cap + kWeightTokens - 1) / kWeightTokens) : 0;
   if (joins + adds == 0) return hipSuccess;
   attn_join_kernel<<<dim3(uint32_t(joins + adds)), kJoinThreads, 0, s>>>(a, int(joins));
   return hipGetLastError();

@@ -11,22 +11,33 @@
 // Sources (slots >= budget) and destinations (slots < budget) are disjoint, so
 // the copies need no order among themselves.
 //
-// First launch, one workgroup per (sequence, head): the key of rank `budget`
-// by a radix selection of eight bits at a time (histograms in LDS), then two
-// ordered passes of ballots that number the movers and the free slots.  The
-// list of movers is kept in the map's own row until the second pass, which
-// runs from the top slot down: the i-th free slot j has j >= i, so an entry is
-// read before anything overwrites it.  Second launch: the rows, a wave per 64
-// slots of the map.
+// Up to 32768 tokens, one workgroup per (sequence, head) does everything, its
+// keys in registers (token r * threads + thread, so that a wave's ballot is 64
+// tokens in order):
+//  1. weights and positions, all requested at once; the newest position.
+//  2. The key of rank `budget` from the top: a histogram of the top 11 bits
+//     (LDS atomics), one wave finds the digit where the budget ends.  If few
+//     keys share that digit they are ranked against each other by counting;
+//     otherwise the next 11 and 10 bits follow.  Keys that are equal in all 32
+//     bits are numbered in slot order.
+//  3. A bit per token says who stays; prefix sums over its words number the
+//     movers and the free slots.
+//  4. The map, the weights and positions, and the rows: a wave per pair, several
+//     in flight.
+// Beyond that, the first launch reads the keys again for every pass and a
+// second one copies the rows; the second launch also serves shorter caches
+// with too few heads to fill the CUs and many rows to move.
 //
-// Bound: the weights and positions are read once (8 bytes per token and
-// head; from LDS after that), the moved rows once; at serving sizes the chain
-// of passes inside a workgroup is what takes the time.
+// Bound: by its bytes (8 per token and head, and the moved rows) a call takes
+// a few us at most; what it takes is the chain of some ten barriers and four
+// memory latencies inside a workgroup.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 
 #include "kernels.h"
+#include "paging.h"
+#include "wave.h"
 
 namespace swm {
 namespace {
@@ -34,7 +45,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kFirst = 0xffffffffu;  // key of the tokens that stay before all others
-constexpr int kLdsTokens = 32768;         // tokens whose keys fit in LDS (128 KiB of the CU's 160)
+constexpr int kMaxTokens = 32768;         // tokens whose keys one workgroup holds
 
 struct EvictArgs {
   uint16_t *k, *v;
@@ -46,15 +57,25 @@ struct EvictArgs {
   int64_t k_p, k_s, k_h, v_p, v_s, v_h, table_b;
   int64_t w_p, w_h, p_p, p_h, wo_p, wo_h, po_p, po_h;
   int32_t B, Hkv, D, S, pages, cap, per_seq, budget, recent;
-  double inv_s;
+  int32_t list_len;  // most tokens that can move
+  PageDiv div;  // by S
 };
 
-// Page and slot of token t < capacity; false where the table names no page.
-__device__ __forceinline__ bool place(const EvictArgs& a, const int32_t* row, int t, int* page, int* slot) {
-  const int i = int((double(t) + 0.5) * a.inv_s);
-  *slot = t - i * a.S;
-  *page = row[min(i, a.per_seq - 1)];
-  return *page >= 0 && *page < a.pages;
+// Page and slot of token t < capacity.  Where the table names no page of the
+// pool, ok is false and the page is 0, so that loads need no branch: a branch
+// around each would make a chain of their latencies.
+struct Place {
+  int page, slot;
+  bool ok;
+};
+__device__ __forceinline__ Place place(const EvictArgs& a, const int32_t* row, int t) {
+  Place p;
+  const int i = page_index(a.div, t);
+  p.slot = t - i * a.S;
+  p.page = row[min(i, a.per_seq - 1)];
+  p.ok = p.page >= 0 && p.page < a.pages;
+  p.page = p.ok ? p.page : 0;
+  return p;
 }
 
 // Weights by size as whole numbers: NaN and +inf before all, -0 like +0.
@@ -62,6 +83,36 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t b = __float_as_uint(w + 0.f);
   if ((b & 0x7fffffffu) > 0x7f800000u || b == 0x7f800000u) return kFirst;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Entry of a per-slot array.  kNear: every offset inside the arrays is below
+// 2^30, so one 32-bit multiply-add does; selecting is bound by instructions.
+template <bool kNear, typename T>
+__device__ __forceinline__ T* entry(T* base, int64_t head, int64_t page, int h, const Place& p) {
+  T* at = base + int64_t(h) * head;
+  return kNear ? at + uint32_t(p.page * int32_t(page) + p.slot) : at + (int64_t(p.page) * page + p.slot);
+}
+template <bool kNear = false>
+__device__ __forceinline__ float weight_at(const EvictArgs& a, int h, const Place& p) {
+  return *entry<kNear>(a.w, a.w_h, a.w_p, h, p);
+}
+template <bool kNear = false>
+__device__ __forceinline__ int32_t position_at(const EvictArgs& a, int h, const Place& p) {
+  return *entry<kNear>(a.pos, a.p_h, a.p_p, h, p);
+}
+template <bool kNear = false>
+__device__ __forceinline__ void put(const EvictArgs& a, int h, const Place& p, float w, int32_t pos) {
+  *entry<kNear>(a.w_out, a.wo_h, a.wo_p, h, p) = w;
+  *entry<kNear>(a.pos_out, a.po_h, a.po_p, h, p) = pos;
+}
+
+// Weight and position of the token in slot `from` become those of slot `to`.
+__device__ __forceinline__ void carry(const EvictArgs& a, const int32_t* row, int h, int from, int to) {
+  if (from == to && a.w_out == a.w && a.pos_out == a.pos) return;
+  const Place p0 = place(a, row, from), p1 = place(a, row, to);
+  const float w = weight_at(a, h, p0);
+  const int32_t pos = position_at(a, h, p0);
+  if (p0.ok && p1.ok) put(a, h, p1, w, pos);
 }
 
 template <int kThreads>
@@ -88,9 +139,12 @@ __device__ __forceinline__ int rank_of(Scan<kThreads>& s, bool on, int* total) {
   return before;
 }
 
-template <int kThreads, bool kLds>
-__global__ __launch_bounds__(kThreads) void evict_select_kernel(EvictArgs a) {
-  extern __shared__ uint32_t keys[];
+// Any length: the keys are read again in every pass.  The list of movers is
+// kept in the map's own row until the last pass, which runs from the top slot
+// down: the i-th free slot j has j >= i, so an entry is read before anything
+// overwrites it.
+template <int kThreads>
+__global__ __launch_bounds__(kThreads) void evict_long_kernel(EvictArgs a) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t chosen[2];
   __shared__ int32_t red[kThreads / 64];
@@ -102,33 +156,19 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(EvictArgs a) {
   if (h == 0 && tid == 0) a.lengths_out[b] = left;
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   int32_t* kept = a.kept + (int64_t(b) * a.Hkv + h) * a.budget;
-  const float* w = a.w + int64_t(h) * a.w_h;
-  const int32_t* pos = a.pos + int64_t(h) * a.p_h;
-  float* wo = a.w_out + int64_t(h) * a.wo_h;
-  int32_t* po = a.pos_out + int64_t(h) * a.po_h;
-  const bool copy = a.w_out != a.w, copy_p = a.pos_out != a.pos;
-
-  // weight and position of the token in slot `from` become those of slot `to`
-  auto carry = [&](int from, int to) {
-    int p0, s0, p1, s1;
-    if (!place(a, row, from, &p0, &s0) || !place(a, row, to, &p1, &s1)) return;
-    if (from != to || copy) wo[int64_t(p1) * a.wo_p + s1] = w[int64_t(p0) * a.w_p + s0];
-    if (from != to || copy_p) po[int64_t(p1) * a.po_p + s1] = pos[int64_t(p0) * a.p_p + s0];
-  };
-
   for (int j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
   if (n <= a.budget || left == 0) {
     for (int j = tid; j < left; j += kThreads) {
       kept[j] = j;
-      carry(j, j);
+      carry(a, row, h, j, j);
     }
     return;
   }
 
   int newest = -2147483647 - 1;
   for (int t = tid; t < n; t += kThreads) {
-    int p, s;
-    if (place(a, row, t, &p, &s)) newest = max(newest, pos[int64_t(p) * a.p_p + s]);
+    const Place p = place(a, row, t);
+    if (p.ok) newest = max(newest, position_at(a, h, p));
   }
 #pragma unroll
   for (int s = 1; s < 64; s *= 2) newest = max(newest, __shfl_xor(newest, s));
@@ -138,17 +178,11 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(EvictArgs a) {
   for (int i = 0; i < kThreads / 64; ++i) newest = max(newest, red[i]);
   const int64_t since = int64_t(newest) - a.recent;
 
-  auto key_of = [&](int t) -> uint32_t {
-    int p, s;
-    if (!place(a, row, t, &p, &s)) return 0;
-    if (int64_t(pos[int64_t(p) * a.p_p + s]) > since) return kFirst;
-    return weight_key(w[int64_t(p) * a.w_p + s]);
+  auto key = [&](int t) -> uint32_t {
+    const Place p = place(a, row, t);
+    if (!p.ok) return 0;
+    return int64_t(position_at(a, h, p)) > since ? kFirst : weight_key(weight_at(a, h, p));
   };
-  if (kLds) {
-    for (int t = tid; t < n; t += kThreads) keys[t] = key_of(t);
-    __syncthreads();
-  }
-  auto key = [&](int t) -> uint32_t { return kLds ? keys[t] : key_of(t); };
 
   // The key of rank `budget` from the top, eight bits at a time; `want` of the
   // keys that share the bits found so far are still to be taken.
@@ -231,13 +265,346 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(EvictArgs a) {
     __syncthreads();  // every entry that this chunk overwrites has been read
     if (in) {
       kept[t] = from;
-      carry(from, t);
+      carry(a, row, h, from, t);
     }
   }
 }
 
-// A wave per 64 slots of the map; lanes 0..31 carry a key row, 32..63 the value
-// row.
+// Copies rows of one head.  Each lane names one pair of slots (from < 0: none);
+// their places are looked up together, then the wave copies pair by pair, lanes
+// 0..31 the key row and 32..63 the value row, kRows in flight (past the last
+// pair, that one is read again).  A pair with a slot on no page is left out.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const int32_t* row, int h, int from, int to) {
+  const int lane = threadIdx.x & 63, half = lane >> 5, d = (lane & 31) * 8;
+  uint16_t* base = half ? a.v + int64_t(h) * a.v_h : a.k + int64_t(h) * a.k_h;
+  const int64_t sp = half ? a.v_p : a.k_p, ss = half ? a.v_s : a.k_s;
+  const Place p0 = place(a, row, max(from, 0)), p1 = place(a, row, to);
+  uint64_t todo = __builtin_amdgcn_ballot_w64(from >= 0 && p0.ok && p1.ok);
+  const int dl = d < a.D ? d : 0;  // lanes past the row read its start and store nothing
+  constexpr int kRows = 8;
+  while (todo) {
+    u32x4 x[kRows];
+    int l[kRows];
+    bool on[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      on[u] = todo != 0;
+      l[u] = on[u] ? __builtin_ctzll(todo) : l[u ? u - 1 : 0];
+      todo &= todo - 1;
+      x[u] = *reinterpret_cast<const u32x4*>(base + int64_t(__builtin_amdgcn_readlane(p0.page, l[u])) * sp +
+                                             int64_t(__builtin_amdgcn_readlane(p0.slot, l[u])) * ss + dl);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (on[u] && d < a.D)
+        *reinterpret_cast<u32x4*>(base + int64_t(__builtin_amdgcn_readlane(p1.page, l[u])) * sp +
+                                  int64_t(__builtin_amdgcn_readlane(p1.slot, l[u])) * ss + d) = x[u];
+  }
+}
+
+constexpr int kDigit = 11;          // bits of a histogram
+constexpr int kBins = 1 << kDigit;
+constexpr int kCandidates = 512;    // keys ranked by counting
+
+// Histogram entries, one word of padding per 32: 64 lanes that read 32 bins
+// each then hit different banks.
+__device__ __forceinline__ uint32_t bin_at(uint32_t bin) { return bin + (bin >> 5); }
+
+// Counts the active lanes' bins.  Lanes that share the first one's bin (recent
+// tokens, tokens nothing looked at) count once together: an atomic per lane
+// would queue up on one address.
+__device__ __forceinline__ void count_bins(uint32_t* hist, uint32_t bin, bool active) {
+  const uint64_t all = __builtin_amdgcn_ballot_w64(active);
+  if (all == 0) return;
+  const int leader = __builtin_ctzll(all);
+  const uint32_t first = uint32_t(__builtin_amdgcn_readlane(int(bin), leader));
+  const uint64_t same = __builtin_amdgcn_ballot_w64(active && bin == first);
+  if (int(threadIdx.x & 63) == leader)
+    atomicAdd(&hist[bin_at(first)], uint32_t(__popcll(same)));
+  else if (active && bin != first)
+    atomicAdd(&hist[bin_at(bin)], 1u);
+}
+
+// Sums of the lanes up to and including this one.
+__device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) {
+    const uint32_t o = __shfl_up(v, s);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+// kR tokens a thread, kThreads * kR in all.  move: also copy the rows.
+template <int kThreads, int kR, bool kNear>
+__global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a, int move) {
+  constexpr int kWaves = kThreads / 64, kWords = kWaves * kR;  // word r * kWaves + wave: 64 tokens in order
+  extern __shared__ uint16_t lists[];  // movers, then free slots: list_len entries each
+  __shared__ uint32_t hist[kBins + kBins / 32];
+  __shared__ uint64_t cand[kCandidates];
+  __shared__ uint64_t stay[kWords];
+  __shared__ uint32_t before[kWords];  // movers << 16 | free slots in earlier words
+  __shared__ uint32_t chosen[4];
+  __shared__ int32_t red[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int32_t* row = a.table + int64_t(b) * a.table_b;
+  const int n = min(max(a.lengths[b], 0), a.cap);
+  const int left = min(n, a.budget);
+  if (h == 0 && tid == 0) a.lengths_out[b] = left;
+  int32_t* kept = a.kept + (int64_t(b) * a.Hkv + h) * a.budget;
+  for (int j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
+  if (n <= a.budget || left == 0) {
+    for (int j = tid; j < left; j += kThreads) {
+      kept[j] = j;
+      carry(a, row, h, j, j);
+    }
+    return;
+  }
+
+  // kR <= 8: weights and positions stay in registers for the end
+  constexpr bool kHold = kR <= 8;
+  float wr[kR];
+  int32_t pr[kR];
+  uint32_t key[kR];
+  uint32_t there = 0;  // bit r: the thread's r-th token is on a page
+  {
+    Place at[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      pr[r] = -2147483647 - 1;
+      wr[r] = 0.f;
+      at[r] = Place{0, 0, false};
+      if (r * kThreads >= n) continue;  // the same for every thread, here and below
+      at[r] = place(a, row, min(r * kThreads + tid, n - 1));
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (r * kThreads >= n) continue;
+      const bool ok = at[r].ok && r * kThreads + tid < n;
+      wr[r] = weight_at<kNear>(a, h, at[r]);
+      pr[r] = position_at<kNear>(a, h, at[r]);
+      there |= uint32_t(ok) << r;
+    }
+    for (int i = tid; i < kBins + kBins / 32; i += kThreads) hist[i] = 0;
+    if (tid < 4) chosen[tid] = 0;
+    int newest = -2147483647 - 1;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) newest = (there >> r) & 1 ? max(newest, pr[r]) : newest;
+    newest = wave_max(newest);
+    if (lane == 0) red[wave] = newest;
+    __syncthreads();
+    newest = wave_max(red[min(lane, kWaves - 1)]);
+    const int64_t since = int64_t(newest) - a.recent;
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      key[r] = !((there >> r) & 1) ? 0u : int64_t(pr[r]) > since ? kFirst : weight_key(wr[r]);
+  }
+
+  // Digit by digit: `prefix` holds the bits found so far (those above `shift`),
+  // `want` of the keys that share them are still to be taken.
+  uint32_t prefix = 0, want = uint32_t(a.budget), sharing = 0;
+  int shift = 32;
+#pragma unroll 1
+  do {
+    const int bits = shift > kDigit ? kDigit : shift;  // 11, 11, 10
+    const int above = shift;
+    shift -= bits;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (r * kThreads >= n) continue;
+      count_bins(hist, (key[r] >> shift) & ((1u << bits) - 1),
+                 r * kThreads + tid < n && (above == 32 || (key[r] >> above) == prefix));
+    }
+    __syncthreads();
+    if (wave == 0) {  // lane l holds the 32 bins from kBins - 1 - 32 l downwards
+      uint32_t sum = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum += hist[bin_at(kBins - 1 - 32 * lane) - i];
+      const uint32_t upto = scan_wave(sum);
+      const uint64_t reach = __builtin_amdgcn_ballot_w64(upto >= want);
+      const int l = __builtin_ctzll(reach);  // the lane whose bins hold the budget's end
+      const uint32_t over = uint32_t(__builtin_amdgcn_readlane(int(upto - sum), l));
+      const uint32_t c = lane < 32 ? hist[bin_at(kBins - 1 - 32 * l) - lane] : 0;
+      const uint32_t u2 = over + scan_wave(c);
+      if (u2 >= want && u2 - c < want && lane < 32) {
+        chosen[0] = uint32_t(kBins - 1 - 32 * l - lane);
+        chosen[1] = want - (u2 - c);
+        chosen[2] = c;
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << bits) | chosen[0];
+    want = chosen[1];
+    sharing = chosen[2];
+    if (shift > 0 && sharing > kCandidates) {
+      for (int i = tid; i < kBins + kBins / 32; i += kThreads) hist[i] = 0;
+      __syncthreads();
+    }
+  } while (shift > 0 && sharing > kCandidates);
+
+  // Keys above the prefix stay; of those that share it the `want` best, by
+  // their key and then the lower slot.
+  uint32_t taken = 0;  // bit r: the thread's r-th token is one of them
+  if (sharing == want) {
+    taken = ~0u;
+  } else if (sharing <= kCandidates) {
+    uint32_t at[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int t = r * kThreads + tid;
+      at[r] = ~0u;
+      if (r * kThreads >= n) continue;
+      if (t < n && (key[r] >> shift) == prefix) {
+        at[r] = atomicAdd(&chosen[3], 1u);
+        cand[at[r]] = uint64_t(key[r]) << 32 | (0xffffffffu - uint32_t(t));
+      }
+    }
+    __syncthreads();
+    // `sharing` threads rank one candidate each
+    if (tid < int(sharing)) {
+      const uint64_t mine = cand[tid];
+      uint32_t rank = 0;
+#pragma unroll 8
+      for (uint32_t j = 0; j < sharing; ++j) rank += cand[j] > mine;
+      hist[tid] = rank < want;
+    }
+    if (kThreads < kCandidates && tid + kThreads < int(sharing)) {
+      const uint64_t mine = cand[tid + kThreads];
+      uint32_t rank = 0;
+#pragma unroll 8
+      for (uint32_t j = 0; j < sharing; ++j) rank += cand[j] > mine;
+      hist[tid + kThreads] = rank < want;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      if (at[r] != ~0u && hist[at[r]]) taken |= 1u << r;
+  } else {  // more equal keys than that: in slot order
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const uint64_t e = __builtin_amdgcn_ballot_w64(r * kThreads + tid < n && key[r] == prefix);
+      if (lane == 0) stay[r * kWaves + wave] = e;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      uint32_t run = 0;
+      for (int w0 = 0; w0 < kWords; w0 += 64) {
+        const uint32_t c = w0 + lane < kWords ? __popcll(stay[w0 + lane]) : 0;
+        const uint32_t upto = scan_wave(c);
+        if (w0 + lane < kWords) before[w0 + lane] = run + upto - c;
+        run += __shfl(upto, 63);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const uint64_t e = stay[r * kWaves + wave];
+      const uint32_t rank = before[r * kWaves + wave] +
+                            __builtin_amdgcn_mbcnt_hi(uint32_t(e >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(e), 0u));
+      if (rank < want) taken |= 1u << r;
+    }
+    __syncthreads();
+  }
+
+  uint32_t mine = 0;  // bit r: the thread's r-th token stays
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    const uint32_t x = key[r] >> shift;
+    const bool on = r * kThreads + tid < n && (x > prefix || (x == prefix && ((taken >> r) & 1)));
+    const uint64_t e = __builtin_amdgcn_ballot_w64(on);
+    mine |= uint32_t(on) << r;
+    if (lane == 0) stay[r * kWaves + wave] = e;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    uint32_t run = 0;
+#pragma unroll 1
+    for (int w0 = 0; w0 < kWords; w0 += 64) {
+      const int first = (w0 + lane) * 64;  // the word's first token
+      uint32_t c = 0;
+      if (w0 + lane < kWords) {
+        const uint64_t e = stay[w0 + lane];
+        const int below = min(max(a.budget - first, 0), 64);  // tokens of the word below the budget
+        const uint64_t m = below == 64 ? ~0ull : (1ull << below) - 1;
+        c = uint32_t(__popcll(e & ~m)) << 16 | uint32_t(__popcll(~e & m));
+      }
+      const uint32_t upto = scan_wave(c);
+      if (w0 + lane < kWords) before[w0 + lane] = run + upto - c;
+      run += __shfl(upto, 63);
+    }
+    if (lane == 0) chosen[0] = run >> 16;  // how many move
+  }
+  __syncthreads();
+  const int movers = int(chosen[0]);
+  uint16_t* from = lists;
+  uint16_t* freed = lists + a.list_len;
+  // Number of the thread's r-th token among the movers, or of its slot among
+  // the free ones.
+  auto rank = [&](int r, bool mover) -> uint32_t {
+    const uint64_t e = stay[r * kWaves + wave], lanes = (1ull << lane) - 1;
+    const uint32_t base = before[r * kWaves + wave];
+    const int below = min(max(a.budget - (r * kThreads + tid - lane), 0), 64);
+    const uint64_t m = below == 64 ? ~0ull : (1ull << below) - 1;
+    return mover ? (base >> 16) + __popcll(e & ~m & lanes) : (base & 0xffffu) + __popcll(~e & m & lanes);
+  };
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    if (r * kThreads >= n) continue;
+    const int t = r * kThreads + tid;
+    const bool on = (mine >> r) & 1;
+    if (t < a.budget && on) kept[t] = t;
+    if (t < a.budget && !on) freed[rank(r, false)] = uint16_t(t);
+    if (t >= a.budget && on) from[rank(r, true)] = uint16_t(t);
+  }
+  __syncthreads();
+  // Every token that stays tells its slot where it is from; eight at a time, so
+  // that their lookups overlap.
+  const bool copy = a.w_out != a.w || a.pos_out != a.pos;
+  constexpr int kG = kR < 8 ? kR : 8;
+#pragma unroll 1
+  for (int r0 = 0; r0 < kR; r0 += kG) {
+    if (r0 * kThreads >= n) break;
+    float w8[kG];
+    int32_t p8[kG];
+    int to[kG];
+    Place at[kG];
+#pragma unroll
+    for (int u = 0; u < kG; ++u) {
+      const int r = r0 + u, t = r * kThreads + tid;
+      const bool on = (mine >> r) & 1;
+      to[u] = !on ? -1 : t < a.budget ? (copy ? t : -1) : int(freed[rank(r, true)]);
+      if (kHold) {
+        w8[u] = wr[u];
+        p8[u] = pr[u];
+      } else {
+        const Place own = place(a, row, min(t, n - 1));
+        w8[u] = weight_at<kNear>(a, h, own);
+        p8[u] = position_at<kNear>(a, h, own);
+      }
+      at[u] = place(a, row, max(to[u], 0));
+    }
+#pragma unroll
+    for (int u = 0; u < kG; ++u) {
+      const int t = (r0 + u) * kThreads + tid;
+      if (to[u] < 0) continue;
+      if (t >= a.budget) kept[to[u]] = t;
+      if (at[u].ok && ((there >> (r0 + u)) & 1)) put<kNear>(a, h, at[u], w8[u], p8[u]);
+    }
+  }
+  if (move) {
+    // the pairs dealt evenly: at most 64 a wave and round
+    const int share = min((movers + kWaves - 1) / kWaves, 64);
+    for (int i0 = 0; i0 < movers; i0 += share * kWaves) {
+      const int i = i0 + wave * share + lane;
+      const bool on = lane < share && i < movers;
+      move_rows(a, row, h, on ? int(from[i]) : -1, on ? int(freed[i]) : 0);
+    }
+  }
+}
+
+// The rows alone, a wave per 64 slots of the map.
 __global__ __launch_bounds__(256) void evict_move_kernel(EvictArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int h = blockIdx.y, b = blockIdx.z;
@@ -245,47 +612,33 @@ __global__ __launch_bounds__(256) void evict_move_kernel(EvictArgs a) {
   if (j0 >= a.budget) return;
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   const int32_t* kept = a.kept + (int64_t(b) * a.Hkv + h) * a.budget;
-  const int j = j0 + lane;
-  const int from = j < a.budget ? kept[j] : -1;
-  // both places of the lane's own slot, as element offsets; -1 where it stays
-  int64_t ks = -1, kd = 0, vs = 0, vd = 0;
-  if (from >= a.budget) {
-    int p0, s0, p1, s1;
-    if (place(a, row, from, &p0, &s0) && place(a, row, j, &p1, &s1)) {
-      ks = int64_t(p0) * a.k_p + int64_t(s0) * a.k_s;
-      kd = int64_t(p1) * a.k_p + int64_t(s1) * a.k_s;
-      vs = int64_t(p0) * a.v_p + int64_t(s0) * a.v_s;
-      vd = int64_t(p1) * a.v_p + int64_t(s1) * a.v_s;
-    }
+  const int from = j0 + lane < a.budget ? kept[j0 + lane] : -1;
+  move_rows(a, row, h, from >= a.budget ? from : -1, j0 + lane);
+}
+
+template <int kThreads, int kR, bool kNear>
+hipError_t launch_near(const EvictArgs& a, int move, hipStream_t s) {
+  const size_t lds = 4 * size_t(a.list_len);
+  constexpr size_t kStatic = 4 * kBins + 8 * kCandidates + 12 * (kThreads / 64) * kR + 2048;
+  if (lds + kStatic > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<kThreads, kR, kNear>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
   }
-  uint64_t todo = __builtin_amdgcn_ballot_w64(ks >= 0);
-  const int half = lane >> 5, d = (lane & 31) * 8;
-  uint16_t* base = half ? a.v + int64_t(h) * a.v_h : a.k + int64_t(h) * a.k_h;
-  while (todo) {
-    constexpr int kRows = 4;  // rows in flight
-    u32x4 x[kRows];
-    int64_t to[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      to[i] = -1;
-      if (todo) {
-        const int l = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        const int64_t k0 = __shfl(ks, l), k1 = __shfl(kd, l), v0 = __shfl(vs, l), v1 = __shfl(vd, l);
-        const int64_t src = half ? v0 : k0;
-        to[i] = half ? v1 : k1;
-        if (d < a.D) x[i] = *reinterpret_cast<const u32x4*>(base + src + d);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (to[i] >= 0 && d < a.D) *reinterpret_cast<u32x4*>(base + to[i] + d) = x[i];
-  }
+  evict_kernel<kThreads, kR, kNear><<<dim3(a.Hkv, a.B), kThreads, lds, s>>>(a, move);
+  return hipGetLastError();
+}
+
+template <int kThreads, int kR>
+hipError_t launch_one(const EvictArgs& a, int move, hipStream_t s) {
+  const int64_t far = std::max({a.w_p, a.p_p, a.wo_p, a.po_p});
+  const bool near = far < (int64_t(1) << 30) && a.pages * far + a.S < (int64_t(1) << 30);
+  return near ? launch_near<kThreads, kR, true>(a, move, s) : launch_near<kThreads, kR, false>(a, move, s);
 }
 
 }  // namespace
 
-hipError_t launch_evict(const KvView& c, const EvictCall& r, hipStream_t s) {
+hipError_t launch_evict(const KvView& c, const EvictCall& r, int num_cus, hipStream_t s) {
   EvictArgs a{};
   a.k = c.k;
   a.v = c.v;
@@ -321,23 +674,24 @@ hipError_t launch_evict(const KvView& c, const EvictCall& r, hipStream_t s) {
   a.cap = int(c.per_seq * c.S);
   a.budget = int(r.budget);
   a.recent = int(r.recent);
-  a.inv_s = 1.0 / double(c.S);
-  constexpr int kThreads = 1024;
-  const dim3 grid(a.Hkv, a.B);
-  if (a.cap <= kLdsTokens) {
-    const size_t lds = 4 * size_t(std::max(a.cap, 1));
-    if (lds > 60 * 1024) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_select_kernel<kThreads, true>),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-      if (e != hipSuccess) return e;
-    }
-    evict_select_kernel<kThreads, true><<<grid, kThreads, lds, s>>>(a);
+  a.div = page_div(c.S);
+  a.list_len = std::max(0, std::min(a.budget, a.cap - a.budget));
+  // The workgroup that selects also moves, unless workgroups are too few to
+  // move many rows at the memory's rate (15 x 8 heads, 7098 to 3549 tokens: 65
+  // us against 47 with a launch of its own; 16 x 8, 2176 to 2048: 19 against 24).
+  const bool move = int64_t(a.Hkv) * a.B >= num_cus || a.list_len <= 512;
+  hipError_t e;
+  if (a.cap <= 2048) {
+    e = launch_one<512, 4>(a, move, s);
+  } else if (a.cap <= 8192) {
+    e = launch_one<1024, 8>(a, move, s);
+  } else if (a.cap <= kMaxTokens) {
+    e = a.cap <= 16384 ? launch_one<1024, 16>(a, move, s) : launch_one<1024, 32>(a, move, s);
   } else {
-    evict_select_kernel<kThreads, false><<<grid, kThreads, 0, s>>>(a);
+    evict_long_kernel<1024><<<dim3(a.Hkv, a.B), 1024, 0, s>>>(a);
+    e = hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
-  // nothing can move unless the capacity is beyond the budget
-  if (e != hipSuccess || a.cap <= a.budget || a.budget == 0) return e;
+  if (e != hipSuccess || a.list_len == 0 || (move && a.cap <= kMaxTokens)) return e;
   evict_move_kernel<<<dim3((a.budget + 255) / 256, a.Hkv, a.B), 256, 0, s>>>(a);
   return hipGetLastError();
 }

@@ -158,7 +158,9 @@ struct AttnCall {
   float scale = 1.f;
 };
 struct AttnPlan {
-  int splits = 1, split_len = 0;
+  int splits = 1, split_len = 0, lrow = 0;
+  bool own_weights = false;                        // the weights are added by the first launch
+  size_t lds = 0;                                  // of a workgroup of the first launch
   size_t off_part = 0, off_logits = 0, bytes = 0;  // workspace
 };
 AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, bool weights, int num_cus);
@@ -172,7 +174,7 @@ struct EvictCall {
   int64_t w_p = 0, w_h = 0, p_p = 0, p_h = 0, wo_p = 0, wo_h = 0, po_p = 0, po_h = 0;
   int64_t budget = 0, recent = 0;
 };
-hipError_t launch_evict(const KvView& c, const EvictCall& r, hipStream_t s);
+hipError_t launch_evict(const KvView& c, const EvictCall& r, int num_cus, hipStream_t s);
 
 // Log probabilities, entropy and top tokens of N rows of V logits.
 constexpr int kLogprobMaxTop = 64;
@@ -184,7 +186,7 @@ struct LogprobCall {
   int32_t top = 0;
   bool fp32 = false, wide = false;  // 32-bit logits, 64-bit targets
 };
-hipError_t launch_logprobs(const LogprobCall& r, hipStream_t s);
+hipError_t launch_logprobs(const LogprobCall& r, int num_cus, hipStream_t s);
 
 hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& p, void* ws, hipStream_t s);
 

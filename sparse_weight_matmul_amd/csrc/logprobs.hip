@@ -30,6 +30,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "wave.h"
 
 // A part's base m log2(e) is one rounded number wherever it is used: fusing
 // its product into a subtraction would give parts of different bases.  The
@@ -43,8 +44,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kGroups = 256;   // groups whose maxima bound the top tokens from below
-constexpr int kList = 1024;    // candidates ranked by counting
+constexpr int kMaxGroups = 128;  // groups whose maxima bound the top tokens from below
 
 struct LogprobArgs {
   const void* x;
@@ -60,6 +60,7 @@ struct Row;
 template <>
 struct Row<_Float16> {
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = 0xfc00fc00u;  // -inf
   static __device__ __forceinline__ void unpack(const u32x4& w, float* f) {
     typedef _Float16 half8 __attribute__((ext_vector_type(8)));
     const half8 h = __builtin_bit_cast(half8, w);
@@ -70,6 +71,7 @@ struct Row<_Float16> {
 template <>
 struct Row<float> {
   static constexpr int kVec = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void unpack(const u32x4& w, float* f) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(w[e]);
@@ -103,14 +105,6 @@ __device__ __forceinline__ void rebase(Part& p, float m) {
   p.l *= r;
   p.m = m;
 }
-__device__ __forceinline__ void merge(Part& p, Part o) {
-  const float m = fmaxf(p.m, o.m);
-  rebase(p, m);
-  rebase(o, m);
-  p.l += o.l;
-  p.s += o.s;
-}
-
 template <int n>
 __device__ __forceinline__ void take(Part& p, const float* f) {
   float top = f[0];
@@ -127,11 +121,13 @@ __device__ __forceinline__ void take(Part& p, const float* f) {
   }
 }
 
-template <typename T, int kThreads, bool kTop>
+// kR > 0: a thread's vectors, kR at most, stay in registers and the top tokens
+// are found there; kR = 0: the row is streamed.
+template <typename T, int kThreads, int kR, bool kTop>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   constexpr int kVec = Row<T>::kVec;
   constexpr int kWaves = kThreads / 64;
-  __shared__ float red[kWaves][3];
+  __shared__ float red[kWaves][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t n = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + n * a.ld;
@@ -140,50 +136,71 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   const int vecs = (a.V - lead) / kVec;
   const int rest = lead + vecs * kVec;
   const u32x4* xv = reinterpret_cast<const u32x4*>(x + lead);
+  const bool head = tid < lead, tail = rest + tid < a.V;  // a logit of either end
 
   Part p{neg_inf(), 0.f, 0.f};
-  constexpr int kUnroll = 4;
-  int i = tid;
-  for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
-    u32x4 w[kUnroll];
+  u32x4 keep[kR > 0 ? kR : 1];
+  if constexpr (kR > 0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) w[u] = xv[i + u * kThreads];
+    for (int r = 0; r < kR; ++r) {
+      constexpr uint32_t z = Row<T>::kNone;
+      keep[r] = tid + r * kThreads < vecs ? xv[tid + r * kThreads] : u32x4{z, z, z, z};
+    }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int r = 0; r < kR; ++r) {
+      if (r * kThreads >= vecs) break;  // the same for every thread
       float f[kVec];
-      Row<T>::unpack(w[u], f);
+      Row<T>::unpack(keep[r], f);
+      take<kVec>(p, f);
+    }
+  } else {
+    constexpr int kUnroll = 4;
+    int i = tid;
+    for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
+      u32x4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) w[u] = xv[i + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float f[kVec];
+        Row<T>::unpack(w[u], f);
+        take<kVec>(p, f);
+      }
+    }
+    for (; i < vecs; i += kThreads) {
+      float f[kVec];
+      Row<T>::unpack(xv[i], f);
       take<kVec>(p, f);
     }
   }
-  for (; i < vecs; i += kThreads) {
-    float f[kVec];
-    Row<T>::unpack(xv[i], f);
-    take<kVec>(p, f);
+  const float xh = head ? float(x[tid]) : neg_inf(), xt = tail ? float(x[rest + tid]) : neg_inf();
+  int64_t target = -1;
+  float at_target = 0.f;
+  if (a.targets && tid == 0) {
+    target = a.wide ? static_cast<const int64_t*>(a.targets)[n] : int64_t(static_cast<const int32_t*>(a.targets)[n]);
+    at_target = float(x[target >= 0 && target < a.V ? target : 0]);
   }
-  if (tid < lead) {
-    const float f = float(x[tid]);
-    take<1>(p, &f);
-  }
-  if (rest + tid < a.V) {
-    const float f = float(x[rest + tid]);
-    take<1>(p, &f);
-  }
+  if (lead > 0) take<1>(p, &xh);
+  if (rest < a.V) take<1>(p, &xt);
   const float own = p.m;  // the largest logit of this thread
 
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    Part o{__shfl_xor(p.m, s), __shfl_xor(p.l, s), __shfl_xor(p.s, s)};
-    merge(p, o);
+  // Maximum first, then every part moves to it once and the sums are added.
+  rebase(p, wave_max(p.m));
+  p.l = wave_sum(p.l);
+  p.s = wave_sum(p.s);
+  if constexpr (kWaves > 1) {
+    if (lane == 0) {
+      red[wave][0] = p.m;
+      red[wave][1] = p.l;
+      red[wave][2] = p.s;
+    }
+    __syncthreads();
+    p = Part{neg_inf(), 0.f, 0.f};
+    if (lane < kWaves) p = Part{red[lane][0], red[lane][1], red[lane][2]};
+    rebase(p, wave_max(p.m));
+    p.l = wave_sum(p.l);
+    p.s = wave_sum(p.s);
   }
-  if (lane == 0) {
-    red[wave][0] = p.m;
-    red[wave][1] = p.l;
-    red[wave][2] = p.s;
-  }
-  __syncthreads();
-  p = Part{red[0][0], red[0][1], red[0][2]};
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) merge(p, Part{red[w][0], red[w][1], red[w][2]});
   const bool none = p.l == 0.f;  // every logit is -inf: log probabilities of -inf, entropy 0
   const float log2l = none ? 0.f : __builtin_log2f(p.l);
   const float base = base_of(p.m);
@@ -191,26 +208,25 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   auto logp_of = [&](float v) { return (__builtin_fmaf(v, kLog2e, -base) - log2l) * kLn2; };
 
   if (tid == 0) {
-    if (a.targets) {
-      const int64_t t = a.wide ? static_cast<const int64_t*>(a.targets)[n] : static_cast<const int32_t*>(a.targets)[n];
-      a.logp[n] = t < 0 ? 0.f : t < a.V ? logp_of(float(x[t])) : __builtin_nanf("");
-    }
+    if (a.targets) a.logp[n] = target < 0 ? 0.f : target < a.V ? logp_of(at_target) : __builtin_nanf("");
     if (a.entropy) a.entropy[n] = none ? 0.f : (log2l - p.s / p.l) * kLn2;
   }
-  if (!kTop) return;
-
+  if constexpr (kTop) {
+  constexpr int kGroups = kThreads < kMaxGroups ? kThreads : kMaxGroups;
+  constexpr int kList = kThreads < 256 ? 512 : 1024;  // candidates ranked by counting
   __shared__ uint32_t group[kGroups];
   __shared__ uint64_t list[kList];
   __shared__ uint32_t bound, count;
   const int k = min(a.top, a.V);
   // a thread without logits has the key 0, below that of -inf
-  const bool has = tid < vecs || tid < lead || rest + tid < a.V;
+  const bool has = tid < vecs || head || tail;
   const uint32_t mine = has ? key_of(own) : 0u;
   constexpr int kPer = kThreads / kGroups;
   uint32_t g = mine;
-#pragma unroll
-  for (int s = 1; s < kPer; s *= 2) g = max(g, uint32_t(__shfl_xor(int(g), s)));
-  if (tid % kPer == 0) group[tid / kPer] = g;
+  if (kPer > 1) g = max(g, rotate_row<1>(g));  // 4 or 8 consecutive lanes of a row: maxima of the last kPer
+  if (kPer > 2) g = max(g, rotate_row<2>(g));
+  if (kPer > 4) g = max(g, rotate_row<4>(g));
+  if (tid % kPer == kPer - 1) group[tid / kPer] = g;
   if (tid == 0) count = 0;
   __syncthreads();
   if (tid < kGroups) {
@@ -236,14 +252,37 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       if (c < kList) list[c] = uint64_t(key) << 32 | (0xffffffffu - uint32_t(at));
     };
     if (has && mine >= least) {
-      for (int j = tid; j < vecs; j += kThreads) {
-        float f[kVec];
-        Row<T>::unpack(xv[j], f);
+      if constexpr (kR > 0) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) push(f[e], lead + j * kVec + e);
+        for (int r = 0; r < kR; ++r) {
+          if (tid + r * kThreads >= vecs) break;
+          float f[kVec];
+          Row<T>::unpack(keep[r], f);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) push(f[e], lead + (tid + r * kThreads) * kVec + e);
+        }
+      } else {
+        constexpr int kUnroll = 4;
+        for (int j = tid; j < vecs; j += kUnroll * kThreads) {
+          u32x4 w[kUnroll];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) w[u] = xv[min(j + u * kThreads, vecs - 1)];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u) {
+            if (j + u * kThreads >= vecs) break;
+            float f[kVec];
+            Row<T>::unpack(w[u], f);
+            float top = f[0];
+#pragma unroll
+            for (int e = 1; e < kVec; ++e) top = fmaxf(top, f[e]);
+            if (key_of(top) < least && !(top != top)) continue;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) push(f[e], lead + (j + u * kThreads) * kVec + e);
+          }
+        }
       }
-      if (tid < lead) push(float(x[tid]), tid);
-      if (rest + tid < a.V) push(float(x[rest + tid]), rest + tid);
+      if (head) push(xh, tid);
+      if (tail) push(xt, rest + tid);
     }
     __syncthreads();
   };
@@ -311,21 +350,38 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     ids[r] = -1;
     lps[r] = neg_inf();
   }
+  }
 }
 
-template <typename T, int kThreads>
+template <typename T, int kThreads, int kR>
 hipError_t launch(const LogprobArgs& a, int64_t N, hipStream_t s) {
   const dim3 grid = dim3(uint32_t(N));
   if (a.top > 0)
-    logprobs_kernel<T, kThreads, true><<<grid, kThreads, 0, s>>>(a);
+    logprobs_kernel<T, kThreads, kR, true><<<grid, kThreads, 0, s>>>(a);
   else
-    logprobs_kernel<T, kThreads, false><<<grid, kThreads, 0, s>>>(a);
+    logprobs_kernel<T, kThreads, kR, false><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Threads of a row: a wave where the rows alone fill the chip, more where they
+// do not, and no more than the row has work for.  Rows whose vectors fit in
+// eight registers' worth a thread stay there.
+template <typename T>
+hipError_t launch_rows(const LogprobArgs& a, int64_t N, int num_cus, hipStream_t s) {
+  constexpr int kR = 8;
+  const int64_t vecs = a.V / Row<T>::kVec + 1;
+  const int by_rows = N >= 8 * num_cus ? 64 : N >= num_cus ? 256 : 1024;
+  const int by_row = vecs <= 256 ? 64 : vecs <= 2048 ? 256 : 1024;
+  switch (std::min(by_rows, by_row)) {
+    case 64: return vecs <= 64 * kR ? launch<T, 64, kR>(a, N, s) : launch<T, 64, 0>(a, N, s);
+    case 256: return vecs <= 256 * kR ? launch<T, 256, kR>(a, N, s) : launch<T, 256, 0>(a, N, s);
+    default: return vecs <= 1024 * kR ? launch<T, 1024, kR>(a, N, s) : launch<T, 1024, 0>(a, N, s);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_logprobs(const LogprobCall& r, hipStream_t s) {
+hipError_t launch_logprobs(const LogprobCall& r, int num_cus, hipStream_t s) {
   LogprobArgs a{};
   a.x = r.logits;
   a.targets = r.targets;
@@ -337,7 +393,7 @@ hipError_t launch_logprobs(const LogprobCall& r, hipStream_t s) {
   a.V = int(r.V);
   a.top = r.top;
   a.wide = r.wide;
-  return r.fp32 ? launch<float, 1024>(a, r.N, s) : launch<_Float16, 1024>(a, r.N, s);
+  return r.fp32 ? launch_rows<float>(a, r.N, num_cus, s) : launch_rows<_Float16>(a, r.N, num_cus, s);
 }
 
 }  // namespace swm

@@ -160,7 +160,9 @@ swm_status swm_kv_evict(const swm_kv_cache* c, const float* weights, int64_t w_p
   r.po_h = po_head;
   r.budget = budget;
   r.recent = recent;
-  SWM_HIP(swm::launch_evict(v, r, static_cast<hipStream_t>(stream)));
+  int dev = 0;
+  SWM_HIP(hipGetDevice(&dev));
+  SWM_HIP(swm::launch_evict(v, r, swm::num_cus(dev), static_cast<hipStream_t>(stream)));
   return SWM_OK;
 }
 
@@ -187,7 +189,9 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
   r.fp32 = fp32 != 0;
   r.wide = wide != 0;
   swm_log("token_logprobs N=%lld V=%lld top=%d: a workgroup per row", (long long)N, (long long)V, top);
-  SWM_HIP(swm::launch_logprobs(r, static_cast<hipStream_t>(stream)));
+  int dev = 0;
+  SWM_HIP(hipGetDevice(&dev));
+  SWM_HIP(swm::launch_logprobs(r, swm::num_cus(dev), static_cast<hipStream_t>(stream)));
   return SWM_OK;
 }
 

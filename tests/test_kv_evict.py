@@ -61,6 +61,8 @@ def make(B, H, D, S, lengths, kind, seed=0):
     elif kind == "wild":  # NaN of both signs, infinities, subnormals, negative weights
         w = r.choice(np.array([np.nan, -np.nan, np.inf, -np.inf, 1e-42, -1e-42, 0.0, -0.0, -1.5, 3.0, 1e30],
                               np.float32), (P, H, S))
+    elif kind == "close":  # thousands of keys that share their top bits, some all of them
+        w = (1 + r.integers(0, 1500, (P, H, S)) * 2.0**-23).astype(np.float32)
     else:
         w = (r.random((P, H, S)) ** 6 * 4).astype(np.float32)
     pos = r.permuted(np.tile(np.arange(P * S, dtype=np.int32), (H, 1)), axis=1).reshape(H, P, S).transpose(1, 0, 2)
@@ -96,6 +98,12 @@ CASES = [
     (1, 2, 8, 128, [40000], 9000, 500, "long", "token"),     # more tokens than the keys that fit on chip
     (1, 1, 8, 256, [33000], 32990, 500, "ties", "token"),
     (1, 1, 8, 100, [20000], 150, 20, "equal", "token"),
+    (2, 2, 64, 16, [2000, 1900], 1100, 10, "close", "token"),
+    (1, 2, 64, 16, [8192], 8191, 0, "close", "head"),
+    (1, 2, 8, 32, [32768], 16384, 300, "long", "token"),
+    (1, 1, 8, 32, [32700], 10, 5, "close", "token"),
+    (300, 1, 8, 8, [21] * 300, 20, 4, "long", "token"),
+    (1, 2, 128, 16, [3000], 1000, 100, "long", "head"),       # few heads, many rows: a second launch moves them
     (2, 2, 64, 16, [100, 50], 0, 3, "long", "token"),
     (2, 2, 64, 16, [100, 50], 1000, 3, "long", "token"),     # a budget beyond the capacity
 ]

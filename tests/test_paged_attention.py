@@ -287,7 +287,10 @@ def test_binding_refuses(gpu_lib):
         odd = torch.zeros(2 * 4 * 64 + 4, dtype=torch.float16, device="cuda")[4:].view(2, 4, 64)
         swm.paged_attention(c, odd)
     with pytest.raises(swm.SwmError):
-        swm.paged_attention(c, dev["q"], weights=torch.zeros((k.shape[0], 2, 16), device="cuda"),
+        # more query heads to a key-value head than one workgroup takes: the scores go through the workspace
+        many = torch.zeros((2, 34, 64), dtype=torch.float16, device="cuda")
+        assert c.attention_workspace_bytes(34, True) > 16
+        swm.paged_attention(c, many, weights=torch.zeros((k.shape[0], 2, 16), device="cuda"),
                             workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
 
 
