@@ -472,14 +472,23 @@ swm_status swm_hbm_stream(const void* buf, size_t bytes, int32_t unroll, int32_t
  *  bias: DEVICE fp16, M entries, or NULL.  act: SWM_ACT_*.  residual: DEVICE
  *  fp16 token-major N x M (ldr >= M), or NULL; it may be Y itself (same
  *  address and ldr == ldy: an update in place), and must not overlap it
- *  otherwise.  The other arguments, the workspace
- *  (swm_spmm_workspace_bytes) and the errors are swm_spmm_ws's; with no bias,
- *  no residual and SWM_ACT_NONE the result is the same bits.
+ *  otherwise.  The other arguments and the errors are swm_spmm_ws's; with no
+ *  bias, no residual and SWM_ACT_NONE the result is the same bits.  At 33 to
+ *  255 tokens it chooses between slices of 32 tokens through the decode
+ *  kernels, W expanded into the workspace and swm_spmm's on-chip kernel by
+ *  what they take for these sizes (the fp32 sums are the same but for their
+ *  order); a workspace that is not there or too small for that only takes the
+ *  expansion off the choice.
  *  SWM_ERR_INVALID_ARG also: an unknown act, ldr < M, residual == Y with
  *  ldr != ldy. */
 swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
                              const void* bias, int32_t act, const void* residual, int64_t ldr, void* workspace,
                              size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace swm_spmm_epilogue uses for N tokens on the current
+ * device: swm_spmm_workspace_bytes, and M*K*2 rounded up to 256 where it would
+ * expand W at 33 to 255 tokens. */
+size_t swm_spmm_epilogue_workspace_bytes(const swm_format* f, int64_t N);
 
 /* ------------------------------------------------------------------ serving
  * What a pruned model's decode step needs between its products. */

@@ -70,6 +70,7 @@ SIGNATURES = {
     "swm_spmm": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp]),
     "swm_spmm_workspace_bytes": (_sz, [_vp, _i64]),
     "swm_spmm_ws": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "swm_spmm_epilogue_workspace_bytes": (_sz, [_vp, _i64]),
     "swm_spmm_epilogue": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _vp, _i64, _vp, _sz, _vp]),
     "swm_spmspv": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp]),
     "swm_spmspv_noalloc": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp]),
@@ -349,11 +350,18 @@ def spmm_ws(fmt: Format, X, workspace, Y=None, stream=None):
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
+def spmm_epilogue_workspace_bytes(fmt: Format, N: int) -> int:
+    """Device workspace bytes spmm_epilogue uses for N tokens (0: none)."""
+    return int(load().swm_spmm_epilogue_workspace_bytes(fmt._h, int(N)))
+
+
 def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, workspace=None, Y=None, stream=None):
     """Y (N, M) = act(X @ (W * mask).T + bias) + residual, rounded once: spmm_ws
     with its epilogue in the same launches.  bias: (M,) fp16 or None; act:
     "none", "relu", "silu" or "gelu"; residual: (N, M) fp16 or None, which may
-    be Y itself; workspace: as for spmm_ws (spmm_workspace_bytes)."""
+    be Y itself; workspace: a contiguous CUDA tensor of
+    spmm_epilogue_workspace_bytes(fmt, N) bytes; None allocates it where the
+    call uses one."""
     import torch
     lib = load()
     if act not in ACTIVATIONS:
@@ -377,8 +385,9 @@ def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, w
             Y = _empty((N, M), X.dtype, X.device, stream)
     yp, ldy = _rows(Y, "Y", N, M)
     wp, wb = None, 0
-    if workspace is not None:
-        workspace, wp, wb = _workspace(workspace, 0, X.device, stream)
+    if N > 32:  # below, W is streamed
+        need = 0 if workspace is not None else int(lib.swm_spmm_epilogue_workspace_bytes(fmt._h, N))
+        workspace, wp, wb = _workspace(workspace, need, X.device, stream)
     _check(lib.swm_spmm_epilogue(fmt._h, xp, ldx, yp, ldy, N, bp, ACTIVATIONS[act], rp, ldr, wp, wb,
                                  _raw_stream(stream, X.device.index)), "swm_spmm_epilogue")
     return Y

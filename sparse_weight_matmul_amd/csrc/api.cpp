@@ -431,7 +431,8 @@ static bool run_smf(const swm_format* f, const void* X, int64_t ldx, void* Y, in
                     const swm::Epilogue& epi, hipStream_t s, swm_status* st);
 
 static swm_status run_products(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy,
-                               int64_t N, bool skip, hipStream_t s, const swm::Epilogue& epi = {}) {
+                               int64_t N, bool skip, hipStream_t s, const swm::Epilogue& epi = {},
+                               bool sliced = false) {
   if (!f || !X || !Y) return SWM_ERR_INVALID_ARG;
   if (N <= 0 || ldx < f->h.k || ldy < f->h.m || ldx <= 0 || ldy <= 0) return SWM_ERR_INVALID_ARG;
   swm_status st = check_tile_supported(f->h);
@@ -453,8 +454,8 @@ static swm_status run_products(const swm_format* f, const void* X, int64_t ldx, 
     return SWM_OK;
   }
   swm_status sst = SWM_OK;
-  if (!skip && run_smf(f, X, ldx, Y, ldy, N, epi, s, &sst)) return sst;
-  if (!skip && swm::prefill_supported(f->h.k, ldx, X) && swm::prefill_sparse_lds(f->h) <= 160 * 1024 &&
+  if (!skip && !sliced && run_smf(f, X, ldx, Y, ldy, N, epi, s, &sst)) return sst;
+  if (!skip && !sliced && swm::prefill_supported(f->h.k, ldx, X) && swm::prefill_sparse_lds(f->h) <= 160 * 1024 &&
       swm::prefill_sparse_fits(f->h, N, ldx)) {
     swm_log("spmm M=%lld K=%lld N=%lld: on-chip prefill (128x256 blocks)", (long long)f->h.m, (long long)f->h.k,
             (long long)N);
@@ -559,13 +560,41 @@ size_t swm_spmm_workspace_bytes(const swm_format* f, int64_t N) {
   return align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
 }
 
+// The product with an epilogue at 33 to 255 tokens, where spmm's on-chip
+// kernel (one 256-token block, bound by its K steps) is slower than token
+// slices through the decode kernels or W expanded once.  The fastest by what
+// each was measured to take, in us with Mi = M K / 2^20 and rounds of blocks
+// over the CUs (4096x4096 at N = 33 / 96 / 192: slices 22 / 46 / 93, expanded
+// 54 / 55 / 56 + 6 for the residual, on chip 86; 4096x11008 at 64 / 192: 64 /
+// 195, 134 / 142, 208; 11008x4096 at 48 / 96: 60 / 128, 69 / 70, 86):
+//   slices of 32    0.9 Mi + 1 each, 5 at least
+//   expanded        0.55 Mi + 11 + 0.62 per 64 columns of K and round
+//   on chip         5 + 1.28 per 64 columns of K and round
+enum class MidRoute { kSlices, kExpand, kOnChip };
+
+static MidRoute mid_route(const swm::Header& h, int64_t N, int64_t cus, bool workspace) {
+  const double mi = double(h.m) * double(h.k) / 1048576.0, steps = double(h.k) / 64.0;
+  const double rounds = double(((h.m + 127) / 128 + cus - 1) / cus);
+  const double slices = double((N + 31) / 32) * std::max(5.0, 0.9 * mi + 1.0);
+  const double expand = 0.55 * mi + 11.0 + 0.62 * steps * rounds, chip = 5.0 + 1.28 * steps * rounds;
+  if (slices <= chip && (!workspace || slices <= expand)) return MidRoute::kSlices;
+  return workspace && expand < chip ? MidRoute::kExpand : MidRoute::kOnChip;
+}
+
+// Where the rule above applies (K and W as the expansion needs them).
+static bool mid_tokens(const swm_format* f, int64_t N) {
+  return N > 32 && N < 256 && f->h.k >= 8 && f->h.k % 8 == 0 && f->h.m > 0 && !smf_route(f, N) &&
+         !expand_route(f->h, N);
+}
+
 static swm_status run_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
                               void* workspace, size_t ws_bytes, hipStream_t s, const swm::Epilogue& epi) {
   if (!f || !X || !Y) return SWM_ERR_INVALID_ARG;
   if (!workspace && ws_bytes == 0) return run_products(f, X, ldx, Y, ldy, N, false, s, epi);
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return SWM_ERR_ALIGN;
   if (!workspace) return SWM_ERR_INVALID_ARG;
-  const size_t need = swm_spmm_workspace_bytes(f, N);
+  size_t need = swm_spmm_workspace_bytes(f, N);
+  if (epi.expand) need = align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
   if (need == 0 || !swm::prefill_supported(f->h.k, ldx, X))
     return run_products(f, X, ldx, Y, ldy, N, false, s, epi);
   if (ws_bytes < need) return SWM_ERR_INVALID_ARG;
@@ -600,7 +629,28 @@ swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, vo
   e.ldr = residual ? ldr : 0;
   e.act = act;
   e.on = bias || residual || act != SWM_ACT_NONE;
-  return run_spmm_ws(f, X, ldx, Y, ldy, N, workspace, ws_bytes, static_cast<hipStream_t>(stream), e);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (e.on && X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X)) {
+    int dev = 0;
+    SWM_HIP(hipGetDevice(&dev));
+    const bool fits = workspace && ws_bytes >= swm_spmm_epilogue_workspace_bytes(f, N) &&
+                      (reinterpret_cast<uintptr_t>(workspace) & 15) == 0;
+    switch (mid_route(f->h, N, num_cus(dev), fits)) {
+      case MidRoute::kSlices: return run_products(f, X, ldx, Y, ldy, N, false, s, e, true);
+      case MidRoute::kExpand: e.expand = 1; break;
+      case MidRoute::kOnChip: return run_products(f, X, ldx, Y, ldy, N, false, s, e);
+    }
+  }
+  return run_spmm_ws(f, X, ldx, Y, ldy, N, workspace, ws_bytes, s, e);
+}
+
+size_t swm_spmm_epilogue_workspace_bytes(const swm_format* f, int64_t N) {
+  const size_t need = swm_spmm_workspace_bytes(f, N);
+  if (need > 0 || !f || !mid_tokens(f, N)) return need;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  if (mid_route(f->h, N, num_cus(dev), true) != MidRoute::kExpand) return 0;
+  return align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
 }
 
 static swm_status run_colruns(const swm_format* f, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t n,

@@ -17,6 +17,7 @@ struct Epilogue {
   int64_t ldr = 0;
   int32_t act = 0;  // 0 none, 1 ReLU, 2 SiLU, 3 GELU
   int32_t on = 0;   // 0: the plain product
+  int32_t expand = 0;  // expand W into the workspace at any token count (host only)
 };
 
 // Device memory of one SWM-TCB v2 handle (16-row tiles).

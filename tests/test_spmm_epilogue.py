@@ -53,7 +53,8 @@ def t(a):
 
 def workspace(f, N):
     import torch
-    need = swm.spmm_workspace_bytes(f, N)
+    need = swm.spmm_epilogue_workspace_bytes(f, N)
+    assert need >= swm.spmm_workspace_bytes(f, N)
     return torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
 
 
@@ -62,7 +63,8 @@ SHAPES = [
     (300, 520, 1), (300, 520, 4), (17, 64, 7), (300, 520, 16), (4096, 1024, 13),     # straight-line decode
     (300, 520, 17), (300, 520, 32),                                                  # two groups of 16 tokens
     (33, 77, 1), (33, 77, 20), (33, 77, 40), (1, 1, 1),                              # unaligned: looped, in slices
-    (300, 520, 33), (300, 520, 200), (1001, 264, 130),                               # on-chip prefill
+    (300, 520, 33), (300, 520, 200), (1001, 264, 130),                               # slices, on-chip, expanded
+    (4096, 1024, 100), (2000, 4096, 255), (130, 64, 64), (5000, 200, 37),
     (300, 520, 257), (260, 136, 1027),                                               # expanded, 128 x 128 blocks
     (4096, 256, 2048), (4099, 128, 3000), (8192, 64, 4096),                          # larger blocks
 ]
@@ -82,6 +84,10 @@ def test_routes(gpu_lib, M, K, N):
             check(Y, W, X, b if bias else None, act, R if res else None)
     a = swm.spmm_epilogue(f, Xd, workspace=ws)
     assert torch.equal(a, swm.spmm_ws(f, Xd, ws))
+    check(swm.spmm_epilogue(f, Xd, bd, "silu", Rd), W, X, b, "silu", R)  # a workspace of its own
+    if 32 < N < 256:  # one that is too small takes the expansion off the choice
+        small = torch.empty(16, dtype=torch.uint8, device="cuda")
+        check(swm.spmm_epilogue(f, Xd, bd, "silu", Rd, small), W, X, b, "silu", R)
     c = swm.spmm_epilogue(f, Xd, bd, "gelu", Rd, ws)
     assert torch.equal(c, swm.spmm_epilogue(f, Xd, bd, "gelu", Rd, ws))
     inplace = Rd.clone()  # the residual stream updated in place
@@ -155,6 +161,12 @@ def test_extreme_sums(gpu_lib):
     f = swm.sparse_compress(W)
     for act in ACTS:
         check(swm.spmm_epilogue(f, t(X), act=act), W, X, None, act, None)
+    # the tail of GELU keeps its relative accuracy down to the subnormal numbers
+    X[:, 0] = -np.array([2, 2.5, 3, 3.5, 4, 4.25, 4.5, 4.75, 5, 5.25, 5.5, 5.75])
+    check(swm.spmm_epilogue(f, t(X), act="gelu"), W, X, None, "gelu", None)
+    X[0, 0] = np.nan
+    for act in ACTS:
+        assert bool(torch.isnan(swm.spmm_epilogue(f, t(X[:1]), act=act, bias=t(np.ones(16, np.float16)))).all())
     X[0, 0] = np.inf
     Y = swm.spmm_epilogue(f, t(X[:1]), act="gelu", bias=t(np.ones(16, np.float16)))
     assert bool((Y == float("inf")).all())
@@ -211,4 +223,5 @@ def test_refusals(gpu_lib):
 
 def test_null_handle():
     lib = swm.load()
+    assert lib.swm_spmm_epilogue_workspace_bytes(None, 100) == 0
     assert lib.swm_spmm_epilogue(None, 4096, 64, 8192, 64, 4, None, 0, None, 0, None, 0, None) == 1
