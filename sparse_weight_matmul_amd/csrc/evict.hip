@@ -12,18 +12,19 @@
 // the copies need no order among themselves.
 //
 // Up to 32768 tokens, one workgroup per (sequence, head) does everything, its
-// keys in registers (token r * threads + thread, so that a wave's ballot is 64
-// tokens in order):
-//  1. weights and positions, all requested at once; the newest position.
+// keys in registers, four consecutive tokens to a thread:
+//  1. Weights and positions, 16 bytes a load, all requested at once; the newest
+//     position.
 //  2. The key of rank `budget` from the top: a histogram of the top 11 bits
 //     (LDS atomics), one wave finds the digit where the budget ends.  If few
 //     keys share that digit they are ranked against each other by counting;
-//     otherwise the next 11 and 10 bits follow.  Keys that are equal in all 32
-//     bits are numbered in slot order.
-//  3. A bit per token says who stays; prefix sums over its words number the
-//     movers and the free slots.
-//  4. The map, the weights and positions, and the rows: a wave per pair, several
-//     in flight.
+//     otherwise the next 11 and 10 bits follow, and keys that are equal in all
+//     bits are numbered in slot order.  (Counting by ballots two or three bits
+//     at a time took longer at every length: 2000 cycles a step, 6 to 16 steps.)
+//  3. Ballots and a prefix sum over the chunks of 256 tokens number the movers
+//     and the free slots.
+//  4. The map, the weights and positions, and the rows: a wave per 64 pairs,
+//     eight rows in flight.
 // Beyond that, the first launch reads the keys again for every pass and a
 // second one copies the rows; the second launch also serves shorter caches
 // with too few heads to fill the CUs and many rows to move.
@@ -58,6 +59,7 @@ struct EvictArgs {
   int64_t w_p, w_h, p_p, p_h, wo_p, wo_h, po_p, po_h;
   int32_t B, Hkv, D, S, pages, cap, per_seq, budget, recent;
   int32_t list_len;  // most tokens that can move
+  int32_t vec;       // four weights or positions by one 16-byte load
   PageDiv div;  // by S
 };
 
@@ -302,9 +304,9 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const int32_t* row
   }
 }
 
-constexpr int kDigit = 11;          // bits of a histogram
+constexpr int kDigit = 11;        // bits of a histogram
 constexpr int kBins = 1 << kDigit;
-constexpr int kCandidates = 512;    // keys ranked by counting
+constexpr int kCandidates = 512;  // keys ranked by counting
 
 // Histogram entries, one word of padding per 32: 64 lanes that read 32 bins
 // each then hit different banks.
@@ -336,16 +338,52 @@ __device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
   return v;
 }
 
-// kR tokens a thread, kThreads * kR in all.  move: also copy the rows.
-template <int kThreads, int kR, bool kNear>
-__global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a, int move) {
-  constexpr int kWaves = kThreads / 64, kWords = kWaves * kR;  // word r * kWaves + wave: 64 tokens in order
+// Set lanes of b before this one.
+__device__ __forceinline__ uint32_t lanes_before(uint64_t b) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), 0u));
+}
+
+// Weights, positions and places of the four tokens from t on (clamped to last).
+// vec: a page holds a multiple of four slots and both arrays are aligned for
+// 16-byte loads, so one place and two loads do.
+template <bool kNear>
+__device__ __forceinline__ void load4(const EvictArgs& a, const int32_t* row, int h, int t, int last, Place (&at)[4],
+                                      float (&w)[4], int32_t (&pos)[4]) {
+  if (a.vec) {
+    at[0] = place(a, row, min(t, last & ~3));
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    const f32x4 wv = *reinterpret_cast<const f32x4*>(entry<kNear>(a.w, a.w_h, a.w_p, h, at[0]));
+    const i32x4 pv = *reinterpret_cast<const i32x4*>(entry<kNear>(a.pos, a.p_h, a.p_p, h, at[0]));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      at[e] = Place{at[0].page, at[0].slot + e, at[0].ok};
+      w[e] = wv[e];
+      pos[e] = pv[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[e] = place(a, row, min(t + e, last));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] = weight_at<kNear>(a, h, at[e]);
+      pos[e] = position_at<kNear>(a, h, at[e]);
+    }
+  }
+}
+
+// Thread i holds tokens 4 (q kThreads + i) .. + 3 for q < kQ: a chunk of 256
+// tokens per wave and q, in order.  move: also copy the rows.
+template <int kThreads, int kQ, bool kNear>
+__global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictArgs a, int move) {
+  constexpr int kWaves = kThreads / 64, kChunks = kWaves * kQ;
+  constexpr bool kHold = kQ <= 2;  // weights and positions stay in registers for the end
+  static_assert(kChunks <= 128, "");
   extern __shared__ uint16_t lists[];  // movers, then free slots: list_len entries each
   __shared__ uint32_t hist[kBins + kBins / 32];
   __shared__ uint64_t cand[kCandidates];
-  __shared__ uint64_t stay[kWords];
-  __shared__ uint32_t before[kWords];  // movers << 16 | free slots in earlier words
-  __shared__ uint32_t chosen[4];
+  __shared__ uint32_t chunk[kChunks];
+  __shared__ uint32_t listed, chosen[3];
   __shared__ int32_t red[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int h = blockIdx.x, b = blockIdx.y;
@@ -363,59 +401,64 @@ __global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a, int move) 
     return;
   }
 
-  // kR <= 8: weights and positions stay in registers for the end
-  constexpr bool kHold = kR <= 8;
-  float wr[kR];
-  int32_t pr[kR];
-  uint32_t key[kR];
-  uint32_t there = 0;  // bit r: the thread's r-th token is on a page
+  float w[kQ][4];
+  int32_t pos[kQ][4];
+  uint32_t key[kQ][4];
+  uint32_t there = 0;  // bit 4q + e: the token is below the length and on a page
   {
-    Place at[kR];
+    Place at[kQ][4];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      pr[r] = -2147483647 - 1;
-      wr[r] = 0.f;
-      at[r] = Place{0, 0, false};
-      if (r * kThreads >= n) continue;  // the same for every thread, here and below
-      at[r] = place(a, row, min(r * kThreads + tid, n - 1));
+    for (int q = 0; q < kQ; ++q) {
+      if (4 * q * kThreads >= n) continue;  // the same for every thread, here and below
+      load4<kNear>(a, row, h, 4 * (q * kThreads + tid), n - 1, at[q], w[q], pos[q]);
     }
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      if (r * kThreads >= n) continue;
-      const bool ok = at[r].ok && r * kThreads + tid < n;
-      wr[r] = weight_at<kNear>(a, h, at[r]);
-      pr[r] = position_at<kNear>(a, h, at[r]);
-      there |= uint32_t(ok) << r;
-    }
-    for (int i = tid; i < kBins + kBins / 32; i += kThreads) hist[i] = 0;
-    if (tid < 4) chosen[tid] = 0;
     int newest = -2147483647 - 1;
 #pragma unroll
-    for (int r = 0; r < kR; ++r) newest = (there >> r) & 1 ? max(newest, pr[r]) : newest;
+    for (int q = 0; q < kQ; ++q) {
+      if (4 * q * kThreads >= n) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool ok = 4 * (q * kThreads + tid) + e < n && at[q][e].ok;
+        there |= uint32_t(ok) << (4 * q + e);
+        newest = ok ? max(newest, pos[q][e]) : newest;
+      }
+    }
     newest = wave_max(newest);
     if (lane == 0) red[wave] = newest;
+    if (tid == 0) listed = 0;
+    for (int i = tid; i < kBins + kBins / 32; i += kThreads) hist[i] = 0;
     __syncthreads();
     newest = wave_max(red[min(lane, kWaves - 1)]);
+    // positions above `since` are recent (none if it would be below the smallest number)
     const int64_t since = int64_t(newest) - a.recent;
+    const bool all = since < -2147483647 - 1;
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
-      key[r] = !((there >> r) & 1) ? 0u : int64_t(pr[r]) > since ? kFirst : weight_key(wr[r]);
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        key[q][e] = 0;
+        if (4 * q * kThreads >= n) continue;
+        const uint32_t k = all || pos[q][e] > int32_t(since) ? kFirst : weight_key(w[q][e]);
+        key[q][e] = (there >> (4 * q + e)) & 1 ? k : 0u;
+      }
   }
 
-  // Digit by digit: `prefix` holds the bits found so far (those above `shift`),
-  // `want` of the keys that share them are still to be taken.
+  // The key of rank `budget` from the top, 11, 11 and 10 bits at a time:
+  // `prefix` holds the bits found so far (those above `shift`), `sharing` keys
+  // have them, of which `want` stay.
   uint32_t prefix = 0, want = uint32_t(a.budget), sharing = 0;
   int shift = 32;
 #pragma unroll 1
   do {
-    const int bits = shift > kDigit ? kDigit : shift;  // 11, 11, 10
-    const int above = shift;
+    const int bits = min(kDigit, shift), over = shift;
     shift -= bits;
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      if (r * kThreads >= n) continue;
-      count_bins(hist, (key[r] >> shift) & ((1u << bits) - 1),
-                 r * kThreads + tid < n && (above == 32 || (key[r] >> above) == prefix));
+    for (int q = 0; q < kQ; ++q) {
+      if (4 * q * kThreads >= n) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        count_bins(hist, (key[q][e] >> shift) & ((1u << bits) - 1),
+                   4 * (q * kThreads + tid) + e < n && (over == 32 || (key[q][e] >> over) == prefix));
     }
     __syncthreads();
     if (wave == 0) {  // lane l holds the 32 bins from kBins - 1 - 32 l downwards
@@ -425,12 +468,12 @@ __global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a, int move) 
       const uint32_t upto = scan_wave(sum);
       const uint64_t reach = __builtin_amdgcn_ballot_w64(upto >= want);
       const int l = __builtin_ctzll(reach);  // the lane whose bins hold the budget's end
-      const uint32_t over = uint32_t(__builtin_amdgcn_readlane(int(upto - sum), l));
+      const uint32_t before = uint32_t(__builtin_amdgcn_readlane(int(upto - sum), l));
       const uint32_t c = lane < 32 ? hist[bin_at(kBins - 1 - 32 * l) - lane] : 0;
-      const uint32_t u2 = over + scan_wave(c);
-      if (u2 >= want && u2 - c < want && lane < 32) {
+      const uint32_t u = before + scan_wave(c);
+      if (u >= want && u - c < want && lane < 32) {
         chosen[0] = uint32_t(kBins - 1 - 32 * l - lane);
-        chosen[1] = want - (u2 - c);
+        chosen[1] = want - (u - c);
         chosen[2] = c;
       }
     }
@@ -444,153 +487,156 @@ __global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a, int move) 
     }
   } while (shift > 0 && sharing > kCandidates);
 
-  // Keys above the prefix stay; of those that share it the `want` best, by
-  // their key and then the lower slot.
-  uint32_t taken = 0;  // bit r: the thread's r-th token is one of them
+  // Keys above stay; of those that share the prefix the `want` best, by their
+  // key and then the lower slot.
+  uint32_t taken = ~0u;  // bit 4q + e: if it shares the prefix, the token stays
   if (sharing == want) {
-    taken = ~0u;
+    // all of them
   } else if (sharing <= kCandidates) {
-    uint32_t at[kR];
+    uint32_t at[kQ][4];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int t = r * kThreads + tid;
-      at[r] = ~0u;
-      if (r * kThreads >= n) continue;
-      if (t < n && (key[r] >> shift) == prefix) {
-        at[r] = atomicAdd(&chosen[3], 1u);
-        cand[at[r]] = uint64_t(key[r]) << 32 | (0xffffffffu - uint32_t(t));
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 4 * (q * kThreads + tid) + e;
+        at[q][e] = ~0u;
+        if (t < n && (key[q][e] >> shift) == prefix) {
+          at[q][e] = atomicAdd(&listed, 1u);
+          cand[at[q][e]] = uint64_t(key[q][e]) << 32 | (0xffffffffu - uint32_t(t));
+        }
       }
-    }
     __syncthreads();
-    // `sharing` threads rank one candidate each
-    if (tid < int(sharing)) {
-      const uint64_t mine = cand[tid];
+    for (int i = tid; i < int(sharing); i += kThreads) {
+      const uint64_t mine = cand[i];
       uint32_t rank = 0;
 #pragma unroll 8
       for (uint32_t j = 0; j < sharing; ++j) rank += cand[j] > mine;
-      hist[tid] = rank < want;
-    }
-    if (kThreads < kCandidates && tid + kThreads < int(sharing)) {
-      const uint64_t mine = cand[tid + kThreads];
-      uint32_t rank = 0;
-#pragma unroll 8
-      for (uint32_t j = 0; j < sharing; ++j) rank += cand[j] > mine;
-      hist[tid + kThreads] = rank < want;
+      hist[i] = rank < want;  // the counts have been read
     }
     __syncthreads();
+    taken = 0;
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
-      if (at[r] != ~0u && hist[at[r]]) taken |= 1u << r;
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (at[q][e] != ~0u && hist[at[q][e]]) taken |= 1u << (4 * q + e);
   } else {  // more equal keys than that: in slot order
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const uint64_t e = __builtin_amdgcn_ballot_w64(r * kThreads + tid < n && key[r] == prefix);
-      if (lane == 0) stay[r * kWaves + wave] = e;
+    for (int q = 0; q < kQ; ++q) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c += __popcll(__builtin_amdgcn_ballot_w64(4 * (q * kThreads + tid) + e < n && key[q][e] == prefix));
+      if (lane == 0) chunk[q * kWaves + wave] = c;
     }
     __syncthreads();
-    if (wave == 0) {
-      uint32_t run = 0;
-      for (int w0 = 0; w0 < kWords; w0 += 64) {
-        const uint32_t c = w0 + lane < kWords ? __popcll(stay[w0 + lane]) : 0;
-        const uint32_t upto = scan_wave(c);
-        if (w0 + lane < kWords) before[w0 + lane] = run + upto - c;
-        run += __shfl(upto, 63);
+    const uint32_t c0 = lane < kChunks ? chunk[lane] : 0, c1 = 64 + lane < kChunks ? chunk[min(64 + lane, kChunks - 1)] : 0;
+    const uint32_t u0 = scan_wave(c0), u1 = __shfl(u0, 63) + scan_wave(c1) - c1;  // u1: before the second 64
+    taken = 0;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const int i = q * kWaves + wave;
+      uint32_t rank = i < 64 ? __shfl(u0 - c0, i) : __shfl(u1, i - 64);
+      bool equal[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        equal[e] = 4 * (q * kThreads + tid) + e < n && key[q][e] == prefix;
+        rank += lanes_before(__builtin_amdgcn_ballot_w64(equal[e]));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (equal[e] && rank < want) taken |= 1u << (4 * q + e);
+        rank += equal[e];
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const uint64_t e = stay[r * kWaves + wave];
-      const uint32_t rank = before[r * kWaves + wave] +
-                            __builtin_amdgcn_mbcnt_hi(uint32_t(e >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(e), 0u));
-      if (rank < want) taken |= 1u << r;
-    }
-    __syncthreads();
+    __syncthreads();  // chunk is written again
   }
 
-  uint32_t mine = 0;  // bit r: the thread's r-th token stays
+  // Who stays, and how many movers and free slots each chunk has.
+  uint32_t mine = 0;
 #pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const uint32_t x = key[r] >> shift;
-    const bool on = r * kThreads + tid < n && (x > prefix || (x == prefix && ((taken >> r) & 1)));
-    const uint64_t e = __builtin_amdgcn_ballot_w64(on);
-    mine |= uint32_t(on) << r;
-    if (lane == 0) stay[r * kWaves + wave] = e;
-  }
-  __syncthreads();
-  if (wave == 0) {
-    uint32_t run = 0;
-#pragma unroll 1
-    for (int w0 = 0; w0 < kWords; w0 += 64) {
-      const int first = (w0 + lane) * 64;  // the word's first token
-      uint32_t c = 0;
-      if (w0 + lane < kWords) {
-        const uint64_t e = stay[w0 + lane];
-        const int below = min(max(a.budget - first, 0), 64);  // tokens of the word below the budget
-        const uint64_t m = below == 64 ? ~0ull : (1ull << below) - 1;
-        c = uint32_t(__popcll(e & ~m)) << 16 | uint32_t(__popcll(~e & m));
-      }
-      const uint32_t upto = scan_wave(c);
-      if (w0 + lane < kWords) before[w0 + lane] = run + upto - c;
-      run += __shfl(upto, 63);
+  for (int q = 0; q < kQ; ++q) {
+    uint32_t movers = 0, holes = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * (q * kThreads + tid) + e;
+      const uint32_t x = key[q][e] >> shift;
+      const bool on = t < n && (x > prefix || (x == prefix && ((taken >> (4 * q + e)) & 1)));
+      mine |= uint32_t(on) << (4 * q + e);
+      movers += __popcll(__builtin_amdgcn_ballot_w64(on && t >= a.budget));
+      holes += __popcll(__builtin_amdgcn_ballot_w64(!on && t < a.budget));
     }
-    if (lane == 0) chosen[0] = run >> 16;  // how many move
+    if (lane == 0) chunk[q * kWaves + wave] = movers << 16 | holes;
   }
   __syncthreads();
-  const int movers = int(chosen[0]);
+  // every wave adds the chunks up for itself
+  const uint32_t c0 = lane < kChunks ? chunk[lane] : 0, u0 = scan_wave(c0);
+  uint32_t total = uint32_t(__builtin_amdgcn_readlane(int(u0), 63)), c1 = 0, u1 = 0;
+  if (kChunks > 64) {
+    c1 = chunk[min(64 + lane, kChunks - 1)];
+    u1 = total + scan_wave(c1);
+    total = uint32_t(__builtin_amdgcn_readlane(int(u1), 63));
+  }
+  const int movers = int(total >> 16);
   uint16_t* from = lists;
   uint16_t* freed = lists + a.list_len;
-  // Number of the thread's r-th token among the movers, or of its slot among
-  // the free ones.
-  auto rank = [&](int r, bool mover) -> uint32_t {
-    const uint64_t e = stay[r * kWaves + wave], lanes = (1ull << lane) - 1;
-    const uint32_t base = before[r * kWaves + wave];
-    const int below = min(max(a.budget - (r * kThreads + tid - lane), 0), 64);
-    const uint64_t m = below == 64 ? ~0ull : (1ull << below) - 1;
-    return mover ? (base >> 16) + __popcll(e & ~m & lanes) : (base & 0xffffu) + __popcll(~e & m & lanes);
-  };
+  uint32_t number[kQ];  // of the thread's first mover and free slot of the group
 #pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    if (r * kThreads >= n) continue;
-    const int t = r * kThreads + tid;
-    const bool on = (mine >> r) & 1;
-    if (t < a.budget && on) kept[t] = t;
-    if (t < a.budget && !on) freed[rank(r, false)] = uint16_t(t);
-    if (t >= a.budget && on) from[rank(r, true)] = uint16_t(t);
+  for (int q = 0; q < kQ; ++q) {
+    const int i = q * kWaves + wave;
+    uint32_t r = uint32_t(i < 64 ? __builtin_amdgcn_readlane(int(u0 - c0), i) : __builtin_amdgcn_readlane(int(u1 - c1), i - 64));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * (q * kThreads + tid) + e;
+      const bool on = (mine >> (4 * q + e)) & 1;
+      r += lanes_before(__builtin_amdgcn_ballot_w64(on && t >= a.budget)) << 16;
+      r += lanes_before(__builtin_amdgcn_ballot_w64(!on && t < a.budget));
+    }
+    number[q] = r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * (q * kThreads + tid) + e;
+      const bool on = (mine >> (4 * q + e)) & 1;
+      if (t < a.budget && on) kept[t] = t;
+      if (t < a.budget && !on) {
+        freed[r & 0xffffu] = uint16_t(t);
+        r += 1;
+      }
+      if (t >= a.budget && on) {
+        from[r >> 16] = uint16_t(t);
+        r += 1u << 16;
+      }
+    }
   }
   __syncthreads();
-  // Every token that stays tells its slot where it is from; eight at a time, so
-  // that their lookups overlap.
+  // Every token that stays tells its slot where it is from.
   const bool copy = a.w_out != a.w || a.pos_out != a.pos;
-  constexpr int kG = kR < 8 ? kR : 8;
-#pragma unroll 1
-  for (int r0 = 0; r0 < kR; r0 += kG) {
-    if (r0 * kThreads >= n) break;
-    float w8[kG];
-    int32_t p8[kG];
-    int to[kG];
-    Place at[kG];
 #pragma unroll
-    for (int u = 0; u < kG; ++u) {
-      const int r = r0 + u, t = r * kThreads + tid;
-      const bool on = (mine >> r) & 1;
-      to[u] = !on ? -1 : t < a.budget ? (copy ? t : -1) : int(freed[rank(r, true)]);
-      if (kHold) {
-        w8[u] = wr[u];
-        p8[u] = pr[u];
-      } else {
-        const Place own = place(a, row, min(t, n - 1));
-        w8[u] = weight_at<kNear>(a, h, own);
-        p8[u] = position_at<kNear>(a, h, own);
-      }
-      at[u] = place(a, row, max(to[u], 0));
+  for (int q = 0; q < kQ; ++q) {
+    const int t0 = 4 * (q * kThreads + tid);
+    if (4 * q * kThreads >= n) continue;
+    // nothing to do for a wave without movers (and without a copy)
+    const uint32_t on4 = (mine >> (4 * q)) & 15u;
+    if (!__builtin_amdgcn_ballot_w64(on4 != 0 && (copy || t0 + 3 >= a.budget))) continue;
+    Place at[4];
+    float w4[4];
+    int32_t p4[4];
+    if (!kHold) load4<kNear>(a, row, h, t0, n - 1, at, w4, p4);
+    uint32_t r = number[q] >> 16;
+    int to[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool on = (on4 >> e) & 1, moves = on && t0 + e >= a.budget;
+      to[e] = moves ? int(freed[r]) : on && copy ? t0 + e : -1;
+      r += moves;
+      at[e] = place(a, row, max(to[e], 0));
     }
 #pragma unroll
-    for (int u = 0; u < kG; ++u) {
-      const int t = (r0 + u) * kThreads + tid;
-      if (to[u] < 0) continue;
-      if (t >= a.budget) kept[to[u]] = t;
-      if (at[u].ok && ((there >> (r0 + u)) & 1)) put<kNear>(a, h, at[u], w8[u], p8[u]);
+    for (int e = 0; e < 4; ++e) {
+      if (to[e] < 0) continue;
+      if (t0 + e >= a.budget) kept[to[e]] = t0 + e;
+      if (at[e].ok && ((there >> (4 * q + e)) & 1))
+        put<kNear>(a, h, at[e], kHold ? w[q][e] : w4[e], kHold ? pos[q][e] : p4[e]);
     }
   }
   if (move) {
@@ -616,24 +662,23 @@ __global__ __launch_bounds__(256) void evict_move_kernel(EvictArgs a) {
   move_rows(a, row, h, from >= a.budget ? from : -1, j0 + lane);
 }
 
-template <int kThreads, int kR, bool kNear>
+template <int kThreads, int kQ, bool kNear>
 hipError_t launch_near(const EvictArgs& a, int move, hipStream_t s) {
   const size_t lds = 4 * size_t(a.list_len);
-  constexpr size_t kStatic = 4 * kBins + 8 * kCandidates + 12 * (kThreads / 64) * kR + 2048;
-  if (lds + kStatic > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<kThreads, kR, kNear>),
+  if (lds > 56 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<kThreads, kQ, kNear>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }
-  evict_kernel<kThreads, kR, kNear><<<dim3(a.Hkv, a.B), kThreads, lds, s>>>(a, move);
+  evict_kernel<kThreads, kQ, kNear><<<dim3(a.Hkv, a.B), kThreads, lds, s>>>(a, move);
   return hipGetLastError();
 }
 
-template <int kThreads, int kR>
+template <int kThreads, int kQ>
 hipError_t launch_one(const EvictArgs& a, int move, hipStream_t s) {
   const int64_t far = std::max({a.w_p, a.p_p, a.wo_p, a.po_p});
   const bool near = far < (int64_t(1) << 30) && a.pages * far + a.S < (int64_t(1) << 30);
-  return near ? launch_near<kThreads, kR, true>(a, move, s) : launch_near<kThreads, kR, false>(a, move, s);
+  return near ? launch_near<kThreads, kQ, true>(a, move, s) : launch_near<kThreads, kQ, false>(a, move, s);
 }
 
 }  // namespace
@@ -675,18 +720,22 @@ hipError_t launch_evict(const KvView& c, const EvictCall& r, int num_cus, hipStr
   a.budget = int(r.budget);
   a.recent = int(r.recent);
   a.div = page_div(c.S);
+  a.vec = c.S % 4 == 0 && (r.w_p | r.w_h | r.p_p | r.p_h) % 4 == 0 &&
+          ((reinterpret_cast<uintptr_t>(r.weights) | reinterpret_cast<uintptr_t>(r.positions)) & 15) == 0;
   a.list_len = std::max(0, std::min(a.budget, a.cap - a.budget));
   // The workgroup that selects also moves, unless workgroups are too few to
   // move many rows at the memory's rate (15 x 8 heads, 7098 to 3549 tokens: 65
   // us against 47 with a launch of its own; 16 x 8, 2176 to 2048: 19 against 24).
   const bool move = int64_t(a.Hkv) * a.B >= num_cus || a.list_len <= 512;
   hipError_t e;
-  if (a.cap <= 2048) {
-    e = launch_one<512, 4>(a, move, s);
+  if (a.cap <= 1024) {
+    e = launch_one<256, 1>(a, move, s);
+  } else if (a.cap <= 2048) {
+    e = launch_one<512, 1>(a, move, s);
   } else if (a.cap <= 8192) {
-    e = launch_one<1024, 8>(a, move, s);
+    e = launch_one<1024, 2>(a, move, s);
   } else if (a.cap <= kMaxTokens) {
-    e = a.cap <= 16384 ? launch_one<1024, 16>(a, move, s) : launch_one<1024, 32>(a, move, s);
+    e = a.cap <= kMaxTokens / 2 ? launch_one<1024, 4>(a, move, s) : launch_one<1024, 8>(a, move, s);
   } else {
     evict_long_kernel<1024><<<dim3(a.Hkv, a.B), 1024, 0, s>>>(a);
     e = hipGetLastError();
