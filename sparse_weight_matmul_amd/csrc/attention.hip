@@ -74,7 +74,9 @@ struct AttnArgs {
   int32_t splits, split_len, lrow;
   int32_t own_weights;  // the only split adds the weights itself, its scores in LDS
   float scale;  // softmax scale * log2(e)
-  PageDiv div;  // by S
+  PageDiv div;              // by S
+  PageDiv per_split, per_b;  // by the units of a split and of a sequence
+  int32_t units;            // sequences x key-value heads x groups of 16 query heads
 };
 
 // Where a token's rows are: its page, clamped into the pool, and whether the
@@ -207,9 +209,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x, b = blockIdx.z;
+  // Split by split, the units rotated by the split: workgroup i runs on XCD i %
+  // 8, so every unit's splits visit all XCDs, and the splits past the end of
+  // short sequences come last.  (Dealt with the splits side by side, 8 of them
+  // put each split on an XCD of its own, and half of those idle when the
+  // sequences fill half of their capacity.)
+  const int split = page_index(a.per_split, blockIdx.x);
+  const int turned = int(blockIdx.x) - split * a.units - (split - page_index(a.per_split, split) * a.units);
+  const int unit = turned < 0 ? turned + a.units : turned;
   const int tiles_h = (a.G + kHeads - 1) / kHeads;
-  const int hkv = blockIdx.y / tiles_h, ht = blockIdx.y % tiles_h;
+  const int b = page_index(a.per_b, unit), y = unit - b * a.Hkv * tiles_h;
+  const int hkv = tiles_h == 1 ? y : y / tiles_h, ht = y - hkv * tiles_h;
   const int gn = min(kHeads, a.G - ht * kHeads);  // query heads here
   const int h0 = hkv * a.G + ht * kHeads;
   const int begin = split * a.split_len;
@@ -571,12 +581,18 @@ hipError_t launch_dim(const AttnArgs& a, bool same8, dim3 grid, size_t lds, hipS
 // The split of the length.  A workgroup's four waves take 128 tokens (a step)
 // at a time, at about 1.1 us; a second launch to join the splits costs 5 us
 // (kernel and gap).  So the length is split only where one workgroup per
-// sequence and group of heads leaves CUs idle and takes more than eight steps,
-// then into one workgroup per CU, of two steps or more.  Measured, us, at 1
-// split / this rule: 1 x 4096 tokens, 32 heads 51 / 17; 1 x 8192, 8 heads
-// 89 / 13; 1 x 1000, 32 heads 13 / 13; with two workgroups per CU 1 x 4096
-// takes 17, with four 2 x 131072 tokens of 8 heads 172 (this rule: 164); a
-// batch that fills the CUs loses 15-30% to any split.
+// sequence and group of heads leaves half of the CUs idle and takes more than
+// eight steps: into as many splits as make one workgroup per CU, of two steps
+// or more.  Rounded down: a CU with one workgroup more than the others ends
+// last (17 sequences of 43648 tokens, one head: 60 us at 255 workgroups, 73 at
+// 272, 60 at 510).  Rows of 64 and less need up to four workgroups per CU to
+// keep the memory busy, and get them where eight steps or more are left to each
+// (7 ragged sequences of up to 103992, 2 heads of 64: 47 us with one, 19 with
+// four); longer rows gain nothing by it (2 x 131072, 8 heads of 128: 166 with
+// one, 169 with two).  Measured, us, at 1 split / this rule: 1 x 4096 tokens,
+// 32 heads 51 / 16; 1 x 8192, 8 heads 89 / 12; 1 x 1000, 32 heads 13 / 13;
+// 2 x 131072, 8 heads 1567 / 166; a batch that fills the CUs loses 15-30% to
+// any split.
 //
 // The weights: one workgroup that sees a whole sequence keeps its scores in
 // LDS and adds the weights itself, as long as three such workgroups fit on a
@@ -588,8 +604,12 @@ AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t c
   const int64_t step = int64_t(kTile) * kWaves;
   const int64_t steps = std::max<int64_t>(1, (cap + step - 1) / step);
   int64_t splits = 1;
-  if (units < num_cus && steps > 8)
-    splits = std::min<int64_t>({(num_cus + units - 1) / units, steps / 2, int64_t(kMaxSplits)});
+  if (units <= num_cus / 2 && steps > 8) {
+    splits = std::min(num_cus / units, steps / 2);
+    for (int64_t k = 2; k <= (D <= 64 ? 4 : 1); ++k)
+      if (k * num_cus / units <= steps / 8) splits = k * num_cus / units;
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
+  }
   const int64_t per = (steps + splits - 1) / splits;
   p.split_len = int(std::min<int64_t>(per * step, (int64_t(1) << 31) - step));
   p.splits = int(std::max<int64_t>(1, (cap + p.split_len - 1) / p.split_len));
@@ -658,7 +678,10 @@ hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& 
   const int tiles_h = (a.G + kHeads - 1) / kHeads;
   const int dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
   const size_t lds = p.lds;
-  const dim3 grid(a.splits, a.Hkv * tiles_h, a.B);
+  a.units = a.B * a.Hkv * tiles_h;
+  a.per_split = page_div(a.units);
+  a.per_b = page_div(int64_t(a.Hkv) * tiles_h);
+  const dim3 grid(uint32_t(a.units) * uint32_t(a.splits));
   const bool same8 = a.S % 8 == 0;
   hipError_t e = dp == 64    ? launch_dim<64>(a, same8, grid, lds, s)
                  : dp == 128 ? launch_dim<128>(a, same8, grid, lds, s)

@@ -95,8 +95,10 @@ swm_status swm_paged_attention(const swm_kv_cache* c, const void* q, int64_t q_b
   swm::AttnPlan p;
   st = plan_for(c, q_heads, weights != nullptr, &p);
   if (st != SWM_OK) return st;
-  // workgroups of the second launch: at most 2^24 - 1 of 256 threads
-  if (c->batch * q_heads + c->batch * c->heads * (cap / 1024 + 1) >= (int64_t(1) << 24)) return SWM_ERR_UNSUPPORTED;
+  // either launch: at most 2^24 - 1 workgroups of 256 threads
+  if (c->batch * q_heads + c->batch * c->heads * (cap / 1024 + 1) >= (int64_t(1) << 24) ||
+      c->batch * q_heads * p.splits >= (int64_t(1) << 24))
+    return SWM_ERR_UNSUPPORTED;
   if (p.bytes > 0) {
     if (!workspace || ws_bytes < p.bytes) return SWM_ERR_INVALID_ARG;
     if (misaligned(workspace)) return SWM_ERR_ALIGN;
