@@ -474,11 +474,12 @@ swm_status swm_hbm_stream(const void* buf, size_t bytes, int32_t unroll, int32_t
  *  address and ldr == ldy: an update in place), and must not overlap it
  *  otherwise.  The other arguments and the errors are swm_spmm_ws's; with no
  *  bias, no residual and SWM_ACT_NONE the result is the same bits.  At 33 to
- *  255 tokens it chooses between slices of 32 tokens through the decode
- *  kernels, W expanded into the workspace and swm_spmm's on-chip kernel by
- *  what they take for these sizes (the fp32 sums are the same but for their
- *  order); a workspace that is not there or too small for that only takes the
- *  expansion off the choice.
+ *  1023 tokens it chooses, by what they take for these sizes, between slices
+ *  of 32 tokens through the decode kernels, W expanded into the workspace and
+ *  swm_spmm's on-chip kernel, whose K it may split over workgroups (fp32 sums
+ *  in the workspace, joined in order by a second launch); the fp32 sums are
+ *  the same but for their order.  There a workspace that is not there or too
+ *  small only takes routes off the choice.
  *  SWM_ERR_INVALID_ARG also: an unknown act, ldr < M, residual == Y with
  *  ldr != ldy. */
 swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
@@ -486,8 +487,8 @@ swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, vo
                              size_t ws_bytes, void* stream);
 
 /* Bytes of device workspace swm_spmm_epilogue uses for N tokens on the current
- * device: swm_spmm_workspace_bytes, and M*K*2 rounded up to 256 where it would
- * expand W at 33 to 255 tokens. */
+ * device: at 33 to 1023 tokens what its route needs, and
+ * swm_spmm_workspace_bytes at least. */
 size_t swm_spmm_epilogue_workspace_bytes(const swm_format* f, int64_t N);
 
 /* ------------------------------------------------------------------ serving

@@ -560,31 +560,59 @@ size_t swm_spmm_workspace_bytes(const swm_format* f, int64_t N) {
   return align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
 }
 
-// The product with an epilogue at 33 to 255 tokens, where spmm's on-chip
-// kernel (one 256-token block, bound by its K steps) is slower than token
-// slices through the decode kernels or W expanded once.  The fastest by what
-// each was measured to take, in us with Mi = M K / 2^20 and rounds of blocks
-// over the CUs (4096x4096 at N = 33 / 96 / 192: slices 22 / 46 / 93, expanded
-// 54 / 55 / 56 + 6 for the residual, on chip 86; 4096x11008 at 64 / 192: 64 /
-// 195, 134 / 142, 208; 11008x4096 at 48 / 96: 60 / 128, 69 / 70, 86):
-//   slices of 32    0.9 Mi + 1 each, 5 at least
-//   expanded        0.55 Mi + 11 + 0.62 per 64 columns of K and round
-//   on chip         5 + 1.28 per 64 columns of K and round
+// The product with an epilogue at 33 to 1023 tokens.  spmm's own routes leave
+// most CUs idle there (the on-chip kernel takes blocks of 128 rows x 256
+// tokens and is bound by its 64-column steps), so the choice is wider: token
+// slices of 32 through the decode kernels, W expanded into the workspace, the
+// on-chip kernel, or that kernel with K split over workgroups and the fp32 sums
+// joined by a second launch.  The fastest by what each was measured to take,
+// in us, with Mi = M K / 2^20:
+//   slices     0.95 Mi each, or 7 + 0.5 Mi where that is more
+//   expanded   0.55 Mi + 11 + 0.62 per step, by the dense kernel's block shape
+//   on chip    5 + 1.28 per step and round of blocks over the CUs
+//   split      that by the steps of one split, 5 for the second launch, and
+//              8 bytes per sum at 4 TB/s
+// (4096x4096 at N = 33 / 96 / 192: slices 22 / 46 / 93, expanded 54 / 55 / 56,
+// on chip 86, split 28 / 28 / 30; 4096x11008 at 64 / 192 / 512: 64 / 195 / -,
+// 134 / 142 / 143, 208 / 210 / 210, 42 / 44 / 73; 11008x4096 at 48 / 96 / 512:
+// 60 / 128 / -, 69 / 70 / 84, 86 / 87 / 91, 49 / 50 / -.)
 enum class MidRoute { kSlices, kExpand, kOnChip };
+struct MidPlan {
+  MidRoute route = MidRoute::kOnChip;
+  int splits = 1;
+  size_t bytes = 0;  // of workspace
+};
 
-static MidRoute mid_route(const swm::Header& h, int64_t N, int64_t cus, bool workspace) {
-  const double mi = double(h.m) * double(h.k) / 1048576.0, steps = double(h.k) / 64.0;
-  const double rounds = double(((h.m + 127) / 128 + cus - 1) / cus);
-  const double slices = double((N + 31) / 32) * std::max(5.0, 0.9 * mi + 1.0);
-  const double expand = 0.55 * mi + 11.0 + 0.62 * steps * rounds, chip = 5.0 + 1.28 * steps * rounds;
-  if (slices <= chip && (!workspace || slices <= expand)) return MidRoute::kSlices;
-  return workspace && expand < chip ? MidRoute::kExpand : MidRoute::kOnChip;
+static MidPlan mid_plan(const swm::Header& h, int64_t N, int64_t cus, size_t workspace) {
+  const double mi = double(h.m) * double(h.k) / 1048576.0;
+  const int64_t steps = (h.k + 63) / 64, tiles = (h.m + 127) / 128 * ((N + 255) / 256);
+  auto rounds = [&](int64_t blocks) { return double((blocks + cus - 1) / cus); };
+  MidPlan best;
+  double least = 5.0 + 1.28 * double(steps) * rounds(tiles);
+  auto offer = [&](MidRoute r, int splits, size_t bytes, double cost) {
+    if (bytes > workspace || cost >= least) return;
+    least = cost;
+    best.route = r;
+    best.splits = splits;
+    best.bytes = bytes;
+  };
+  offer(MidRoute::kSlices, 1, 0, double((N + 31) / 32) * std::max(0.95 * mi, 7.0 + 0.5 * mi));
+  const int64_t m256 = (h.m + 255) / 256, n128 = (N + 127) / 128;
+  const double shape = std::min({rounds(m256 * ((N + 255) / 256)), 0.73 * rounds(m256 * n128),
+                                 0.54 * rounds((h.m + 127) / 128 * n128)});
+  offer(MidRoute::kExpand, 1, align_up(size_t(h.m) * size_t(h.k) * 2, 256),
+        0.55 * mi + 11.0 + 0.62 * double(steps) * shape / 0.54);
+  for (int s = 2; s <= 16 && s <= steps; ++s)
+    offer(MidRoute::kOnChip, s, swm::prefill_split_bytes(h, N, s),
+          10.0 + 1.28 * double((steps + s - 1) / s) * rounds(tiles * s) +
+              double(s) * double(h.m) * double((N + 31) / 32 * 32) * 8.0 / 4e6);
+  return best;
 }
 
-// Where the rule above applies (K and W as the expansion needs them).
+// Where the rule above applies: shapes the on-chip kernel takes.
 static bool mid_tokens(const swm_format* f, int64_t N) {
-  return N > 32 && N < 256 && f->h.k >= 8 && f->h.k % 8 == 0 && f->h.m > 0 && !smf_route(f, N) &&
-         !expand_route(f->h, N);
+  return N > 32 && N < 1024 && f->h.k >= 8 && f->h.k % 8 == 0 && f->h.m > 0 && f->h.tm == 16 && f->h.tk == 64 &&
+         f->h.max_tile <= 1024 && swm::prefill_sparse_lds(f->h) <= 160 * 1024 && !smf_route(f, N);
 }
 
 static swm_status run_spmm_ws(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,
@@ -630,27 +658,31 @@ swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, vo
   e.act = act;
   e.on = bias || residual || act != SWM_ACT_NONE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (e.on && X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X)) {
+  if (e.on && X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X) &&
+      swm::prefill_sparse_fits(f->h, N, ldx)) {
+    if (ldx < f->h.k || ldy < f->h.m || ldy <= 0 || !on_current_device(f)) return SWM_ERR_INVALID_ARG;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15)) return SWM_ERR_ALIGN;
     int dev = 0;
     SWM_HIP(hipGetDevice(&dev));
-    const bool fits = workspace && ws_bytes >= swm_spmm_epilogue_workspace_bytes(f, N) &&
-                      (reinterpret_cast<uintptr_t>(workspace) & 15) == 0;
-    switch (mid_route(f->h, N, num_cus(dev), fits)) {
-      case MidRoute::kSlices: return run_products(f, X, ldx, Y, ldy, N, false, s, e, true);
-      case MidRoute::kExpand: e.expand = 1; break;
-      case MidRoute::kOnChip: return run_products(f, X, ldx, Y, ldy, N, false, s, e);
+    const MidPlan p = mid_plan(f->h, N, num_cus(dev), workspace ? ws_bytes : 0);
+    if (p.route == MidRoute::kSlices) return run_products(f, X, ldx, Y, ldy, N, false, s, e, true);
+    if (p.route == MidRoute::kOnChip) {
+      swm_log("spmm_epilogue M=%lld K=%lld N=%lld: on-chip prefill, %d splits of K", (long long)f->h.m,
+              (long long)f->h.k, (long long)N, p.splits);
+      SWM_HIP(swm::launch_prefill_sparse(f->d, static_cast<const uint16_t*>(X), ldx, static_cast<uint16_t*>(Y), ldy,
+                                         N, s, e, p.splits, workspace));
+      return SWM_OK;
     }
+    e.expand = 1;
   }
   return run_spmm_ws(f, X, ldx, Y, ldy, N, workspace, ws_bytes, s, e);
 }
 
 size_t swm_spmm_epilogue_workspace_bytes(const swm_format* f, int64_t N) {
   const size_t need = swm_spmm_workspace_bytes(f, N);
-  if (need > 0 || !f || !mid_tokens(f, N)) return need;
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 0;
-  if (mid_route(f->h, N, num_cus(dev), true) != MidRoute::kExpand) return 0;
-  return align_up(size_t(f->h.m) * size_t(f->h.k) * 2, 256);
+  if (!f || !mid_tokens(f, N) || hipGetDevice(&dev) != hipSuccess) return need;
+  return std::max(need, mid_plan(f->h, N, num_cus(dev), ~size_t(0)).bytes);
 }
 
 static swm_status run_colruns(const swm_format* f, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t n,

@@ -33,10 +33,11 @@ __device__ __forceinline__ float gelu(float v) {
   return __builtin_fmaf(0.5f, v + fabsf(v), -(u * q));
 }
 
-// The epilogues a product kernel is built with: none, the gated FFN step's, or
-// `Epilogue`.  Kernels without one keep their own instances: the epilogue's
-// operands and code would cost some of them registers and occupancy.
-enum { kPlain, kGated, kFused };
+// The epilogues a product kernel is built with: none, the gated FFN step's,
+// `Epilogue`, or none yet: the fp32 sums of one split of K.  Kernels without
+// one keep their own instances: the epilogue's operands and code would cost
+// some of them registers and occupancy.
+enum { kPlain, kGated, kFused, kPartial };
 
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {

@@ -116,7 +116,10 @@ hipError_t launch_prefill_dense_glu(const uint16_t* W, int64_t ldw, const uint16
                                     int num_cus, hipStream_t s);
 bool prefill_dense_dma_fits(int64_t M, int64_t ldw, int64_t K, int64_t N, int64_t ldx);
 hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t ldx, uint16_t* Y,
-                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi = {});
+                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi = {},
+                                 int splits = 1, void* part = nullptr);
+// fp32 sums of `splits` K splits of that product (part above).
+size_t prefill_split_bytes(const Header& h, int64_t N, int splits);
 // The prefill kernels need K >= 8, K % 8 == 0, ldx % 8 == 0 and a 16-byte aligned X.
 bool prefill_supported(int64_t K, int64_t ldx, const void* X);
 size_t prefill_sparse_lds(const Header& h);

@@ -39,6 +39,7 @@ namespace swm {
 namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -83,6 +84,13 @@ struct PrefillArgs {
 struct PrefillFusedArgs : PrefillArgs {
   Epilogue epi;
 };
+// A K split: `steps` 64-column steps per split, one split per blockIdx.y, its
+// sums into `part`: 32 x 32 accumulators as their lanes hold them, 16 bytes a
+// lane, by (split, group of 32 tokens, 128-row tile, accumulator row, quarter).
+struct PrefillPartialArgs : PrefillArgs {
+  float* part;
+  int steps;
+};
 template <int kEpi>
 struct PrefillArgsOf {
   using type = PrefillArgs;
@@ -90,6 +98,10 @@ struct PrefillArgsOf {
 template <>
 struct PrefillArgsOf<kFused> {
   using type = PrefillFusedArgs;
+};
+template <>
+struct PrefillArgsOf<kPartial> {
+  using type = PrefillPartialArgs;
 };
 
 // Map the workgroup id to an output tile: regroup ids so that each XCD (id % 8)
@@ -560,7 +572,16 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m0 = tm * WBM, n0 = tn * WBN;
-  const int nsteps = (a.K + BK - 1) / BK;
+  int k0 = 0, most = 0x7fffffff;  // first tile column and steps of this split
+  if constexpr (kEpi == kPartial) {
+    k0 = int(blockIdx.y) * a.steps;
+    most = a.steps;
+    a.X += int64_t(k0) * BK;
+    a.K -= k0 * BK;
+    a.tile_ptr += k0;
+    a.bits += int64_t(k0) * 16;
+  }
+  const int nsteps = min((a.K + BK - 1) / BK, most);
   constexpr uint32_t tile_run_bytes = uint32_t(kRC) * 512u;
   const uint32_t sA = lds_addr(smem), sB = sA + 2 * kWATile;
   const uint32_t runbuf = sB + 2 * kWBTile + uint32_t(wave) * tile_run_bytes;
@@ -573,7 +594,7 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
   uint32_t wreg = 0, wsave = 0;  // lane l: dword l%32 of the tile's 16 bitmap words
   // tile pointers: lane 0 / 1 hold the run's first / one-past-last index
   auto fetch_tp = [&](int ks) -> uint32_t {
-    return a.tile_ptr[uint64_t(slab) * a.kt + min(ks, a.kt - 1) + (lane & 1)];
+    return a.tile_ptr[uint64_t(slab) * a.kt + min(ks, a.kt - 1 - k0) + (lane & 1)];
   };
   auto fetch_runs = [&](int ks, uint32_t tpv) {
     const uint32_t p0 = __builtin_amdgcn_readlane(tpv, 0);
@@ -584,7 +605,7 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
       const uint32_t off = min(p0 + uint32_t(cc * 256 + lane * 4), last);
       runreg[cc] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a.vals + off));
     }
-    wreg = reinterpret_cast<const uint32_t*>(a.bits + (uint64_t(slab) * a.kt + min(ks, a.kt - 1)) * 16)[lane & 31];
+    wreg = reinterpret_cast<const uint32_t*>(a.bits + (uint64_t(slab) * a.kt + min(ks, a.kt - 1 - k0)) * 16)[lane & 31];
   };
   auto stage_runs = [&]() {
 #pragma unroll
@@ -744,6 +765,23 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
       fuse_and_store(a.epi, acc, m0, n0 + c * 64, a.M, a.N, a.Y, a.ldy, lane);
       return;
     }
+    if constexpr (kEpi == kPartial) {
+      const int groups = (a.N + 31) / 32;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int g = (n0 + c * 64) / 32 + j;
+        if (g >= groups) continue;
+        f32x4* dst = reinterpret_cast<f32x4*>(a.part) +
+                     ((int64_t(blockIdx.y) * groups + g) * a.tiles_m + tm) * (16 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[(i * 4 + q) * 64] = f32x4{acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2],
+                                          acc[i][j][q * 4 + 3]};
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -780,6 +818,31 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
       __syncthreads();
     }
   }
+}
+
+// Adds the splits up, in order, and finishes: a wave per 32 x 32 accumulator.
+__global__ __launch_bounds__(256) void split_finish_kernel(PrefillFusedArgs a, const float* part, int splits) {
+  const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+  const int tm = blockIdx.x, g = blockIdx.y, groups = gridDim.y;
+  const f32x4* src = reinterpret_cast<const f32x4*>(part) + (int64_t(g) * a.tiles_m + tm) * (16 * 64) + i * 256 + lane;
+  const int64_t stride = int64_t(groups) * a.tiles_m * (16 * 64);
+  epi_f32x16 acc[1][1];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[0][0][v] = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    f32x4 w[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[u][q] = src[min(s0 + u, splits - 1) * stride + q * 64];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (s0 + u >= splits) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[0][0][v] += w[u][v / 4][v % 4];
+    }
+  }
+  fuse_and_store<1, 1>(a.epi, acc, tm * 128 + i * 32, g * 32, a.M, a.N, a.Y, a.ldy, lane);
 }
 
 PrefillArgs make_args(int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, uint16_t* Y,
@@ -919,6 +982,10 @@ size_t prefill_sparse_lds(const Header& h) {
   return size_t(2) * kWATile + size_t(2) * kWBTile + 8 /*waves*/ * chunks * 512;
 }
 
+size_t prefill_split_bytes(const Header& h, int64_t N, int splits) {
+  return size_t(splits) * size_t((N + 31) / 32) * size_t((h.m + WBM - 1) / WBM) * (16 * 64 * 16);
+}
+
 template <int kEpi>
 static void launch_ws(const typename PrefillArgsOf<kEpi>::type& a, dim3 grid, size_t lds, hipStream_t s) {
   const dim3 block{512, 1, 1};
@@ -931,7 +998,8 @@ static void launch_ws(const typename PrefillArgsOf<kEpi>::type& a, dim3 grid, si
 }
 
 hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t ldx, uint16_t* Y,
-                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi) {
+                                 int64_t ldy, int64_t N, hipStream_t s, const Epilogue& epi,
+                                 int splits, void* part) {
   PrefillArgs a = make_args(f.h.m, N, f.h.k, X, ldx, Y, ldy);
   a.tile_ptr = f.tile_ptr;
   a.bits = f.bits;
@@ -949,7 +1017,15 @@ hipError_t launch_prefill_sparse(const DevFormat& f, const uint16_t* X, int64_t 
   a.tiles_m = int((f.h.m + WBM - 1) / WBM);
   a.tiles_n = int((N + WBN - 1) / WBN);
   const dim3 grid{grid_size(a), 1, 1};
-  if (epi.on)
+  if (splits > 1) {
+    const int nsteps = int((f.h.k + BK - 1) / BK), steps = (nsteps + splits - 1) / splits;
+    splits = (nsteps + steps - 1) / steps;  // none is empty
+    launch_ws<kPartial>(PrefillPartialArgs{a, static_cast<float*>(part), steps}, dim3(grid.x, splits), lds, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    split_finish_kernel<<<dim3(a.tiles_m, unsigned((N + 31) / 32)), 256, 0, s>>>(PrefillFusedArgs{a, epi},
+                                                                               static_cast<const float*>(part), splits);
+  } else if (epi.on)
     launch_ws<kFused>(PrefillFusedArgs{a, epi}, grid, lds, s);
   else
     launch_ws<kPlain>(a, grid, lds, s);

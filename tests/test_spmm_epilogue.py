@@ -65,6 +65,7 @@ SHAPES = [
     (33, 77, 1), (33, 77, 20), (33, 77, 40), (1, 1, 1),                              # unaligned: looped, in slices
     (300, 520, 33), (300, 520, 200), (1001, 264, 130),                               # slices, on-chip, expanded
     (4096, 1024, 100), (2000, 4096, 255), (130, 64, 64), (5000, 200, 37),
+    (1001, 2056, 130), (391, 3440, 60), (130, 8200, 513), (17, 1096, 1023), (2049, 1928, 300),  # K split
     (300, 520, 257), (260, 136, 1027),                                               # expanded, 128 x 128 blocks
     (4096, 256, 2048), (4099, 128, 3000), (8192, 64, 4096),                          # larger blocks
 ]
@@ -93,6 +94,23 @@ def test_routes(gpu_lib, M, K, N):
     inplace = Rd.clone()  # the residual stream updated in place
     swm.spmm_epilogue(f, Xd, bd, "gelu", inplace, ws, inplace)
     assert torch.equal(c, inplace)
+
+
+@gpu
+@pytest.mark.parametrize("M,K,N", [(1001, 2056, 130), (130, 8200, 513)])
+def test_split_of_k(gpu_lib, M, K, N):
+    import torch
+    W, X, b, R = case(M, K, N)
+    f = swm.sparse_compress(W)
+    need = swm.spmm_epilogue_workspace_bytes(f, N)
+    assert 0 < need and need != M * K * 2  # the sums of the splits, not W
+    guard = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    Y = swm.spmm_epilogue(f, t(X), t(b), "silu", t(R), guard[:need])
+    check(Y, W, X, b, "silu", R)
+    assert bool((guard[need:] == 0xA5).all())  # nothing past what was asked for
+    assert torch.equal(Y, swm.spmm_epilogue(f, t(X), t(b), "silu", t(R), guard[:need]))
+    less = swm.spmm_epilogue(f, t(X), t(b), "silu", t(R), guard[:need - 16])  # one split fewer, or another route
+    check(less, W, X, b, "silu", R)
 
 
 @gpu
