@@ -13,18 +13,21 @@
 // rounding.
 //
 // The top tokens need no second pass over the row.  The k-th largest of the
-// maxima of 256 groups of threads is a lower bound of the k-th largest logit,
-// and only the threads whose own maximum reaches it look at their logits
-// again (a few more than k logits pass).  The candidates are ranked by
+// maxima of 64 or 128 groups of threads is a lower bound of the k-th largest
+// logit, and only the logits of threads whose own maximum reaches it are looked
+// at again (a few more than k of them pass).  The candidates are ranked by
 // counting; a token's rank is the number of candidates with a larger logit, or
 // an equal one at a lower index.  Rows with so many equal logits that the list
 // overflows (a constant row) take the larger ones first and then the equal
 // ones in index order, and stop at k; if even the larger ones overflow, k
 // rounds of a maximum over the row.
 //
-// Bound: the read of the logits (2 or 4 bytes each); with fp16 logits the
+// Bound: with many rows the read of the logits (2 or 4 bytes each), the
 // exponentials (one per logit, at a quarter of the vector rate) and the five
-// other vector instructions come close to it.
+// other vector instructions close behind: 4096 x 32000 fp16 45 us in the
+// kernel, 262 MB at 5.8 TB/s.  With few rows the chain of one load, two
+// reductions and the choice of the top tokens: 1 x 32000 fp16 with 5 of them
+// 11 us, 61 x 50021 fp32 with 20 14.6 us, none 9 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -148,10 +151,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      if (r * kThreads >= vecs) break;  // the same for every thread
-      float f[kVec];
-      Row<T>::unpack(keep[r], f);
-      take<kVec>(p, f);
+      if (r * kThreads < vecs) {  // the same for every thread
+        float f[kVec];
+        Row<T>::unpack(keep[r], f);
+        take<kVec>(p, f);
+      }
     }
   } else {
     constexpr int kUnroll = 4;
@@ -216,7 +220,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   constexpr int kList = kThreads < 256 ? 512 : 1024;  // candidates ranked by counting
   __shared__ uint32_t group[kGroups];
   __shared__ uint64_t list[kList];
-  __shared__ uint32_t bound, count;
+  __shared__ uint16_t who[kThreads];  // threads whose maximum reaches the bound
+  __shared__ uint32_t bound, count, passed;
   const int k = min(a.top, a.V);
   // a thread without logits has the key 0, below that of -inf
   const bool has = tid < vecs || head || tail;
@@ -227,11 +232,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   if (kPer > 2) g = max(g, rotate_row<2>(g));
   if (kPer > 4) g = max(g, rotate_row<4>(g));
   if (tid % kPer == kPer - 1) group[tid / kPer] = g;
-  if (tid == 0) count = 0;
+  if (tid == 0) count = passed = 0;
   __syncthreads();
   if (tid < kGroups) {
     const uint32_t v = group[tid];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < kGroups; j += 4) {
       const u32x4 o = *reinterpret_cast<const u32x4*>(&group[j]);
 #pragma unroll
@@ -242,8 +248,12 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   __syncthreads();
   const uint32_t low = bound;
 
-  // Appends the thread's logits with keys of at least `least`; the count keeps
-  // growing past the end of the list.
+  // Appends the logits with keys of at least `least`; the count keeps growing
+  // past the end of the list.  The threads whose maximum reaches it are listed
+  // first, and their vectors are dealt to all threads: a few hundred loads at
+  // once, in a loop of few instructions.  (Every thread searching its own
+  // registers was a long unrolled code that each wave met cold: 300 x 50021 fp32,
+  // 20 top tokens 43 us so, 24 this way.)
   auto collect = [&](uint32_t least) {
     auto push = [&](float f, int at) {
       const uint32_t key = key_of(f);
@@ -251,38 +261,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
       const uint32_t c = atomicAdd(&count, 1u);
       if (c < kList) list[c] = uint64_t(key) << 32 | (0xffffffffu - uint32_t(at));
     };
-    if (has && mine >= least) {
-      if constexpr (kR > 0) {
+    const bool pass = has && mine >= least;
+    if (pass && tid < vecs) who[atomicAdd(&passed, 1u)] = uint16_t(tid);
+    if (pass && head) push(xh, tid);
+    if (pass && tail) push(xt, rest + tid);
+    __syncthreads();
+    const uint32_t n_pass = passed, rounds = uint32_t(vecs + kThreads - 1) / kThreads;
+    for (uint32_t i = tid; i < n_pass * rounds; i += kThreads) {
+      if (*const_cast<volatile uint32_t*>(&count) > kList) break;  // many equal logits: this list is not used
+      const uint32_t r = i / n_pass, v = who[i - r * n_pass] + r * kThreads;
+      if (v >= uint32_t(vecs)) continue;
+      float f[kVec];
+      Row<T>::unpack(xv[v], f);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          if (tid + r * kThreads >= vecs) break;
-          float f[kVec];
-          Row<T>::unpack(keep[r], f);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) push(f[e], lead + (tid + r * kThreads) * kVec + e);
-        }
-      } else {
-        constexpr int kUnroll = 4;
-        for (int j = tid; j < vecs; j += kUnroll * kThreads) {
-          u32x4 w[kUnroll];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) w[u] = xv[min(j + u * kThreads, vecs - 1)];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            if (j + u * kThreads >= vecs) break;
-            float f[kVec];
-            Row<T>::unpack(w[u], f);
-            float top = f[0];
-#pragma unroll
-            for (int e = 1; e < kVec; ++e) top = fmaxf(top, f[e]);
-            if (key_of(top) < least && !(top != top)) continue;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) push(f[e], lead + (j + u * kThreads) * kVec + e);
-          }
-        }
-      }
-      if (head) push(xh, tid);
-      if (tail) push(xt, rest + tid);
+      for (int e = 0; e < kVec; ++e) push(f[e], lead + int(v) * kVec + e);
     }
     __syncthreads();
   };
@@ -292,7 +284,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   float* lps = a.top_logp + n * a.top;
   if (found > kList) {
     __syncthreads();
-    if (tid == 0) count = 0;
+    if (tid == 0) count = passed = 0;
     __syncthreads();
     if (low != 0xffffffffu) collect(low + 1);
     found = int(count);
@@ -340,6 +332,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   for (int c = tid; c < found; c += kThreads) {
     const uint64_t v = list[c];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < found; ++j) rank += list[j] > v;
     if (rank < k) {
       ids[rank] = int64_t(0xffffffffu - uint32_t(v));
@@ -363,19 +356,29 @@ hipError_t launch(const LogprobArgs& a, int64_t N, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Threads of a row: a wave where the rows alone fill the chip, more where they
-// do not, and no more than the row has work for.  Rows whose vectors fit in
-// eight registers' worth a thread stay there.
+// Threads of a row: more where the rows do not fill the chip, and no more than
+// the row has work for.  Rows whose vectors fit in the registers of their
+// threads (8 a thread; 16 of 1024 threads) stay there.  Measured, us:
+//   below one row per CU    255 x 50021 fp32, 20 top tokens: 1024 threads 17,
+//                           256 threads 22; 1 x 128000 fp16, 20: 18 and 24
+//   from one row per CU on  300 x 50021 fp32, 20: 256 threads 24, 1024 30, 64
+//                           78; 1500 x 32000 fp16: 20, 28, 24
+//   from eight, no top      4096 x 32000 fp16: 64 threads 42, 256 44, 1024 67
+//   tokens                  (with 20 of fp32: 64 threads 173, 256 118: a wave
+//                           alone looks at its candidates in many rounds)
 template <typename T>
 hipError_t launch_rows(const LogprobArgs& a, int64_t N, int num_cus, hipStream_t s) {
-  constexpr int kR = 8;
+  constexpr int kR = 8, kWide = 16;
   const int64_t vecs = a.V / Row<T>::kVec + 1;
-  const int by_rows = N >= 8 * num_cus ? 64 : N >= num_cus ? 256 : 1024;
+  const int by_rows = N >= 8 * num_cus && a.top == 0 ? 64 : N >= num_cus ? 256 : 1024;
   const int by_row = vecs <= 256 ? 64 : vecs <= 2048 ? 256 : 1024;
   switch (std::min(by_rows, by_row)) {
-    case 64: return vecs <= 64 * kR ? launch<T, 64, kR>(a, N, s) : launch<T, 64, 0>(a, N, s);
+    case 64:
+      if (vecs <= 64 * kR) return launch<T, 64, kR>(a, N, s);
+      logprobs_kernel<T, 64, 0, false><<<uint32_t(N), 64, 0, s>>>(a);  // by its rows, so no top tokens
+      return hipGetLastError();
     case 256: return vecs <= 256 * kR ? launch<T, 256, kR>(a, N, s) : launch<T, 256, 0>(a, N, s);
-    default: return vecs <= 1024 * kR ? launch<T, 1024, kR>(a, N, s) : launch<T, 1024, 0>(a, N, s);
+    default: return vecs <= 1024 * kWide ? launch<T, 1024, kWide>(a, N, s) : launch<T, 1024, 0>(a, N, s);
   }
 }
 
