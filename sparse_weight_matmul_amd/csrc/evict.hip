@@ -31,7 +31,9 @@
 //
 // Bound: by its bytes (8 per token and head, and the moved rows) a call takes
 // a few us at most; what it takes is the chain of some ten barriers and four
-// memory latencies inside a workgroup.
+// memory latencies inside a workgroup.  Measured, in the kernel: 1 x 1025 to
+// 1024, 32 heads 10.4 us; 16 x 2176 to 2048, 8 heads 16.6 us; 8 x 4096 to 1024,
+// 32 heads 32.8 us, of them 19 for 27 MB of rows, read and written.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -506,12 +508,15 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
         }
       }
     __syncthreads();
-    for (int i = tid; i < int(sharing); i += kThreads) {
+    // four lanes to a candidate, each counting a quarter of the list
+    for (uint32_t i = tid / 4; i < sharing; i += kThreads / 4) {
       const uint64_t mine = cand[i];
       uint32_t rank = 0;
 #pragma unroll 8
-      for (uint32_t j = 0; j < sharing; ++j) rank += cand[j] > mine;
-      hist[i] = rank < want;  // the counts have been read
+      for (uint32_t j = tid % 4; j < sharing; j += 4) rank += cand[j] > mine;
+      rank += uint32_t(__builtin_amdgcn_mov_dpp(int(rank), 0xb1, 0xf, 0xf, true));  // lanes 1 0 3 2
+      rank += uint32_t(__builtin_amdgcn_mov_dpp(int(rank), 0x4e, 0xf, 0xf, true));  // lanes 2 3 0 1
+      if (tid % 4 == 0) hist[i] = rank < want;  // the counts have been read
     }
     __syncthreads();
     taken = 0;
