@@ -950,7 +950,24 @@ hipError_t launch_dense_any(const uint16_t* W, int64_t ldw, const uint16_t* X, i
     return launch_dense<2, 2, kGated>(a, s);
   }
   if (epi.on) {
-    const PrefillFusedArgs fa{a, epi};
+    PrefillFusedArgs fa{a, epi};
+    // Where the last round of 256 x 256 blocks would fill at most half of the
+    // CUs, the rows of the full rounds go first and the others get a launch and
+    // a block shape of their own (no sum changes).  Measured with K = 4096 and
+    // GELU, us, one launch / two: 11008 rows x 2048 tokens (a rest of 88 blocks)
+    // 237 / 222, x 1536 (6) 230 / 194, 6000 x 4096 (128) 234 / 217; beyond half
+    // it does not pay: 11008 x 4096 (176) 365 / 371, 14336 x 1800 (192) 253 / 257.
+    const int64_t tn = (N + 255) / 256, lead = tn <= cus ? blocks[0] / cus * cus / tn : 0;  // tile rows
+    if (shape == 1 && lead > 0 && lead < mb && 2 * (mb - lead) * tn <= cus) {
+      const int64_t m0 = lead * 256;
+      fa.M = int(m0);
+      const hipError_t e = launch_dense<4, 4, kFused>(fa, s);
+      if (e != hipSuccess) return e;
+      Epilogue rest = epi;
+      if (rest.bias) rest.bias += m0;
+      if (rest.residual) rest.residual += m0;
+      return launch_dense_any(W + m0 * ldw, ldw, X, ldx, Y + m0, ldy, M - m0, K, N, num_cus, glu, tau, rest, s);
+    }
     if (shape == 1) return launch_dense<4, 4, kFused>(fa, s);
     if (shape == 2) return launch_dense<4, 2, kFused>(fa, s);
     return launch_dense<2, 2, kFused>(fa, s);

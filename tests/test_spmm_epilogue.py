@@ -68,6 +68,7 @@ SHAPES = [
     (1001, 2056, 130), (391, 3440, 60), (130, 8200, 513), (17, 1096, 1023), (2049, 1928, 300),  # K split
     (300, 520, 257), (260, 136, 1027),                                               # expanded, 128 x 128 blocks
     (4096, 256, 2048), (4099, 128, 3000), (8192, 64, 4096),                          # larger blocks
+    (8203, 64, 2050), (4200, 72, 4100),                                              # and a launch for the last rows
 ]
 
 
