@@ -32,8 +32,9 @@
 // Bound: by its bytes (8 per token and head, and the moved rows) a call takes
 // a few us at most; what it takes is the chain of some ten barriers and four
 // memory latencies inside a workgroup.  Measured, in the kernel: 1 x 1025 to
-// 1024, 32 heads 10.4 us; 16 x 2176 to 2048, 8 heads 16.6 us; 8 x 4096 to 1024,
-// 32 heads 32.8 us, of them 19 for 27 MB of rows, read and written.
+// 1024, 32 heads 10.4 us; 16 x 2176 to 2048, 8 heads 16.6 us; 8 ragged
+// sequences of up to 4096 to 1024, 32 heads 32.8 us, of them 20 for 51 MB of
+// rows, read and written.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -730,7 +731,8 @@ hipError_t launch_evict(const KvView& c, const EvictCall& r, int num_cus, hipStr
   a.list_len = std::max(0, std::min(a.budget, a.cap - a.budget));
   // The workgroup that selects also moves, unless workgroups are too few to
   // move many rows at the memory's rate (15 x 8 heads, 7098 to 3549 tokens: 65
-  // us against 47 with a launch of its own; 16 x 8, 2176 to 2048: 19 against 24).
+  // us against 47 with a launch of its own; 16 x 8, 2176 to 2048: 19 against 24;
+  // 32 x 32, 2048 to 512: 8 less than with one).
   const bool move = int64_t(a.Hkv) * a.B >= num_cus || a.list_len <= 512;
   hipError_t e;
   if (a.cap <= 1024) {
