@@ -587,8 +587,8 @@ size_t swm_paged_attention_workspace_bytes(const swm_kv_cache* cache, int64_t q_
  *  budget >= 0, recent >= 0, both below 2^31.
  *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, lengths_out
  *  == lengths, an output at its input's address with other strides.  Cache
- *  errors as above.  No workspace; two launches, asynchronous on stream; whole
- *  numbers and copies, so bitwise reproducible. */
+ *  errors as above.  No workspace; one or two launches, asynchronous on stream;
+ *  whole numbers and copies, so bitwise reproducible. */
 swm_status swm_kv_evict(const swm_kv_cache* cache, const float* weights, int64_t w_page, int64_t w_head,
                         const int32_t* positions, int64_t p_page, int64_t p_head, int64_t budget, int64_t recent,
                         float* weights_out, int64_t wo_page, int64_t wo_head, int32_t* positions_out,

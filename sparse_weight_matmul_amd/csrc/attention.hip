@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
     asm volatile("" ::"v"(pk.page), "v"(pv.page), "v"(q[0]));  // not moved past the branch
   }
   n = min(max(n, 0), a.cap);
-  const int end = min(begin + a.split_len, n);
+  const int end = n - begin < a.split_len ? n : begin + a.split_len;  // begin + split_len may pass 2^31
   if (begin >= end && a.splits > 1) return;  // the join does not read splits past the length
 
   f32x4 o[kU][kJ];
@@ -439,6 +439,11 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   }
 }
 
+// Splits that hold tokens of a sequence of n (unsigned: the sum may pass 2^31).
+__device__ __forceinline__ int splits_of(const AttnArgs& a, int n) {
+  return int((uint32_t(n) + uint32_t(a.split_len) - 1) / uint32_t(a.split_len));
+}
+
 constexpr int kJoinThreads = 256;
 constexpr int kWeightTokens = 4 * kJoinThreads;  // tokens whose weights one workgroup adds
 constexpr int kMaxSplits = 1024;
@@ -466,7 +471,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   if (int(blockIdx.x) < joins) {
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
     const int n = min(max(a.lengths[b], 0), a.cap);
-    const int valid = (n + a.split_len - 1) / a.split_len;
+    const int valid = splits_of(a, n);
     const int64_t bh = int64_t(b) * a.Hq + h;
     const float* ml = a.ml + bh * a.splits * 2;
     // every wave finds the maximum and the sum; wave 0 leaves the factors
@@ -517,7 +522,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   const int n = min(max(a.lengths[b], 0), a.cap);
   const int t0 = chunk * kWeightTokens, t = t0 + 4 * tid;
   if (t0 >= n) return;
-  const int valid = (n + a.split_len - 1) / a.split_len;
+  const int valid = splits_of(a, n);
   // lanes per head for its maximum and sum over the splits
   int width = 1;
   while (width < valid && width < 64) width *= 2;

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void evict_long_kernel(EvictArgs a) {
   if (h == 0 && tid == 0) a.lengths_out[b] = left;
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   int32_t* kept = a.kept + (int64_t(b) * a.Hkv + h) * a.budget;
-  for (int j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
+  for (int64_t j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
   if (n <= a.budget || left == 0) {
     for (int j = tid; j < left; j += kThreads) {
       kept[j] = j;
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
   const int left = min(n, a.budget);
   if (h == 0 && tid == 0) a.lengths_out[b] = left;
   int32_t* kept = a.kept + (int64_t(b) * a.Hkv + h) * a.budget;
-  for (int j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
+  for (int64_t j = tid + left; j < a.budget; j += kThreads) kept[j] = -1;
   if (n <= a.budget || left == 0) {
     for (int j = tid; j < left; j += kThreads) {
       kept[j] = j;

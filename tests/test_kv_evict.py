@@ -192,6 +192,21 @@ def test_graph_and_stream(gpu_lib):
 
 
 @gpu
+def test_largest_budget(gpu_lib):
+    import torch
+    S, D, n = 16, 64, 37
+    k = torch.zeros((4, S, 1, D), dtype=torch.float16, device="cuda")
+    cache = swm.PagedCache(k, k.clone(), torch.tensor([[2, 0, 3]], dtype=torch.int32, device="cuda"),
+                           torch.tensor([n], dtype=torch.int32, device="cuda"))
+    w = torch.rand((4, 1, S), device="cuda")
+    pos = torch.arange(4 * S, dtype=torch.int32, device="cuda").view(4, 1, S)
+    lengths, kept = swm.kv_evict(cache, w, pos, (1 << 31) - 1, 4)
+    assert lengths.tolist() == [n]
+    assert torch.equal(kept[0, 0, :n], torch.arange(n, dtype=torch.int32, device="cuda"))
+    assert int(kept[0, 0, n:].max()) == -1 and int(kept[0, 0, n:].min()) == -1
+
+
+@gpu
 def test_missing_pages_are_never_touched(gpu_lib):
     import torch
     k, v, w, pos, table = make(1, 2, 64, 16, [100], "long")

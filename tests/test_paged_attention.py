@@ -106,6 +106,8 @@ CASES = [
     (1, 2, 2, 200, 100, [350], "token"),
     (1, 8, 1, 128, 128, [20001], "head"),
     (2, 2, 2, 64, 20, [9000, 4097], "token"),
+    (1, 16, 1, 256, 16, [700], "token"),                    # the most shared memory
+    (1, 32, 2, 248, 24, [5000], "head"),
 ]
 
 
@@ -221,6 +223,24 @@ def test_offsets_past_32_bits(gpu_lib):
     cache = swm.PagedCache(pool, pool, torch.from_numpy(table).cuda(), torch.tensor([150], dtype=torch.int32).cuda())
     ref, tol, _, _ = reference(q, rows, rows, table - (P - 3), [150], D ** -0.5)
     check(swm.paged_attention(cache, torch.from_numpy(q).cuda()), ref, tol)
+
+
+@gpu
+@pytest.mark.parametrize("tokens", [2047 * 1049056, 2047 * 1049056 - 1000000])
+def test_capacities_next_to_2_31(gpu_lib, tokens):
+    import torch
+    # 2046 times a page of zeros, then a page of 2047: exact sums, a mean of 2047 * (its share)
+    S, D, n = 1049056, 8, 2047
+    k = torch.zeros((2, S, 1, D), dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    v[1] = 2047
+    table = torch.zeros((1, n), dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    cache = swm.PagedCache(k, v, table, torch.tensor([tokens], dtype=torch.int32, device="cuda"))
+    out = swm.paged_attention(cache, torch.ones((1, 1, D), dtype=torch.float16, device="cuda"))
+    want = 2047 * (tokens - (n - 1) * S) / tokens
+    # sums of up to 2^31 in fp32, one rounding per split and two: far below one rounding to fp16
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0**-10 * want)
 
 
 @gpu
