@@ -717,13 +717,14 @@ def kv_evict(cache: PagedCache, weights, positions, budget: int, recent: int = 0
         raise ValueError("budget must not be negative")
     if lengths_out is None:
         lengths_out = _empty_like(cache.lengths, stream)
-    elif (not lengths_out.is_cuda or lengths_out.dtype != torch.int32 or lengths_out.shape != (cache.batch,)
-          or not lengths_out.is_contiguous()):
+    elif (lengths_out.device != cache.device or lengths_out.dtype != torch.int32
+          or lengths_out.shape != (cache.batch,) or not lengths_out.is_contiguous()):
         raise TypeError("lengths_out must be a contiguous int32 CUDA tensor, one entry per sequence")
     shape = (cache.batch, cache.heads, budget)
     if kept is None:
         kept = _empty(shape, torch.int32, cache.device, stream)
-    elif not kept.is_cuda or kept.dtype != torch.int32 or kept.shape != shape or not kept.is_contiguous():
+    elif (kept.device != cache.device or kept.dtype != torch.int32 or kept.shape != shape
+          or not kept.is_contiguous()):
         raise TypeError(f"kept must be a contiguous {shape} int32 CUDA tensor")
     s = _raw_stream(stream, cache.device.index)
     _check(lib.swm_kv_evict(cache._p, *w, *p, budget, int(recent), *wo, *po, lengths_out.data_ptr(),
