@@ -538,9 +538,11 @@ typedef struct swm_kv_cache {
  *  each cached row: weights[page * w_page + head * w_head + slot] grows by
  *  the sum of p_t over the head's group of query heads.  The adds are atomic:
  *  where sequences share a page their order, and with it the last bit, is not
- *  fixed; everything else of this call is bitwise reproducible.
+ *  fixed; everything else of this call is bitwise reproducible (the order of
+ *  a sequence's sums depends on the lengths of its batch).
  *  workspace: DEVICE memory of at least swm_paged_attention_workspace_bytes
- *  bytes (0 for few splits and no weights: NULL is fine then), 16-byte
+ *  bytes (0 for batches that fill the device, short
+ *  sequences and no weights: NULL is fine then), 16-byte
  *  aligned; calls that share it must be ordered on one stream.
  *  Scores, maxima, sums and outputs are fp32; out is rounded once.
  *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of

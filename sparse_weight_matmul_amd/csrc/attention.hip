@@ -43,6 +43,7 @@
 
 #include "kernels.h"
 #include "paging.h"
+#include "wave.h"
 
 namespace swm {
 namespace {
@@ -54,6 +55,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 32;   // tokens a wave takes at a time
 constexpr int kWaves = 4;   // waves of a workgroup; they take tiles in turn
+constexpr int kMaxSorted = 128;  // sequences whose lengths a wave holds, two a lane
 constexpr int kHeads = 16;  // query heads of a workgroup (columns of the matrix instruction)
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -64,19 +66,22 @@ struct AttnArgs {
   const int32_t *table, *lengths;
   const uint8_t* mask;
   float* weights;
-  float* ml;      // [B][Hq][splits][2] maximum (in units of log2) and sum
-  float* part;    // [B][Hq][splits][D] unnormalised outputs
+  int32_t* plan;  // tokens of a split, then the first split of each sequence
+  float* ml;      // [piece][query head of it][2] maximum (in units of log2) and sum
+  float* part;    // [piece][query head of it][D] unnormalised outputs
   float* logits;  // [B][Hq][lrow] scores in units of log2
   int64_t q_b, q_h, o_b, o_h;
   int64_t k_p, k_s, k_h, v_p, v_s, v_h;
   int64_t table_b, mask_b, w_p, w_h;
   int32_t B, Hq, Hkv, G, D, S, pages, cap, per_seq;
-  int32_t splits, split_len, lrow;
+  int32_t room;  // pieces of all sequences at most; 0: every sequence is one
+  int32_t lrow, order, cus;
   int32_t own_weights;  // the only split adds the weights itself, its scores in LDS
   float scale;  // softmax scale * log2(e)
-  PageDiv div;              // by S
-  PageDiv per_split, per_b;  // by the units of a split and of a sequence
-  int32_t units;            // sequences x key-value heads x groups of 16 query heads
+  PageDiv div;    // by S
+  PageDiv per_b;  // by the units of a sequence: key-value heads x groups of 16 query heads
+  PageDiv per_hq, per_g;  // by the query heads, and those of a key-value head
+  int32_t units;  // of all sequences
 };
 
 // Where a token's rows are: its page, clamped into the pool, and whether the
@@ -200,6 +205,101 @@ __device__ __forceinline__ void add_weights(const AttnArgs& a, const int32_t* ro
   }
 }
 
+// Lengths of sequences 2 lane and 2 lane + 1 (0 past the batch), in tokens.
+__device__ __forceinline__ void two_lengths(const AttnArgs& a, int lane, int* n0, int* n1) {
+  const int x0 = a.lengths[min(2 * lane, a.B - 1)], x1 = a.lengths[min(2 * lane + 1, a.B - 1)];
+  *n0 = 2 * lane < a.B ? min(max(x0, 0), a.cap) : 0;
+  *n1 = 2 * lane + 1 < a.B ? min(max(x1, 0), a.cap) : 0;
+}
+
+// The pieces that the sequences of a batch are cut into, by their lengths: `len`
+// tokens each, the fewest steps with which they are a.room at most, or every
+// sequence whole if that ends no later.  Sequence 2 lane owns pieces first0 ..
+// first1 - 1, the next one first1 .. last1 - 1.
+struct Plan {
+  int n0, n1, len, first0, first1, last1;
+};
+
+// s / q rounded up, inv = 1 / q to fp32's precision: the quotient of s < 2^31 is
+// off by two at most (a division of whole numbers takes three times as long).
+__device__ __forceinline__ uint32_t ceil_div(uint32_t s, uint32_t q, float inv) {
+  const uint32_t t = uint32_t(float(s) * inv);
+  const int64_t r = int64_t(s) - int64_t(t) * q;
+  return t + (r > 0) + (r > q) - (r <= -int64_t(q)) - (r <= -2 * int64_t(q));
+}
+__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int lane) {
+  Plan p;
+  two_lengths(a, lane, &p.n0, &p.n1);
+  constexpr uint32_t kStep = kTile * kWaves;
+  const uint32_t s0 = (uint32_t(p.n0) + kStep - 1) / kStep, s1 = (uint32_t(p.n1) + kStep - 1) / kStep;
+  const uint32_t total = wave_sum(s0 + s1), room = a.room;
+  uint32_t c0, c1;  // pieces of either sequence
+  auto cut = [&](uint32_t q) {
+    const float inv = __builtin_amdgcn_rcpf(float(q));
+    c0 = ceil_div(s0, q, inv);
+    c1 = ceil_div(s1, q, inv);
+    return wave_sum(c0 + c1);
+  };
+  uint32_t q = max((total + room - 1) / room, 2u);
+  uint32_t all = cut(q);
+  if (all > room) {
+    // every sequence rounds up by less than one piece: this many steps fit; the
+    // least that do, to a sixteenth
+    uint32_t low = q;
+    q = (total + room - a.B - 1) / (room - a.B);
+    while (q - low > max(low / 16, 1u)) {
+      const uint32_t mid = low + (q - low) / 2;
+      if (cut(mid) > room)
+        low = mid;
+      else
+        q = mid;
+    }
+    all = cut(q);
+  }
+  if (2 * a.units > a.cus) {
+    // rounds over the CUs times the steps of one
+    const uint32_t most = uint32_t(wave_max(int(max(s0, s1)))), cus = a.cus, rows = uint32_t(a.units) / a.B;
+    if ((a.units + cus - 1) / cus * most <= (all * rows + cus - 1) / cus * q) {
+      q = max(most, q);
+      cut(q);
+    }
+  }
+  const uint32_t upto = scan_wave(c0 + c1);
+  p.len = int(q * kStep);
+  p.last1 = int(upto);
+  p.first1 = int(upto - c1);
+  p.first0 = int(upto - c1 - c0);
+  return p;
+}
+
+// The workgroups in the order of their work, the longest first in the first
+// round over the CUs, the shortest first in the second and so on: a CU's
+// workgroups then add up to about the same length.  Returns the unit within
+// sequence *b.
+__device__ __forceinline__ int sorted_unit(const AttnArgs& a, int lane, int per_b, int* b) {
+  int n0, n1;
+  two_lengths(a, lane, &n0, &n1);
+  constexpr uint32_t kStep = kTile * kWaves;
+  // unique keys: steps, then the lower sequence; those past the batch have none below them
+  auto key = [&](int n, int i) {
+    return i < a.B ? (uint32_t(n) + kStep - 1) / kStep << 7 | uint32_t(127 - i) : 0u;
+  };
+  const uint32_t k0 = key(n0, 2 * lane), k1 = key(n1, 2 * lane + 1);
+  int r0 = 0, r1 = 0;
+  for (int l = 0; l < (a.B + 1) / 2; ++l) {
+    const uint32_t x = __builtin_amdgcn_readlane(k0, l), z = __builtin_amdgcn_readlane(k1, l);
+    r0 += int(x > k0) + int(z > k0);
+    r1 += int(x > k1) + int(z > k1);
+  }
+  const int i = blockIdx.x, round = i / a.cus;
+  const int s = round & 1 ? round * a.cus + min((round + 1) * a.cus, a.units) - 1 - i : i;
+  const int rank = page_index(a.per_b, s);
+  const uint64_t in0 = __builtin_amdgcn_ballot_w64(2 * lane < a.B && r0 == rank);
+  const uint64_t in1 = __builtin_amdgcn_ballot_w64(2 * lane + 1 < a.B && r1 == rank);
+  *b = in0 ? 2 * __builtin_ctzll(in0) : 2 * __builtin_ctzll(in1) + 1;
+  return s - rank * per_b;
+}
+
 // One workgroup: one split of one sequence, up to 16 query heads of one
 // key-value head.
 template <int DP, bool kFull, bool kSame8>
@@ -209,20 +309,42 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   extern __shared__ float smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Split by split, the units rotated by the split: workgroup i runs on XCD i %
-  // 8, so every unit's splits visit all XCDs, and the splits past the end of
-  // short sequences come last.  (Dealt with the splits side by side, 8 of them
-  // put each split on an XCD of its own, and half of those idle when the
-  // sequences fill half of their capacity.)
-  const int split = page_index(a.per_split, blockIdx.x);
-  const int turned = int(blockIdx.x) - split * a.units - (split - page_index(a.per_split, split) * a.units);
-  const int unit = turned < 0 ? turned + a.units : turned;
-  const int tiles_h = (a.G + kHeads - 1) / kHeads;
-  const int b = page_index(a.per_b, unit), y = unit - b * a.Hkv * tiles_h;
+  const int tiles_h = (a.G + kHeads - 1) / kHeads, per_b = a.Hkv * tiles_h;
+  int b, y, n, begin = 0, end;
+  int piece = blockIdx.x;  // where its sums go
+  if (a.room > 0) {
+    const Plan p = make_plan(a, lane);
+    if (blockIdx.x == 0 && wave == 0) {
+      if (lane == 0) a.plan[0] = p.len;
+      if (2 * lane < a.B) a.plan[1 + 2 * lane] = p.first0;
+      if (2 * lane + 1 < a.B) a.plan[2 + 2 * lane] = p.first1;
+    }
+    const int split = page_index(a.per_b, piece);  // of the batch's
+    y = piece - split * per_b;
+    const uint64_t in = __builtin_amdgcn_ballot_w64(split >= p.first0 && split < p.last1);
+    if (in == 0) return;  // more workgroups than pieces
+    const int l = __builtin_ctzll(in);
+    const bool odd = split >= __builtin_amdgcn_readlane(p.first1, l);
+    b = 2 * l + odd;
+    n = __builtin_amdgcn_readlane(odd ? p.n1 : p.n0, l);
+    begin = (split - __builtin_amdgcn_readlane(odd ? p.first1 : p.first0, l)) * p.len;
+    end = n - begin < p.len ? n : begin + p.len;
+  } else {
+    const int unit = a.order ? sorted_unit(a, lane, per_b, &b) : piece;
+    if (!a.order) b = page_index(a.per_b, unit);
+    y = a.order ? unit : unit - b * per_b;
+    piece = b * per_b + y;
+    n = min(max(a.lengths[b], 0), a.cap);
+    end = n;
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  y = __builtin_amdgcn_readfirstlane(y);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  end = __builtin_amdgcn_readfirstlane(end);
+  piece = __builtin_amdgcn_readfirstlane(piece);
   const int hkv = tiles_h == 1 ? y : y / tiles_h, ht = y - hkv * tiles_h;
   const int gn = min(kHeads, a.G - ht * kHeads);  // query heads here
   const int h0 = hkv * a.G + ht * kHeads;
-  const int begin = split * a.split_len;
   const int first = begin + kTile * wave;
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   const uint8_t* mask = a.mask ? a.mask + int64_t(b) * a.mask_b : nullptr;
@@ -230,9 +352,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   const uint16_t* vh = a.v + int64_t(hkv) * a.v_h;
   const int g = lane >> 4, c = lane & 15;
 
-  // The length, the query and the first pages are requested together: each
-  // waited for in turn would add its latency to the shortest calls.
-  int n = a.lengths[b];
+  // The query and the first pages are requested together, the length too where
+  // nothing depends on it: each waited for in turn would add its latency to the
+  // shortest calls.
   half8 q[DP / 32];
   {
     const uint16_t* src = a.q + int64_t(b) * a.q_b + int64_t(h0 + min(c, gn - 1)) * a.q_h;
@@ -250,9 +372,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
     pv = place(a, row, first + 8 * g);
     asm volatile("" ::"v"(pk.page), "v"(pv.page), "v"(q[0]));  // not moved past the branch
   }
-  n = min(max(n, 0), a.cap);
-  const int end = n - begin < a.split_len ? n : begin + a.split_len;  // begin + split_len may pass 2^31
-  if (begin >= end && a.splits > 1) return;  // the join does not read splits past the length
 
   f32x4 o[kU][kJ];
 #pragma unroll
@@ -394,14 +513,14 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       sum += r * sm_l[w * kHeads + h];
       acc += r * *reinterpret_cast<const f32x4*>(&sm_o[(w * gn + h) * kRow + d]);
     }
-    const int64_t bh = int64_t(b) * a.Hq + h0 + h;
+    const int64_t at = int64_t(piece) * min(a.G, kHeads) + h;
     if (d == 0 && a.ml) {
-      a.ml[(bh * a.splits + split) * 2] = mm;
-      a.ml[(bh * a.splits + split) * 2 + 1] = sum;
+      a.ml[at * 2] = mm;
+      a.ml[at * 2 + 1] = sum;
     }
     if (d >= a.D) continue;  // D is a multiple of 8
-    if (a.splits > 1) {
-      *reinterpret_cast<f32x4*>(&a.part[(bh * a.splits + split) * a.D + d]) = acc;
+    if (a.room > 0) {
+      *reinterpret_cast<f32x4*>(&a.part[at * a.D + d]) = acc;
     } else {
       uint16_t* dst = a.out + int64_t(b) * a.o_b + int64_t(h0 + h) * a.o_h + d;
 #pragma unroll
@@ -439,14 +558,27 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   }
 }
 
-// Splits that hold tokens of a sequence of n (unsigned: the sum may pass 2^31).
-__device__ __forceinline__ int splits_of(const AttnArgs& a, int n) {
-  return int((uint32_t(n) + uint32_t(a.split_len) - 1) / uint32_t(a.split_len));
+// The pieces of a sequence of n tokens: how many, and where the sums of the
+// first one are for query head h of the sequence; the next piece's are `step`
+// entries on.
+struct Pieces {
+  int count;
+  int64_t at, step;
+};
+__device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int b, int n, int h) {
+  const int hs = min(a.G, kHeads), tiles_h = (a.G + kHeads - 1) / kHeads, per_b = a.Hkv * tiles_h;
+  const int hkv = page_index(a.per_g, h), g = h - hkv * a.G, ht = g / kHeads;
+  const int first = a.room > 0 ? a.plan[1 + b] : b;
+  Pieces p;
+  p.count = a.room > 0 ? int((uint32_t(n) + uint32_t(a.plan[0]) - 1) / uint32_t(a.plan[0])) : n > 0;
+  p.step = int64_t(per_b) * hs;
+  p.at = (int64_t(first) * per_b + hkv * tiles_h + ht) * hs + g - ht * kHeads;
+  return p;
 }
 
 constexpr int kJoinThreads = 256;
 constexpr int kWeightTokens = 4 * kJoinThreads;  // tokens whose weights one workgroup adds
-constexpr int kMaxSplits = 1024;
+constexpr int kMaxPieces = 1024;  // of a batch, so of a sequence
 constexpr int kStatHeads = 128;  // heads whose maxima and sums a workgroup holds at a time
 
 // Maximum and sum over groups of `width` lanes, a power of two.
@@ -465,24 +597,25 @@ __device__ __forceinline__ float sum_over(float v, int width) {
 // of a few memory latencies, so every loop requests several rounds before it
 // uses one.
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int joins) {
-  __shared__ float sc[kMaxSplits];
+  __shared__ float sc[kMaxPieces];
   __shared__ f32x4 red[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (int(blockIdx.x) < joins) {
-    const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
+    const int b = page_index(a.per_hq, blockIdx.x), h = blockIdx.x - b * a.Hq;
     const int n = min(max(a.lengths[b], 0), a.cap);
-    const int valid = splits_of(a, n);
-    const int64_t bh = int64_t(b) * a.Hq + h;
-    const float* ml = a.ml + bh * a.splits * 2;
+    const Pieces p = pieces_of(a, b, n, h);
+    const int valid = p.count;
+    const float* ml = a.ml + p.at * 2;
+    const int64_t next = 2 * p.step;
     // every wave finds the maximum and the sum; wave 0 leaves the factors
     float m = neg_inf();
-    for (int s = lane; s < valid; s += 64) m = fmaxf(m, ml[2 * s]);
+    for (int s = lane; s < valid; s += 64) m = fmaxf(m, ml[next * s]);
     m = max_over(m, 64);
     const float base = m == neg_inf() ? 0.f : m;
     float l = 0.f;
     for (int s = lane; s < valid; s += 64) {
-      const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
-      l += f * ml[2 * s + 1];
+      const float f = __builtin_amdgcn_exp2f(ml[next * s] - base);
+      l += f * ml[next * s + 1];
       if (wave == 0) sc[s] = f;
     }
     l = sum_over(l, 64);
@@ -492,13 +625,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     const int parts = kJoinThreads / per, part = tid / per, d = tid % per * 4;
     f32x4 acc = {0, 0, 0, 0};
     if (d < a.D) {
-      const float* src = a.part + bh * a.splits * a.D + d;
+      const float* src = a.part + p.at * a.D + d;
+      const int64_t row = p.step * a.D;
       constexpr int kUnroll = 8;
       for (int s0 = part; s0 < valid; s0 += kUnroll * parts) {
         f32x4 v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          v[u] = *reinterpret_cast<const f32x4*>(src + int64_t(min(s0 + u * parts, valid - 1)) * a.D);
+          v[u] = *reinterpret_cast<const f32x4*>(src + min(s0 + u * parts, valid - 1) * row);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
           if (s0 + u * parts < valid) acc += sc[s0 + u * parts] * v[u];
@@ -507,7 +641,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     red[tid] = acc;
     __syncthreads();
     if (part == 0 && d < a.D) {
-      for (int p = 1; p < parts; ++p) acc += red[p * per + tid];
+      for (int o = 1; o < parts; ++o) acc += red[o * per + tid];
       uint16_t* dst = a.out + int64_t(b) * a.o_b + int64_t(h) * a.o_h + d;
 #pragma unroll
       for (int e = 0; e < 4; ++e) dst[e] = __builtin_bit_cast(uint16_t, _Float16(l == 0.f ? 0.f : acc[e] / l));
@@ -522,7 +656,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   const int n = min(max(a.lengths[b], 0), a.cap);
   const int t0 = chunk * kWeightTokens, t = t0 + 4 * tid;
   if (t0 >= n) return;
-  const int valid = splits_of(a, n);
+  const int valid = pieces_of(a, b, n, 0).count;
   // lanes per head for its maximum and sum over the splits
   int width = 1;
   while (width < valid && width < 64) width *= 2;
@@ -531,13 +665,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     const int gn = min(a.G - g0, kStatHeads);
     const int64_t head = int64_t(b) * a.Hq + hkv * a.G + g0;
     for (int g = tid / width; g < (gn + 63) / 64 * 64; g += kJoinThreads / width) {
-      const float* ml = a.ml + (head + min(g, gn - 1)) * a.splits * 2;
+      const Pieces p = pieces_of(a, b, n, hkv * a.G + g0 + min(g, gn - 1));
+      const float* ml = a.ml + p.at * 2;
+      const int64_t next = 2 * p.step;
       const int s0 = tid % width;
       float m = neg_inf(), l = 0.f;
-      for (int s = s0; s < valid; s += width) m = fmaxf(m, ml[2 * s]);
+      for (int s = s0; s < valid; s += width) m = fmaxf(m, ml[next * s]);
       m = max_over(m, width);
       const float base = m == neg_inf() ? 0.f : m;
-      for (int s = s0; s < valid; s += width) l += __builtin_amdgcn_exp2f(ml[2 * s] - base) * ml[2 * s + 1];
+      for (int s = s0; s < valid; s += width) l += __builtin_amdgcn_exp2f(ml[next * s] - base) * ml[next * s + 1];
       l = sum_over(l, width);
       if (s0 == 0 && g < gn) {
         sc[2 * g] = base;
@@ -608,27 +744,36 @@ AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t c
   const int64_t units = B * Hkv * ((G + kHeads - 1) / kHeads);
   const int64_t step = int64_t(kTile) * kWaves;
   const int64_t steps = std::max<int64_t>(1, (cap + step - 1) / step);
-  int64_t splits = 1;
-  if (units <= num_cus / 2 && steps > 8) {
-    splits = std::min(num_cus / units, steps / 2);
-    for (int64_t k = 2; k <= (D <= 64 ? 4 : 1); ++k)
-      if (k * num_cus / units <= steps / 8) splits = k * num_cus / units;
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
+  if (B >= 1 && B <= kMaxSorted && units <= num_cus && steps > 8) {
+    const int64_t rows = units / B;  // units of a sequence
+    int64_t k = 0;                   // workgroups per CU
+    if (units <= num_cus / 2) {
+      k = 1;
+      while (D <= 64 && k < 4 && (k + 1) * num_cus / units <= steps / 8) ++k;
+    } else if (steps >= 32) {
+      k = D <= 128 ? 2 : 3;
+    }
+    p.room = int(std::min<int64_t>(k * num_cus / rows, kMaxPieces));
+    if (p.room < 2 * B) p.room = 0;
   }
-  const int64_t per = (steps + splits - 1) / splits;
-  p.split_len = int(std::min<int64_t>(per * step, (int64_t(1) << 31) - step));
-  p.splits = int(std::max<int64_t>(1, (cap + p.split_len - 1) / p.split_len));
+  p.order = p.room == 0 && B > 1 && B <= kMaxSorted && units > num_cus && steps > 4 + B / 32;
+  p.cus = num_cus;
   p.lrow = int((cap + kTile - 1) / kTile * kTile);
   const int64_t dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   const int64_t join = 4 * (2 * kWaves * kHeads + kWaves * std::min<int64_t>(G, kHeads) * (dp + 4));
-  p.own_weights = weights && p.splits == 1 && G <= kHeads && join + 4 * G * p.lrow <= 52 * 1024;
+  p.own_weights = weights && p.room == 0 && G <= kHeads && join + 4 * G * p.lrow <= 52 * 1024;
   p.lds = size_t(join + (p.own_weights ? 4 * G * p.lrow : 0));
   const size_t rows = size_t(B) * size_t(Hq);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const bool scores = weights && !p.own_weights;
-  if (p.splits > 1 || scores) p.bytes += up(rows * p.splits * 2 * 4);
+  const int64_t pieces = p.room > 0 ? p.room * (units / B) : units;
+  const size_t sums = size_t(pieces) * size_t(std::min<int64_t>(G, kHeads));
+  p.grid = pieces;
+  if (p.room > 0) p.bytes += up((1 + size_t(B)) * 4);
+  p.off_ml = p.bytes;
+  if (p.room > 0 || scores) p.bytes += up(sums * 2 * 4);
   p.off_part = p.bytes;
-  if (p.splits > 1) p.bytes += up(rows * p.splits * size_t(D) * 4);
+  if (p.room > 0) p.bytes += up(sums * size_t(D) * 4);
   p.off_logits = p.bytes;
   if (scores) p.bytes += up(rows * size_t(p.lrow) * 4);
   return p;
@@ -667,32 +812,35 @@ hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& 
   a.pages = int(c.pages);
   a.per_seq = int(c.per_seq);
   a.cap = int(c.per_seq * c.S);
-  a.splits = p.splits;
-  a.split_len = p.split_len;
+  a.room = p.room;
   a.lrow = p.lrow;
+  a.order = p.order;
+  a.cus = p.cus;
   a.scale = r.scale * 1.44269504088896340736f;
   a.div = page_div(c.S);
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool scores = r.weights && !p.own_weights;
-  const bool second = p.splits > 1 || scores;
+  const bool second = p.room > 0 || scores;
   a.own_weights = p.own_weights;
-  if (second) a.ml = reinterpret_cast<float*>(w);
-  if (p.splits > 1) a.part = reinterpret_cast<float*>(w + p.off_part);
+  if (p.room > 0) a.plan = reinterpret_cast<int32_t*>(w);
+  if (second) a.ml = reinterpret_cast<float*>(w + p.off_ml);
+  if (p.room > 0) a.part = reinterpret_cast<float*>(w + p.off_part);
   if (scores) a.logits = reinterpret_cast<float*>(w + p.off_logits);
 
   const int tiles_h = (a.G + kHeads - 1) / kHeads;
   const int dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
   const size_t lds = p.lds;
   a.units = a.B * a.Hkv * tiles_h;
-  a.per_split = page_div(a.units);
   a.per_b = page_div(int64_t(a.Hkv) * tiles_h);
-  const dim3 grid(uint32_t(a.units) * uint32_t(a.splits));
+  a.per_hq = page_div(a.Hq);
+  a.per_g = page_div(a.G);
+  const dim3 grid(uint32_t(p.grid));
   const bool same8 = a.S % 8 == 0;
   hipError_t e = dp == 64    ? launch_dim<64>(a, same8, grid, lds, s)
                  : dp == 128 ? launch_dim<128>(a, same8, grid, lds, s)
                              : launch_dim<256>(a, same8, grid, lds, s);
   if (e != hipSuccess || !second) return e;
-  const int64_t joins = p.splits > 1 ? int64_t(a.B) * a.Hq : 0;
+  const int64_t joins = p.room > 0 ? int64_t(a.B) * a.Hq : 0;
   const int64_t adds = scores ? int64_t(a.B) * a.Hkv * ((a.cap + kWeightTokens - 1) / kWeightTokens) : 0;
   if (joins + adds == 0) return hipSuccess;
   attn_join_kernel<<<dim3(uint32_t(joins + adds)), kJoinThreads, 0, s>>>(a, int(joins));

@@ -330,17 +330,6 @@ __device__ __forceinline__ void count_bins(uint32_t* hist, uint32_t bin, bool ac
     atomicAdd(&hist[bin_at(bin)], 1u);
 }
 
-// Sums of the lanes up to and including this one.
-__device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int s = 1; s < 64; s *= 2) {
-    const uint32_t o = __shfl_up(v, s);
-    if (lane >= s) v += o;
-  }
-  return v;
-}
-
 // Set lanes of b before this one.
 __device__ __forceinline__ uint32_t lanes_before(uint64_t b) {
   return __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), 0u));

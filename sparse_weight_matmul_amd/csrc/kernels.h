@@ -162,10 +162,14 @@ struct AttnCall {
   float scale = 1.f;
 };
 struct AttnPlan {
-  int splits = 1, split_len = 0, lrow = 0;
-  bool own_weights = false;                        // the weights are added by the first launch
-  size_t lds = 0;                                  // of a workgroup of the first launch
-  size_t off_part = 0, off_logits = 0, bytes = 0;  // workspace
+  int room = 0;              // pieces of all sequences at most; 0: every sequence is one
+  int64_t grid = 0;          // workgroups of the first launch
+  int lrow = 0;              // scores per row
+  bool order = false;        // units sorted by their length,
+  int cus = 256;             // a round of this many at a time
+  bool own_weights = false;  // the weights are added by the first launch
+  size_t lds = 0;            // of a workgroup of the first launch
+  size_t off_ml = 0, off_part = 0, off_logits = 0, bytes = 0;  // workspace
 };
 AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, bool weights, int num_cus);
 // Eviction down to `budget` tokens per sequence and head.

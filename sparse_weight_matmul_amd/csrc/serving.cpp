@@ -97,15 +97,15 @@ swm_status swm_paged_attention(const swm_kv_cache* c, const void* q, int64_t q_b
   if (st != SWM_OK) return st;
   // either launch: at most 2^24 - 1 workgroups of 256 threads
   if (c->batch * q_heads + c->batch * c->heads * (cap / 1024 + 1) >= (int64_t(1) << 24) ||
-      c->batch * q_heads * p.splits >= (int64_t(1) << 24))
+      p.grid >= (int64_t(1) << 24))
     return SWM_ERR_UNSUPPORTED;
   if (p.bytes > 0) {
     if (!workspace || ws_bytes < p.bytes) return SWM_ERR_INVALID_ARG;
     if (misaligned(workspace)) return SWM_ERR_ALIGN;
   }
-  swm_log("paged_attention B=%lld heads=%lld/%lld D=%lld capacity=%lld: %d splits of %d tokens%s", (long long)c->batch,
-          (long long)q_heads, (long long)c->heads, (long long)c->dim, (long long)cap, p.splits, p.split_len,
-          weights ? ", weights added" : "");
+  swm_log("paged_attention B=%lld heads=%lld/%lld D=%lld capacity=%lld: %lld workgroups%s%s", (long long)c->batch,
+          (long long)q_heads, (long long)c->heads, (long long)c->dim, (long long)cap, (long long)p.grid,
+          p.room > 0  ? ", split by length" : p.order ? ", sorted by length" : "", weights ? ", weights added" : "");
   swm::AttnCall r;
   r.q = static_cast<const uint16_t*>(q);
   r.out = static_cast<uint16_t*>(out);

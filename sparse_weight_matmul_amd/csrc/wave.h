@@ -41,8 +41,27 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
 }
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return a + b; });
+}
 __device__ __forceinline__ int wave_max(int v) {
   return int(wave_reduce(uint32_t(v), [](uint32_t a, uint32_t b) { return uint32_t(max(int(a), int(b))); }));
+}
+
+// Sums of the lanes up to and including this one: shifts inside rows of 16
+// lanes, then the last lane of a row to the next row, of a half to the other
+// (lanes without a source add zero).
+template <int ctrl, int rows>
+__device__ __forceinline__ uint32_t add_from(uint32_t v) {
+  return v + uint32_t(__builtin_amdgcn_update_dpp(0, int(v), ctrl, rows, 0xf, false));
+}
+__device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
+  v = add_from<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v = add_from<0x112, 0xf>(v);
+  v = add_from<0x114, 0xf>(v);
+  v = add_from<0x118, 0xf>(v);
+  v = add_from<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+  return add_from<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
 }
 
 }  // namespace swm

@@ -87,6 +87,14 @@ def check(out, ref, tol, what=""):
     assert not bad.any(), (what, int(bad.sum()), float(np.max(np.abs(got - ref) - tol)))
 
 
+def ragged(B, most, seed=0):
+    r = np.random.default_rng([seed, B, most])
+    n = r.integers(0, most + 1, B)
+    n[r.integers(0, B, 1 + B // 8)] = 0
+    n[r.integers(0, B)] = most
+    return n.tolist()
+
+
 CASES = [
     # B, Hq, Hkv, D, S, lengths, layout
     (1, 1, 1, 64, 16, [1], "token"),
@@ -108,6 +116,13 @@ CASES = [
     (2, 2, 2, 64, 20, [9000, 4097], "token"),
     (1, 16, 1, 256, 16, [700], "token"),                    # the most shared memory
     (1, 32, 2, 248, 24, [5000], "head"),
+    (40, 8, 8, 64, 16, ragged(40, 1500), "token"),          # more units than CUs: sorted
+    (128, 4, 4, 64, 8, ragged(128, 1300), "head"),
+    (129, 3, 3, 64, 16, ragged(129, 1400), "token"),        # too many sequences to sort
+    (100, 2, 1, 128, 32, ragged(100, 1600), "token"),       # cut by the lengths
+    (21, 16, 8, 64, 16, ragged(21, 4300), "head"),
+    (9, 34, 2, 256, 16, ragged(9, 5000), "token"),
+    (20, 8, 8, 64, 16, [4200] * 20, "token"),               # of one length: whole
 ]
 
 
