@@ -541,9 +541,9 @@ typedef struct swm_kv_cache {
  *  fixed; everything else of this call is bitwise reproducible (the order of
  *  a sequence's sums depends on the lengths of its batch).
  *  workspace: DEVICE memory of at least swm_paged_attention_workspace_bytes
- *  bytes (0 for batches that fill the device, short
- *  sequences and no weights: NULL is fine then), 16-byte
- *  aligned; calls that share it must be ordered on one stream.
+ *  bytes (0 for short sequences, or a batch that fills the device, without
+ *  weights: NULL is fine then), 16-byte aligned; calls that share it must be
+ *  ordered on one stream.
  *  Scores, maxima, sums and outputs are fp32; out is rounded once.
  *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
  *  heads, a scale that is not finite, negative strides, mask_ld below the

@@ -193,16 +193,18 @@ __device__ __forceinline__ float sum_groups(float v) {
   return a + b;
 }
 
-// Adds the weights of tokens t..t+3 (those below n) to the accumulator.
-// Atomic because sequences may share a page.
+// Adds the weights of tokens t, t + 64, t + 128 and t + 192 (those below n) to
+// the accumulator: a wave's 64 lanes add to consecutive slots.  Atomic because
+// sequences may share a page.
 __device__ __forceinline__ void add_weights(const AttnArgs& a, const int32_t* row, int hkv, int t, int n,
                                             const f32x4& w) {
+  Place p[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (t + e >= n || w[e] == 0.f) continue;
-    const Place p = place(a, row, t + e);
-    if (p.ok) unsafeAtomicAdd(a.weights + int64_t(p.page) * a.w_p + int64_t(hkv) * a.w_h + p.slot, w[e]);
-  }
+  for (int e = 0; e < 4; ++e) p[e] = place(a, row, min(t + 64 * e, n - 1));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (t + 64 * e < n && w[e] != 0.f && p[e].ok)
+      unsafeAtomicAdd(a.weights + int64_t(p[e].page) * a.w_p + int64_t(hkv) * a.w_h + p[e].slot, w[e]);
 }
 
 // Lengths of sequences 2 lane and 2 lane + 1 (0 past the batch), in tokens.
@@ -547,12 +549,13 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
     sm_l[threadIdx.x] = inv;
   }
   __syncthreads();
-  for (int t = 4 * threadIdx.x; t < n; t += 4 * 64 * kWaves) {
+  for (int t = 256 * wave + lane; t < n; t += 256 * kWaves) {
     f32x4 w = {0, 0, 0, 0};
     for (int h = 0; h < gn; ++h) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sm_x + h * a.lrow + t);
+      const float* x = sm_x + h * a.lrow;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(x[e] - sm_m[h]) * sm_l[h];
+      for (int e = 0; e < 4; ++e)
+        w[e] += __builtin_amdgcn_exp2f(x[min(t + 64 * e, n - 1)] - sm_m[h]) * sm_l[h];
     }
     add_weights(a, row, hkv, t, n, w);
   }
@@ -654,7 +657,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   i /= chunks;
   const int hkv = i % a.Hkv, b = i / a.Hkv;
   const int n = min(max(a.lengths[b], 0), a.cap);
-  const int t0 = chunk * kWeightTokens, t = t0 + 4 * tid;
+  const int t0 = chunk * kWeightTokens, t = t0 + 256 * wave + lane;
   if (t0 >= n) return;
   const int valid = pieces_of(a, b, n, 0).count;
   // lanes per head for its maximum and sum over the splits
@@ -682,13 +685,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     }
     __syncthreads();
     if (t < n) {
-      const float* x = a.logits + head * a.lrow + t;  // rows are padded: four tokens are always there
+      const float* x = a.logits + head * a.lrow;
       constexpr int kUnroll = 4;
       for (int g = 0; g < gn; g += kUnroll) {
-        f32x4 v[kUnroll];
+        float v[kUnroll][4];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          v[u] = *reinterpret_cast<const f32x4*>(x + int64_t(min(g + u, gn - 1)) * a.lrow);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[u][e] = x[int64_t(min(g + u, gn - 1)) * a.lrow + min(t + 64 * e, n - 1)];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
           if (g + u < gn) {
