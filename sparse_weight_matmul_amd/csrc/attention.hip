@@ -1,5 +1,5 @@
-// Attention of one new token per sequence over a paged key-value cache, the
-// length split over workgroups and joined.
+// Attention of one new token per sequence over a paged key-value cache, long
+// sequences cut into pieces that a second launch joins.
 //
 //   x_t = scale * q . k_t ;  p_t = e^(x_t - m) / sum_u e^(x_u - m), m = max x
 //   o   = sum_t p_t v_t   ;  weight_t += sum over the query heads of a group p_t
@@ -8,7 +8,9 @@
 // pool, not masked).  Every key and value row is used once per group of query
 // heads, so the bound is the read of the live rows (4 D bytes per token and
 // key-value head); the arithmetic of up to 16 query heads fits beside it on
-// the matrix cores.
+// the matrix cores.  Measured: 2 x 131072 tokens, 64 heads on 8: 1.07 GB in 167
+// us, 6.4 TB/s; 16 ragged x 4096, 32 heads, weights added: 554 MB in 88 us (6.3
+// TB/s) where a part of the cache is in the last-level cache, 99 otherwise.
 //
 // One pass with a running maximum and sum.  A wave takes 32 tokens at a time
 // and keeps everything in registers: there is no LDS in the loop, no barrier
@@ -193,14 +195,16 @@ __device__ __forceinline__ float sum_groups(float v) {
   return a + b;
 }
 
-// Adds the weights of tokens t, t + 64, t + 128 and t + 192 (those below n) to
-// the accumulator: a wave's 64 lanes add to consecutive slots.  Atomic because
-// sequences may share a page.
-__device__ __forceinline__ void add_weights(const AttnArgs& a, const int32_t* row, int hkv, int t, int n,
-                                            const f32x4& w) {
-  Place p[4];
+// Tokens t, t + 64, t + 128 and t + 192: a wave's 64 lanes hold consecutive
+// slots, 64 a word.  Their places (of those from n on, the last one's), and the
+// adding of their weights to the accumulator, atomic because sequences may share
+// a page.
+__device__ __forceinline__ void four_places(const AttnArgs& a, const int32_t* row, int t, int n, Place (&p)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = place(a, row, min(t + 64 * e, n - 1));
+}
+__device__ __forceinline__ void add_weights(const AttnArgs& a, const Place (&p)[4], int hkv, int t, int n,
+                                            const f32x4& w) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (t + 64 * e < n && w[e] != 0.f && p[e].ok)
@@ -302,7 +306,7 @@ __device__ __forceinline__ int sorted_unit(const AttnArgs& a, int lane, int per_
   return s - rank * per_b;
 }
 
-// One workgroup: one split of one sequence, up to 16 query heads of one
+// One workgroup: a sequence or a piece of one, up to 16 query heads of one
 // key-value head.
 template <int DP, bool kFull, bool kSame8>
 __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(AttnArgs a) {
@@ -550,6 +554,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
   }
   __syncthreads();
   for (int t = 256 * wave + lane; t < n; t += 256 * kWaves) {
+    Place p[4];
+    four_places(a, row, t, n, p);
     f32x4 w = {0, 0, 0, 0};
     for (int h = 0; h < gn; ++h) {
       const float* x = sm_x + h * a.lrow;
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       for (int e = 0; e < 4; ++e)
         w[e] += __builtin_amdgcn_exp2f(x[min(t + 64 * e, n - 1)] - sm_m[h]) * sm_l[h];
     }
-    add_weights(a, row, hkv, t, n, w);
+    add_weights(a, p, hkv, t, n, w);
   }
 }
 
@@ -594,7 +600,7 @@ __device__ __forceinline__ float sum_over(float v, int width) {
   return v;
 }
 
-// After the splits: the first `joins` workgroups add up the splits of one
+// After the pieces: the first `joins` workgroups add up the pieces of one
 // query head each; the others add the attention weights of kWeightTokens
 // tokens of a sequence and key-value head to the accumulator.  Both are chains
 // of a few memory latencies, so every loop requests several rounds before it
@@ -623,7 +629,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     }
     l = sum_over(l, 64);
     __syncthreads();
-    // four dimensions a thread, the splits dealt over the threads left
+    // four dimensions a thread, the pieces dealt over the threads left
     const int per = a.D <= 64 ? 16 : a.D <= 128 ? 32 : 64;
     const int parts = kJoinThreads / per, part = tid / per, d = tid % per * 4;
     f32x4 acc = {0, 0, 0, 0};
@@ -659,14 +665,27 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   const int n = min(max(a.lengths[b], 0), a.cap);
   const int t0 = chunk * kWeightTokens, t = t0 + 256 * wave + lane;
   if (t0 >= n) return;
+  // requested before the maxima and sums, whose chain they would lengthen: the
+  // places and the scores of the first heads
+  Place at[4];
+  four_places(a, a.table + int64_t(b) * a.table_b, t, n, at);
+  constexpr int kUnroll = 4;
+  const float* x = a.logits + (int64_t(b) * a.Hq + hkv * a.G) * a.lrow;
+  auto scores = [&](int g, float (&v)[kUnroll][4]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = x[int64_t(min(g + u, a.G - 1)) * a.lrow + min(t + 64 * e, n - 1)];
+  };
+  float v[kUnroll][4];
+  scores(0, v);
   const int valid = pieces_of(a, b, n, 0).count;
-  // lanes per head for its maximum and sum over the splits
+  // lanes per head for its maximum and sum over the pieces
   int width = 1;
   while (width < valid && width < 64) width *= 2;
   f32x4 w = {0, 0, 0, 0};
   for (int g0 = 0; g0 < a.G; g0 += kStatHeads) {
     const int gn = min(a.G - g0, kStatHeads);
-    const int64_t head = int64_t(b) * a.Hq + hkv * a.G + g0;
     for (int g = tid / width; g < (gn + 63) / 64 * 64; g += kJoinThreads / width) {
       const Pieces p = pieces_of(a, b, n, hkv * a.G + g0 + min(g, gn - 1));
       const float* ml = a.ml + p.at * 2;
@@ -684,27 +703,19 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
       }
     }
     __syncthreads();
-    if (t < n) {
-      const float* x = a.logits + head * a.lrow;
-      constexpr int kUnroll = 4;
-      for (int g = 0; g < gn; g += kUnroll) {
-        float v[kUnroll][4];
+    for (int g = 0; g < gn; g += kUnroll) {
+      if (g0 + g > 0) scores(g0 + g, v);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < kUnroll; ++u)
+        if (g + u < gn) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[u][e] = x[int64_t(min(g + u, gn - 1)) * a.lrow + min(t + 64 * e, n - 1)];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if (g + u < gn) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
-          }
-      }
+          for (int e = 0; e < 4; ++e)
+            w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
+        }
     }
     __syncthreads();
   }
-  add_weights(a, a.table + int64_t(b) * a.table_b, hkv, t, n, w);
+  add_weights(a, at, hkv, t, n, w);
 }
 
 template <int DP, bool kFull>
@@ -723,21 +734,32 @@ hipError_t launch_dim(const AttnArgs& a, bool same8, dim3 grid, size_t lds, hipS
 
 }  // namespace
 
-// The split of the length.  A workgroup's four waves take 128 tokens (a step)
-// at a time, at about 1.1 us; a second launch to join the splits costs 5 us
-// (kernel and gap).  So the length is split only where one workgroup per
-// sequence and group of heads leaves half of the CUs idle and takes more than
-// eight steps: into as many splits as make one workgroup per CU, of two steps
-// or more.  Rounded down: a CU with one workgroup more than the others ends
-// last (17 sequences of 43648 tokens, one head: 60 us at 255 workgroups, 73 at
-// 272, 60 at 510).  Rows of 64 and less need up to four workgroups per CU to
-// keep the memory busy, and get them where eight steps or more are left to each
-// (7 ragged sequences of up to 103992, 2 heads of 64: 47 us with one, 19 with
-// four); longer rows gain nothing by it (2 x 131072, 8 heads of 128: 166 with
-// one, 169 with two).  Measured, us, at 1 split / this rule: 1 x 4096 tokens,
-// 32 heads 51 / 16; 1 x 8192, 8 heads 89 / 12; 1 x 1000, 32 heads 13 / 13;
-// 2 x 131072, 8 heads 1567 / 166; a batch that fills the CUs loses 15-30% to
-// any split.
+// How the work is dealt.  A unit, up to 16 query heads of one key-value head of
+// one sequence, is one workgroup, or several pieces along the length: four waves
+// take 128 tokens (a step) at a time, at about 1.1 us, and a second launch that
+// joins the pieces costs 5 us.  The lengths are in device memory, so the host
+// decides by the capacity alone whether there are pieces and how many at most,
+// and the kernel sizes them by the lengths.  Measured, us:
+//  - Up to half as many units as CUs, more than eight steps: as many pieces as
+//    CUs, of two steps or more (1 x 4096 tokens, 32 heads 51 whole / 17; 2 x
+//    131072, 8 heads 1567 / 167; 1 x 1000, 32 heads 13 / 13).  Pieces of one
+//    size for all sequences, not so many per sequence: 24 ragged sequences of up
+//    to 19030, 2 heads of 256 98 / 71, 11 of up to 19823, 4 heads 52 / 37, for
+//    0.7 us of planning (1 x 4096 16.4 / 17.1).  One workgroup per CU: a CU with
+//    one more than the others ends last (17 x 43648, one head: 60 at 255
+//    workgroups, 73 at 272).  Rows of 64 and less need up to four to keep the
+//    memory busy and get them where eight steps or more are left to each (7
+//    ragged x 103992, 2 heads: 47 with one, 17 with four).
+//  - Up to as many units as CUs, 32 steps or more: two pieces per CU (three with
+//    rows above 128, of which a CU holds one workgroup at a time), for batches
+//    of unlike lengths (20 ragged x 4096, 8 heads 53 whole / 40; 32 x 8192 126 /
+//    115; of one length 94 / 103; 12 ragged x 8000, 12 heads of 256 214 / 104).
+//    Below 32 steps the join costs as much as it saves.
+//  - More units than CUs: whole sequences, dealt by their length (16 ragged x
+//    4096, 32 heads 101 in the batch's order / 82; 64 ragged x 2000, 8 heads 51
+//    / 44; cut into pieces no faster), unless they are too short for the sorting
+//    in every workgroup to pay (64 x 300 of 32 heads: 32 unsorted / 37; 64 x
+//    1000 101 / 94).
 //
 // The weights: one workgroup that sees a whole sequence keeps its scores in
 // LDS and adds the weights itself, as long as three such workgroups fit on a
