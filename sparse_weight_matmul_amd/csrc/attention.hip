@@ -68,7 +68,7 @@ struct AttnArgs {
   const int32_t *table, *lengths;
   const uint8_t* mask;
   float* weights;
-  int32_t* plan;  // tokens of a split, then the first split of each sequence
+  int32_t* plan;  // tokens of a piece, then the first piece of each sequence
   float* ml;      // [piece][query head of it][2] maximum (in units of log2) and sum
   float* part;    // [piece][query head of it][D] unnormalised outputs
   float* logits;  // [B][Hq][lrow] scores in units of log2
@@ -78,7 +78,7 @@ struct AttnArgs {
   int32_t B, Hq, Hkv, G, D, S, pages, cap, per_seq;
   int32_t room;  // pieces of all sequences at most; 0: every sequence is one
   int32_t lrow, order, cus;
-  int32_t own_weights;  // the only split adds the weights itself, its scores in LDS
+  int32_t own_weights;  // a whole sequence's workgroup adds the weights itself, its scores in LDS
   float scale;  // softmax scale * log2(e)
   PageDiv div;    // by S
   PageDiv per_b;  // by the units of a sequence: key-value heads x groups of 16 query heads
@@ -325,15 +325,15 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       if (2 * lane < a.B) a.plan[1 + 2 * lane] = p.first0;
       if (2 * lane + 1 < a.B) a.plan[2 + 2 * lane] = p.first1;
     }
-    const int split = page_index(a.per_b, piece);  // of the batch's
-    y = piece - split * per_b;
-    const uint64_t in = __builtin_amdgcn_ballot_w64(split >= p.first0 && split < p.last1);
+    const int cut = page_index(a.per_b, piece);  // the batch's cut-th piece of a row of units
+    y = piece - cut * per_b;
+    const uint64_t in = __builtin_amdgcn_ballot_w64(cut >= p.first0 && cut < p.last1);
     if (in == 0) return;  // more workgroups than pieces
     const int l = __builtin_ctzll(in);
-    const bool odd = split >= __builtin_amdgcn_readlane(p.first1, l);
+    const bool odd = cut >= __builtin_amdgcn_readlane(p.first1, l);
     b = 2 * l + odd;
     n = __builtin_amdgcn_readlane(odd ? p.n1 : p.n0, l);
-    begin = (split - __builtin_amdgcn_readlane(odd ? p.first1 : p.first0, l)) * p.len;
+    begin = (cut - __builtin_amdgcn_readlane(odd ? p.first1 : p.first0, l)) * p.len;
     end = n - begin < p.len ? n : begin + p.len;
   } else {
     const int unit = a.order ? sorted_unit(a, lane, per_b, &b) : piece;
