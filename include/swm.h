@@ -6,7 +6,9 @@
  * activations, in the decode regime (N = 1..16 tokens, bandwidth bound), with
  * optional skipping of input channels whose activation is zero, and in the
  * prefill regime (N in the hundreds to thousands, matrix-core bound).  A dense
- * GEMM of the same shapes is exported beside it as the honest baseline.
+ * GEMM of the same shapes is exported beside it as the honest baseline, and the
+ * operators of a decode step around these products (attention over a paged
+ * cache, its eviction, log probabilities) under "serving".
  *
  * Sources of the operations (the pages this library is built from):
  *  - "Unified Static-Dynamic Pruning for Efficient LLM Inference" (SPDP),
