@@ -27,7 +27,7 @@
 // other vector instructions close behind: 4096 x 32000 fp16 45 us in the
 // kernel, 262 MB at 5.8 TB/s.  With few rows the chain of one load, two
 // reductions and the choice of the top tokens: 1 x 32000 fp16 with 5 of them
-// 11 us, 61 x 50021 fp32 with 20 14.6 us, none 9 us.
+// 7.8 us in the kernel (4.7 with none), 61 x 50021 fp32 with 20 10.9 (7.6).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -188,6 +188,25 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   if (rest < a.V) take<1>(p, &xt);
   const float own = p.m;  // the largest logit of this thread
 
+  // A thread without logits has the key 0, below that of -inf.
+  constexpr int kGroups = kThreads < kMaxGroups ? kThreads : kMaxGroups;
+  __shared__ alignas(16) uint32_t group[kTop ? kGroups : 1];  // maxima of kThreads / kGroups threads
+  __shared__ uint32_t bound, count, passed;
+  const bool has = tid < vecs || head || tail;
+  const uint32_t mine = has ? key_of(own) : 0u;
+  if constexpr (kTop) {
+    constexpr int kPer = kThreads / kGroups;
+    uint32_t g = mine;
+    if (kPer > 1) g = max(g, rotate_row<1>(g));  // 2 or 8 consecutive lanes of a row: maxima of the last kPer
+    if (kPer > 2) g = max(g, rotate_row<2>(g));
+    if (kPer > 4) g = max(g, rotate_row<4>(g));
+    if (tid % kPer == kPer - 1) group[tid / kPer] = g;
+    if (tid == 0) {
+      count = passed = 0;
+      bound = 0xffffffffu;
+    }
+  }
+
   // Maximum first, then every part moves to it once and the sums are added.
   rebase(p, wave_max(p.m));
   p.l = wave_sum(p.l);
@@ -216,34 +235,24 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     if (a.entropy) a.entropy[n] = none ? 0.f : (log2l - p.s / p.l) * kLn2;
   }
   if constexpr (kTop) {
-  constexpr int kGroups = kThreads < kMaxGroups ? kThreads : kMaxGroups;
   constexpr int kList = kThreads < 256 ? 512 : 1024;  // candidates ranked by counting
-  __shared__ uint32_t group[kGroups];
   __shared__ uint64_t list[kList];
   __shared__ uint16_t who[kThreads];  // threads whose maximum reaches the bound
-  __shared__ uint32_t bound, count, passed;
   const int k = min(a.top, a.V);
-  // a thread without logits has the key 0, below that of -inf
-  const bool has = tid < vecs || head || tail;
-  const uint32_t mine = has ? key_of(own) : 0u;
-  constexpr int kPer = kThreads / kGroups;
-  uint32_t g = mine;
-  if (kPer > 1) g = max(g, rotate_row<1>(g));  // 4 or 8 consecutive lanes of a row: maxima of the last kPer
-  if (kPer > 2) g = max(g, rotate_row<2>(g));
-  if (kPer > 4) g = max(g, rotate_row<4>(g));
-  if (tid % kPer == kPer - 1) group[tid / kPer] = g;
-  if (tid == 0) count = passed = 0;
-  __syncthreads();
+  if (kWaves == 1) __syncthreads();
+  // The k-th largest of the groups' maxima is the least of those that fewer than
+  // k exceed.
   if (tid < kGroups) {
     const uint32_t v = group[tid];
-    int rank = 0;
+    int above = 0;
 #pragma unroll 8
     for (int j = 0; j < kGroups; j += 4) {
       const u32x4 o = *reinterpret_cast<const u32x4*>(&group[j]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) rank += o[e] > v || (o[e] == v && j + e < tid);
+      for (int e = 0; e < 4; ++e) above += o[e] > v;
     }
-    if (rank == k - 1) bound = v;
+    const uint32_t least = wave_min(above < k ? v : 0xffffffffu);
+    if (lane == 0) atomicMin(&bound, least);
   }
   __syncthreads();
   const uint32_t low = bound;
@@ -359,12 +368,12 @@ hipError_t launch(const LogprobArgs& a, int64_t N, hipStream_t s) {
 // Threads of a row: more where the rows do not fill the chip, and no more than
 // the row has work for.  Rows whose vectors fit in the registers of their
 // threads (8 a thread; 16 of 1024 threads) stay there.  Measured, us:
-//   below one row per CU    255 x 50021 fp32, 20 top tokens: 1024 threads 17,
-//                           256 threads 22; 1 x 128000 fp16, 20: 18 and 24
-//   from one row per CU on  300 x 50021 fp32, 20: 256 threads 24, 1024 30, 64
-//                           78; 1500 x 32000 fp16: 20, 28, 24
+//   below one row per CU    255 x 50021 fp32, 20 top tokens: 1024 threads 14,
+//                           256 threads 19; 1 x 128000 fp16, 20: 15 and 21
+//   from one row per CU on  300 x 50021 fp32, 20: 256 threads 20, 1024 23, 64
+//                           76; 1500 x 32000 fp16: 20, 28, 25
 //   from eight, no top      4096 x 32000 fp16: 64 threads 42, 256 44, 1024 67
-//   tokens                  (with 20 of fp32: 64 threads 173, 256 118: a wave
+//   tokens                  (with 20 of fp32: 64 threads 171, 256 117: a wave
 //                           alone looks at its candidates in many rounds)
 template <typename T>
 hipError_t launch_rows(const LogprobArgs& a, int64_t N, int num_cus, hipStream_t s) {

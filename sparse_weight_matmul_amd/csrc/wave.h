@@ -44,6 +44,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
   return wave_reduce(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
 __device__ __forceinline__ int wave_max(int v) {
   return int(wave_reduce(uint32_t(v), [](uint32_t a, uint32_t b) { return uint32_t(max(int(a), int(b))); }));
 }
