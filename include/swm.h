@@ -474,14 +474,14 @@ swm_status swm_hbm_stream(const void* buf, size_t bytes, int32_t unroll, int32_t
  *  bias: DEVICE fp16, M entries, or NULL.  act: SWM_ACT_*.  residual: DEVICE
  *  fp16 token-major N x M (ldr >= M), or NULL; it may be Y itself (same
  *  address and ldr == ldy: an update in place), and must not overlap it
- *  otherwise.  The other arguments and the errors are swm_spmm_ws's; with no
- *  bias, no residual and SWM_ACT_NONE the result is the same bits.  At 33 to
- *  1023 tokens it chooses, by what they take for these sizes, between slices
+ *  otherwise.  The other arguments and the errors are swm_spmm_ws's, and with
+ *  no bias, no residual and SWM_ACT_NONE so are the bits of the result, but at
+ *  33 to 1023 tokens: there it chooses, by what they take for these sizes, between slices
  *  of 32 tokens through the decode kernels, W expanded into the workspace and
  *  swm_spmm's on-chip kernel, whose K it may split over workgroups (fp32 sums
  *  in the workspace, joined in order by a second launch); the fp32 sums are
- *  the same but for their order.  There a workspace that is not there or too
- *  small only takes routes off the choice.
+ *  the same but for their order.  A workspace that is not there or too small
+ *  only takes routes off that choice.
  *  SWM_ERR_INVALID_ARG also: an unknown act, ldr < M, residual == Y with
  *  ldr != ldy. */
 swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, void* Y, int64_t ldy, int64_t N,

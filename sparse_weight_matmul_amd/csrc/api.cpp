@@ -569,9 +569,10 @@ size_t swm_spmm_workspace_bytes(const swm_format* f, int64_t N) {
 // in us, with Mi = M K / 2^20:
 //   slices     0.95 Mi each, or 7 + 0.5 Mi where that is more
 //   expanded   0.55 Mi + 11 + 0.62 per step, by the dense kernel's block shape
-//   on chip    5 + 1.28 per step and round of blocks over the CUs
-//   split      that by the steps of one split, 5 for the second launch, and
-//              8 bytes per sum at 4 TB/s
+//   on chip    8 + 1.28 per step and round of blocks over the CUs
+//   split      10 + 1.28 per step of one split, and 8 bytes per sum at 4 TB/s
+// and, where the product's own workgroups do it, what the epilogue adds (a
+// split's second launch spreads it over all CUs)
 // (4096x4096 at N = 33 / 96 / 192: slices 22 / 46 / 93, expanded 54 / 55 / 56,
 // on chip 86, split 28 / 28 / 30; 4096x11008 at 64 / 192 / 512: 64 / 195 / -,
 // 134 / 142 / 143, 208 / 210 / 210, 42 / 44 / 73; 11008x4096 at 48 / 96 / 512:
@@ -583,12 +584,22 @@ struct MidPlan {
   size_t bytes = 0;  // of workspace
 };
 
-static MidPlan mid_plan(const swm::Header& h, int64_t N, int64_t cus, size_t workspace) {
+// An epilogue on chip, measured at 896 x 72 and 885 x 72, 174 tokens: 10.4 with a
+// bias alone, 11.2 with a residual, 14.8 with GELU; 14.2 where Y's rows are not
+// aligned for 16 bytes, 17.0 where the residual's are not either (split: 14).
+constexpr double kMostEpilogue = 4.5 + 0.8 + 4.0 + 2.0;
+static double epilogue_cost(const swm::Epilogue& e, const void* Y, int64_t ldy) {
+  auto rows16 = [](const void* p, int64_t ld) { return ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  return (e.act == SWM_ACT_GELU ? 4.5 : e.act == SWM_ACT_SILU ? 2.0 : 0.0) +
+         (e.residual ? 0.8 + (rows16(e.residual, e.ldr) ? 0.0 : 2.0) : 0.0) + (rows16(Y, ldy) ? 0.0 : 4.0);
+}
+
+static MidPlan mid_plan(const swm::Header& h, int64_t N, int64_t cus, size_t workspace, double epilogue) {
   const double mi = double(h.m) * double(h.k) / 1048576.0;
   const int64_t steps = (h.k + 63) / 64, tiles = (h.m + 127) / 128 * ((N + 255) / 256);
   auto rounds = [&](int64_t blocks) { return double((blocks + cus - 1) / cus); };
   MidPlan best;
-  double least = 5.0 + 1.28 * double(steps) * rounds(tiles);
+  double least = 8.0 + 1.28 * double(steps) * rounds(tiles) + epilogue;
   auto offer = [&](MidRoute r, int splits, size_t bytes, double cost) {
     if (bytes > workspace || cost >= least) return;
     least = cost;
@@ -601,7 +612,7 @@ static MidPlan mid_plan(const swm::Header& h, int64_t N, int64_t cus, size_t wor
   const double shape = std::min({rounds(m256 * ((N + 255) / 256)), 0.73 * rounds(m256 * n128),
                                  0.54 * rounds((h.m + 127) / 128 * n128)});
   offer(MidRoute::kExpand, 1, align_up(size_t(h.m) * size_t(h.k) * 2, 256),
-        0.55 * mi + 11.0 + 0.62 * double(steps) * shape / 0.54);
+        0.55 * mi + 11.0 + 0.62 * double(steps) * shape / 0.54 + epilogue);
   for (int s = 2; s <= 16 && s <= steps; ++s)
     offer(MidRoute::kOnChip, s, swm::prefill_split_bytes(h, N, s),
           10.0 + 1.28 * double((steps + s - 1) / s) * rounds(tiles * s) +
@@ -658,13 +669,13 @@ swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, vo
   e.act = act;
   e.on = bias || residual || act != SWM_ACT_NONE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (e.on && X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X) &&
+  if (X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X) &&
       swm::prefill_sparse_fits(f->h, N, ldx)) {
     if (ldx < f->h.k || ldy < f->h.m || ldy <= 0 || !on_current_device(f)) return SWM_ERR_INVALID_ARG;
     if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15)) return SWM_ERR_ALIGN;
     int dev = 0;
     SWM_HIP(hipGetDevice(&dev));
-    const MidPlan p = mid_plan(f->h, N, num_cus(dev), workspace ? ws_bytes : 0);
+    const MidPlan p = mid_plan(f->h, N, num_cus(dev), workspace ? ws_bytes : 0, epilogue_cost(e, Y, ldy));
     if (p.route == MidRoute::kSlices) return run_products(f, X, ldx, Y, ldy, N, false, s, e, true);
     if (p.route == MidRoute::kOnChip) {
       swm_log("spmm_epilogue M=%lld K=%lld N=%lld: on-chip prefill, %d splits of K", (long long)f->h.m,
@@ -682,7 +693,11 @@ size_t swm_spmm_epilogue_workspace_bytes(const swm_format* f, int64_t N) {
   const size_t need = swm_spmm_workspace_bytes(f, N);
   int dev = 0;
   if (!f || !mid_tokens(f, N) || hipGetDevice(&dev) != hipSuccess) return need;
-  return std::max(need, mid_plan(f->h, N, num_cus(dev), ~size_t(0)).bytes);
+  // the epilogue decides between the better of the routes that it adds to and
+  // the better of the others
+  const int cus = num_cus(dev);
+  return std::max({need, mid_plan(f->h, N, cus, ~size_t(0), 0.0).bytes,
+                   mid_plan(f->h, N, cus, ~size_t(0), kMostEpilogue).bytes});
 }
 
 static swm_status run_colruns(const swm_format* f, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t n,

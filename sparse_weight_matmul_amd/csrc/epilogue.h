@@ -70,6 +70,7 @@ typedef float epi_f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t epi_u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t epi_u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) epi_u32x2 epi_lds_u32x2;
+typedef __attribute__((address_space(3))) uint16_t epi_lds_u16;
 
 // Four consecutive halves from p[at]; those from p[end] on read p[end - 1].
 __device__ __forceinline__ epi_u32x2 halves4(const uint16_t* p, int at, int end, bool aligned8) {
@@ -112,22 +113,39 @@ __device__ __forceinline__ epi_u32x2 fuse4(const epi_f32x16& acc, int q, const e
 // Outputs into the wave's LDS region, a row of `stride` bytes per token, from
 // where the kernel stores them.  The residual comes in by the same way: whole
 // rows, 16 bytes a lane, and every lane finds the values of its outputs in
-// their places; read directly, a load would take 8 bytes from 32 rows.  The
-// barriers keep the scheduler from starting every output at once, which would
+// their places; read directly, a load would take 8 bytes from 32 rows.  Rows
+// that are not aligned for 16 bytes come in by halves, consecutive ones of a row
+// in consecutive lanes (with eight loads of a half a lane 885 x 72 at 174 tokens
+// took 20.6 us, 17.0 so).  The barriers keep the scheduler from starting every output at once, which would
 // spill the accumulators.
 template <int kI, int kJ>
 __device__ __forceinline__ void fuse_to_lds(const Epilogue& e, const epi_f32x16 (&acc)[kI][kJ], uint32_t reg,
                                             int stride, int m0, int n0, int M, int N, int lane) {
   constexpr int kTM = 32 * kI, kTN = 32 * kJ, kLPR = kTM / 8, kRPI = 64 / kLPR;
+  constexpr int kU = kTN / kRPI < 4 ? kTN / kRPI : 4;  // rounds of rows at a time
+  static_assert(kTN % (kU * kRPI) == 0, "");
   epi_u32x2 bias[kI][4];
   load_bias(e, m0, M, lane, bias);
   if (e.residual) {
     const int gm = m0 + (lane % kLPR) * 8;
-    const bool vec = e.ldr % 8 == 0 && aligned(e.residual, 16) && gm + 8 <= M;
-    for (int r = 0; r < kTN; r += 4 * kRPI) {
-      epi_u32x4 v[4];
+    const bool rows = e.ldr % 8 == 0 && aligned(e.residual, 16), vec = gm + 8 <= M;
+    for (int i0 = 0; !rows && i0 < kTM * kTN / 64; i0 += 8) {
+      uint16_t v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
+        const int at = (i0 + u) * 64 + lane;
+        v[u] = e.residual[int64_t(min(n0 + at / kTM, N - 1)) * e.ldr + min(m0 + at % kTM, M - 1)];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = (i0 + u) * 64 + lane;
+        *reinterpret_cast<epi_lds_u16*>(static_cast<uintptr_t>(reg + at / kTM * stride + at % kTM * 2)) = v[u];
+      }
+    }
+    for (int r = 0; rows && r < kTN; r += kU * kRPI) {
+      epi_u32x4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
         const uint16_t* src = e.residual + int64_t(min(n0 + r + u * kRPI + lane / kLPR, N - 1)) * e.ldr;
         if (vec) {
           v[u] = *reinterpret_cast<const epi_u32x4*>(src + gm);
@@ -137,7 +155,7 @@ __device__ __forceinline__ void fuse_to_lds(const Epilogue& e, const epi_f32x16 
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kU; ++u) {
         const uint32_t at = reg + (r + u * kRPI + lane / kLPR) * stride + (lane % kLPR) * 16;  // a multiple of 8
         *reinterpret_cast<epi_lds_u32x2*>(static_cast<uintptr_t>(at)) = epi_u32x2{v[u][0], v[u][1]};
         *reinterpret_cast<epi_lds_u32x2*>(static_cast<uintptr_t>(at + 8)) = epi_u32x2{v[u][2], v[u][3]};
@@ -163,6 +181,46 @@ __device__ __forceinline__ void fuse_to_lds(const Epilogue& e, const epi_f32x16 
         __builtin_amdgcn_sched_barrier(0);
       }
   });
+}
+
+// Outputs through the wave's LDS region to Y, 16 bytes of a token's row a lane.
+// Straight from the accumulators a store would take 8 bytes, or 2 where rows are
+// not aligned, of 32 rows (2001 x 480 at 300 tokens, residual and SiLU OLDUS us so,
+// NEWUS this way).
+template <int kI, int kJ>
+__device__ __forceinline__ void fuse_and_store_rows(const Epilogue& e, const epi_f32x16 (&acc)[kI][kJ], uint32_t reg,
+                                                    int m0, int n0, int M, int N, uint16_t* Y, int64_t ldy,
+                                                    int lane) {
+  constexpr int kTM = 32 * kI, kTN = 32 * kJ, kLPR = kTM / 8, kRPI = 64 / kLPR, kStride = 2 * kTM + 8;
+  fuse_to_lds(e, acc, reg, kStride, m0, n0, M, N, lane);
+  if (ldy % 8 != 0 || !aligned(Y, 16)) {  // by halves, as above
+#pragma unroll 8
+    for (int i = 0; i < kTM * kTN / 64; ++i) {
+      const int at = i * 64 + lane, n = n0 + at / kTM, m = m0 + at % kTM;
+      const uint16_t v = *reinterpret_cast<const epi_lds_u16*>(static_cast<uintptr_t>(reg + at / kTM * kStride + at % kTM * 2));
+      if (n < N && m < M) Y[int64_t(n) * ldy + m] = v;
+    }
+    return;
+  }
+  const int gm = m0 + (lane % kLPR) * 8;
+  const bool vec = gm + 8 <= M;
+#pragma unroll 4
+  for (int r = 0; r < kTN; r += kRPI) {
+    const int nl = r + lane / kLPR, n = n0 + nl;
+    const uint32_t at = reg + nl * kStride + (lane % kLPR) * 16;
+    const epi_u32x2 lo = *reinterpret_cast<const epi_lds_u32x2*>(static_cast<uintptr_t>(at));
+    const epi_u32x2 hi = *reinterpret_cast<const epi_lds_u32x2*>(static_cast<uintptr_t>(at + 8));
+    const epi_u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+    if (n >= N) continue;
+    uint16_t* dst = Y + int64_t(n) * ldy + gm;
+    if (vec) {
+      *reinterpret_cast<epi_u32x4*>(dst) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (gm + k < M) dst[k] = uint16_t(v[k / 2] >> (16 * (k % 2)));
+    }
+  }
 }
 
 // Outputs straight to Y, four rows of a token at a time.

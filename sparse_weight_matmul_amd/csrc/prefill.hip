@@ -491,10 +491,12 @@ __global__ __launch_bounds__(64 * kWM * kWN) void dense_dma_kernel(typename Pref
   // output rows per wave quadrant: 32 kWI, or half as many gated channels
   constexpr int kTM = kGlu ? 16 * kWI : 32 * kWI, kTN = 32 * kWJ, kRS = 2 * kTM + 8;
   const uint32_t reg = base + wave * (kTN * kRS);
-  if constexpr (kEpi == kFused)
-    fuse_to_lds(a.epi, acc, reg, kRS, m0 + wm * kTM, n0 + wn * kTN, a.M, a.N, lane);
+  if constexpr (kEpi == kFused) {
+    fuse_and_store_rows(a.epi, acc, reg, m0 + wm * kTM, n0 + wn * kTN, a.M, a.N, a.Y, a.ldy, lane);
+    return;
+  }
 #pragma unroll
-  for (int i = 0; i < (kEpi == kFused ? 0 : kWI); ++i)
+  for (int i = 0; i < kWI; ++i)
 #pragma unroll
     for (int j = 0; j < kWJ; ++j)
 #pragma unroll
@@ -762,7 +764,8 @@ __global__ __launch_bounds__(512, 1) void prefill_ws_kernel(typename PrefillArgs
 
     // Epilogue: fp16 round-to-nearest-even, 4 consecutive rows per 8-byte store.
     if constexpr (kEpi == kFused) {
-      fuse_and_store(a.epi, acc, m0, n0 + c * 64, a.M, a.N, a.Y, a.ldy, lane);
+      // both operands' stages are free: 64 tokens x 264 bytes a wave
+      fuse_and_store_rows(a.epi, acc, sA + c * (64 * 264), m0, n0 + c * 64, a.M, a.N, a.Y, a.ldy, lane);
       return;
     }
     if constexpr (kEpi == kPartial) {
@@ -842,7 +845,8 @@ __global__ __launch_bounds__(256) void split_finish_kernel(PrefillFusedArgs a, c
       for (int v = 0; v < 16; ++v) acc[0][0][v] += w[u][v / 4][v % 4];
     }
   }
-  fuse_and_store<1, 1>(a.epi, acc, tm * 128 + i * 32, g * 32, a.M, a.N, a.Y, a.ldy, lane);
+  __shared__ __attribute__((aligned(16))) uint8_t rows[4][32 * 72];
+  fuse_and_store_rows<1, 1>(a.epi, acc, lds_addr(rows[i]), tm * 128 + i * 32, g * 32, a.M, a.N, a.Y, a.ldy, lane);
 }
 
 PrefillArgs make_args(int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, uint16_t* Y,

@@ -68,6 +68,7 @@ SHAPES = [
     (1001, 2056, 130), (391, 3440, 60), (130, 8200, 513), (17, 1096, 1023), (2049, 1928, 300),  # K split
     (300, 520, 257), (260, 136, 1027),                                               # expanded, 128 x 128 blocks
     (4096, 256, 2048), (4099, 128, 3000), (8192, 64, 4096),                          # larger blocks
+    (707, 480, 304), (885, 72, 174), (4096, 4096, 73), (132, 2048, 1000),            # rows not aligned for 8 or 16 bytes
     (8203, 64, 2050), (4200, 72, 4100),                                              # and a launch for the last rows
 ]
 
@@ -85,7 +86,9 @@ def test_routes(gpu_lib, M, K, N):
             swm.spmm_epilogue(f, Xd, bd if bias else None, act, Rd if res else None, ws, Y)
             check(Y, W, X, b if bias else None, act, R if res else None)
     a = swm.spmm_epilogue(f, Xd, workspace=ws)
-    assert torch.equal(a, swm.spmm_ws(f, Xd, ws))
+    check(a, W, X, None, "none", None)
+    if not 32 < N < 1024:
+        assert torch.equal(a, swm.spmm_ws(f, Xd, ws))
     check(swm.spmm_epilogue(f, Xd, bd, "silu", Rd), W, X, b, "silu", R)  # a workspace of its own
     if 32 < N < 256:  # one that is too small takes the expansion off the choice
         small = torch.empty(16, dtype=torch.uint8, device="cuda")
@@ -95,6 +98,24 @@ def test_routes(gpu_lib, M, K, N):
     inplace = Rd.clone()  # the residual stream updated in place
     swm.spmm_epilogue(f, Xd, bd, "gelu", inplace, ws, inplace)
     assert torch.equal(c, inplace)
+
+
+@gpu
+@pytest.mark.parametrize("M,K,N", [(512, 64, 60), (512, 512, 512), (1000, 264, 400), (512, 72, 1500)])
+@pytest.mark.parametrize("aligned", ["residual", "output", "neither"])
+def test_rows_of_unlike_alignment(gpu_lib, M, K, N, aligned):
+    import torch
+    W, X, b, R = case(M, K, N)
+    f = swm.sparse_compress(W)
+    res = torch.zeros((N, M + 24), dtype=torch.float16, device="cuda")
+    at = 0 if aligned == "residual" else 3
+    res = res[:, at:at + M]
+    res.copy_(t(R))
+    out = torch.full((N, M + 24), 7.0, dtype=torch.float16, device="cuda")
+    at = 8 if aligned == "output" else 5
+    swm.spmm_epilogue(f, t(X), t(b), "silu", res, None, out[:, at:at + M])
+    check(out[:, at:at + M], W, X, b, "silu", R)
+    assert bool((out[:, :at] == 7).all()) and bool((out[:, at + M:] == 7).all())
 
 
 @gpu
