@@ -275,35 +275,49 @@ __global__ __launch_bounds__(kThreads) void evict_long_kernel(EvictArgs a) {
   }
 }
 
+// Set lanes of b before this one.
+__device__ __forceinline__ uint32_t lanes_before(uint64_t b) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), 0u));
+}
+
 // Copies rows of one head.  Each lane names one pair of slots (from < 0: none);
-// their places are looked up together, then the wave copies pair by pair, lanes
-// 0..31 the key row and 32..63 the value row, kRows in flight (past the last
-// pair, that one is read again).  A pair with a slot on no page is left out.
+// their places are looked up together and gathered into the first lanes (a pair
+// with a slot on no page is left out).  Then lanes 0..31 copy key rows and 32..63
+// value rows, as many pairs at a time as their rows fill lanes, eight such loads
+// in flight (past the last pair, that one is read again): a CU's rate is what it
+// has in flight (one pair a load: 32 x 2048 to 512, 32 heads of 64 79 us, 67 so; 8
+// ragged x 4096 to 1024 of 128 49, 47).
 __device__ __forceinline__ void move_rows(const EvictArgs& a, const int32_t* row, int h, int from, int to) {
-  const int lane = threadIdx.x & 63, half = lane >> 5, d = (lane & 31) * 8;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int shift = a.D <= 64 ? 3 : a.D <= 128 ? 4 : 5;  // of the lanes of a row
+  const int per = 32 >> shift, sub = (lane & 31) >> shift, d = (lane & ((1 << shift) - 1)) * 8;
   uint16_t* base = half ? a.v + int64_t(h) * a.v_h : a.k + int64_t(h) * a.k_h;
   const int64_t sp = half ? a.v_p : a.k_p, ss = half ? a.v_s : a.k_s;
   const Place p0 = place(a, row, max(from, 0)), p1 = place(a, row, to);
-  uint64_t todo = __builtin_amdgcn_ballot_w64(from >= 0 && p0.ok && p1.ok);
+  const bool on = from >= 0 && p0.ok && p1.ok;
+  const uint64_t pairs = __builtin_amdgcn_ballot_w64(on);
+  const int n = __popcll(pairs), rank = int(lanes_before(pairs));
+  const int lane4 = 4 * (on ? rank : n + lane - rank);
+  const int from_page = __builtin_amdgcn_ds_permute(lane4, p0.page);
+  const int from_slot = __builtin_amdgcn_ds_permute(lane4, p0.slot);
+  const int to_page = __builtin_amdgcn_ds_permute(lane4, p1.page);
+  const int to_slot = __builtin_amdgcn_ds_permute(lane4, p1.slot);
   const int dl = d < a.D ? d : 0;  // lanes past the row read its start and store nothing
   constexpr int kRows = 8;
-  while (todo) {
+  for (int i0 = 0; i0 < n; i0 += kRows * per) {
     u32x4 x[kRows];
-    int l[kRows];
-    bool on[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      on[u] = todo != 0;
-      l[u] = on[u] ? __builtin_ctzll(todo) : l[u ? u - 1 : 0];
-      todo &= todo - 1;
-      x[u] = *reinterpret_cast<const u32x4*>(base + int64_t(__builtin_amdgcn_readlane(p0.page, l[u])) * sp +
-                                             int64_t(__builtin_amdgcn_readlane(p0.slot, l[u])) * ss + dl);
+      const int i = min(i0 + u * per + sub, n - 1);
+      x[u] = *reinterpret_cast<const u32x4*>(base + int64_t(__shfl(from_page, i)) * sp +
+                                             int64_t(__shfl(from_slot, i)) * ss + dl);
     }
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
-      if (on[u] && d < a.D)
-        *reinterpret_cast<u32x4*>(base + int64_t(__builtin_amdgcn_readlane(p1.page, l[u])) * sp +
-                                  int64_t(__builtin_amdgcn_readlane(p1.slot, l[u])) * ss + d) = x[u];
+    for (int u = 0; u < kRows; ++u) {
+      const int i = i0 + u * per + sub, j = min(i, n - 1);
+      const int page = __shfl(to_page, j), slot = __shfl(to_slot, j);
+      if (i < n && d < a.D) *reinterpret_cast<u32x4*>(base + int64_t(page) * sp + int64_t(slot) * ss + d) = x[u];
+    }
   }
 }
 
@@ -328,11 +342,6 @@ __device__ __forceinline__ void count_bins(uint32_t* hist, uint32_t bin, bool ac
     atomicAdd(&hist[bin_at(first)], uint32_t(__popcll(same)));
   else if (active && bin != first)
     atomicAdd(&hist[bin_at(bin)], 1u);
-}
-
-// Set lanes of b before this one.
-__device__ __forceinline__ uint32_t lanes_before(uint64_t b) {
-  return __builtin_amdgcn_mbcnt_hi(uint32_t(b >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(b), 0u));
 }
 
 // Weights, positions and places of the four tokens from t on (clamped to last).
