@@ -672,10 +672,11 @@ swm_status swm_spmm_epilogue(const swm_format* f, const void* X, int64_t ldx, vo
   if (X && Y && mid_tokens(f, N) && swm::prefill_supported(f->h.k, ldx, X) &&
       swm::prefill_sparse_fits(f->h, N, ldx)) {
     if (ldx < f->h.k || ldy < f->h.m || ldy <= 0 || !on_current_device(f)) return SWM_ERR_INVALID_ARG;
-    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15)) return SWM_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15) return SWM_ERR_ALIGN;
+    if (!workspace && ws_bytes > 0) return SWM_ERR_INVALID_ARG;
     int dev = 0;
     SWM_HIP(hipGetDevice(&dev));
-    const MidPlan p = mid_plan(f->h, N, num_cus(dev), workspace ? ws_bytes : 0, epilogue_cost(e, Y, ldy));
+    const MidPlan p = mid_plan(f->h, N, num_cus(dev), ws_bytes, epilogue_cost(e, Y, ldy));
     if (p.route == MidRoute::kSlices) return run_products(f, X, ldx, Y, ldy, N, false, s, e, true);
     if (p.route == MidRoute::kOnChip) {
       swm_log("spmm_epilogue M=%lld K=%lld N=%lld: on-chip prefill, %d splits of K", (long long)f->h.m,

@@ -259,6 +259,13 @@ def test_refusals(gpu_lib):
     assert lib.swm_spmm_epilogue(f._h, p, 64, y, 64, 4, None, 0, y, 65, None, 0, s) == 1
     assert lib.swm_spmm_epilogue(f._h, p, 63, y, 64, 4, None, 1, q, 64, None, 0, s) == 1
     assert lib.swm_spmm_epilogue(f._h, p, 64, y, 64, 0, None, 1, q, 64, None, 0, s) == 1
+    long = torch.zeros((40, 64), dtype=torch.float16, device="cuda")
+    out = torch.zeros_like(long)
+    p, y = long.data_ptr(), out.data_ptr()
+    assert lib.swm_spmm_epilogue(f._h, p, 64, y, 64, 40, None, 1, None, 0, None, 4096, s) == 1
+    assert lib.swm_spmm_epilogue(f._h, p, 64, y, 64, 40, None, 1, None, 0, q + 2, 4096, s) == 3
+    assert lib.swm_spmm_epilogue(f._h, p, 63, y, 64, 40, None, 1, None, 0, None, 0, s) == 1
+    assert lib.swm_spmm_epilogue(f._h, p, 64, y, 63, 40, None, 1, None, 0, None, 0, s) == 1
 
 
 def test_null_handle():
