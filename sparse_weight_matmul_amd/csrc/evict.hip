@@ -90,25 +90,20 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Entry of a per-slot array.  kNear: every offset inside the arrays is below
-// 2^30, so one 32-bit multiply-add does; selecting is bound by instructions.
-template <bool kNear, typename T>
+// Entry of a per-slot array.
+template <typename T>
 __device__ __forceinline__ T* entry(T* base, int64_t head, int64_t page, int h, const Place& p) {
-  T* at = base + int64_t(h) * head;
-  return kNear ? at + uint32_t(p.page * int32_t(page) + p.slot) : at + (int64_t(p.page) * page + p.slot);
+  return base + int64_t(h) * head + (int64_t(p.page) * page + p.slot);
 }
-template <bool kNear = false>
 __device__ __forceinline__ float weight_at(const EvictArgs& a, int h, const Place& p) {
-  return *entry<kNear>(a.w, a.w_h, a.w_p, h, p);
+  return *entry(a.w, a.w_h, a.w_p, h, p);
 }
-template <bool kNear = false>
 __device__ __forceinline__ int32_t position_at(const EvictArgs& a, int h, const Place& p) {
-  return *entry<kNear>(a.pos, a.p_h, a.p_p, h, p);
+  return *entry(a.pos, a.p_h, a.p_p, h, p);
 }
-template <bool kNear = false>
 __device__ __forceinline__ void put(const EvictArgs& a, int h, const Place& p, float w, int32_t pos) {
-  *entry<kNear>(a.w_out, a.wo_h, a.wo_p, h, p) = w;
-  *entry<kNear>(a.pos_out, a.po_h, a.po_p, h, p) = pos;
+  *entry(a.w_out, a.wo_h, a.wo_p, h, p) = w;
+  *entry(a.pos_out, a.po_h, a.po_p, h, p) = pos;
 }
 
 // Weight and position of the token in slot `from` become those of slot `to`.
@@ -347,15 +342,14 @@ __device__ __forceinline__ void count_bins(uint32_t* hist, uint32_t bin, bool ac
 // Weights, positions and places of the four tokens from t on (clamped to last).
 // vec: a page holds a multiple of four slots and both arrays are aligned for
 // 16-byte loads, so one place and two loads do.
-template <bool kNear>
 __device__ __forceinline__ void load4(const EvictArgs& a, const int32_t* row, int h, int t, int last, Place (&at)[4],
                                       float (&w)[4], int32_t (&pos)[4]) {
   if (a.vec) {
     at[0] = place(a, row, min(t, last & ~3));
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-    const f32x4 wv = *reinterpret_cast<const f32x4*>(entry<kNear>(a.w, a.w_h, a.w_p, h, at[0]));
-    const i32x4 pv = *reinterpret_cast<const i32x4*>(entry<kNear>(a.pos, a.p_h, a.p_p, h, at[0]));
+    const f32x4 wv = *reinterpret_cast<const f32x4*>(entry(a.w, a.w_h, a.w_p, h, at[0]));
+    const i32x4 pv = *reinterpret_cast<const i32x4*>(entry(a.pos, a.p_h, a.p_p, h, at[0]));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       at[e] = Place{at[0].page, at[0].slot + e, at[0].ok};
@@ -367,15 +361,15 @@ __device__ __forceinline__ void load4(const EvictArgs& a, const int32_t* row, in
     for (int e = 0; e < 4; ++e) at[e] = place(a, row, min(t + e, last));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[e] = weight_at<kNear>(a, h, at[e]);
-      pos[e] = position_at<kNear>(a, h, at[e]);
+      w[e] = weight_at(a, h, at[e]);
+      pos[e] = position_at(a, h, at[e]);
     }
   }
 }
 
 // Thread i holds tokens 4 (q kThreads + i) .. + 3 for q < kQ: a chunk of 256
 // tokens per wave and q, in order.  move: also copy the rows.
-template <int kThreads, int kQ, bool kNear>
+template <int kThreads, int kQ>
 __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictArgs a, int move) {
   constexpr int kWaves = kThreads / 64, kChunks = kWaves * kQ;
   constexpr bool kHold = kQ <= 2;  // weights and positions stay in registers for the end
@@ -411,7 +405,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       if (4 * q * kThreads >= n) continue;  // the same for every thread, here and below
-      load4<kNear>(a, row, h, 4 * (q * kThreads + tid), n - 1, at[q], w[q], pos[q]);
+      load4(a, row, h, 4 * (q * kThreads + tid), n - 1, at[q], w[q], pos[q]);
     }
     int newest = -2147483647 - 1;
 #pragma unroll
@@ -625,7 +619,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
     Place at[4];
     float w4[4];
     int32_t p4[4];
-    if (!kHold) load4<kNear>(a, row, h, t0, n - 1, at, w4, p4);
+    if (!kHold) load4(a, row, h, t0, n - 1, at, w4, p4);
     uint32_t r = number[q] >> 16;
     int to[4];
 #pragma unroll
@@ -640,7 +634,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
       if (to[e] < 0) continue;
       if (t0 + e >= a.budget) kept[to[e]] = t0 + e;
       if (at[e].ok && ((there >> (4 * q + e)) & 1))
-        put<kNear>(a, h, at[e], kHold ? w[q][e] : w4[e], kHold ? pos[q][e] : p4[e]);
+        put(a, h, at[e], kHold ? w[q][e] : w4[e], kHold ? pos[q][e] : p4[e]);
     }
   }
   if (move) {
@@ -666,23 +660,16 @@ __global__ __launch_bounds__(256) void evict_move_kernel(EvictArgs a) {
   move_rows(a, row, h, from >= a.budget ? from : -1, j0 + lane);
 }
 
-template <int kThreads, int kQ, bool kNear>
-hipError_t launch_near(const EvictArgs& a, int move, hipStream_t s) {
+template <int kThreads, int kQ>
+hipError_t launch_one(const EvictArgs& a, int move, hipStream_t s) {
   const size_t lds = 4 * size_t(a.list_len);
   if (lds > 56 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<kThreads, kQ, kNear>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<kThreads, kQ>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }
-  evict_kernel<kThreads, kQ, kNear><<<dim3(a.Hkv, a.B), kThreads, lds, s>>>(a, move);
+  evict_kernel<kThreads, kQ><<<dim3(a.Hkv, a.B), kThreads, lds, s>>>(a, move);
   return hipGetLastError();
-}
-
-template <int kThreads, int kQ>
-hipError_t launch_one(const EvictArgs& a, int move, hipStream_t s) {
-  const int64_t far = std::max({a.w_p, a.p_p, a.wo_p, a.po_p});
-  const bool near = far < (int64_t(1) << 30) && a.pages * far + a.S < (int64_t(1) << 30);
-  return near ? launch_near<kThreads, kQ, true>(a, move, s) : launch_near<kThreads, kQ, false>(a, move, s);
 }
 
 }  // namespace
@@ -732,6 +719,11 @@ hipError_t launch_evict(const KvView& c, const EvictCall& r, int num_cus, hipStr
   // us against 47 with a launch of its own; 16 x 8, 2176 to 2048: 19 against 24;
   // 32 x 32, 2048 to 512: 8 less than with one).
   const bool move = int64_t(a.Hkv) * a.B >= num_cus || a.list_len <= 512;
+  // The fewest threads that hold all keys, eight each at most up to 8192 tokens:
+  // 16 x 32 heads, 2000 tokens by 512 x 4 keys 21 us, by 1024 x 8 31; 8 x 32,
+  // 8000 tokens by 1024 x 8 32, by 1024 x 16 41.  Above 32768 tokens the keys
+  // would not fit; reading them again takes 70-180% longer (4 x 8, 30000: 95
+  // and 181).
   hipError_t e;
   if (a.cap <= 1024) {
     e = launch_one<256, 1>(a, move, s);
