@@ -77,7 +77,7 @@ struct AttnArgs {
   int64_t table_b, mask_b, w_p, w_h;
   int32_t B, Hq, Hkv, G, D, S, pages, cap, per_seq;
   int32_t room;  // pieces of all sequences at most; 0: every sequence is one
-  int32_t lrow, order, cus;
+  int32_t lrow, order, cus, adds;
   int32_t own_weights;  // a whole sequence's workgroup adds the weights itself, its scores in LDS
   float scale;  // softmax scale * log2(e)
   PageDiv div;    // by S
@@ -587,7 +587,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int b, int n, int
 }
 
 constexpr int kJoinThreads = 256;
-constexpr int kWeightTokens = 4 * kJoinThreads;  // tokens whose weights one workgroup adds
+constexpr int kWeightTokens = 4 * kJoinThreads;  // tokens whose weights one workgroup adds at a time
 constexpr int kMaxPieces = 1024;  // of a batch, so of a sequence
 constexpr int kStatHeads = 128;  // heads whose maxima and sums a workgroup holds at a time
 
@@ -602,8 +602,8 @@ __device__ __forceinline__ float sum_over(float v, int width) {
 }
 
 // After the pieces: the first `joins` workgroups add up the pieces of one
-// query head each; the others add the attention weights of kWeightTokens
-// tokens of a sequence and key-value head to the accumulator.  Both are chains
+// query head each; the others, a.adds to a sequence and key-value head, add the
+// attention weights of kWeightTokens tokens at a time to the accumulator.  Both are chains
 // of a few memory latencies, so every loop requests several rounds before it
 // uses one.
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int joins) {
@@ -658,18 +658,19 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
     }
     return;
   }
-  const int chunks = (a.cap + kWeightTokens - 1) / kWeightTokens;
   int i = blockIdx.x - joins;
-  const int chunk = i % chunks;
-  i /= chunks;
+  const int chunk = i % a.adds;
+  i /= a.adds;
   const int hkv = i % a.Hkv, b = i / a.Hkv;
   const int n = min(max(a.lengths[b], 0), a.cap);
-  const int t0 = chunk * kWeightTokens, t = t0 + 256 * wave + lane;
+  const int64_t t0 = int64_t(chunk) * kWeightTokens, next_t = int64_t(a.adds) * kWeightTokens;
   if (t0 >= n) return;
   // requested before the maxima and sums, whose chain they would lengthen: the
-  // places and the scores of the first heads
+  // places and the scores of the first tokens and heads
+  const int32_t* row = a.table + int64_t(b) * a.table_b;
   Place at[4];
-  four_places(a, a.table + int64_t(b) * a.table_b, t, n, at);
+  int t = int(t0) + 256 * wave + lane;
+  four_places(a, row, t, n, at);
   constexpr int kUnroll = 4;
   const float* x = a.logits + (int64_t(b) * a.Hq + hkv * a.G) * a.lrow;
   auto scores = [&](int g, float (&v)[kUnroll][4]) {
@@ -684,7 +685,6 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
   // lanes per head for its maximum and sum over the pieces
   int width = 1;
   while (width < valid && width < 64) width *= 2;
-  f32x4 w = {0, 0, 0, 0};
   for (int g0 = 0; g0 < a.G; g0 += kStatHeads) {
     const int gn = min(a.G - g0, kStatHeads);
     for (int g = tid / width; g < (gn + 63) / 64 * 64; g += kJoinThreads / width) {
@@ -704,19 +704,27 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
       }
     }
     __syncthreads();
-    for (int g = 0; g < gn; g += kUnroll) {
-      if (g0 + g > 0) scores(g0 + g, v);
+    for (int64_t c = t0; c < n; c += next_t) {
+      if (c != t0 || g0 > 0) {
+        t = int(c) + 256 * wave + lane;
+        four_places(a, row, t, n, at);
+        scores(g0, v);
+      }
+      f32x4 w = {0, 0, 0, 0};
+      for (int g = 0; g < gn; g += kUnroll) {
+        if (g > 0) scores(g0 + g, v);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        if (g + u < gn) {
+        for (int u = 0; u < kUnroll; ++u)
+          if (g + u < gn) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
-        }
+            for (int e = 0; e < 4; ++e)
+              w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
+          }
+      }
+      add_weights(a, at, hkv, t, n, w);
     }
     __syncthreads();
   }
-  add_weights(a, at, hkv, t, n, w);
 }
 
 template <int DP, bool kFull>
@@ -794,6 +802,12 @@ AttnPlan plan_attention(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t c
   const size_t rows = size_t(B) * size_t(Hq);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const bool scores = weights && !p.own_weights;
+  // workgroups of a sequence and head that add the weights: one per 1024 tokens
+  // of the capacity, but eight per CU in all; the lengths may be far below it
+  // (16 ragged x 4096, 32 heads, tables for 131072 tokens: 155 us with one per
+  // 1024, 110 so)
+  p.adds = int(std::max<int64_t>(1, std::min<int64_t>((cap + kWeightTokens - 1) / kWeightTokens,
+                                                      8 * int64_t(num_cus) / (B * Hkv))));
   const int64_t pieces = p.room > 0 ? p.room * (units / B) : units;
   const size_t sums = size_t(pieces) * size_t(std::min<int64_t>(G, kHeads));
   p.grid = pieces;
@@ -869,7 +883,8 @@ hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& 
                              : launch_dim<256>(a, same8, grid, lds, s);
   if (e != hipSuccess || !second) return e;
   const int64_t joins = p.room > 0 ? int64_t(a.B) * a.Hq : 0;
-  const int64_t adds = scores ? int64_t(a.B) * a.Hkv * ((a.cap + kWeightTokens - 1) / kWeightTokens) : 0;
+  a.adds = p.adds;
+  const int64_t adds = scores ? int64_t(a.B) * a.Hkv * p.adds : 0;
   if (joins + adds == 0) return hipSuccess;
   attn_join_kernel<<<dim3(uint32_t(joins + adds)), kJoinThreads, 0, s>>>(a, int(joins));
   return hipGetLastError();

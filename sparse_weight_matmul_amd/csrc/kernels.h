@@ -165,6 +165,7 @@ struct AttnPlan {
   int room = 0;              // pieces of all sequences at most; 0: every sequence is one
   int64_t grid = 0;          // workgroups of the first launch
   int lrow = 0;              // scores per row
+  int adds = 1;              // workgroups that add a sequence and head's weights in the second launch
   bool order = false;        // units sorted by their length,
   int cus = 256;             // a round of this many at a time
   bool own_weights = false;  // the weights are added by the first launch

@@ -96,7 +96,7 @@ swm_status swm_paged_attention(const swm_kv_cache* c, const void* q, int64_t q_b
   st = plan_for(c, q_heads, weights != nullptr, &p);
   if (st != SWM_OK) return st;
   // either launch: at most 2^24 - 1 workgroups of 256 threads
-  if (c->batch * q_heads + c->batch * c->heads * (cap / 1024 + 1) >= (int64_t(1) << 24) ||
+  if (c->batch * q_heads + c->batch * c->heads * p.adds >= (int64_t(1) << 24) ||
       p.grid >= (int64_t(1) << 24))
     return SWM_ERR_UNSUPPORTED;
   if (p.bytes > 0) {
