@@ -98,6 +98,8 @@ CASES = [
     (1, 2, 8, 128, [40000], 9000, 500, "long", "token"),     # more tokens than the keys that fit on chip
     (1, 1, 8, 256, [33000], 32990, 500, "ties", "token"),
     (1, 1, 8, 100, [20000], 150, 20, "equal", "token"),
+    (4, 2, 8, 64, [33000, 1025, 32768, 300], 1000, 200, "long", "token"),   # short sequences in a table for long ones
+    (3, 1, 8, 64, [40000, 32700, 21000], 16500, 100, "close", "head"),
     (2, 2, 64, 16, [2000, 1900], 1100, 10, "close", "token"),
     (1, 2, 64, 16, [8192], 8191, 0, "close", "head"),
     (1, 2, 8, 32, [32768], 16384, 300, "long", "token"),
