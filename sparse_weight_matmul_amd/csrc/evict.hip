@@ -523,7 +523,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
     for (int q = 0; q < kQ; ++q) {
       uint32_t c = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4 && 4 * q * kThreads < n; ++e)
         c += __popcll(__builtin_amdgcn_ballot_w64(4 * (q * kThreads + tid) + e < n && key[q][e] == prefix));
       if (lane == 0) chunk[q * kWaves + wave] = c;
     }
@@ -533,6 +533,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
     taken = 0;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
+      if (4 * q * kThreads >= n) continue;
       const int i = q * kWaves + wave;
       uint32_t rank = i < 64 ? __shfl(u0 - c0, i) : __shfl(u1, i - 64);
       bool equal[4];
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
   for (int q = 0; q < kQ; ++q) {
     uint32_t movers = 0, holes = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4 && 4 * q * kThreads < n; ++e) {
       const int t = 4 * (q * kThreads + tid) + e;
       const uint32_t x = key[q][e] >> shift;
       const bool on = t < n && (x > prefix || (x == prefix && ((taken >> (4 * q + e)) & 1)));
@@ -581,6 +582,8 @@ __global__ __launch_bounds__(kThreads, kThreads / 256) void evict_kernel(EvictAr
   uint32_t number[kQ];  // of the thread's first mover and free slot of the group
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
+    number[q] = 0;
+    if (4 * q * kThreads >= n) continue;
     const int i = q * kWaves + wave;
     uint32_t r = uint32_t(i < 64 ? __builtin_amdgcn_readlane(int(u0 - c0), i) : __builtin_amdgcn_readlane(int(u1 - c1), i - 64));
 #pragma unroll
