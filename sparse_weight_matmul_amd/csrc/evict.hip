@@ -32,8 +32,8 @@
 // Bound: by its bytes (8 per token and head, and the moved rows) a call takes
 // a few us at most; what it takes is the chain of some ten barriers and four
 // memory latencies inside a workgroup.  Measured, in the kernel: 1 x 1025 to
-// 1024, 32 heads 9.8 us; 16 x 2176 to 2048, 8 heads 15.4 us; 8 ragged
-// sequences of up to 4096 to 1024, 32 heads 29.0 us, of them 17 for 51 MB of
+// 1024, 32 heads 9.9 us; 16 x 2176 to 2048, 8 heads 15.2 us; 8 ragged
+// sequences of up to 4096 to 1024, 32 heads 28.4 us, of them 16 for 51 MB of
 // rows, read and written.
 #include <hip/hip_runtime.h>
 
