@@ -20,7 +20,9 @@
 // an equal one at a lower index.  Rows with so many equal logits that the list
 // overflows (a constant row) take the larger ones first and then the equal
 // ones in index order, and stop at k; if even the larger ones overflow, k
-// rounds of a maximum over the row.
+// rounds of a maximum over the row.  NaN stand before all numbers in this order,
+// in the threads' maxima as among the candidates: were a bound taken without
+// them, a row of NaN would have no logit at its bound.
 //
 // Bound: with many rows the read of the logits (2 or 4 bytes each), the
 // exponentials (one per logit, at a quarter of the vector rate) and the five
@@ -193,8 +195,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
   __shared__ alignas(16) uint32_t group[kTop ? kGroups : 1];  // maxima of kThreads / kGroups threads
   __shared__ uint32_t bound, count, passed;
   const bool has = tid < vecs || head || tail;
-  const uint32_t mine = has ? key_of(own) : 0u;
+  uint32_t mine = has ? key_of(own) : 0u;
   if constexpr (kTop) {
+    // The maximum leaves NaN out, the candidates' order puts them first: a thread
+    // whose sum tells of a NaN (or +inf) looks at its logits by that order.
+    if (p.l != p.l) {
+      mine = max(head ? key_of(xh) : 0u, tail ? key_of(xt) : 0u);
+      for (int i = tid; i < vecs; i += kThreads) {
+        float f[kVec];
+        Row<T>::unpack(xv[i], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) mine = max(mine, key_of(f[e]));
+      }
+    }
     constexpr int kPer = kThreads / kGroups;
     uint32_t g = mine;
     if (kPer > 1) g = max(g, rotate_row<1>(g));  // 2 or 8 consecutive lanes of a row: maxima of the last kPer
@@ -301,8 +314,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
     if (low != 0xffffffffu) collect(low + 1);
     found = int(count);
     if (found <= kList - 64) {
-      // the lowest indices with the bound's own key fill up the k
-      for (int j = tid; found < k; j += kThreads) {
+      // the lowest indices with the bound's own key fill up the k; the row's end
+      // is a second limit, so that the loop ends whatever the row holds
+      for (int j0 = 0; found < k && j0 < a.V; j0 += kThreads) {
+        const int j = j0 + tid;
         __syncthreads();
         const bool on = j < a.V && key_of(float(x[j])) == low;
         const uint64_t b = __builtin_amdgcn_ballot_w64(on);

@@ -136,6 +136,38 @@ def test_infinities_and_nan(gpu_lib):
 
 
 @gpu
+@pytest.mark.parametrize("N,V,top", [(5, 3, 1), (5, 7, 20), (5, 300, 5), (5, 900, 64), (5, 1500, 1), (5, 50021, 20),
+                                     (5, 131072, 64), (300, 517, 3), (300, 9000, 20)])
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_rows_of_nan(gpu_lib, N, V, top, dtype):
+    """Rows of nothing but NaN, of a few numbers among NaN, half and one: NaN throughout, the top tokens in the
+    order NaN first, then by size, equal ones by the lower index."""
+    import torch
+    x = rows("plain", N, V, dtype)
+    r = np.random.default_rng(V)
+    x[0::5] = np.nan
+    some = x[1::5]
+    some[:, r.permutation(V)[min(3, V // 2):]] = np.nan
+    half = x[2::5]
+    half[r.random(half.shape) < 0.5] = np.nan
+    half[:, 0] = np.nan
+    x[3::5] = -np.inf
+    x[3::5, V // 2] = np.nan
+    t = np.where(np.arange(N) % 2, V - 1, 0)
+    logp, ent, ids, lps = swm.token_logprobs(torch.from_numpy(x).cuda(), torch.from_numpy(t).cuda(), top=top)
+    k = min(top, V)
+    key = np.where(np.isnan(x), np.inf, x).astype(np.float64)  # no +inf among them
+    assert np.array_equal(ids.cpu().numpy()[:, :k], np.argsort(-key, axis=-1, kind="stable")[:, :k])
+    bad = np.isnan(x).any(-1)
+    assert bad[np.arange(N) % 5 < 4].all() and not bad[4::5].any()
+    for got in (logp, ent, lps[:, :k]):
+        assert np.isnan(got.cpu().numpy()[bad]).all()
+    lp, h, _ = reference(x[4::5], k)
+    close(logp.cpu().numpy()[4::5], lp[np.arange(len(lp)), t[4::5]], 16.0)
+    close(ent.cpu().numpy()[4::5], h, 1 + np.log(V) + h)
+
+
+@gpu
 def test_graph_and_stream(gpu_lib):
     import torch
     X, T = torch.from_numpy(rows("plain", 9, 3333, np.float16)).cuda(), torch.arange(9, device="cuda")
