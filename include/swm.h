@@ -605,8 +605,8 @@ swm_status swm_kv_evict(const swm_kv_cache* cache, const float* weights, int64_t
  *  logits: DEVICE, fp16 (fp32 == 0) or fp32 (fp32 != 0), N rows of V, leading
  *  dimension ld >= V.  A logit of -inf rules its token out (log p = -inf); a
  *  row with nothing but -inf has log probabilities of -inf and entropy 0; a
- *  row with a NaN or +inf gives NaN (log p of its logits below +inf may be
- *  -inf instead), and its top_ids take NaN before all numbers.
+ *  row with a NaN or +inf gives NaN, and its top_ids take NaN before all
+ *  numbers.  Finite logits may have any size.
  *  targets: DEVICE int32 (wide == 0) or int64 (wide != 0), one per row, or
  *  NULL (then logp is not written and may be NULL).  A negative target means
  *  "none": log p = 0.  A target >= V gives NaN.

@@ -168,6 +168,41 @@ def test_rows_of_nan(gpu_lib, N, V, top, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("N,V,top", [(8, 300, 5), (8, 5001, 20), (8, 50021, 0), (8, 140000, 64), (2100, 700, 0),
+                                     (300, 3001, 3)])
+@pytest.mark.parametrize("dtype,fill", [(np.float16, x) for x in (-1e4, -65504.0, 6e4)] + [
+    (np.float32, x) for x in (-1e4, -1.6777e7, -1.6778e7, -1e9, -1e10, -1e12, -1e20, -1e30, -1e37, -2.4e38,
+                              float(np.finfo(np.float32).min), 1.6777e7, 1.6778e7, 1e10, 3e38)])
+def test_finite_masks(gpu_lib, fill, N, V, top, dtype):
+    """Tokens ruled out by a large finite number: single ones, ranges, all but one token, all of a row; and single
+    logits as large the other way.  The definition gives finite numbers wherever they fit 32 bits."""
+    import torch
+    x = rows("plain", N, V, dtype)
+    r = np.random.default_rng(V)
+    part = x[0::8]
+    part[r.random(part.shape) < 0.5] = fill
+    x[1::8, :V // 3] = fill           # whole vectors, threads and waves of them, first
+    x[2::8, V // 2:] = fill           # and last: a padded vocabulary
+    x[3::8] = fill                    # the whole row
+    x[4::8, 1:] = fill                # all but one
+    x[5::8, V // 2] = -fill           # one token that takes all
+    x[6::8] = fill
+    x[6::8, ::7] = fill / 2           # two sizes of them
+    t = np.where(np.arange(N) % 2, V - 1, 0)
+    logp, ent, ids, lps = swm.token_logprobs(torch.from_numpy(x).cuda(), torch.from_numpy(t).cuda(), top=top)
+    lp, h, want_ids = reference(x, top)
+    lp = np.where(np.abs(lp) > np.finfo(np.float32).max, -np.inf, lp)
+    want = lp[np.arange(N), t]
+    close(logp.cpu().numpy(), want, np.maximum(1, np.abs(want)))
+    spread = 1 + np.log(V) + np.where(np.isfinite(lp), np.exp(lp) * np.abs(np.where(np.isfinite(lp), lp, 0)), 0).sum(-1)
+    close(ent.cpu().numpy(), h, spread)
+    if top:
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        want = np.take_along_axis(lp, want_ids, -1)
+        close(lps.cpu().numpy(), want, np.maximum(1, np.abs(want)))
+
+
+@gpu
 def test_graph_and_stream(gpu_lib):
     import torch
     X, T = torch.from_numpy(rows("plain", 9, 3333, np.float16)).cuda(), torch.arange(9, device="cuda")
