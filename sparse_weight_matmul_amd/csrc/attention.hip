@@ -31,8 +31,13 @@
 // The weights e^(x - m) go into the second product as two fp16 parts (value
 // and remainder): one part alone would put its rounding (2^-12 relative) on
 // every weight, which is as large as the output's own rounding; the matrix
-// cores are idle anyway.  Scores, maxima, sums and outputs are fp32, and the
-// output is rounded once.
+// cores are idle anyway.  They go in times 2^15, the most that fits: the parts
+// of a weight are then off by 2^-23 of it down to weights of 2^-17, by 2^-40
+// below.  Without the factor that would be 2^-25, and a hundred thousand tokens
+// some 17 nats below one of value zero (an attention sink) would lose their
+// share of the output while the sum counts it.  The sum adds a tile's weights up
+// before it takes them, for the same reason.  Scores, maxima, sums and outputs
+// are fp32, and the output is rounded once.
 //
 // Values of tokens that are not live are replaced by zeros before the second
 // product (their weight is zero, but a stale row may hold an infinity or a
@@ -59,6 +64,7 @@ constexpr int kTile = 32;   // tokens a wave takes at a time
 constexpr int kWaves = 4;   // waves of a workgroup; they take tiles in turn
 constexpr int kMaxSorted = 128;  // sequences whose lengths a wave holds, two a lane
 constexpr int kHeads = 16;  // query heads of a workgroup (columns of the matrix instruction)
+constexpr float kUp = 32768.f;  // of the weights in the second product
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -452,13 +458,15 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       m = mx;
     }
     half8 hi, lo;
+    float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = __builtin_amdgcn_exp2f(x[e] - base);
-      l += p;
-      hi[e] = _Float16(p);
-      lo[e] = _Float16(p - float(hi[e]));
+      sum += p;
+      hi[e] = _Float16(p * kUp);
+      lo[e] = _Float16(p * kUp - float(hi[e]));
     }
+    l += sum;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -520,6 +528,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       sum += r * sm_l[w * kHeads + h];
       acc += r * *reinterpret_cast<const f32x4*>(&sm_o[(w * gn + h) * kRow + d]);
     }
+    acc *= 1.f / kUp;
     const int64_t at = int64_t(piece) * min(a.G, kHeads) + h;
     if (d == 0 && a.ml) {
       a.ml[at * 2] = mm;

@@ -162,6 +162,40 @@ def test_against_64_bits(gpu_lib, B, Hq, Hkv, D, S, lengths, layout, masked):
 
 
 @gpu
+@pytest.mark.parametrize("B,Hq,Hkv,D,lengths", [
+    (2, 4, 2, 64, [1000, 517]),           # whole sequences
+    (130, 1, 1, 128, [1500] * 130),       # longer ones
+    (1, 2, 1, 128, [131072]),             # cut into pieces
+    (5, 6, 3, 256, [4000, 9000, 1, 2, 40]),
+])
+@pytest.mark.parametrize("gap", [4, 8, 12, 16, 18])
+def test_one_token_far_above_the_others(gpu_lib, B, Hq, Hkv, D, lengths, gap):
+    """A token `gap` nats above all others whose value row is zero: the output is the others' small share."""
+    import torch
+    S = 16
+    q, k, v, table, dev = make(B, Hq, Hkv, D, S, lengths)
+    r = np.random.default_rng(gap)
+    q[:] = 0
+    q[:, :, 0] = 8
+    k[:, :, :, 0] = 0
+    v[:] = np.where(np.isnan(v), v, 1 + v / 8)
+    for b, n in enumerate(lengths):
+        t = 0 if b % 2 == 0 else int(r.integers(0, n))
+        k[table[b][t // S], t % S, :, 0] = gap / (8 * D ** -0.5)
+        v[table[b][t // S], t % S] = 0
+    cache = swm.PagedCache(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), dev["table"], dev["lengths"])
+    w = torch.zeros((k.shape[0], Hkv, S), device="cuda")
+    out = swm.paged_attention(cache, torch.from_numpy(q).cuda(), weights=w)
+    ref, tol, add, addtol = reference(q, k, v, table, lengths, D ** -0.5)
+    check(out, ref, tol)
+    got = w.double().cpu().numpy()
+    for b, n in enumerate(lengths):
+        t = np.arange(n)
+        at = got[table[b][t // S], :, t % S].T
+        assert np.all(np.abs(at - add[b, :, :n]) <= addtol[b, :, :n])
+
+
+@gpu
 def test_strided_operands_stream_and_scale(gpu_lib):
     import torch
     B, H, D, S = 3, 4, 128, 16
