@@ -135,6 +135,28 @@ def test_infinities_and_nan(gpu_lib):
     close(ent[3:].cpu().numpy(), h, 8.0)
 
 
+def closer(got, want, d):
+    """close, and a number wherever one is wanted."""
+    assert np.isfinite(got[np.isfinite(want)]).all()
+    close(got, want, d)
+
+
+@gpu
+@pytest.mark.parametrize("N,V,top,kind", CASES)
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_numbers_where_the_definition_has_them(gpu_lib, N, V, top, kind, dtype):
+    import torch
+    x = rows(kind, N, V, dtype)
+    t = np.random.default_rng(1).integers(0, V, N)
+    logp, ent, ids, lps = swm.token_logprobs(torch.from_numpy(x).cuda(), torch.from_numpy(t).cuda(), top=top)
+    lp, h, want_ids = reference(x, top)
+    got = [(logp, lp[np.arange(N), t]), (ent, h)]
+    if top:
+        got.append((lps[:, :min(top, V)], np.take_along_axis(lp, want_ids, -1)))
+    for a, b in got:
+        assert np.array_equal(np.isfinite(a.cpu().numpy()), np.isfinite(b))
+
+
 @gpu
 @pytest.mark.parametrize("N,V,top", [(5, 3, 1), (5, 7, 20), (5, 300, 5), (5, 900, 64), (5, 1500, 1), (5, 50021, 20),
                                      (5, 131072, 64), (300, 517, 3), (300, 9000, 20)])
@@ -163,8 +185,8 @@ def test_rows_of_nan(gpu_lib, N, V, top, dtype):
     for got in (logp, ent, lps[:, :k]):
         assert np.isnan(got.cpu().numpy()[bad]).all()
     lp, h, _ = reference(x[4::5], k)
-    close(logp.cpu().numpy()[4::5], lp[np.arange(len(lp)), t[4::5]], 16.0)
-    close(ent.cpu().numpy()[4::5], h, 1 + np.log(V) + h)
+    closer(logp.cpu().numpy()[4::5], lp[np.arange(len(lp)), t[4::5]], 16.0)
+    closer(ent.cpu().numpy()[4::5], h, 1 + np.log(V) + h)
 
 
 @gpu
@@ -193,13 +215,13 @@ def test_finite_masks(gpu_lib, fill, N, V, top, dtype):
     lp, h, want_ids = reference(x, top)
     lp = np.where(np.abs(lp) > np.finfo(np.float32).max, -np.inf, lp)
     want = lp[np.arange(N), t]
-    close(logp.cpu().numpy(), want, np.maximum(1, np.abs(want)))
+    closer(logp.cpu().numpy(), want, np.maximum(1, np.abs(want)))
     spread = 1 + np.log(V) + np.where(np.isfinite(lp), np.exp(lp) * np.abs(np.where(np.isfinite(lp), lp, 0)), 0).sum(-1)
-    close(ent.cpu().numpy(), h, spread)
+    closer(ent.cpu().numpy(), h, spread)
     if top:
         assert np.array_equal(ids.cpu().numpy(), want_ids)
         want = np.take_along_axis(lp, want_ids, -1)
-        close(lps.cpu().numpy(), want, np.maximum(1, np.abs(want)))
+        closer(lps.cpu().numpy(), want, np.maximum(1, np.abs(want)))
 
 
 @gpu
