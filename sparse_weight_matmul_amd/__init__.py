@@ -535,22 +535,34 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor, kept from reuse until `stream` is done with it where that is not the current stream."""
+def _on_stream(make, stream):
+    """What make() allocates, as memory of `stream`: a block that the current stream has given back may still be
+    in use there, and `stream` need not wait for it.  It is not used again before the current stream, which may
+    read it, is done with it either."""
     import torch
-    t = torch.empty(*shape, dtype=dtype, device=device)  # 0.4 us less than with the tuple
-    if stream is not None:
-        t.record_stream(stream)
+    current = torch.cuda.current_stream()
+    if stream == current:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
     return t
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of `stream` (None: the current one)."""
+    import torch
+    if stream is not None:
+        return _on_stream(lambda: torch.empty(shape, dtype=dtype, device=device), stream)
+    return torch.empty(*shape, dtype=dtype, device=device)  # 0.4 us less than with the tuple
 
 
 def _empty_like(t, stream):
     """As _empty, with the shape and type of a contiguous tensor."""
     import torch
-    t = torch.empty_like(t)
     if stream is not None:
-        t.record_stream(stream)
-    return t
+        return _on_stream(lambda: torch.empty_like(t), stream)
+    return torch.empty_like(t)
 
 
 def _rows(t, name, rows, cols):
