@@ -171,6 +171,8 @@ def _dev2d(t, name, rows=None, cols=None):
         raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
     if cols is not None and t.shape[1] != cols:
         raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"rows of {name} must not overlap")
     return ctypes.c_void_p(t.data_ptr()), max(int(t.stride(0)), int(t.shape[1]), 1)
 
 
@@ -575,6 +577,8 @@ def _rows(t, name, rows, cols):
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
+    if ld < cols and rows > 1:  # expanded ones among them: the library steps by a row at least
+        raise ValueError(f"rows of {name} must not overlap")
     return t.data_ptr(), max(ld, cols, 1) if rows > 1 else max(cols, 1)
 
 

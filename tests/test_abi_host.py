@@ -210,3 +210,23 @@ def test_colruns_encoder_rejects_bad_input():
     assert lib.swm_colruns_encode_blob(bad, len(tcb), None, 0, ctypes.byref(size)) == 6
     assert lib.swm_format_enable_skipping(None, None, None) == 1
     assert lib.swm_format_enable_smfmac(None, None, None) == 1
+
+
+def test_overlapping_rows_are_refused():
+    """A leading dimension below the row length, such as an expanded row's 0, names no memory of the tensor's own:
+    taken for the row length it would run past the end."""
+    import torch
+
+    class OnGpu(torch.Tensor):
+        is_cuda = property(lambda self: True)
+
+    row = torch.zeros(1, 64, dtype=torch.float16)
+    wide = torch.zeros(400, dtype=torch.float16)
+    for bad in (row.expand(4, 64), wide.as_strided((4, 64), (32, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            swm._rows(bad.as_subclass(OnGpu), "X", 4, 64)
+        with pytest.raises(ValueError, match="overlap"):
+            swm._dev2d(bad.as_subclass(OnGpu), "X")
+    for good, ld in ((row, 64), (wide.as_strided((4, 64), (80, 1)), 80), (wide.as_strided((4, 64), (64, 1)), 64)):
+        assert swm._rows(good.as_subclass(OnGpu), "X", good.shape[0], 64)[1] == ld
+        swm._dev2d(good.as_subclass(OnGpu), "X")
