@@ -548,8 +548,9 @@ typedef struct swm_kv_cache {
  *  ordered on one stream.
  *  Scores, maxima, sums and outputs are fp32; out is rounded once.
  *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
- *  heads, a scale that is not finite, negative strides, mask_ld below the
- *  capacity, a workspace too small.  SWM_ERR_ALIGN: q or the workspace.
+ *  heads, a scale that is not finite, negative strides, rows of out that share
+ *  memory (a stride below dim, or the same twice), mask_ld below the capacity, a
+ *  workspace too small.  SWM_ERR_ALIGN: q or the workspace.
  *  SWM_ERR_UNSUPPORTED: q_heads above 65535 or a grid beyond the device's.
  *  One or two launches, asynchronous on stream. */
 swm_status swm_paged_attention(const swm_kv_cache* cache, const void* q, int64_t q_batch, int64_t q_head,
@@ -581,16 +582,20 @@ size_t swm_paged_attention_workspace_bytes(const swm_kv_cache* cache, int64_t q_
  *  page * w_page + head * w_head + slot (p_*: positions).
  *  weights_out, positions_out: where the slots below the new length get their
  *  values, with strides of their own; the inputs themselves (same address and
- *  strides) or memory that does not overlap them.
+ *  strides) or memory that does not overlap them.  Every page and head has its
+ *  own entries there; in the inputs alone heads may share them (a stride of 0).
  *  lengths_out: DEVICE int32, one per sequence: min(length, budget); not the
  *  cache's own lengths.
  *  kept: DEVICE int32, batch x heads x budget, contiguous: the slot each slot's
  *  token came from, -1 from the new length on.
- *  No page may be shared by two sequences, or appear twice in one.  A token
+ *  No page may be shared by two sequences, or appear twice in one, and no row
+ *  of the pools by two heads.  A token
  *  whose table entry names no page has the lowest key and is not copied.
  *  budget >= 0, recent >= 0, both below 2^31.
  *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, lengths_out
- *  == lengths, an output at its input's address with other strides.  Cache
+ *  == lengths, an output at its input's address with other strides or with
+ *  strides below page_size (heads that share entries), page or head strides of
+ *  a pool below dim.  Cache
  *  errors as above.  No workspace; one or two launches, asynchronous on stream;
  *  whole numbers and copies, so bitwise reproducible. */
 swm_status swm_kv_evict(const swm_kv_cache* cache, const float* weights, int64_t w_page, int64_t w_head,

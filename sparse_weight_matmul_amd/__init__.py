@@ -718,7 +718,8 @@ def kv_evict(cache: PagedCache, weights, positions, budget: int, recent: int = 0
     accumulated attention weight stay, ties going to the lower slot; the ones
     that stay above the budget move into the slots freed below it.
     weights (fp32) and positions (int32): (pages, heads, page_size), one entry
-    per cached row, updated in place unless outputs are given.  Returns the
+    per cached row, updated in place unless outputs are given (what is written
+    must not be shared by heads or pages, as an expanded tensor is).  Returns the
     new lengths (B,) (the cache's own tensor is left alone: copy them into it)
     and kept (B, heads, budget), the slot each slot's token came from (-1
     where there is none).  No page may belong to two sequences."""

@@ -64,6 +64,11 @@ swm_status plan_for(const swm_kv_cache* c, int64_t q_heads, bool weights, swm::A
   return SWM_OK;
 }
 
+// Whether rows of `len` entries, n0 at one stride by n1 at another, surely share memory.
+bool rows_overlap(int64_t len, int64_t n0, int64_t stride0, int64_t n1, int64_t stride1) {
+  return (n0 > 1 && stride0 < len) || (n1 > 1 && stride1 < len) || (n0 > 1 && n1 > 1 && stride0 == stride1);
+}
+
 bool heads_fit(const swm_kv_cache* c, int64_t q_heads) {
   return q_heads >= 1 && q_heads % c->heads == 0;
 }
@@ -91,6 +96,7 @@ swm_status swm_paged_attention(const swm_kv_cache* c, const void* q, int64_t q_b
   const int64_t cap = c->pages_per_seq * c->page_size;
   if (!q || !out || q_batch < 0 || q_head < 0 || out_batch < 0 || out_head < 0) return SWM_ERR_INVALID_ARG;
   if ((mask && mask_ld < cap) || (weights && (w_page < 0 || w_head < 0))) return SWM_ERR_INVALID_ARG;
+  if (rows_overlap(c->dim, c->batch, out_batch, q_heads, out_head)) return SWM_ERR_INVALID_ARG;
   if (q_batch % 8 || q_head % 8 || misaligned(q)) return SWM_ERR_ALIGN;
   swm::AttnPlan p;
   st = plan_for(c, q_heads, weights != nullptr, &p);
@@ -141,6 +147,13 @@ swm_status swm_kv_evict(const swm_kv_cache* c, const float* weights, int64_t w_p
     return SWM_ERR_INVALID_ARG;
   if (lengths_out == c->lengths || (weights_out == weights && (wo_page != w_page || wo_head != w_head)) ||
       (positions_out == positions && (po_page != p_page || po_head != p_head)))
+    return SWM_ERR_INVALID_ARG;
+  // rows move within a head, so heads own theirs
+  if (rows_overlap(c->dim, c->pages, c->k_page, c->heads, c->k_head) ||
+      rows_overlap(c->dim, c->pages, c->v_page, c->heads, c->v_head))
+    return SWM_ERR_INVALID_ARG;
+  if (rows_overlap(c->page_size, c->pages, wo_page, c->heads, wo_head) ||
+      rows_overlap(c->page_size, c->pages, po_page, c->heads, po_head))
     return SWM_ERR_INVALID_ARG;
   swm_log("kv_evict B=%lld heads=%lld D=%lld capacity=%lld: budget %lld, recent %lld", (long long)c->batch,
           (long long)c->heads, (long long)c->dim, (long long)(c->pages_per_seq * c->page_size), (long long)budget,

@@ -244,6 +244,52 @@ def test_binding_refuses(gpu_lib):
         swm.kv_evict(c, W, Q, 50, lengths_out=c.lengths)
 
 
+@pytest.mark.parametrize("change", [
+    dict(weights_out=8192, w_head=0, wo_head=0), dict(positions_out=12288, p_head=0, po_head=0),  # in place, expanded
+    dict(wo_head=0), dict(po_head=15), dict(wo_page=0), dict(po_page=8), dict(wo_page=16, wo_head=16),
+])
+def test_entries_shared_by_heads_or_pages_are_not_written(change):
+    """Heads of one sequence keep different tokens: entries that two of them wrote would be either's."""
+    lib = swm.load()
+    c = swm.KvCache(4096, 4096, 4096, 4096, 1024, 64, 64, 1024, 64, 64, 4, 8, 16, 3, 64, 2, 4)
+    a = dict(weights=8192, w_page=48, w_head=16, positions=12288, p_page=48, p_head=16, budget=20, recent=4,
+             weights_out=16384, wo_page=48, wo_head=16, positions_out=20480, po_page=48, po_head=16,
+             lengths_out=24576, kept=28672, stream=None)
+    a.update(change)
+    assert lib.swm_kv_evict(ctypes.addressof(c), *a.values()) == 1
+
+
+@pytest.mark.parametrize("stride", ["k_head", "v_head", "k_page", "v_page"])
+def test_rows_shared_by_heads_or_pages_do_not_move(stride):
+    lib = swm.load()
+    f = dict(k=4096, v=4096, table=4096, lengths=4096, k_page=3072, k_slot=192, k_head=64, v_page=3072, v_slot=192,
+             v_head=64, table_ld=4, pages=8, page_size=16, heads=3, dim=64, batch=2, pages_per_seq=4)
+    f[stride] = 0
+    c = swm.KvCache(**f)
+    assert lib.swm_kv_evict(ctypes.addressof(c), 8192, 48, 16, 12288, 48, 16, 20, 4, 16384, 48, 16, 20480, 48, 16,
+                            24576, 28672, None) == 1
+
+
+@gpu
+def test_heads_share_their_inputs(gpu_lib):
+    """Positions and weights of a cache that nothing has been evicted from yet, the same for every head: expanded
+    tensors as inputs alone; in place they are refused."""
+    import torch
+    B, H, D, S = 2, 3, 64, 16
+    k, v, w, pos, table = make(B, H, D, S, [300, 180], "long")
+    w[:], pos[:] = w[:, :1], pos[:, :1]
+    want = reference(k, v, w, pos, table, np.array([300, 180]), 150, 10)
+    K, V = dev(k), dev(v)
+    W, Q = dev(np.ascontiguousarray(w[:, :1])).expand(-1, H, -1), dev(np.ascontiguousarray(pos[:, :1])).expand(-1, H, -1)
+    cache = swm.PagedCache(K, V, dev(table), torch.tensor([300, 180], dtype=torch.int32, device="cuda"))
+    with pytest.raises(swm.SwmError):
+        swm.kv_evict(cache, W, Q, 150, 10)
+    wo, po = W.contiguous(), Q.contiguous()
+    n, kept = swm.kv_evict(cache, W, Q, 150, 10, weights_out=wo, positions_out=po)
+    for x, y in zip((K, V, wo, po, n, kept), want):
+        assert same(x.cpu().numpy(), y)
+
+
 @pytest.mark.parametrize("change,code", [
     (dict(weights=None), 1), (dict(positions=None), 1), (dict(weights_out=None), 1), (dict(positions_out=None), 1),
     (dict(lengths_out=None), 1), (dict(kept=None), 1), (dict(budget=-1), 1), (dict(recent=-1), 1),

@@ -405,6 +405,14 @@ def test_call_refusals(change, code):
     assert lib.swm_paged_attention(None, *a.values()) == 1
 
 
+@pytest.mark.parametrize("strides", [(0, 64), (63, 64), (256, 0), (256, 32), (64, 64)])
+def test_outputs_that_share_memory_are_refused(strides):
+    lib = swm.load()
+    c = cache_struct(heads=4)
+    assert lib.swm_paged_attention(ctypes.addressof(c), 4096, 256, 64, 4, 0.125, None, 0, None, 0, 0, 8192, *strides,
+                                   None, 0, None) == 1
+
+
 def test_query_heads_are_a_multiple():
     lib = swm.load()
     c = cache_struct(heads=4)
