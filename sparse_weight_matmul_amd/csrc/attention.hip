@@ -218,6 +218,13 @@ __device__ __forceinline__ void add_weights(const AttnArgs& a, const Place (&p)[
       unsafeAtomicAdd(a.weights + int64_t(p[e].page) * a.w_p + int64_t(hkv) * a.w_h + p[e].slot, w[e]);
 }
 
+// A head's weight of a token with score x.  A token that is not live has none,
+// also where the head's sum is NaN (a live key or the query holds one).
+__device__ __forceinline__ float weight_of(float x, float base, float inv) {
+  const float p = __builtin_amdgcn_exp2f(x - base) * inv;
+  return x == neg_inf() ? 0.f : p;
+}
+
 // Lengths of sequences 2 lane and 2 lane + 1 (0 past the batch), in tokens.
 __device__ __forceinline__ void two_lengths(const AttnArgs& a, int lane, int* n0, int* n1) {
   const int x0 = a.lengths[min(2 * lane, a.B - 1)], x1 = a.lengths[min(2 * lane + 1, a.B - 1)];
@@ -571,7 +578,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 1 : 3) void attn_kernel(At
       const float* x = sm_x + h * a.lrow;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        w[e] += __builtin_amdgcn_exp2f(x[min(t + 64 * e, n - 1)] - sm_m[h]) * sm_l[h];
+        w[e] += weight_of(x[min(t + 64 * e, n - 1)], sm_m[h], sm_l[h]);
     }
     add_weights(a, p, hkv, t, n, w);
   }
@@ -727,7 +734,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a, int
           if (g + u < gn) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] += __builtin_amdgcn_exp2f(v[u][e] - sc[2 * (g + u)]) * sc[2 * (g + u) + 1];
+              w[e] += weight_of(v[u][e], sc[2 * (g + u)], sc[2 * (g + u) + 1]);
           }
       }
       add_weights(a, at, hkv, t, n, w);

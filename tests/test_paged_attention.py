@@ -332,6 +332,43 @@ def test_infinite_scores_and_no_sequences(gpu_lib):
 
 
 @gpu
+@pytest.mark.parametrize("B,Hq,Hkv,lengths", [(2, 4, 2, [200, 90]),       # weights added by the first launch
+                                              (2, 4, 2, [5000, 3000]),    # cut into pieces
+                                              (2, 40, 2, [300, 170])])    # scores through the workspace
+@pytest.mark.parametrize("where", ["key", "query"])
+def test_nan_among_live_tokens_adds_nothing_elsewhere(gpu_lib, B, Hq, Hkv, lengths, where):
+    import torch
+    D, S = 64, 16
+    q, k, v, table, dev = make(B, Hq, Hkv, D, S, lengths)
+    r = np.random.default_rng(11)
+    mask = r.random((B, table.shape[1] * S)) < 0.6
+    mask[0, 5] = True
+    table[0, 2] = -1  # tokens on no page
+    dev["table"].copy_(torch.from_numpy(table))
+    if where == "key":
+        dev["k"][int(table[0, 0]), 5, 0] = float("nan")
+    else:
+        dev["q"][0, 1] = float("nan")
+    cache = swm.PagedCache(dev["k"], dev["v"], dev["table"], dev["lengths"])
+    w0 = r.random((k.shape[0], Hkv, S)).astype(np.float32)
+    w = torch.from_numpy(w0).cuda()
+    out = swm.paged_attention(cache, dev["q"], mask=torch.from_numpy(mask).cuda(), weights=w)
+    hit = np.zeros((B, Hq), bool)  # the first sequence: the heads of key-value head 0, or the one query head
+    hit[0, slice(0, Hq // Hkv) if where == "key" else 1] = True
+    assert np.array_equal(np.isnan(out.float().cpu().numpy()).any(-1), hit)
+    got = w.cpu().numpy()
+    live = np.zeros((k.shape[0], S), bool)
+    for b, n in enumerate(lengths):
+        t = np.arange(n)[mask[b, :n]]
+        t = t[table[b][t // S] >= 0]
+        live[table[b][t // S], t % S] = True
+        at = got[table[b][t // S], :, t % S]
+        assert np.array_equal(np.isnan(at), np.broadcast_to(np.arange(Hkv) == 0, at.shape) & (b == 0))
+    live = np.broadcast_to(live[:, None], got.shape)
+    assert np.array_equal(got[~live], w0[~live])
+
+
+@gpu
 def test_binding_refuses(gpu_lib):
     import torch
     q, k, v, table, dev = make(2, 4, 2, 64, 16, [20, 30])
