@@ -375,17 +375,23 @@ def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, w
     if bias is not None:
         if not bias.is_cuda or bias.dtype is not torch.float16 or bias.shape != (M,):
             raise TypeError(f"bias must be a float16 CUDA tensor, ({M},)")
+        if bias.device != X.device:
+            raise ValueError(f"bias must be on {X.device}")
         if M > 1 and bias.stride(0) != 1:
             raise ValueError("bias must be contiguous")
         bp = bias.data_ptr()
     if residual is not None:
         rp, ldr = _rows(residual, "residual", N, M)
+        if residual.device != X.device:
+            raise ValueError(f"residual must be on {X.device}")
     if Y is None:
         if residual is not None and residual.is_contiguous():
             Y = _empty_like(residual, stream)
         else:
             Y = _empty((N, M), X.dtype, X.device, stream)
     yp, ldy = _rows(Y, "Y", N, M)
+    if Y.device != X.device:
+        raise ValueError(f"Y must be on {X.device}")
     wp, wb = None, 0
     if N > 32:  # below, W is streamed
         need = 0 if workspace is not None else int(lib.swm_spmm_epilogue_workspace_bytes(fmt._h, N))

@@ -73,6 +73,28 @@ SHAPES = [
 ]
 
 
+@pytest.mark.parametrize("where", ["bias", "residual", "Y"])
+def test_operands_on_another_device_are_refused(where):
+    import torch
+
+    class OnGpu(torch.Tensor):
+        is_cuda = property(lambda self: True)
+        device = property(lambda self: torch.device("cuda", self.at))
+
+    class Fmt:
+        M, K, _h = 24, 16, None
+
+    def made(at, *shape):
+        x = torch.zeros(shape, dtype=torch.float16).as_subclass(OnGpu)
+        x.at = at
+        return x
+
+    a = {"bias": made(0, 24), "residual": made(0, 4, 24), "Y": made(0, 4, 24)}
+    a[where] = made(1, *a[where].shape)
+    with pytest.raises(ValueError, match=f"{where} must be on cuda:0"):
+        swm.spmm_epilogue(Fmt, made(0, 4, 16), **a)
+
+
 @gpu
 @pytest.mark.parametrize("M,K,N", SHAPES)
 def test_routes(gpu_lib, M, K, N):
