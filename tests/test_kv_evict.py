@@ -222,6 +222,80 @@ def test_missing_pages_are_never_touched(gpu_lib):
     assert np.all((kept < 60) | ((page >= 0) & (page < k.shape[0])))
 
 
+def reference_with_holes(k, v, w, pos, table, lengths, budget, recent, w_out, pos_out):
+    """reference where the table may name no page: such tokens come after all others, and neither they nor what
+    would move into their slots is copied.  w_out, pos_out: contents before the call (copies of w, pos: in place)."""
+    P, S, H = k.shape[:3]
+    k, v = k.copy(), v.copy()
+    kept = np.full((len(lengths), H, budget), -1, np.int32)
+    for b, n in enumerate(lengths):
+        t = np.arange(n)
+        page, slot = table[b][t // S], t % S
+        there = (page >= 0) & (page < P)
+        at = np.where(there, page, 0)
+        for h in range(H):
+            wt, pt = w[at, h, slot], pos[at, h, slot]
+            newest = int(pt[there].max()) if there.any() else 0
+            first = (pt.astype(np.int64) > newest - recent) | np.isnan(wt) | (wt == np.inf)
+            order = sorted(t, key=lambda i: (2, 0.0, i) if not there[i] else
+                           (0 if first[i] else 1, 0.0 if first[i] else -float(wt[i]), i))
+            stay = np.array(sorted(order[:budget]), int)
+            place = np.arange(min(n, budget))
+            free = np.setdiff1d(place, stay)
+            place[free] = stay[stay >= budget]
+            kept[b, h, :len(place)] = place
+            for to, src in enumerate(place):
+                if there[to] and there[src]:
+                    w_out[page[to], h, slot[to]], pos_out[page[to], h, slot[to]] = wt[src], pt[src]
+                    for x in (k, v):
+                        x[page[to], slot[to], h] = x[page[src], slot[src], h]
+    return k, v, w_out, pos_out, np.minimum(lengths, budget).astype(np.int32), kept
+
+
+HOLES = [
+    # B, H, D, S, lengths, budget, recent, every how many-th page is missing
+    (1, 2, 64, 16, [100], 60, 8, 3),
+    (2, 2, 64, 5, [513, 130], 100, 10, 2),
+    (2, 2, 128, 16, [2000, 700], 1990, 50, 4),       # more slots than tokens that are there
+    (1, 2, 64, 16, [3000], 1200, 100, 3),            # a second launch moves the rows
+    (1, 1, 8, 64, [40000], 15000, 500, 3),           # more tokens than the keys that fit on chip
+    (1, 1, 8, 64, [40000], 39000, 500, 3),
+    (300, 1, 8, 8, [21] * 300, 16, 4, 3),
+    (2, 1, 64, 16, [90, 40], 100, 4, 3),             # within the budget
+    (2, 1, 64, 16, [90, 40], 20, 4, 1),              # nothing there at all
+]
+
+
+@gpu
+@pytest.mark.parametrize("B,H,D,S,lengths,budget,recent,every", HOLES)
+@pytest.mark.parametrize("inplace", [True, False])
+def test_everything_around_missing_pages(gpu_lib, B, H, D, S, lengths, budget, recent, every, inplace):
+    """Bits of the pools, weights and positions where table entries name no page, page 0 and pages that no table
+    names among them."""
+    import torch
+    k, v, w, pos, table = make(B, H, D, S, lengths, "long")
+    wrong = np.array([-1, -(1 << 31), k.shape[0], 1 << 30], np.int32)
+    for b in range(B):
+        gone = np.arange(b % every, table.shape[1], every)
+        table[b, gone] = wrong[gone % 4]
+    assert not (np.unique(table[(table >= 0) & (table < k.shape[0])], return_counts=True)[1] > 1).any()
+    K, V, W, Q = dev(k), dev(v), dev(w), dev(pos)
+    cache = swm.PagedCache(K, V, dev(table), torch.tensor(lengths, dtype=torch.int32, device="cuda"))
+    if inplace:
+        want = reference_with_holes(k, v, w, pos, table, lengths, budget, recent, w.copy(), pos.copy())
+        n, kept = swm.kv_evict(cache, W, Q, budget, recent)
+        got_w, got_q = W, Q
+    else:
+        want = reference_with_holes(k, v, w, pos, table, lengths, budget, recent, np.full_like(w, -7.0),
+                                    np.full_like(pos, -7))
+        got_w, got_q = torch.full_like(W, -7.0), torch.full_like(Q, -7)
+        n, kept = swm.kv_evict(cache, W, Q, budget, recent, weights_out=got_w, positions_out=got_q)
+        assert same(W.cpu().numpy(), w) and same(Q.cpu().numpy(), pos)
+    for name, x, y in zip("lengths kept k v weights positions".split(), (n, kept, K, V, got_w, got_q),
+                          (want[4], want[5], *want[:4])):
+        assert same(x.cpu().numpy(), y), name
+
+
 @gpu
 def test_binding_refuses(gpu_lib):
     import torch
