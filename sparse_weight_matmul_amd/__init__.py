@@ -370,19 +370,20 @@ def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, w
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
     N, M, K = X.shape[0], fmt.M, fmt.K
     xp, ldx = _rows(X, "X", N, K)
+    device = X.get_device()
     bp = rp = None
     ldr = 0
     if bias is not None:
         if not bias.is_cuda or bias.dtype is not torch.float16 or bias.shape != (M,):
             raise TypeError(f"bias must be a float16 CUDA tensor, ({M},)")
-        if bias.device != X.device:
+        if bias.get_device() != device:
             raise ValueError(f"bias must be on {X.device}")
         if M > 1 and bias.stride(0) != 1:
             raise ValueError("bias must be contiguous")
         bp = bias.data_ptr()
     if residual is not None:
         rp, ldr = _rows(residual, "residual", N, M)
-        if residual.device != X.device:
+        if residual.get_device() != device:
             raise ValueError(f"residual must be on {X.device}")
     if Y is None:
         if residual is not None and residual.is_contiguous():
@@ -390,14 +391,14 @@ def spmm_epilogue(fmt: Format, X, bias=None, act: str = "none", residual=None, w
         else:
             Y = _empty((N, M), X.dtype, X.device, stream)
     yp, ldy = _rows(Y, "Y", N, M)
-    if Y.device != X.device:
+    if Y.get_device() != device:
         raise ValueError(f"Y must be on {X.device}")
     wp, wb = None, 0
     if N > 32:  # below, W is streamed
         need = 0 if workspace is not None else int(lib.swm_spmm_epilogue_workspace_bytes(fmt._h, N))
         workspace, wp, wb = _workspace(workspace, need, X.device, stream)
     _check(lib.swm_spmm_epilogue(fmt._h, xp, ldx, yp, ldy, N, bp, ACTIVATIONS[act], rp, ldr, wp, wb,
-                                 _raw_stream(stream, X.device.index)), "swm_spmm_epilogue")
+                                 _raw_stream(stream, device)), "swm_spmm_epilogue")
     return Y
 
 

@@ -81,6 +81,9 @@ def test_operands_on_another_device_are_refused(where):
         is_cuda = property(lambda self: True)
         device = property(lambda self: torch.device("cuda", self.at))
 
+        def get_device(self):
+            return self.at
+
     class Fmt:
         M, K, _h = 24, 16, None
 
