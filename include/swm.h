@@ -530,7 +530,8 @@ typedef struct swm_kv_cache {
  * key-value head h / (q_heads / heads).  A token is live if it is below its
  * sequence's length, on a page of the pool and not masked; a row without live
  * tokens gives zeros.  Rows that are not live may hold anything, infinities
- * and NaN included.
+ * and NaN included.  An infinity in a live value row makes the outputs of its
+ * dimension an infinity or NaN.
  *  q, out: DEVICE fp16, element (b, h, d) at b * q_batch + h * q_head + d
  *  (out likewise; out must not alias q).  q 16-byte aligned with strides that
  *  are multiples of 8.

@@ -332,6 +332,21 @@ def test_infinite_scores_and_no_sequences(gpu_lib):
 
 
 @gpu
+@pytest.mark.parametrize("lengths", [[200, 90], [5000, 3000]])
+def test_infinite_values_stay_in_their_dimension(gpu_lib, lengths):
+    import torch
+    q, k, v, table, dev = make(2, 4, 2, 64, 16, lengths)
+    dev["v"][int(table[0, 1]), 3, 1, 17] = float("inf")  # sequence 0, query heads 2 and 3
+    cache = swm.PagedCache(dev["k"], dev["v"], dev["table"], dev["lengths"])
+    out = swm.paged_attention(cache, dev["q"])
+    hit = np.zeros((2, 4, 64), bool)
+    hit[0, 2:, 17] = True
+    assert np.array_equal(~np.isfinite(out.float().cpu().numpy()), hit)
+    ref, tol, _, _ = reference(q, k, v, table, lengths, 64 ** -0.5)
+    check(torch.where(torch.from_numpy(hit).cuda(), torch.zeros_like(out), out), np.where(hit, 0, ref), tol)
+
+
+@gpu
 @pytest.mark.parametrize("B,Hq,Hkv,lengths", [(2, 4, 2, [200, 90]),       # weights added by the first launch
                                               (2, 4, 2, [5000, 3000]),    # cut into pieces
                                               (2, 40, 2, [300, 170])])    # scores through the workspace
