@@ -781,10 +781,10 @@ hipError_t launch_dim(const AttnArgs& a, bool same8, dim3 grid, size_t lds, hipS
 //    115; of one length 94 / 103; 12 ragged x 8000, 12 heads of 256 214 / 104).
 //    Below 32 steps the join costs as much as it saves.
 //  - More units than CUs: whole sequences, dealt by their length (16 ragged x
-//    4096, 32 heads 101 in the batch's order / 82; 64 ragged x 2000, 8 heads 51
-//    / 44; cut into pieces no faster), unless they are too short for the sorting
+//    4096, 32 heads 110 in the batch's order / 89; 64 ragged x 2000, 8 heads 58
+//    / 49; cut into pieces no faster), unless they are too short for the sorting
 //    in every workgroup to pay (64 x 300 of 32 heads: 32 unsorted / 37; 64 x
-//    1000 101 / 94).
+//    1000 101 / 90).
 //
 // The weights: one workgroup that sees a whole sequence keeps its scores in
 // LDS and adds the weights itself, as long as three such workgroups fit on a

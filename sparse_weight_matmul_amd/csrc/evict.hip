@@ -32,9 +32,10 @@
 // Bound: by its bytes (8 per token and head, and the moved rows) a call takes
 // a few us at most; what it takes is the chain of some ten barriers and four
 // memory latencies inside a workgroup.  Measured, in the kernel: 1 x 1025 to
-// 1024, 32 heads 9.9 us; 16 x 2176 to 2048, 8 heads 15.2 us; 8 ragged
-// sequences of up to 4096 to 1024, 32 heads 28.4 us, of them 16 for 51 MB of
-// rows, read and written.
+// 1024, 32 heads 10.1 us; 16 x 2176 to 2048, 8 heads 15.2 us; 8 ragged
+// sequences of up to 4096 to 1024, 32 heads 43 us with another cache in every
+// call, 31 of them for 51 MB of rows, read and written (28.6 us, 16 of them,
+// where the rows are in the last-level cache from the call before).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

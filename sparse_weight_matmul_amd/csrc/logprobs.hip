@@ -35,10 +35,10 @@
 //
 // Bound: with many rows the read of the logits (2 or 4 bytes each), the
 // exponentials (one per logit, at a quarter of the vector rate) and the five
-// other vector instructions close behind: 4096 x 32000 fp16 45 us in the
-// kernel, 262 MB at 5.8 TB/s.  With few rows the chain of one load, two
+// other vector instructions close behind: 4096 x 32000 fp16 44 us in the
+// kernel, 262 MB at 5.9 TB/s.  With few rows the chain of one load, two
 // reductions and the choice of the top tokens: 1 x 32000 fp16 with 5 of them
-// 7.8 us in the kernel (4.7 with none), 61 x 50021 fp32 with 20 10.9 (7.6).
+// 7.5 us in the kernel (4.6 with none), 61 x 50021 fp32 with 20 11.4 (7.4).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

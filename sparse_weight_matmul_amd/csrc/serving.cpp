@@ -203,7 +203,7 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
   r.top = top;
   r.fp32 = fp32 != 0;
   r.wide = wide != 0;
-  swm_log("token_logprobs N=%lld V=%lld top=%d: a workgroup per row", (long long)N, (long long)V, top);
+  swm_log("token_logprobs N=%lld V=%lld top=%d, %s logits", (long long)N, (long long)V, top, fp32 ? "fp32" : "fp16");
   int dev = 0;
   SWM_HIP(hipGetDevice(&dev));
   SWM_HIP(swm::launch_logprobs(r, swm::num_cus(dev), static_cast<hipStream_t>(stream)));
