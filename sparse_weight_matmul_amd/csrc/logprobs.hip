@@ -378,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobArgs a) {
         uint64_t best = 0;
         for (int j = tid; j < a.V; j += kThreads) {
           const uint64_t c = uint64_t(key_of(float(x[j]))) << 32 | (0xffffffffu - uint32_t(j));
-          if (c < last && c > best) best = c;
+          if ((r == 0 || c < last) && c > best) best = c;  // a NaN at index 0 has the largest number there is
         }
 #pragma unroll
         for (int s = 1; s < 64; s *= 2) best = max(best, uint64_t(__shfl_xor((unsigned long long)best, s)));

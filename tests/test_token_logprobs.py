@@ -190,6 +190,31 @@ def test_rows_of_nan(gpu_lib, N, V, top, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,V,threads,top", [(np.float16, 2040, 64, 32), (np.float32, 1020, 64, 32),
+                                                 (np.float32, 1 << 20, 1024, 3)])
+@pytest.mark.parametrize("fill", [np.nan, 60.0])
+def test_more_above_the_bound_than_the_list_holds(gpu_lib, dtype, V, threads, top, fill):
+    """Fewer than `top` threads of a row hold hundreds of logits above all others, the first logit among them:
+    found in rounds over the row."""
+    import torch
+    x = rows("plain", 1, V, dtype)
+    vec = 16 // np.dtype(dtype).itemsize
+    x[0, np.arange(V) // vec % threads < top - 1] = fill
+    assert np.count_nonzero(x[0] != x[0]) + np.count_nonzero(x[0] == 60) > 448
+    x[0, 1::5] += dtype(0.5)  # unlike sizes among the numbers
+    _, ent, ids, lps = swm.token_logprobs(torch.from_numpy(x).cuda(), top=top)
+    key = np.where(np.isnan(x), np.inf, x).astype(np.float64)
+    want = np.argsort(-key, axis=-1, kind="stable")[:, :top]
+    assert np.array_equal(ids.cpu().numpy(), want)
+    if np.isnan(fill):
+        assert bool(torch.isnan(lps).all()) and bool(torch.isnan(ent).all())
+    else:
+        lp, h, _ = reference(x, top)
+        closer(lps.cpu().numpy(), np.take_along_axis(lp, want, -1), 16.0)
+        closer(ent.cpu().numpy(), h, 1 + np.log(V) + h)
+
+
+@gpu
 @pytest.mark.parametrize("N,V,top", [(8, 300, 5), (8, 5001, 20), (8, 50021, 0), (8, 140000, 64), (2100, 700, 0),
                                      (300, 3001, 3)])
 @pytest.mark.parametrize("dtype,fill", [(np.float16, x) for x in (-1e4, -65504.0, 6e4)] + [
