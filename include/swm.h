@@ -628,6 +628,38 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
                               const void* targets, int32_t wide, float* logp, float* entropy, int32_t top,
                               int64_t* top_ids, float* top_logp, void* stream);
 
+/* prompt_attention: attention over whole prompts, packed one behind the other,
+ *   x_ij = scale * q_i . k_j,  p = softmax of a row's x over its tokens j,
+ *   out_i = sum_j p_ij v_j,
+ * where row i of sequence b, rows starts[b] .. starts[b + 1] - 1, sees the
+ * tokens j of its own sequence, j <= i only if causal != 0.  q_heads query
+ * heads, a multiple of heads: query head h reads key-value head h / (q_heads /
+ * heads).
+ *  q, k, v, out: DEVICE fp16; element (t, h, d) of q at t * q_token + h *
+ *  q_head + d, the others likewise, so views of a stacked product's rows and
+ *  head-major tensors are the same call; out must not alias the inputs.  q, k, v
+ *  16-byte aligned with strides that are multiples of 8; k_token, v_token >= dim.
+ *  tokens: rows of each.  starts: DEVICE int32, batch + 1, not decreasing,
+ *  0 <= starts[b] <= tokens (others are clamped to that); rows that belong to
+ *  no sequence are neither read nor written.  Read by the kernel, so a captured
+ *  graph follows them.
+ *  Scores, maxima, sums and outputs are fp32; a weight is rounded to fp16 once
+ *  before it meets its value row, out is rounded once.  A value that is not
+ *  finite makes the outputs of its dimension an infinity or NaN in the rows
+ *  that see its token, and in no other.
+ *  Limits: dim a multiple of 8 up to 256, batch and q_heads at most 65535,
+ *  tokens below 2^31 - 65536, k_token and v_token below 2^23, and (tokens / 128 +
+ *  batch) * q_heads below 2^24 (SWM_ERR_UNSUPPORTED).
+ *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, q_heads not a
+ *  positive multiple of heads, a scale that is not finite, rows of k, v or out
+ *  that share memory.  SWM_ERR_ALIGN: q, k, v.  No workspace; one launch,
+ *  asynchronous on stream, bitwise reproducible. */
+swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                                int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int64_t tokens,
+                                int64_t q_heads, int64_t heads, int64_t dim, const int32_t* starts, int64_t batch,
+                                float scale, int32_t causal, void* out, int64_t out_token, int64_t out_head,
+                                void* stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static string for a status code (never NULL). */

@@ -90,6 +90,8 @@ SIGNATURES = {
     "swm_kv_evict": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
                             _vp, _vp]),
     "swm_token_logprobs": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "swm_prompt_attention": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64,
+                                    ctypes.c_float, _i32, _vp, _i64, _i64, _vp]),
     "swm_status_str": (ctypes.c_char_p, [_i32]),
     "swm_last_hip_error": (_i32, []),
     "swm_version": (_i32, []),
@@ -794,6 +796,60 @@ def token_logprobs(logits, targets=None, top: int = 0, stream=None):
                                   None if ids is None else ids.data_ptr(), None if lps is None else lps.data_ptr(),
                                   s), "swm_token_logprobs")
     return logp, entropy, ids, lps
+
+
+def _heads(t, name, device=None):
+    """(pointer, token stride, head stride) of a (tokens, heads, dim) fp16 CUDA tensor with unit stride along dim."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.float16 or t.dim() != 3:
+        raise TypeError(f"{name} must be a 3-D float16 CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    T, H, D = t.shape
+    token, head, unit = t.stride()
+    if unit != 1 and D > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    # a stride along one token or one head is never used
+    return t.data_ptr(), token if T > 1 else D, head if H > 1 else 0
+
+
+def prompt_attention(q, k, v, starts, scale: Optional[float] = None, causal: bool = True, out=None, stream=None):
+    """Attention over whole prompts, packed one behind the other: rows
+    starts[b] .. starts[b + 1] - 1 of q (T, Hq, D) and of k and v (T, H, D),
+    fp16, are sequence b; out (T, Hq, D) = softmax(scale * q . k) v over each
+    row's own sequence, up to the row itself if causal.  Hq is a multiple of H,
+    D of 8 up to 256; scale defaults to D ** -0.5; any strides that are
+    multiples of 8 (views of a stacked product's rows, head-major tensors).
+    starts: (B + 1,) int32 on the device.  Rows that belong to no sequence are
+    not written."""
+    import torch
+    lib = load()
+    qp, device = _heads(q, "q"), q.device
+    T, Hq, D = q.shape
+    kp, vp = _heads(k, "k", device), _heads(v, "v", device)
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k and v must be ({T}, heads, {D})")
+    B = _starts(starts, device)
+    if out is None:
+        out = _empty((T, Hq, D), q.dtype, device, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    op = _heads(out, "out", device)
+    s = _raw_stream(stream, device.index)
+    _check(lib.swm_prompt_attention(*qp, *kp, *vp, T, Hq, k.shape[1], D, starts.data_ptr(), B,
+                                    D ** -0.5 if scale is None else scale, int(bool(causal)), *op, s),
+           "swm_prompt_attention")
+    return out
+
+
+def _starts(starts, device) -> int:
+    """Sequences that a (B + 1,) int32 tensor of row bounds describes."""
+    import torch
+    if not isinstance(starts, torch.Tensor) or starts.dtype is not torch.int32 or starts.device != device:
+        raise TypeError(f"starts must be an int32 tensor on {device}")
+    if starts.dim() != 1 or starts.shape[0] < 1 or not starts.is_contiguous():
+        raise ValueError("starts must be contiguous, one entry more than sequences")
+    return starts.shape[0] - 1
 
 
 def status_str(code: int) -> str:

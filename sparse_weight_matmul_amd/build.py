@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libswm.so")
 
 SOURCES = ["format.cpp", "colruns.cpp", "api.cpp", "serving.cpp", "decode.hip", "decode_fused.hip", "prefill.hip", "spmspv.hip",
-           "smfmac.hip", "attention.hip", "evict.hip", "logprobs.hip"]
+           "smfmac.hip", "attention.hip", "evict.hip", "logprobs.hip", "prompt.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

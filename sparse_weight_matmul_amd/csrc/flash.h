@@ -1,0 +1,186 @@
+// Pieces of an attention with many query rows, on v_mfma_f32_32x32x16_f16: a
+// wave takes 32 query rows and 64 tokens at a time, from key and value tiles in
+// LDS.
+//
+// Scores are formed transposed, S^T = K Q^T (A: 32 tokens, B: 32 query rows):
+// lane l of the result holds, for the one row l % 32, the tokens 8 (i / 4) + 4
+// (l / 32) + i % 4 of its registers i.  Maxima and sums are then per lane but
+// for one exchange with lane l ^ 32, and the weights are the second product's
+// B operand as they stand, O^T = V^T P^T: step s of 16 tokens takes registers
+// 8 (s % 2) .. + 7 of score block s / 2, which are tokens 16 s + 8 (e / 4) + 4
+// (l / 32) + e % 4.  Its A operand, the same tokens of dimension l % 32, is
+// read from the row-major value tile by the transposing LDS read
+// (ds_read_b64_tr_b16: of 16 lanes, lane j gets element j of four rows).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace swm {
+namespace flash {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int kTokens = 64;  // of a tile
+constexpr int kRows = 32;    // query rows of a wave
+
+// The weights go into the second product as fp16, once rounded (2^-11 of each
+// weight, as large as the output's own rounding), times 2^kUp or up to 2^(kUp +
+// kLazy) where the running maximum is kLazy behind: 2^15 at most.  Weights down
+// to 2^-25 of the largest then keep their relative precision, and smaller ones
+// are off by 2^-36 of it at most.
+constexpr float kUp = 11.f;
+constexpr float kLazy = 4.f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// Where a tile's 16-byte chunk c of a row is kept: the row's chunks are
+// permuted so that the reads of eight or sixteen rows meet all banks.
+// C: chunks of a row in LDS, 8, 16 or 32.
+template <int C>
+__device__ __forceinline__ int key_chunk(int row, int c) {
+  return C == 8 ? c ^ ((row >> 1) & 7) : c ^ (row & 15);
+}
+template <int C>
+__device__ __forceinline__ int value_chunk(int row, int c) {
+  return C == 8 ? c ^ (((row >> 1) & 1) << 2) : c ^ ((row & 3) << 2 | ((row >> 2) & 3));
+}
+
+__device__ __forceinline__ void both_halves(float v, float* a, float* b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  *a = __uint_as_float(r[0]);
+  *b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_halves(float v) {
+  float a, b;
+  both_halves(v, &a, &b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  float a, b;
+  both_halves(v, &a, &b);
+  return a + b;
+}
+
+// A wave's running state for 32 rows: maximum (of the unscaled scores) and sum
+// per lane's row, the sum over the lane's own tokens only; O^T.
+template <int ND>
+struct State {
+  float m, l;
+  f32x16 o[ND];
+  __device__ __forceinline__ void clear() {
+    m = neg_inf();
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  }
+};
+
+// Scores of 64 tokens of a tile, before the scale.
+template <int NK, int C>
+__device__ __forceinline__ void scores(const uint16_t* k, int lane, const half8 (&q)[NK], f32x16 (&s)[2]) {
+  const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < NK; ++x) {
+      const int row = 32 * b + r;
+      const half8 a = *reinterpret_cast<const half8*>(k + (row * C + key_chunk<C>(row, 2 * x + h)) * 8);
+      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[x], s[b], 0, 0, 0);
+    }
+  }
+}
+
+// The weights of a tile's scores and the running maximum and sum; c > 0: scale
+// in units of log2.  The maximum follows when a row has outgrown it by kLazy.
+template <int ND>
+__device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], float c, half8 (&p)[4]) {
+  float mx = s[0][0];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+  mx = max_halves(mx);
+  if (__builtin_amdgcn_ballot_w64((mx - st.m) * c > kLazy)) {
+    const float m = fmaxf(mx, st.m);
+    const float f = m == st.m ? 1.f : __builtin_amdgcn_exp2f((st.m - m) * c);
+    st.m = m;
+    st.l *= f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st.o[d][i] *= f;
+  }
+  const float base = st.m == neg_inf() ? 0.f : kUp - st.m * c;  // nothing live so far: weights of 2^-inf
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e], c, base));
+      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e + 1], c, base));
+      sum[(e >> 1) & 3] += p0 + p1;
+      w[e >> 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{p0, p1}, half2v));
+    }
+    p[x] = __builtin_bit_cast(half8, w);
+  }
+  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// O^T += V^T P^T over a tile of 64 tokens.
+template <int ND, int C>
+__device__ __forceinline__ void outputs(State<ND>& st, const uint16_t* v, int lane, const half8 (&p)[4]) {
+  const int j = lane & 15, d16 = (lane >> 4) & 1, h = lane >> 5;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * x + 8 * e + 4 * h + (j >> 2);
+        const int at = (row * C + value_chunk<C>(row, 4 * d + 2 * d16 + ((j & 3) >> 1))) * 8 + 4 * (j & 1);
+        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(const_cast<uint16_t*>(v) + at));
+        const u32x2 u = __builtin_bit_cast(u32x2, t);
+        w[2 * e] = u[0];
+        w[2 * e + 1] = u[1];
+      }
+      st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, w), p[x], st.o[d], 0, 0, 0);
+    }
+}
+
+// A wave's part of a tile, n loads of 1 KiB straight into LDS: 16 bytes at
+// `off` from `src` a lane, those from `bytes` on as zeros.
+__device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const uint32_t* off, int n, uint16_t* dst,
+                                          int step) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the resource type
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(src), 0, bytes, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + i * step), 16, off[i], 0, 0, 0);
+#endif
+}
+
+// s_waitcnt: at most n vector memory operations of this wave outstanding.
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | (((n >> 4) & 3) << 14));
+}
+
+}  // namespace flash
+}  // namespace swm

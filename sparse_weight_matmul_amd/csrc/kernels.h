@@ -199,4 +199,17 @@ hipError_t launch_logprobs(const LogprobCall& r, int num_cus, hipStream_t s);
 
 hipError_t launch_attention(const KvView& c, const AttnCall& r, const AttnPlan& p, void* ws, hipStream_t s);
 
+// Attention over packed prompts: token t, head h of q at t * q_t + h * q_h.
+struct PromptCall {
+  const uint16_t *q = nullptr, *k = nullptr, *v = nullptr;
+  uint16_t* out = nullptr;
+  const int32_t* starts = nullptr;  // B + 1
+  int64_t q_t = 0, q_h = 0, k_t = 0, k_h = 0, v_t = 0, v_h = 0, o_t = 0, o_h = 0;
+  int64_t B = 0, T = 0, Hq = 0, Hkv = 0, D = 0;
+  float scale = 1.f;
+  bool causal = true;
+};
+int64_t prompt_grid(int64_t T, int64_t B, int64_t Hq);  // workgroups
+hipError_t launch_prompt(const PromptCall& r, hipStream_t s);
+
 }  // namespace swm

@@ -210,4 +210,52 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
   return SWM_OK;
 }
 
+swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                                int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int64_t tokens,
+                                int64_t q_heads, int64_t heads, int64_t dim, const int32_t* starts, int64_t batch,
+                                float scale, int32_t causal, void* out, int64_t out_token, int64_t out_head,
+                                void* stream) {
+  if (tokens < 0 || batch < 0 || heads < 1 || q_heads < 1 || q_heads % heads || dim < 1 || !std::isfinite(scale))
+    return SWM_ERR_INVALID_ARG;
+  if (dim % 8 || dim > 256 || batch > 65535 || q_heads > 65535 || tokens >= (int64_t(1) << 31) - 65536)
+    return SWM_ERR_UNSUPPORTED;
+  if (tokens == 0 || batch == 0) return SWM_OK;
+  if (!q || !k || !v || !out || !starts) return SWM_ERR_INVALID_ARG;
+  if (q_token < 0 || q_head < 0 || k_head < 0 || v_head < 0 || out_token < 0 || out_head < 0) return SWM_ERR_INVALID_ARG;
+  if (k_token < dim || v_token < dim) return SWM_ERR_INVALID_ARG;
+  if (rows_overlap(dim, tokens, out_token, q_heads, out_head)) return SWM_ERR_INVALID_ARG;
+  if (q_token % 8 || q_head % 8 || k_token % 8 || k_head % 8 || v_token % 8 || v_head % 8 || misaligned(q) ||
+      misaligned(k) || misaligned(v))
+    return SWM_ERR_ALIGN;
+  // a tile's rows are addressed with 32-bit byte offsets
+  const int64_t most = int64_t(1) << 23;
+  if (k_token >= most || v_token >= most || swm::prompt_grid(tokens, batch, q_heads) >= (int64_t(1) << 24))
+    return SWM_ERR_UNSUPPORTED;
+  swm_log("prompt_attention tokens=%lld sequences=%lld heads=%lld/%lld D=%lld%s", (long long)tokens,
+          (long long)batch, (long long)q_heads, (long long)heads, (long long)dim, causal ? ", causal" : "");
+  swm::PromptCall r;
+  r.q = static_cast<const uint16_t*>(q);
+  r.k = static_cast<const uint16_t*>(k);
+  r.v = static_cast<const uint16_t*>(v);
+  r.out = static_cast<uint16_t*>(out);
+  r.starts = starts;
+  r.q_t = q_token;
+  r.q_h = q_head;
+  r.k_t = k_token;
+  r.k_h = k_head;
+  r.v_t = v_token;
+  r.v_h = v_head;
+  r.o_t = out_token;
+  r.o_h = out_head;
+  r.B = batch;
+  r.T = tokens;
+  r.Hq = q_heads;
+  r.Hkv = heads;
+  r.D = dim;
+  r.scale = scale;
+  r.causal = causal != 0;
+  SWM_HIP(swm::launch_prompt(r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
 }  // extern "C"
