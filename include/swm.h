@@ -660,6 +660,102 @@ swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, 
                                 float scale, int32_t causal, void* out, int64_t out_token, int64_t out_head,
                                 void* stream);
 
+/* kv_reserve: pages for the tokens that a step adds to each sequence of the
+ * cache, pages back from those that it drops, and the slot of every added
+ * token.  Sequence b goes from lengths[b] to lengths[b] + counts[b] tokens
+ * (negative: its last ones are dropped, down to none).
+ *  1. Pages behind the new length of a sequence that shrinks go back, in order
+ *     of sequence and place, on top of the free ones; their table entries
+ *     become -1 (entries that name no page are not given back).
+ *  2. Sequences that grow take the pages they need from the top, in order.
+ *     One that needs more than are left gets none, and after it only those
+ *     that need none; one that would outgrow pages_per_seq pages is left as it is.
+ *  cache: table and lengths are WRITTEN, in place (the memory behind them is
+ *  not const); the pools are not looked at.  Entries of the table from a
+ *  sequence's pages on are overwritten as pages come.  No page may belong to
+ *  two sequences, or to one and the free ones.
+ *  free_pages: DEVICE int32, free_size >= pages entries, the free pages in the
+ *  first free_count[0] (DEVICE int32); both are updated.
+ *  tokens: rows of slots, the sum of the positive counts.
+ *  starts: DEVICE int32, batch + 1: the sums of the positive counts, i.e. where
+ *  each sequence's added tokens begin among all (also those not granted).
+ *  slots: DEVICE int64, one per added token, packed so: page * page_size + slot
+ *  in the page, -1 where a sequence was not granted its tokens, where the table
+ *  names no page and from starts[batch] on.
+ *  granted: DEVICE int32, batch: by how much each length changed.
+ *  SWM_ERR_INVALID_ARG: null pointers, negative sizes, table rows that share
+ *  memory, outputs at an input's address or each other's.  SWM_ERR_SHAPE:
+ *  free_size below pages.  SWM_ERR_UNSUPPORTED: free_size or tokens of 2^31 -
+ *  65536 and more.  Cache errors as above.  No workspace; one or two launches,
+ *  asynchronous on stream; whole numbers, so bitwise reproducible. */
+swm_status swm_kv_reserve(const swm_kv_cache* cache, const int32_t* counts, int32_t* free_pages, int64_t free_size,
+                          int32_t* free_count, int64_t tokens, int32_t* starts, int64_t* slots, int32_t* granted,
+                          void* stream);
+
+/* kv_append: key and value rows of new tokens into their slots of the pools.
+ *  k, v: DEVICE fp16, element (t, h, d) at t * k_token + h * k_head + d, for
+ *  tokens rows of cache->heads heads of cache->dim; 16-byte aligned with
+ *  strides that are multiples of 8; no part of the pools.
+ *  slots: DEVICE int64, one per token, as swm_kv_reserve gives them; tokens
+ *  with a slot outside the pool are not written.  No slot may appear twice.
+ *  weights: DEVICE fp32 or NULL, the accumulator of swm_paged_attention,
+ *  page * w_page + head * w_head + slot: set to 0 for the new rows.
+ *  positions: DEVICE int32 or NULL, as swm_kv_evict reads them, at page *
+ *  p_page + head * p_head + slot: set to at[t] (DEVICE int32, one per token).
+ *  The cache's table and lengths are not looked at.
+ *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, rows of the
+ *  pools or entries of weights or positions that share memory.
+ *  SWM_ERR_ALIGN: k or v.  SWM_ERR_UNSUPPORTED: 2^34 halves of keys or more.
+ *  Cache errors as above.  No workspace; one launch, asynchronous on stream. */
+swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, int64_t tokens, const int64_t* slots, float* weights,
+                         int64_t w_page, int64_t w_head, int32_t* positions, int64_t p_page, int64_t p_head,
+                         const int32_t* at, void* stream);
+
+/* tree_attention: attention of several new tokens per sequence over the cache
+ * that holds their keys and values: drafted tokens that are to be verified, as
+ * a tree or in a row.  The tokens of sequence b are rows starts[b] .. starts[b +
+ * 1] - 1 of q, n_b of them, and the last n_b tokens of the cache's sequence b
+ * (lengths[b] counts them).  Row i sees the live tokens before the drafted
+ * ones, itself, its parent, the parent's parent and so on:
+ *   x_it = scale * q_i . k_t,  p = softmax of a row's x over the tokens t it
+ *   sees,  out_i = sum_t p_it v_t;  a row that sees none gives zeros.
+ * Live tokens and what other rows may hold: as in swm_paged_attention; the
+ * values of drafted tokens that a row does not see do not reach it, whatever
+ * they are.
+ *  q, out: DEVICE fp16, element (t, h, d) at t * q_token + h * q_head + d, the
+ *  others likewise; out must not alias q.  q 16-byte aligned with strides that
+ *  are multiples of 8.  tokens: rows of q and out.
+ *  starts: DEVICE int32, batch + 1, not decreasing, 0 <= starts[b] <= tokens
+ *  (others are clamped to that); rows that belong to no sequence are neither
+ *  read nor written.
+ *  parents: DEVICE int32, one per row: the parent's index among the sequence's
+ *  drafted tokens, below the row's own; anything else means that the sequence
+ *  itself is the parent.  NULL: the tokens follow each other.
+ *  max_tokens: at least the largest n_b, at most 64; rows of a sequence past it
+ *  are left alone.
+ *  mask: as in swm_paged_attention, drafted tokens included.
+ *  workspace: DEVICE memory of at least swm_tree_attention_workspace_bytes
+ *  bytes (0: NULL is fine), 16-byte aligned; calls that share it must be
+ *  ordered on one stream.
+ *  Scores, maxima, sums and outputs are fp32; a weight is rounded to fp16 once
+ *  before it meets its value row, out is rounded once.
+ *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
+ *  heads, a scale that is not finite, negative sizes or strides, rows of out
+ *  that share memory, mask_ld below the capacity, a workspace too small.
+ *  SWM_ERR_ALIGN: q or the workspace.  SWM_ERR_UNSUPPORTED: q_heads above
+ *  65535, max_tokens above 64, tokens * q_heads of 2^26 and more, or a grid beyond the
+ *  device's.  Cache errors as above.  One or two launches, asynchronous on
+ *  stream, bitwise reproducible. */
+swm_status swm_tree_attention(const swm_kv_cache* cache, const void* q, int64_t q_token, int64_t q_head,
+                              int64_t q_heads, int64_t tokens, const int32_t* starts, const int32_t* parents,
+                              int64_t max_tokens, float scale, const uint8_t* mask, int64_t mask_ld, void* out,
+                              int64_t out_token, int64_t out_head, void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace swm_tree_attention uses for this cache's sizes on
+ * the current device.  0 for sizes that call refuses. */
+size_t swm_tree_attention_workspace_bytes(const swm_kv_cache* cache, int64_t q_heads, int64_t max_tokens);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Static string for a status code (never NULL). */

@@ -92,6 +92,12 @@ SIGNATURES = {
     "swm_token_logprobs": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp]),
     "swm_prompt_attention": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64,
                                     ctypes.c_float, _i32, _vp, _i64, _i64, _vp]),
+    "swm_kv_reserve": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "swm_kv_append": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                             _vp]),
+    "swm_tree_attention": (_i32, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _vp,
+                                  _i64, _i64, _vp, _sz, _vp]),
+    "swm_tree_attention_workspace_bytes": (_sz, [_vp, _i64, _i64]),
     "swm_status_str": (ctypes.c_char_p, [_i32]),
     "swm_last_hip_error": (_i32, []),
     "swm_version": (_i32, []),
@@ -647,7 +653,7 @@ class PagedCache:
         self._c = KvCache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lengths.data_ptr(), *ks, *vs,
                           table.stride(0), *k.shape, *table.shape)
         self._p = ctypes.addressof(self._c)
-        self._attn_bytes = {}
+        self._attn_bytes, self._tree_bytes = {}, {}
 
     def attention_workspace_bytes(self, q_heads: int, weights: bool = False) -> int:
         """Device workspace bytes paged_attention uses (0: none)."""
@@ -655,6 +661,13 @@ class PagedCache:
         if key not in self._attn_bytes:
             self._attn_bytes[key] = int(load().swm_paged_attention_workspace_bytes(self._p, *key))
         return self._attn_bytes[key]
+
+    def tree_workspace_bytes(self, q_heads: int, max_tokens: int) -> int:
+        """Device workspace bytes tree_attention uses (0: none)."""
+        key = (int(q_heads), int(max_tokens))
+        if key not in self._tree_bytes:
+            self._tree_bytes[key] = int(load().swm_tree_attention_workspace_bytes(self._p, *key))
+        return self._tree_bytes[key]
 
     def _per_slot(self, t, name, dtype):
         """(pointer, page stride, head stride) of an array with one entry per cached row, (pages, heads, page_size)."""
@@ -666,6 +679,25 @@ class PagedCache:
         if self.page_size > 1 and slot != 1:
             raise ValueError(f"{name} must have unit stride along its last dimension")
         return t.data_ptr(), page, head
+
+
+def _mask(cache, mask):
+    """(pointer, leading dimension) of a mask over the cache's tokens."""
+    import torch
+    if mask is None:
+        return None, 0
+    if not mask.is_cuda or mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 2:
+        raise TypeError("mask must be a 2-D bool or uint8 CUDA tensor")
+    B = cache.batch
+    if mask.shape[0] != B or mask.shape[1] < cache.capacity or mask.device != cache.device:
+        raise ValueError(f"mask must be ({B}, >= {cache.capacity}) on {cache.device}")
+    if mask.shape[1] > 1 and mask.stride(1) != 1:
+        raise ValueError("mask must have unit stride along its last dimension")
+    # of one sequence only the first row is read, whatever its stride says
+    ld = mask.stride(0) if B > 1 else max(mask.shape[1], 1)
+    if B > 1 and ld < cache.capacity:
+        raise ValueError("mask rows must not overlap")
+    return mask.data_ptr(), ld
 
 
 def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=None, weights=None, out=None,
@@ -694,18 +726,7 @@ def paged_attention(cache: PagedCache, q, scale: Optional[float] = None, mask=No
         raise TypeError("out must be a float16 CUDA tensor of q's shape")
     elif out.stride(2) != 1:
         raise ValueError("out must have unit stride along its last dimension")
-    mp, mask_ld = None, 0
-    if mask is not None:
-        if not mask.is_cuda or mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 2:
-            raise TypeError("mask must be a 2-D bool or uint8 CUDA tensor")
-        if mask.shape[0] != B or mask.shape[1] < cache.capacity or mask.device != q.device:
-            raise ValueError(f"mask must be ({B}, >= {cache.capacity}) on {cache.device}")
-        if mask.shape[1] > 1 and mask.stride(1) != 1:
-            raise ValueError("mask must have unit stride along its last dimension")
-        # of one sequence only the first row is read, whatever its stride says
-        mp, mask_ld = mask.data_ptr(), mask.stride(0) if B > 1 else max(mask.shape[1], 1)
-        if B > 1 and mask_ld < cache.capacity:
-            raise ValueError("mask rows must not overlap")
+    mp, mask_ld = _mask(cache, mask)
     wp, w_page, w_head = None, 0, 0
     if weights is not None:
         wp, w_page, w_head = cache._per_slot(weights, "weights", torch.float32)
@@ -850,6 +871,124 @@ def _starts(starts, device) -> int:
     if starts.dim() != 1 or starts.shape[0] < 1 or not starts.is_contiguous():
         raise ValueError("starts must be contiguous, one entry more than sequences")
     return starts.shape[0] - 1
+
+
+def tree_attention(cache: PagedCache, q, starts, parents=None, max_tokens: Optional[int] = None,
+                   scale: Optional[float] = None, mask=None, out=None, workspace=None, stream=None):
+    """Attention of drafted tokens over a paged cache that holds their keys and
+    values: rows starts[b] .. starts[b + 1] - 1 of q (T, Hq, D) fp16 are the last
+    tokens of sequence b (the cache's lengths count them).  Each sees the tokens
+    before the drafted ones, itself, its parent, the parent's parent and so on.
+    starts: (B + 1,) int32 on the device.  parents: (T,) int32, a lower index
+    among the sequence's drafted tokens, -1 for the sequence itself; None: the
+    tokens follow each other.  max_tokens: at least the drafted tokens of any
+    sequence, at most 64 (None: the lesser of 64 and T).  mask: (B, >= capacity)
+    bool or uint8, false drops a token.  workspace: a CUDA tensor of
+    cache.tree_workspace_bytes(Hq, max_tokens) bytes; None allocates it.  Rows
+    that belong to no sequence are not written."""
+    import torch
+    lib = load()
+    device = cache.device
+    qp = _heads(q, "q", device)
+    T, Hq, D = q.shape
+    if D != cache.dim:
+        raise ValueError(f"q must be (tokens, heads, {cache.dim})")
+    if _starts(starts, device) != cache.batch:
+        raise ValueError(f"starts must have {cache.batch + 1} entries")
+    pp = None
+    if parents is not None:
+        if parents.dtype is not torch.int32 or parents.device != device:
+            raise TypeError(f"parents must be an int32 tensor on {device}")
+        if parents.shape != (T,) or not parents.is_contiguous():
+            raise ValueError(f"parents must be contiguous, ({T},)")
+        pp = parents.data_ptr()
+    most = min(64, T) if max_tokens is None else int(max_tokens)
+    if out is None:
+        out = _empty((T, Hq, D), q.dtype, device, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    op = _heads(out, "out", device)
+    mp, mask_ld = _mask(cache, mask)
+    s = _raw_stream(stream, device.index)
+    keep, ws, ws_bytes = _workspace(workspace, cache.tree_workspace_bytes(Hq, most), device, stream)
+    _check(lib.swm_tree_attention(cache._p, *qp, Hq, T, starts.data_ptr(), pp, most,
+                                  D ** -0.5 if scale is None else scale, mp, mask_ld, *op, ws, ws_bytes, s),
+           "swm_tree_attention")
+    return out
+
+
+def _ints(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of whole numbers."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, {tuple(shape)}")
+    return t.data_ptr()
+
+
+def kv_reserve(cache: PagedCache, counts, free, free_count, tokens: int, starts=None, slots=None, granted=None,
+               stream=None):
+    """Pages for the tokens that a step adds to each sequence of a paged cache,
+    pages back from those that it drops.  Sequence b goes from lengths[b] to
+    lengths[b] + counts[b] tokens (negative: dropped from its end); the cache's
+    table and lengths change in place, and so do free (int32, one entry per page
+    of the pool at least: the free pages) and free_count ((1,) int32, how many).
+    Pages come back before any are given out, in order of the sequences; one
+    that needs more than are left gets none, and after it only those that need
+    none; one that would outgrow the table is left as it is.
+    tokens: the sum of the positive counts.  Returns starts (B + 1,) int32, where
+    each sequence's added tokens begin among all, slots (tokens,) int64, the
+    slot of each of them in the pool (-1: not granted) and granted (B,) int32, by
+    how much each length changed."""
+    import torch
+    lib = load()
+    device, B, tokens = cache.device, cache.batch, int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    cp = _ints(counts, "counts", (B,), torch.int32, device)
+    if not isinstance(free, torch.Tensor) or free.dim() != 1:
+        raise TypeError("free must be a 1-D int32 CUDA tensor")
+    fp = _ints(free, "free", free.shape, torch.int32, device)
+    np_ = _ints(free_count, "free_count", (1,), torch.int32, device)
+    if starts is None:
+        starts = _empty((B + 1,), torch.int32, device, stream)
+    if slots is None:
+        slots = _empty((tokens,), torch.int64, device, stream)
+    if granted is None:
+        granted = _empty((B,), torch.int32, device, stream)
+    sp, lp, gp = (_ints(starts, "starts", (B + 1,), torch.int32, device),
+                  _ints(slots, "slots", (tokens,), torch.int64, device),
+                  _ints(granted, "granted", (B,), torch.int32, device))
+    s = _raw_stream(stream, device.index)
+    _check(lib.swm_kv_reserve(cache._p, cp, fp, free.shape[0], np_, tokens, sp, lp, gp, s), "swm_kv_reserve")
+    return starts, slots, granted
+
+
+def kv_append(cache: PagedCache, k, v, slots, weights=None, positions=None, at=None, stream=None):
+    """Write key and value rows of new tokens, k and v (T, heads, dim) fp16, into
+    their slots of a paged cache: slots (T,) int64 as kv_reserve gives them,
+    page * page_size + slot in the page (a slot outside the pool is not
+    written; none may appear twice).  weights (fp32) and positions (int32):
+    (pages, heads, page_size), as paged_attention and kv_evict use them; the new
+    rows' weights become 0 and their positions at[t], at (T,) int32."""
+    import torch
+    lib = load()
+    device = cache.device
+    kp, vp = _heads(k, "k", device), _heads(v, "v", device)
+    T = k.shape[0]
+    if k.shape != (T, cache.heads, cache.dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be (tokens, {cache.heads}, {cache.dim})")
+    sp = _ints(slots, "slots", (T,), torch.int64, device)
+    w = (None, 0, 0) if weights is None else cache._per_slot(weights, "weights", torch.float32)
+    p, ap = (None, 0, 0), None
+    if (positions is None) != (at is None):
+        raise ValueError("positions and at go together")
+    if positions is not None:
+        p = cache._per_slot(positions, "positions", torch.int32)
+        ap = _ints(at, "at", (T,), torch.int32, device)
+    s = _raw_stream(stream, device.index)
+    _check(lib.swm_kv_append(cache._p, *kp, *vp, T, sp, *w, *p, ap, s), "swm_kv_append")
 
 
 def status_str(code: int) -> str:

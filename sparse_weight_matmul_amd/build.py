@@ -22,7 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libswm.so")
 
 SOURCES = ["format.cpp", "colruns.cpp", "api.cpp", "serving.cpp", "decode.hip", "decode_fused.hip", "prefill.hip", "spmspv.hip",
-           "smfmac.hip", "attention.hip", "evict.hip", "logprobs.hip", "prompt.hip"]
+           "smfmac.hip", "attention.hip", "evict.hip", "logprobs.hip", "prompt.hip",
+           "tree.hip", "pages.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

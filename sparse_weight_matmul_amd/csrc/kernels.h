@@ -212,4 +212,44 @@ struct PromptCall {
 int64_t prompt_grid(int64_t T, int64_t B, int64_t Hq);  // workgroups
 hipError_t launch_prompt(const PromptCall& r, hipStream_t s);
 
+// Pages for what a step adds to each sequence, and back.
+struct ReserveCall {
+  const int32_t* counts = nullptr;
+  int32_t *free_pages = nullptr, *free_count = nullptr, *starts = nullptr, *granted = nullptr;
+  int64_t* slots = nullptr;
+  int64_t free_size = 0, tokens = 0;
+};
+hipError_t launch_reserve(const KvView& c, const ReserveCall& r, hipStream_t s);
+
+// Rows of T new tokens into their slots (page * S + slot in the page).
+struct AppendCall {
+  const uint16_t *k = nullptr, *v = nullptr;
+  const int64_t* slots = nullptr;
+  float* weights = nullptr;      // page * w_p + head * w_h + slot, set to 0
+  int32_t* positions = nullptr;  // page * p_p + head * p_h + slot, set to at[t]
+  const int32_t* at = nullptr;
+  int64_t k_t = 0, k_h = 0, v_t = 0, v_h = 0, w_p = 0, w_h = 0, p_p = 0, p_h = 0, T = 0;
+};
+hipError_t launch_append(const KvView& c, const AppendCall& r, hipStream_t s);
+
+// Attention of drafted tokens, the last ones of each sequence, over the cache.
+struct TreeCall {
+  const uint16_t* q = nullptr;
+  uint16_t* out = nullptr;
+  const int32_t *starts = nullptr, *parents = nullptr;
+  const uint8_t* mask = nullptr;
+  int64_t q_t = 0, q_h = 0, o_t = 0, o_h = 0, mask_b = 0;
+  int64_t T = 0, Hq = 0, most = 0;  // most: drafted tokens of a sequence
+  float scale = 1.f;
+};
+constexpr int kTreeMost = 64;
+struct TreePlan {
+  int pieces = 1;      // of a sequence
+  int64_t tiles = 1;   // workgroups along the rows of a sequence and key-value head
+  int64_t grid = 0;    // workgroups of the first launch
+  size_t off_part = 0, bytes = 0;  // workspace
+};
+TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, int64_t most, int num_cus);
+hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, void* ws, hipStream_t s);
+
 }  // namespace swm

@@ -69,6 +69,14 @@ bool rows_overlap(int64_t len, int64_t n0, int64_t stride0, int64_t n1, int64_t 
   return (n0 > 1 && stride0 < len) || (n1 > 1 && stride1 < len) || (n0 > 1 && n1 > 1 && stride0 == stride1);
 }
 
+// Whether rows of a cache's pools surely share memory.
+bool cache_rows_overlap(const swm_kv_cache* c) {
+  return rows_overlap(c->dim, c->pages, c->k_page, c->heads, c->k_head) ||
+         rows_overlap(c->dim, c->pages, c->v_page, c->heads, c->v_head) ||
+         rows_overlap(c->dim, c->page_size, c->k_slot, c->heads, c->k_head) ||
+         rows_overlap(c->dim, c->page_size, c->v_slot, c->heads, c->v_head);
+}
+
 bool heads_fit(const swm_kv_cache* c, int64_t q_heads) {
   return q_heads >= 1 && q_heads % c->heads == 0;
 }
@@ -255,6 +263,136 @@ swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, 
   r.scale = scale;
   r.causal = causal != 0;
   SWM_HIP(swm::launch_prompt(r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
+swm_status swm_kv_reserve(const swm_kv_cache* c, const int32_t* counts, int32_t* free_pages, int64_t free_size,
+                          int32_t* free_count, int64_t tokens, int32_t* starts, int64_t* slots, int32_t* granted,
+                          void* stream) {
+  swm::KvView v;
+  swm_status st = check_cache(c, &v);
+  if (st != SWM_OK) return st;
+  if (free_size < 0 || tokens < 0) return SWM_ERR_INVALID_ARG;
+  if (free_size >= (int64_t(1) << 31) - 65536 || tokens >= (int64_t(1) << 31) - 65536) return SWM_ERR_UNSUPPORTED;
+  if (!starts || !free_count || (!free_pages && free_size > 0) || (!slots && tokens > 0)) return SWM_ERR_INVALID_ARG;
+  if (c->batch > 0 && (!counts || !granted)) return SWM_ERR_INVALID_ARG;
+  if (free_size < c->pages) return SWM_ERR_SHAPE;
+  // what is written is nobody else's
+  if (c->batch > 1 && c->table_ld < c->pages_per_seq) return SWM_ERR_INVALID_ARG;
+  if (c->batch > 0 && (granted == counts || granted == c->lengths || counts == c->lengths || starts == c->lengths ||
+                       starts == counts || starts == granted))
+    return SWM_ERR_INVALID_ARG;
+  swm_log("kv_reserve B=%lld capacity=%lld: %lld tokens, %lld free pages at most", (long long)c->batch,
+          (long long)(c->pages_per_seq * c->page_size), (long long)tokens, (long long)free_size);
+  swm::ReserveCall r;
+  r.counts = counts;
+  r.free_pages = free_pages;
+  r.free_size = free_size;
+  r.free_count = free_count;
+  r.tokens = tokens;
+  r.starts = starts;
+  r.slots = slots;
+  r.granted = granted;
+  SWM_HIP(swm::launch_reserve(v, r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
+swm_status swm_kv_append(const swm_kv_cache* c, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, int64_t tokens, const int64_t* slots, float* weights,
+                         int64_t w_page, int64_t w_head, int32_t* positions, int64_t p_page, int64_t p_head,
+                         const int32_t* at, void* stream) {
+  swm::KvView w;
+  swm_status st = check_cache(c, &w);
+  if (st != SWM_OK) return st;
+  if (tokens < 0 || k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return SWM_ERR_INVALID_ARG;
+  if ((weights && (w_page < 0 || w_head < 0)) || (positions && (p_page < 0 || p_head < 0 || (!at && tokens > 0))))
+    return SWM_ERR_INVALID_ARG;
+  if (tokens == 0) return SWM_OK;
+  if (!c->k || !c->v || !k || !v || !slots) return SWM_ERR_INVALID_ARG;
+  if (k_token % 8 || k_head % 8 || v_token % 8 || v_head % 8 || misaligned(k) || misaligned(v)) return SWM_ERR_ALIGN;
+  if (cache_rows_overlap(c)) return SWM_ERR_INVALID_ARG;
+  if ((weights && rows_overlap(c->page_size, c->pages, w_page, c->heads, w_head)) ||
+      (positions && rows_overlap(c->page_size, c->pages, p_page, c->heads, p_head)))
+    return SWM_ERR_INVALID_ARG;
+  const int64_t most = (int64_t(1) << 31) - 65536;
+  if (tokens >= most || tokens * (c->heads * (c->dim / 8)) / 1024 >= (int64_t(1) << 24) - 1)
+    return SWM_ERR_UNSUPPORTED;
+  swm_log("kv_append tokens=%lld heads=%lld D=%lld%s%s", (long long)tokens, (long long)c->heads, (long long)c->dim,
+          weights ? ", weights" : "", positions ? ", positions" : "");
+  swm::AppendCall r;
+  r.k = static_cast<const uint16_t*>(k);
+  r.v = static_cast<const uint16_t*>(v);
+  r.k_t = k_token;
+  r.k_h = k_head;
+  r.v_t = v_token;
+  r.v_h = v_head;
+  r.T = tokens;
+  r.slots = slots;
+  r.weights = weights;
+  r.w_p = w_page;
+  r.w_h = w_head;
+  r.positions = positions;
+  r.p_p = p_page;
+  r.p_h = p_head;
+  r.at = at;
+  SWM_HIP(swm::launch_append(w, r, static_cast<hipStream_t>(stream)));
+  return SWM_OK;
+}
+
+size_t swm_tree_attention_workspace_bytes(const swm_kv_cache* c, int64_t q_heads, int64_t max_tokens) {
+  if (check_sizes(c) != SWM_OK || !heads_fit(c, q_heads) || q_heads > 65535 || c->batch == 0 || max_tokens < 1 ||
+      max_tokens > swm::kTreeMost)
+    return 0;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  return swm::plan_tree(c->batch, q_heads, c->heads, c->dim, c->pages_per_seq * c->page_size, max_tokens,
+                        swm::num_cus(dev)).bytes;
+}
+
+swm_status swm_tree_attention(const swm_kv_cache* c, const void* q, int64_t q_token, int64_t q_head, int64_t q_heads,
+                              int64_t tokens, const int32_t* starts, const int32_t* parents, int64_t max_tokens,
+                              float scale, const uint8_t* mask, int64_t mask_ld, void* out, int64_t out_token,
+                              int64_t out_head, void* workspace, size_t ws_bytes, void* stream) {
+  swm::KvView v;
+  swm_status st = check_cache(c, &v);
+  if (st != SWM_OK) return st;
+  if (!heads_fit(c, q_heads) || !std::isfinite(scale) || tokens < 0 || max_tokens < 0) return SWM_ERR_INVALID_ARG;
+  if (q_heads > 65535 || max_tokens > swm::kTreeMost || tokens >= (int64_t(1) << 31) - 65536)
+    return SWM_ERR_UNSUPPORTED;
+  if (c->batch == 0 || tokens == 0 || max_tokens == 0) return SWM_OK;
+  const int64_t cap = c->pages_per_seq * c->page_size;
+  if (!q || !out || !starts || q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0) return SWM_ERR_INVALID_ARG;
+  if (mask && mask_ld < cap) return SWM_ERR_INVALID_ARG;
+  if (rows_overlap(c->dim, tokens, out_token, q_heads, out_head)) return SWM_ERR_INVALID_ARG;
+  if (q_token % 8 || q_head % 8 || misaligned(q)) return SWM_ERR_ALIGN;
+  int dev = 0;
+  SWM_HIP(hipGetDevice(&dev));
+  const swm::TreePlan p = swm::plan_tree(c->batch, q_heads, c->heads, c->dim, cap, max_tokens, swm::num_cus(dev));
+  // either launch: at most 2^24 - 1 workgroups of 256 threads
+  if (p.grid >= (int64_t(1) << 24) || tokens * q_heads >= (int64_t(1) << 26)) return SWM_ERR_UNSUPPORTED;
+  if (p.bytes > 0) {
+    if (!workspace || ws_bytes < p.bytes) return SWM_ERR_INVALID_ARG;
+    if (misaligned(workspace)) return SWM_ERR_ALIGN;
+  }
+  swm_log("tree_attention B=%lld tokens=%lld heads=%lld/%lld D=%lld capacity=%lld: %lld workgroups, %d pieces",
+          (long long)c->batch, (long long)tokens, (long long)q_heads, (long long)c->heads, (long long)c->dim,
+          (long long)cap, (long long)p.grid, p.pieces);
+  swm::TreeCall r;
+  r.q = static_cast<const uint16_t*>(q);
+  r.out = static_cast<uint16_t*>(out);
+  r.starts = starts;
+  r.parents = parents;
+  r.mask = mask;
+  r.q_t = q_token;
+  r.q_h = q_head;
+  r.o_t = out_token;
+  r.o_h = out_head;
+  r.mask_b = mask_ld;
+  r.T = tokens;
+  r.Hq = q_heads;
+  r.most = max_tokens;
+  r.scale = scale;
+  SWM_HIP(swm::launch_tree(v, r, p, workspace, static_cast<hipStream_t>(stream)));
   return SWM_OK;
 }
 
