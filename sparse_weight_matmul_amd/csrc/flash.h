@@ -90,17 +90,30 @@ struct State {
 template <int NK, int C>
 __device__ __forceinline__ void scores(const uint16_t* k, int lane, const half8 (&q)[NK], f32x16 (&s)[2]) {
   const int r = lane & 31, h = lane >> 5;
+  half8 f[2][NK];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int x = 0; x < NK; ++x) {
+      const int row = 32 * b + r;
+      f[b][x] = *reinterpret_cast<const half8*>(k + (row * C + key_chunk<C>(row, 2 * x + h)) * 8);
+    }
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
 #pragma unroll
-    for (int x = 0; x < NK; ++x) {
-      const int row = 32 * b + r;
-      const half8 a = *reinterpret_cast<const half8*>(k + (row * C + key_chunk<C>(row, 2 * x + h)) * 8);
-      s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[x], s[b], 0, 0, 0);
-    }
+    for (int x = 0; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][x], q[x], s[b], 0, 0, 0);
   }
+  if (NK > 8) return;  // no registers for it
+  // half of the fragments are on their way before the first product
+  __builtin_amdgcn_sched_group_barrier(0x100, NK, 0);
+#pragma unroll
+  for (int x = 0; x < NK; ++x) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
 }
 
 // The weights of a tile's scores and the running maximum and sum; c > 0: scale
@@ -144,6 +157,7 @@ __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], flo
 template <int ND, int C>
 __device__ __forceinline__ void outputs(State<ND>& st, const uint16_t* v, int lane, const half8 (&p)[4]) {
   const int j = lane & 15, d16 = (lane >> 4) & 1, h = lane >> 5;
+  half8 f[4][ND];
 #pragma unroll
   for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -159,8 +173,20 @@ __device__ __forceinline__ void outputs(State<ND>& st, const uint16_t* v, int la
         w[2 * e] = u[0];
         w[2 * e + 1] = u[1];
       }
-      st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, w), p[x], st.o[d], 0, 0, 0);
+      f[x][d] = __builtin_bit_cast(half8, w);
     }
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[x][d], p[x], st.o[d], 0, 0, 0);
+  if (ND > 4) return;
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * ND, 0);
+#pragma unroll
+  for (int x = 0; x < 3 * ND; ++x) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, ND, 0);
 }
 
 // A wave's part of a tile, n loads of 1 KiB straight into LDS: 16 bytes at
