@@ -86,24 +86,43 @@ struct State {
   }
 };
 
-// Scores of 64 tokens of a tile, before the scale.
-template <int NK, int C>
-__device__ __forceinline__ void scores(const uint16_t* k, int lane, const half8 (&q)[NK], f32x16 (&s)[2]) {
-  const int r = lane & 31, h = lane >> 5;
+// What a lane reads of a tile, in bytes from the tile's start: key chunks 2 x +
+// h of row r, and value chunks of four rows (e: of eight).  The rest of an
+// address is the same for all lanes and goes into the instruction.
+typedef const __attribute__((address_space(3))) uint8_t* lds_bytes;
+template <int NK, int ND, int C>
+struct Reads {
+  lds_bytes base;
+  uint32_t k[NK], v[2][ND];
+  __device__ __forceinline__ Reads(const uint16_t* lds, int lane) : base((lds_bytes)lds) {
+    const int r = lane & 31, j = lane & 15, d16 = (lane >> 4) & 1, h = lane >> 5;
+#pragma unroll
+    for (int x = 0; x < NK; ++x) k[x] = (r * C + key_chunk<C>(r, 2 * x + h)) * 16;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const int row = 8 * e + 4 * h + (j >> 2);
+        v[e][d] = (row * C + value_chunk<C>(row, 4 * d + 2 * d16 + ((j & 3) >> 1))) * 16 + 8 * (j & 1);
+      }
+  }
+};
+
+// Scores of 64 tokens of the key tile at `at` (bytes), before the scale.
+template <int NK, int ND, int C>
+__device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const half8 (&q)[NK], f32x16 (&s)[2]) {
   half8 f[2][NK];
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int x = 0; x < NK; ++x) {
-      const int row = 32 * b + r;
-      f[b][x] = *reinterpret_cast<const half8*>(k + (row * C + key_chunk<C>(row, 2 * x + h)) * 8);
-    }
+    for (int x = 0; x < NK; ++x)  // rows 32 apart have their chunks in the same order
+      f[b][x] = *reinterpret_cast<const __attribute__((address_space(3))) half8*>(a.base + a.k[x] +
+                                                                                   (at + b * 32 * C * 16));
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
+    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][0], q[0], f32x16{}, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
-#pragma unroll
-    for (int x = 0; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][x], q[x], s[b], 0, 0, 0);
+    for (int x = 1; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][x], q[x], s[b], 0, 0, 0);
   }
   if (NK > 8) return;  // no registers for it
   // half of the fragments are on their way before the first product
@@ -153,10 +172,9 @@ __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], flo
   st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-// O^T += V^T P^T over a tile of 64 tokens.
-template <int ND, int C>
-__device__ __forceinline__ void outputs(State<ND>& st, const uint16_t* v, int lane, const half8 (&p)[4]) {
-  const int j = lane & 15, d16 = (lane >> 4) & 1, h = lane >> 5;
+// O^T += V^T P^T over the 64 tokens of the value tile at `at` (bytes).
+template <int NK, int ND, int C>
+__device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a, int at, const half8 (&p)[4]) {
   half8 f[4][ND];
 #pragma unroll
   for (int x = 0; x < 4; ++x)
@@ -164,11 +182,9 @@ __device__ __forceinline__ void outputs(State<ND>& st, const uint16_t* v, int la
     for (int d = 0; d < ND; ++d) {
       u32x4 w;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * x + 8 * e + 4 * h + (j >> 2);
-        const int at = (row * C + value_chunk<C>(row, 4 * d + 2 * d16 + ((j & 3) >> 1))) * 8 + 4 * (j & 1);
+      for (int e = 0; e < 2; ++e) {  // rows 16 apart have their chunks in the same order
         const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(const_cast<uint16_t*>(v) + at));
+            (__attribute__((address_space(3))) s16x4*)(a.base + a.v[e][d] + (at + x * 16 * C * 16)));
         const u32x2 u = __builtin_bit_cast(u32x2, t);
         w[2 * e] = u[0];
         w[2 * e + 1] = u[1];
@@ -200,6 +216,20 @@ __device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const 
   for (int i = 0; i < n; ++i)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + i * step), 16, off[i], 0, 0, 0);
 #endif
+}
+
+// Zeros for the infinities and NaN among eight halves in LDS; whether there were any.
+__device__ __forceinline__ bool clear_odd(uint16_t* at) {
+  u32x4 w = *reinterpret_cast<u32x4*>(at);
+  bool any = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bool lo = (w[e] & 0x7c00u) == 0x7c00u, hi = (w[e] & 0x7c000000u) == 0x7c000000u;
+    any |= lo | hi;
+    w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+  }
+  if (any) *reinterpret_cast<u32x4*>(at) = w;
+  return any;
 }
 
 // s_waitcnt: at most n vector memory operations of this wave outstanding.

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "flash.h"
 #include "kernels.h"
@@ -112,49 +113,44 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
                       sv + buf * kTile + wave * 512, kWaves * 512);
   };
 
+  // Bytes from the start of LDS: two key tiles, then two value tiles.
+  const Reads<NK, ND, C> at(smem, lane);
   State<ND> st;
   st.clear();
-  load(0, 0);
-  int buf = 0;
   bool odd = false;  // a value that is no number, in a tile that some rows see only a part of
-  for (int t0 = 0; t0 < end; t0 += kTokens, buf ^= 1) {
+  // One tile, in buffer `buf`, a constant so that it is part of the reads' offsets.
+  auto step = [&](int t0, auto constant) {
+    constexpr int buf = decltype(constant)::value;
     wait_vm<0>();
     __syncthreads();
     if (t0 + kTokens < end) load(t0 + kTokens, buf ^ 1);
-    uint16_t* kt = sk + buf * kTile;
-    uint16_t* vt = sv + buf * kTile;
     if (kCausal && t0 + kTokens > j * kBlock) {
       // An infinity or NaN times a weight of zero would reach rows that do not
       // see its token: zeros in its place here, added to the rows that do at the end.
+      uint16_t* vt = sv + buf * kTile;
       bool bad = false;
-      for (int i = threadIdx.x; i < kTokens * C; i += 64 * kWaves) {
-        u32x4 w = *reinterpret_cast<u32x4*>(vt + i * 8);
-        bool here = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool lo = (w[e] & 0x7c00u) == 0x7c00u, hi = (w[e] & 0x7c000000u) == 0x7c000000u;
-          here |= lo | hi;
-          w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-        }
-        if (here) *reinterpret_cast<u32x4*>(vt + i * 8) = w;
-        bad |= here;
-      }
+      for (int i = threadIdx.x; i < kTokens * C; i += 64 * kWaves) bad |= clear_odd(vt + i * 8);
       odd |= __syncthreads_or(bad);
     }
-    if (kCausal && t0 > q0 + kRows - 1) continue;
+    if (kCausal && t0 > q0 + kRows - 1) return;
     f32x16 s[2];
-    scores<NK, C>(kt, lane, q, s);
+    scores(at, buf * kTile * 2, q, s);
     if (t0 + kTokens > n || (kCausal && t0 + kTokens - 1 > q0)) {
-      const int last = kCausal ? min(qi, n - 1) : n - 1;
+      const int last = (kCausal ? min(qi, n - 1) : n - 1) - t0 - 4 * h;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (t0 + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3) > last) s[b][i] = neg_inf();
+          if (32 * b + 8 * (i >> 2) + (i & 3) > last) s[b][i] = neg_inf();
     }
     half8 p[4];
     weights(st, s, a.c, p);
-    outputs<ND, C>(st, vt, lane, p);
+    outputs(st, at, (2 + buf) * kTile * 2, p);
+  };
+  load(0, 0);
+  for (int t0 = 0; t0 < end; t0 += 2 * kTokens) {
+    step(t0, std::integral_constant<int, 0>());
+    if (t0 + kTokens < end) step(t0 + kTokens, std::integral_constant<int, 1>());
   }
   const float l = sum_halves(st.l);
   const float inv = l == 0.f ? 0.f : 1.f / l;

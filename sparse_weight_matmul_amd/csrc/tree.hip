@@ -161,6 +161,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     }
   };
 
+  const Reads<NK, ND, C> at(smem, lane);
   State<ND> st;
   st.clear();
   __syncthreads();
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     }
     if (idle) continue;
     f32x16 s[2];
-    scores<NK, C>(kt, lane, q, s);
+    scores(at, buf * kTile * 2, q, s);
     if (drafts_here || ~live) {
       uint64_t on = live;
       if (drafts_here) {
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     }
     half8 p[4];
     weights(st, s, a.c, p);
-    outputs<ND, C>(st, vt, lane, p);
+    outputs(st, at, (2 + buf) * kTile * 2, p);
   }
   if (idle) return;
   const float l = sum_halves(st.l);
