@@ -678,7 +678,8 @@ swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, 
  *  first free_count[0] (DEVICE int32); both are updated.
  *  tokens: rows of slots, the sum of the positive counts.
  *  starts: DEVICE int32, batch + 1: the sums of the positive counts, i.e. where
- *  each sequence's added tokens begin among all (also those not granted).
+ *  each sequence's added tokens begin among all (also those not granted); 2^31 -
+ *  1 where a sum passes it.
  *  slots: DEVICE int64, one per added token, packed so: page * page_size + slot
  *  in the page, -1 where a sequence was not granted its tokens, where the table
  *  names no page and from starts[batch] on.
@@ -732,7 +733,8 @@ swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_tok
  *  parents: DEVICE int32, one per row: the parent's index among the sequence's
  *  drafted tokens, below the row's own; anything else means that the sequence
  *  itself is the parent.  NULL: the tokens follow each other.
- *  max_tokens: at least the largest n_b, at most 64; rows of a sequence past it
+ *  max_tokens: at least the largest n_b, at most 64.  Of a sequence with more
+ *  rows the first max_tokens count, as the cache's last tokens, and the others
  *  are left alone.
  *  mask: as in swm_paged_attention, drafted tokens included.
  *  workspace: DEVICE memory of at least swm_tree_attention_workspace_bytes
