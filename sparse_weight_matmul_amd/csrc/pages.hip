@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 1024;  // of the planning workgroup: sequences of a round
 constexpr int kOwnSlots = 4 * kThreads;  // slots that it fills itself
+constexpr int kRun = 4;         // pages a thread takes or gives back at a time
 constexpr int kFill = 256;      // threads of a workgroup that fills slots, and tokens of it
 constexpr int kHeld = 4096;     // sequences whose starts it holds in LDS
 
@@ -37,36 +38,57 @@ struct ReserveArgs {
 struct Step {
   int old, want, had, has;
 };
-__device__ __forceinline__ Step step_of(const ReserveArgs& a, int b) {
+__device__ __forceinline__ Step step_of(const ReserveArgs& a, int b, int* count) {
   Step s{0, 0, 0, 0};
+  *count = 0;
   if (b >= a.B) return s;
+  *count = a.counts[b];
   s.old = min(max(a.lengths[b], 0), a.cap);
-  const int64_t want = int64_t(s.old) + a.counts[b];
+  const int64_t want = int64_t(s.old) + *count;
   s.want = want > a.cap ? s.old : int(max(want, int64_t(0)));
   s.had = s.old > 0 ? page_index(a.div, s.old - 1) + 1 : 0;
   s.has = s.want > 0 ? page_index(a.div, s.want - 1) + 1 : 0;
   return s;
 }
 
-// Sums of the workgroup's threads up to and including this one; *all: of all.
-// sums: kThreads / 64 entries that nothing else uses until the next barrier but one.
-__device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* sums, int64_t* all) {
+// Sums of three numbers below 2^31 over the workgroup's threads up to and
+// including this one, and of all, by halves of 16 bits, so that 1024 of them
+// stay within 32 bits.  part: where the waves leave theirs, another half every
+// other time, so that one barrier is enough.
+constexpr int kParts = kThreads / 64;  // 16, a row of lanes
+struct Three {
+  int64_t upto[3], all[3];
+};
+__device__ __forceinline__ Three scan_three(int x, int y, int z, uint32_t (*part)[6 * kParts], int* turn) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int o = 1; o < 64; o *= 2) {
-    const int64_t x = __shfl_up(v, o);
-    if (lane >= o) v += x;
+  uint32_t* p = part[*turn];
+  *turn ^= 1;
+  uint32_t v[6] = {uint32_t(x) & 0xffffu, uint32_t(x) >> 16, uint32_t(y) & 0xffffu,
+                   uint32_t(y) >> 16,     uint32_t(z) & 0xffffu, uint32_t(z) >> 16};
+#pragma unroll
+  for (int e = 0; e < 6; ++e) {
+    v[e] = scan_wave(v[e]);
+    if (lane == 63) p[e * kParts + wave] = v[e];
   }
   __syncthreads();
-  if (lane == 63) sums[wave] = v;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int w = 0; w < kThreads / 64; ++w) {
-    const int64_t x = sums[w];
-    if (w < wave) before += x;
-    total += x;
+  // lanes 16 e .. + 15: the waves' sums of half e (e < 4), and of 4 and 5
+  const uint32_t a = scan_wave_rows(p[lane]), b = scan_wave_rows(p[4 * kParts + (lane & 31)]);
+  Three r;
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    uint32_t before[2], all[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int row = 2 * e + f;
+      const uint32_t sums = row < 4 ? a : b;
+      const int first = 16 * (row < 4 ? row : row - 4);
+      all[f] = __builtin_amdgcn_readlane(sums, first + kParts - 1);
+      before[f] = wave ? __builtin_amdgcn_readlane(sums, first + (wave ? wave - 1 : 0)) : 0;
+    }
+    r.upto[e] = (int64_t(before[1]) + v[2 * e + 1] << 16) + before[0] + v[2 * e];
+    r.all[e] = (int64_t(all[1]) << 16) + all[0];
   }
-  *all = total;
-  return v + before;
+  return r;
 }
 
 // The entry of a rising list whose value is the first above i.
@@ -91,36 +113,53 @@ __device__ __forceinline__ int64_t slot_of(const ReserveArgs& a, int b, int at) 
 }
 
 __global__ __launch_bounds__(kThreads) void reserve_kernel(ReserveArgs a) {
-  __shared__ int64_t upto[kThreads];
-  __shared__ int64_t sums[kThreads / 64];
-  __shared__ int32_t first[kThreads];
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ int64_t upto[kThreads];   // pages of the round's sequences, summed
+  __shared__ int64_t rows[kThreads];   // added tokens, summed
+  __shared__ int32_t first[kThreads];  // where a sequence's pages go
+  __shared__ int32_t old[kThreads], got[kThreads];
+  __shared__ uint32_t part[2][6 * kParts];
+  const int tid = threadIdx.x;
+  const bool one = a.B <= kThreads;  // all sequences in one round: nothing is read again
+  int turn = 0;
   int64_t have = min(max(a.free_count[0], 0), a.room);
+  Step s{};
+  int count = 0;
+  Three sums{};
   // pages that come back
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const Step s = step_of(a, b0 + tid);
-    int64_t total;
-    const int64_t u = scan_block(max(s.had - s.has, 0), sums, &total);
+    s = step_of(a, b0 + tid, &count);
+    sums = scan_three(max(s.had - s.has, 0), max(s.has - s.had, 0), max(count, 0), part, &turn);
+    const int64_t total = sums.all[0];
     if (total == 0) continue;
-    upto[tid] = u;
+    upto[tid] = sums.upto[0];
     first[tid] = s.has;
     __syncthreads();
-    for (int64_t i0 = 0; i0 < total; i0 += kThreads) {
-      const int64_t i = i0 + tid;
-      int page = -1;
-      if (i < total) {
-        const int x = first_above(upto, kThreads, i);
-        const int64_t begin = x ? upto[x - 1] : 0;
-        int32_t* e = a.table + int64_t(b0 + x) * a.table_b + first[x] + (i - begin);
-        page = *e;
-        *e = -1;
+    for (int64_t i0 = 0; i0 < total; i0 += kRun * kThreads) {
+      const int64_t i = i0 + kRun * tid;
+      int page[kRun], some = 0;
+      int x = i < total ? first_above(upto, kThreads, i) : 0;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        page[e] = -1;
+        if (i + e >= total) continue;
+        while (upto[x] <= i + e) ++x;
+        int32_t* entry = a.table + int64_t(b0 + x) * a.table_b + first[x] + (i + e - (x ? upto[x - 1] : 0));
+        page[e] = *entry;
+        *entry = -1;
       }
-      const bool is = page >= 0 && page < a.pages;
-      int64_t some;
-      const int64_t at = have + scan_block(is, sums, &some) - 1;
-      if (is && at < a.room) a.free_pages[at] = page;
-      have = min(have + some, int64_t(a.room));
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) some += page[e] >= 0 && page[e] < a.pages;
+      const Three p = scan_three(some, 0, 0, part, &turn);
+      int64_t at = have + p.upto[0] - some;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e)
+        if (page[e] >= 0 && page[e] < a.pages) {
+          if (at < a.room) a.free_pages[at] = page[e];
+          ++at;
+        }
+      have = min(have + p.all[0], int64_t(a.room));
     }
+    __syncthreads();
   }
   __threadfence_block();
   __syncthreads();
@@ -128,47 +167,68 @@ __global__ __launch_bounds__(kThreads) void reserve_kernel(ReserveArgs a) {
   int64_t taken = 0, asked = 0, packed = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
     const int b = b0 + tid;
-    const Step s = step_of(a, b);
-    const int count = b < a.B ? a.counts[b] : 0;
-    int64_t total, rows;
+    if (!one) {
+      s = step_of(a, b, &count);
+      sums = scan_three(0, max(s.has - s.had, 0), max(count, 0), part, &turn);
+    }
     const int need = max(s.has - s.had, 0);
-    const int64_t u = asked + scan_block(need, sums, &total);
-    const int64_t p = packed + scan_block(max(count, 0), sums, &rows);
+    const int64_t u = asked + sums.upto[1], p = packed + sums.upto[2];
     const bool fits = need == 0 || u <= have;
+    const int more = fits ? s.want - s.old : 0;
     if (b < a.B) {
-      if (fits) a.lengths[b] = s.want;
-      else if (a.lengths[b] != s.old) a.lengths[b] = s.old;
-      a.granted[b] = fits ? s.want - s.old : 0;
+      a.lengths[b] = s.old + more;
+      a.granted[b] = more;
       a.starts[b + 1] = int32_t(min(p, int64_t(0x7fffffff)));
       if (b == 0) a.starts[0] = 0;
     }
-    int64_t here;
     upto[tid] = u;
+    rows[tid] = p;
     first[tid] = s.had;
-    scan_block(fits ? need : 0, sums, &here);  // the barriers of the lists too
-    for (int64_t i = asked + tid; i < asked + here; i += kThreads) {
-      const int x = first_above(upto, kThreads, i);
-      const int64_t begin = x ? upto[x - 1] : asked;
-      a.table[int64_t(b0 + x) * a.table_b + first[x] + (i - begin)] = a.free_pages[have - 1 - i];
+    old[tid] = s.old;
+    got[tid] = more;
+    const Three f = scan_three(fits ? need : 0, 0, 0, part, &turn);  // its barrier is the lists' too
+    const int64_t here = asked + f.all[0];
+    for (int64_t i = asked + kRun * tid; i < here; i += kRun * kThreads) {
+      int x = first_above(upto, kThreads, i);
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        if (i + e >= here) break;
+        while (upto[x] <= i + e) ++x;
+        a.table[int64_t(b0 + x) * a.table_b + first[x] + (i + e - (x ? upto[x - 1] : asked))] =
+            a.free_pages[have - 1 - (i + e)];
+      }
     }
-    __syncthreads();
-    taken += here;
-    asked += total;
-    packed += rows;
+    if (!one) __syncthreads();
+    taken += f.all[0];
+    asked += sums.all[1];
+    packed += sums.all[2];
   }
   if (tid == 0) {
     a.free_count[0] = int32_t(have - taken);
     if (a.B == 0) a.starts[0] = 0;
   }
   if (a.tokens > kOwnSlots) return;
-  __threadfence_block();
-  __syncthreads();
+  if (!one) {
+    __threadfence_block();
+    __syncthreads();
+  }
   for (int64_t i = tid; i < a.tokens; i += kThreads) {
     int64_t slot = -1;
     if (i < packed) {
-      const int b = first_above(a.starts + 1, a.B, i);
-      const int g = a.granted[b];
-      if (g > 0) slot = slot_of(a, b, a.lengths[b] - g + int(i - a.starts[b]));
+      if (one) {
+        const int b = first_above(rows, a.B, i);
+        if (got[b] > 0) {
+          const int at = old[b] + int(i - (b ? rows[b - 1] : 0)), x = page_index(a.div, at);
+          // a page just taken comes from the list of free ones: the table's entry may be on its way
+          const int page = x >= first[b] ? a.free_pages[have - 1 - ((b ? upto[b - 1] : 0) + x - first[b])]
+                                         : a.table[int64_t(b) * a.table_b + x];
+          if (page >= 0 && page < a.pages) slot = int64_t(page) * a.S + (at - x * a.S);
+        }
+      } else {
+        const int b = first_above(a.starts + 1, a.B, i);
+        const int g = a.granted[b];
+        if (g > 0) slot = slot_of(a, b, a.lengths[b] - g + int(i - a.starts[b]));
+      }
     }
     a.slots[i] = slot;
   }

@@ -66,5 +66,12 @@ __device__ __forceinline__ uint32_t scan_wave(uint32_t v) {
   v = add_from<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
   return add_from<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
 }
+// The same within each row of 16 lanes.
+__device__ __forceinline__ uint32_t scan_wave_rows(uint32_t v) {
+  v = add_from<0x111, 0xf>(v);
+  v = add_from<0x112, 0xf>(v);
+  v = add_from<0x114, 0xf>(v);
+  return add_from<0x118, 0xf>(v);
+}
 
 }  // namespace swm
