@@ -834,6 +834,18 @@ def _heads(t, name, device=None):
     return t.data_ptr(), token if T > 1 else D, head if H > 1 else 0
 
 
+def _out_like(q, out, stream):
+    """(out, its (pointer, token stride, head stride)) for rows like those of q; a new tensor if there is none."""
+    T, Hq, D = q.shape
+    if out is None:
+        out = _empty((T, Hq, D), q.dtype, q.device, stream)
+        return out, (out.data_ptr(), Hq * D, D)
+    p = _heads(out, "out", q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    return out, p
+
+
 def prompt_attention(q, k, v, starts, scale: Optional[float] = None, causal: bool = True, out=None, stream=None):
     """Attention over whole prompts, packed one behind the other: rows
     starts[b] .. starts[b + 1] - 1 of q (T, Hq, D) and of k and v (T, H, D),
@@ -851,11 +863,7 @@ def prompt_attention(q, k, v, starts, scale: Optional[float] = None, causal: boo
     if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
         raise ValueError(f"k and v must be ({T}, heads, {D})")
     B = _starts(starts, device)
-    if out is None:
-        out = _empty((T, Hq, D), q.dtype, device, stream)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    op = _heads(out, "out", device)
+    out, op = _out_like(q, out, stream)
     s = _raw_stream(stream, device.index)
     _check(lib.swm_prompt_attention(*qp, *kp, *vp, T, Hq, k.shape[1], D, starts.data_ptr(), B,
                                     D ** -0.5 if scale is None else scale, int(bool(causal)), *op, s),
@@ -903,11 +911,7 @@ def tree_attention(cache: PagedCache, q, starts, parents=None, max_tokens: Optio
             raise ValueError(f"parents must be contiguous, ({T},)")
         pp = parents.data_ptr()
     most = min(64, T) if max_tokens is None else int(max_tokens)
-    if out is None:
-        out = _empty((T, Hq, D), q.dtype, device, stream)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    op = _heads(out, "out", device)
+    out, op = _out_like(q, out, stream)
     mp, mask_ld = _mask(cache, mask)
     s = _raw_stream(stream, device.index)
     keep, ws, ws_bytes = _workspace(workspace, cache.tree_workspace_bytes(Hq, most), device, stream)
@@ -953,15 +957,19 @@ def kv_reserve(cache: PagedCache, counts, free, free_count, tokens: int, starts=
     np_ = _ints(free_count, "free_count", (1,), torch.int32, device)
     if starts is None:
         starts = _empty((B + 1,), torch.int32, device, stream)
+    else:
+        _ints(starts, "starts", (B + 1,), torch.int32, device)
     if slots is None:
         slots = _empty((tokens,), torch.int64, device, stream)
+    else:
+        _ints(slots, "slots", (tokens,), torch.int64, device)
     if granted is None:
-        granted = _empty((B,), torch.int32, device, stream)
-    sp, lp, gp = (_ints(starts, "starts", (B + 1,), torch.int32, device),
-                  _ints(slots, "slots", (tokens,), torch.int64, device),
-                  _ints(granted, "granted", (B,), torch.int32, device))
+        granted = _empty_like(counts, stream)
+    else:
+        _ints(granted, "granted", (B,), torch.int32, device)
     s = _raw_stream(stream, device.index)
-    _check(lib.swm_kv_reserve(cache._p, cp, fp, free.shape[0], np_, tokens, sp, lp, gp, s), "swm_kv_reserve")
+    _check(lib.swm_kv_reserve(cache._p, cp, fp, free.shape[0], np_, tokens, starts.data_ptr(), slots.data_ptr(),
+                              granted.data_ptr(), s), "swm_kv_reserve")
     return starts, slots, granted
 
 

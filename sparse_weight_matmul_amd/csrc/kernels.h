@@ -244,10 +244,10 @@ struct TreeCall {
 };
 constexpr int kTreeMost = 64;
 struct TreePlan {
-  int pieces = 1;      // of a sequence
+  int room = 0;        // pieces of all sequences at most; 0: every sequence is one
   int64_t tiles = 1;   // workgroups along the rows of a sequence and key-value head
   int64_t grid = 0;    // workgroups of the first launch
-  size_t off_part = 0, bytes = 0;  // workspace
+  size_t off_ml = 0, off_part = 0, bytes = 0;  // workspace
 };
 TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, int64_t most, int num_cus);
 hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, void* ws, hipStream_t s);

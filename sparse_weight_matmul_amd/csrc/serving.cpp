@@ -359,6 +359,8 @@ swm_status swm_tree_attention(const swm_kv_cache* c, const void* q, int64_t q_to
   if (!heads_fit(c, q_heads) || !std::isfinite(scale) || tokens < 0 || max_tokens < 0) return SWM_ERR_INVALID_ARG;
   if (q_heads > 65535 || max_tokens > swm::kTreeMost || tokens >= (int64_t(1) << 31) - 65536)
     return SWM_ERR_UNSUPPORTED;
+  // a load's rows are addressed from its first with 32-bit byte offsets
+  if (c->k_slot >= (int64_t(1) << 26) || c->v_slot >= (int64_t(1) << 26)) return SWM_ERR_UNSUPPORTED;
   if (c->batch == 0 || tokens == 0 || max_tokens == 0) return SWM_OK;
   const int64_t cap = c->pages_per_seq * c->page_size;
   if (!q || !out || !starts || q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0) return SWM_ERR_INVALID_ARG;
@@ -374,9 +376,9 @@ swm_status swm_tree_attention(const swm_kv_cache* c, const void* q, int64_t q_to
     if (!workspace || ws_bytes < p.bytes) return SWM_ERR_INVALID_ARG;
     if (misaligned(workspace)) return SWM_ERR_ALIGN;
   }
-  swm_log("tree_attention B=%lld tokens=%lld heads=%lld/%lld D=%lld capacity=%lld: %lld workgroups, %d pieces",
+  swm_log("tree_attention B=%lld tokens=%lld heads=%lld/%lld D=%lld capacity=%lld: %lld workgroups, %d pieces at most",
           (long long)c->batch, (long long)tokens, (long long)q_heads, (long long)c->heads, (long long)c->dim,
-          (long long)cap, (long long)p.grid, p.pieces);
+          (long long)cap, (long long)p.grid, p.room);
   swm::TreeCall r;
   r.q = static_cast<const uint16_t*>(q);
   r.out = static_cast<uint16_t*>(out);

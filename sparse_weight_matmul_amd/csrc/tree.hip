@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "flash.h"
 #include "kernels.h"
@@ -22,23 +23,26 @@ using namespace flash;
 
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
+constexpr int kMaxCut = 128;            // sequences whose lengths a wave holds, two a lane
 
 struct TreeArgs {
   const uint16_t *q, *k, *v;
   uint16_t* out;
   const int32_t *starts, *parents, *table, *lengths;
   const uint8_t* mask;
-  float* ml;    // [unit][piece][row of the unit][2] maximum (in units of log2) and sum
-  float* part;  // [unit][piece][row of the unit][D] unnormalised outputs
+  int32_t* plan;  // first piece and number of pieces of each sequence
+  float* ml;      // [piece][key-value head][row][2] maximum (in units of log2) and sum
+  float* part;    // [piece][key-value head][row][D] unnormalised outputs
   int64_t q_t, q_h, o_t, o_h;
   int64_t k_p, k_s, k_h, v_p, v_s, v_h;
   int64_t table_b, mask_b;
   int32_t B, T, Hq, Hkv, G, D, S, pages, cap, per_seq, most;
-  int32_t pieces, tiles, rows;  // rows: of a unit in the workspace, whole workgroups
+  int32_t room;         // pieces of all sequences at most; 0: every sequence is one
+  int32_t tiles, rows;  // workgroups along a unit's rows; rows of a piece in the workspace
   float c;
   uint32_t flip;
   bool zero;
-  PageDiv div, per_g;
+  PageDiv div, per_g, per_pair, per_hkv;
 };
 
 // A sequence's drafted tokens: packed rows *first .. + *n - 1.
@@ -71,21 +75,91 @@ __device__ __forceinline__ uint64_t ancestors(const TreeArgs& a, int first, int 
   return sees;
 }
 
-template <int NK, int ND, int C>
+// The pieces that the sequences are cut into: `each` tiles of 64 tokens, the
+// fewest (two at least) with which they are a.room in all.  Lane l has sequences 2 l and
+// 2 l + 1, pieces first .. mid - 1 and mid .. last - 1.  A quotient that is
+// one off only moves the last piece's end.
+struct Cuts {
+  uint32_t each;
+  int first, mid, last;
+};
+__device__ __forceinline__ uint32_t tiles_of(const TreeArgs& a, int b) {
+  if (b >= a.B) return 0;
+  int first, n;
+  drafted(a, b, &first, &n);
+  return n ? max((min(max(a.lengths[b], 0), a.cap) + kTokens - 1) / kTokens, 1) : 0;
+}
+__device__ __forceinline__ Cuts cut(const TreeArgs& a, int lane) {
+  const uint32_t t0 = tiles_of(a, 2 * lane), t1 = tiles_of(a, 2 * lane + 1);
+  const uint32_t total = wave_sum(t0 + t1), room = a.room;
+  uint32_t c0, c1;
+  auto count = [&](uint32_t q) {
+    const float inv = 1.f / float(q);
+    c0 = t0 ? max(uint32_t(float(t0 + q - 1) * inv), 1u) : 0;
+    c1 = t1 ? max(uint32_t(float(t1 + q - 1) * inv), 1u) : 0;
+    return wave_sum(c0 + c1);
+  };
+  uint32_t q = max((total + room - 1) / room, 2u);
+  if (count(q) > room) {
+    uint32_t low = q;
+    q = max(uint32_t(wave_max(int(max(t0, t1)))), low + 1);  // whole sequences fit
+    while (q - low > max(low / 16, 1u)) {
+      const uint32_t mid = low + (q - low) / 2;
+      if (count(mid) > room)
+        low = mid;
+      else
+        q = mid;
+    }
+    count(q);
+  }
+  Cuts r;
+  const uint32_t upto = scan_wave(c0 + c1);
+  r.each = q;
+  r.last = int(upto);
+  r.mid = int(upto - c1);
+  r.first = int(upto - c1 - c0);
+  return r;
+}
+
+// One workgroup: 128 query rows (drafted token x query head of the group) of a
+// sequence and key-value head, over a piece of its tokens.  kUniform: the rows of
+// one load instruction are on one page, so that its address is scalar.
+template <int NK, int ND, int C, bool kUniform>
 __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs a) {
   constexpr int kTile = kTokens * C * 8;  // halves
   constexpr int kLoads = C / kWaves;      // 1 KiB each, of a wave and tile
+  constexpr int kSpan = 64 / C;           // rows of one
   extern __shared__ uint16_t smem[];
   uint16_t* sk = smem;              // [2][kTile]
   uint16_t* sv = smem + 2 * kTile;  // [2][kTile]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
-  int x = blockIdx.x;
-  const int unit = x / (a.pieces * a.tiles);
-  x -= unit * a.pieces * a.tiles;
-  const int piece = x / a.tiles, tile = x - piece * a.tiles;
-  const int b = unit / a.Hkv, hkv = unit - b * a.Hkv;
+  // Workgroups go round the eight XCDs: those that read the same tokens are
+  // eight apart, so that they share an L2.
+  const int group = page_index(a.per_pair, blockIdx.x), rest = blockIdx.x - group * 8 * a.tiles;
+  const int tile = rest >> 3, pair = group * 8 + (rest & 7);
+  const int piece = page_index(a.per_hkv, pair), hkv = pair - piece * a.Hkv;
+  if (piece >= (a.room > 0 ? a.room : a.B)) return;
+  int b = piece, nth = 0, count = 1;
+  uint32_t each = 0;
+  if (a.room > 0) {
+    const Cuts c = cut(a, lane);
+    if (blockIdx.x == 0 && wave == 0) {
+      if (2 * lane < a.B) a.plan[4 * lane] = c.first, a.plan[4 * lane + 1] = c.mid - c.first;
+      if (2 * lane + 1 < a.B) a.plan[4 * lane + 2] = c.mid, a.plan[4 * lane + 3] = c.last - c.mid;
+    }
+    const uint64_t in = __builtin_amdgcn_ballot_w64(piece >= c.first && piece < c.last);
+    if (in == 0) return;  // more workgroups than pieces
+    const int l = __builtin_ctzll(in);
+    const int mid = __builtin_amdgcn_readlane(c.mid, l);
+    const bool second = piece >= mid;
+    b = 2 * l + second;
+    nth = piece - (second ? mid : __builtin_amdgcn_readlane(c.first, l));
+    count = second ? __builtin_amdgcn_readlane(c.last, l) - mid : mid - __builtin_amdgcn_readlane(c.first, l);
+    each = __builtin_amdgcn_readfirstlane(c.each);
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
   int first, drafts;
   drafted(a, b, &first, &drafts);
   first = __builtin_amdgcn_readfirstlane(first);
@@ -94,10 +168,9 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
   if (tile * kBlock >= rows) return;
   const int n = __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), a.cap));
   const int own = n - drafts;  // tokens before the drafted ones; negative where the length does not count them all
-  // the piece's tokens
-  const int tiles_n = (n + kTokens - 1) / kTokens;
-  const int each = (tiles_n + a.pieces - 1) / a.pieces * kTokens;
-  const int begin = min(piece * each, n), end = min(begin + each, n);
+  const int begin = __builtin_amdgcn_readfirstlane(min(int64_t(nth) * each * kTokens, int64_t(n)));
+  const int end = __builtin_amdgcn_readfirstlane(
+      nth == count - 1 ? n : min(int64_t(nth + 1) * each * kTokens, int64_t(n)));
   const int32_t* row = a.table + int64_t(b) * a.table_b;
   const uint8_t* mask = a.mask ? a.mask + int64_t(b) * a.mask_b : nullptr;
   const uint16_t* kh = a.k + int64_t(hkv) * a.k_h;
@@ -125,80 +198,94 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     sees = uint64_t(hi) << 32 | lo;
   }
 
-  // Rows that are not loaded hold what was there before: zeros, or rows that
-  // were live for all.
-  for (int i = threadIdx.x; i < 4 * kTile / 8; i += 64 * kWaves) *reinterpret_cast<u32x4*>(smem + i * 8) = u32x4{0, 0, 0, 0};
+  // Key dimensions that only pad the products: zeros, never loaded.
+  if (a.D < 16 * NK) {
+    for (int i = threadIdx.x; i < 2 * kTile / 8; i += 64 * kWaves)
+      *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
+  }
 
-  // The place of token t0 + lane: its page, or -1 where it is not live.
+  // The page of token t0 + lane, always one of the pool; the top bit is set
+  // where the token is not live.
+  constexpr int kDead = int(0x80000000u), kPage = 0x7fffffff;
   auto place = [&](int t0) {
     const int t = t0 + lane;
-    const int i = page_index(a.div, min(t, a.cap - 1));
-    int page = t < end ? row[min(i, a.per_seq - 1)] : -1;
-    if (page >= a.pages) page = -1;
-    if (mask && t < end && mask[t] == 0) page = -1;
+    int page = kDead;
+    if (t < end) {
+      const int id = row[page_index(a.div, t)];
+      if (id >= 0 && id < a.pages) page = mask && mask[t] == 0 ? id | kDead : id;
+    }
     return page;
   };
+  // Of the wave's loads: the row of a tile and the lane's bytes in it, by the first row of each.
+  const int lr = lane / C, lc = lane % C;
+  uint32_t k_off[kLoads], v_off[kLoads];
+  bool k_in[kLoads], v_in[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int rw = (i * kWaves + wave) * kSpan + lr;
+    const int kc = key_chunk<C>(rw, lc) * 8, vc = value_chunk<C>(rw, lc) * 8;
+    k_in[i] = kc < a.D;
+    v_in[i] = vc < a.D;
+    k_off[i] = uint32_t(lr * int(a.k_s) + kc) * 2;
+    v_off[i] = uint32_t(lr * int(a.v_s) + vc) * 2;
+  }
+  // A tile into buffer buf; rows that are not live become zeros.
   auto load = [&](int t0, int pages, int buf) {
+    const uint64_t live = __builtin_amdgcn_ballot_w64(pages >= 0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int at = (i * kWaves + wave) * 64 + lane, rw = at / C, c = at % C;
-      const int page = __shfl(pages, rw);
-      const int t = t0 + rw, slot = t - page_index(a.div, t) * a.S;
-      const int kc = key_chunk<C>(rw, c) * 8;
-      if (page >= 0 && kc < a.D)
-        __builtin_amdgcn_global_load_lds(kh + page * a.k_p + slot * a.k_s + kc,
-                                         (lds_ptr)(sk + buf * kTile + (i * kWaves + wave) * 512), 16, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int at = (i * kWaves + wave) * 64 + lane, rw = at / C, c = at % C;
-      const int page = __shfl(pages, rw);
-      const int t = t0 + rw, slot = t - page_index(a.div, t) * a.S;
-      const int vc = value_chunk<C>(rw, c) * 8;
-      if (page >= 0 && vc < a.D)
-        __builtin_amdgcn_global_load_lds(vh + page * a.v_p + slot * a.v_s + vc,
-                                         (lds_ptr)(sv + buf * kTile + (i * kWaves + wave) * 512), 16, 0, 0);
+      const int r0 = (i * kWaves + wave) * kSpan, rw = r0 + lr;
+      uint16_t* dk = sk + buf * kTile + (i * kWaves + wave) * 512;
+      uint16_t* dv = sv + buf * kTile + (i * kWaves + wave) * 512;
+      const uint8_t *ks, *vs;
+      if (kUniform) {
+        const int page = __builtin_amdgcn_readlane(pages, r0) & kPage, t = t0 + r0, slot = t - page_index(a.div, t) * a.S;
+        ks = reinterpret_cast<const uint8_t*>(kh + page * a.k_p + slot * a.k_s) + k_off[i];
+        vs = reinterpret_cast<const uint8_t*>(vh + page * a.v_p + slot * a.v_s) + v_off[i];
+      } else {
+        const int page = __shfl(pages, rw) & kPage, t = t0 + rw, slot = t - page_index(a.div, t) * a.S;
+        ks = reinterpret_cast<const uint8_t*>(kh + page * a.k_p + (slot - lr) * a.k_s) + k_off[i];
+        vs = reinterpret_cast<const uint8_t*>(vh + page * a.v_p + (slot - lr) * a.v_s) + v_off[i];
+      }
+      if (~live == 0 && a.D == C * 8) {
+        __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
+      } else {
+        const bool on = (live >> rw) & 1;
+        if (on && k_in[i]) __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
+        if (on && v_in[i]) __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
+        if (!on) *reinterpret_cast<u32x4*>(dv + lane * 8) = u32x4{0, 0, 0, 0};
+      }
     }
   };
 
   const Reads<NK, ND, C> at(smem, lane);
   State<ND> st;
   st.clear();
-  __syncthreads();
-  int now = place(begin), next = place(begin + kTokens);
-  if (begin < end) load(begin, now, 0);
-  int buf = 0;
   bool odd = false;
-  for (int t0 = begin; t0 < end; t0 += kTokens, buf ^= 1) {
+  int now = place(begin), next = place(begin + kTokens);
+  if (a.D < 16 * NK) __syncthreads();
+  if (begin < end) load(begin, now, 0);
+  // One tile, in buffer `buf`.
+  auto step = [&](int t0, auto constant) {
+    constexpr int buf = decltype(constant)::value;
     const uint64_t live = __builtin_amdgcn_ballot_w64(now >= 0);
     now = next;
     wait_vm<0>();
     __syncthreads();
-    if (t0 + kTokens < end) load(t0 + kTokens, next, buf ^ 1);
+    if (t0 + kTokens < end) load(t0 + kTokens, now, buf ^ 1);
     next = place(t0 + 2 * kTokens);
-    uint16_t* kt = sk + buf * kTile;
-    uint16_t* vt = sv + buf * kTile;
     const bool drafts_here = t0 + kTokens > own;
     if (drafts_here) {
       // A drafted token's infinity or NaN must not reach rows that do not see
       // it (its weight there is zero): zeros in its place, added at the end.
+      uint16_t* vt = sv + buf * kTile;
       bool bad = false;
-      for (int i = threadIdx.x; i < kTokens * C; i += 64 * kWaves) {
-        if (t0 + i / C < own) continue;
-        u32x4 w = *reinterpret_cast<u32x4*>(vt + i * 8);
-        bool here = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool lo = (w[e] & 0x7c00u) == 0x7c00u, hi = (w[e] & 0x7c000000u) == 0x7c000000u;
-          here |= lo | hi;
-          w[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
-        }
-        if (here) *reinterpret_cast<u32x4*>(vt + i * 8) = w;
-        bad |= here;
-      }
+      for (int i = threadIdx.x; i < kTokens * C; i += 64 * kWaves)
+        if (t0 + i / C >= own && value_chunk<C>(i / C, i % C) * 8 < a.D) bad |= clear_odd(vt + i * 8);
       odd |= __syncthreads_or(bad);
     }
-    if (idle) continue;
+    if (idle) return;
     f32x16 s[2];
     scores(at, buf * kTile * 2, q, s);
     if (drafts_here || ~live) {
@@ -219,6 +306,10 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     half8 p[4];
     weights(st, s, a.c, p);
     outputs(st, at, (2 + buf) * kTile * 2, p);
+  };
+  for (int t0 = begin; t0 < end; t0 += 2 * kTokens) {
+    step(t0, std::integral_constant<int, 0>());
+    if (t0 + kTokens < end) step(t0 + kTokens, std::integral_constant<int, 1>());
   }
   if (idle) return;
   const float l = sum_halves(st.l);
@@ -238,13 +329,13 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     }
   }
   if (m0 + r >= rows) return;
-  if (a.pieces > 1) {
-    const int64_t at = (int64_t(unit) * a.pieces + piece) * a.rows + m0 + r;
+  if (count > 1) {
+    const int64_t to = (int64_t(piece) * a.Hkv + hkv) * a.rows + m0 + r;
     if (h == 0) {
-      a.ml[2 * at] = st.m * a.c;
-      a.ml[2 * at + 1] = l;
+      a.ml[2 * to] = st.m * a.c;
+      a.ml[2 * to + 1] = l;
     }
-    float* dst = a.part + at * a.D;
+    float* dst = a.part + to * a.D;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -291,16 +382,18 @@ __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
   drafted(a, lo, &first, &drafts);
   const int i = int(t) - first;
   if (i < 0 || i >= drafts) return;
+  const int pieces = a.plan[2 * lo + 1];
+  if (pieces < 2) return;  // written already
   const int hkv = page_index(a.per_g, qh);
-  const int64_t unit = int64_t(lo) * a.Hkv + hkv;
-  const int64_t from = unit * a.pieces * a.rows + int64_t(i) * a.G + (qh - hkv * a.G);
+  const int64_t next = int64_t(a.Hkv) * a.rows;
+  const int64_t from = (int64_t(a.plan[2 * lo]) * a.Hkv + hkv) * a.rows + int64_t(i) * a.G + (qh - hkv * a.G);
   float m = neg_inf();
-  for (int p = 0; p < a.pieces; ++p) m = fmaxf(m, a.ml[2 * (from + int64_t(p) * a.rows)]);
+  for (int p = 0; p < pieces; ++p) m = fmaxf(m, a.ml[2 * (from + p * next)]);
   const float base = m == neg_inf() ? 0.f : m;
   float l = 0.f;
   float4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p < a.pieces; ++p) {
-    const int64_t x = from + int64_t(p) * a.rows;
+  for (int p = 0; p < pieces; ++p) {
+    const int64_t x = from + p * next;
     const float f = __builtin_amdgcn_exp2f(a.ml[2 * x] - base);
     const float4 v = *reinterpret_cast<const float4*>(a.part + x * a.D + d);
     l += f * a.ml[2 * x + 1];
@@ -317,32 +410,46 @@ __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
   dst[3] = __builtin_bit_cast(uint16_t, _Float16(o.w * inv));
 }
 
-template <int NK, int ND, int C>
-hipError_t launch(const TreeArgs& a, uint32_t grid, hipStream_t s) {
+template <int NK, int ND, int C, bool kUniform>
+hipError_t launch_as(const TreeArgs& a, uint32_t grid, hipStream_t s) {
   constexpr int kLds = 4 * kTokens * C * 16;
   if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C, kUniform>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  tree_kernel<NK, ND, C><<<grid, 64 * kWaves, kLds, s>>>(a);
+  tree_kernel<NK, ND, C, kUniform><<<grid, 64 * kWaves, kLds, s>>>(a);
   return hipGetLastError();
+}
+
+template <int NK, int ND, int C>
+hipError_t launch(const TreeArgs& a, uint32_t grid, hipStream_t s) {
+  return a.S % (64 / C) == 0 ? launch_as<NK, ND, C, true>(a, grid, s) : launch_as<NK, ND, C, false>(a, grid, s);
 }
 
 }  // namespace
 
+// How the work is dealt: see the kernel.
 TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, int64_t most, int num_cus) {
   TreePlan p;
   const int64_t rows = most * (Hq / Hkv);
   p.tiles = std::max<int64_t>(1, (rows + kBlock - 1) / kBlock);
-  const int64_t units = B * Hkv;
+  const int64_t units = Hkv * p.tiles;  // of a sequence
   const int64_t steps = (cap + kTokens - 1) / kTokens;
-  p.pieces = int(std::max<int64_t>(1, std::min<int64_t>(2 * num_cus / std::max<int64_t>(1, units * p.tiles), steps / 4)));
-  p.grid = units * p.pieces * p.tiles;
+  const int64_t slots = (D <= 128 ? 2 : 1) * int64_t(num_cus);  // workgroups at a time
+  if (B >= 1 && B <= kMaxCut && steps > 2 && units * B <= 4 * slots) {
+    int64_t k = 1;
+    while (B > 1 && k < 4 && k * slots < 4 * B * units) ++k;
+    p.room = int(std::min<int64_t>(k * slots / units, (steps + 1) / 2 * B));
+    if (p.room <= B) p.room = 0;
+  }
+  const int64_t pairs = (p.room ? p.room : B) * Hkv;
+  p.grid = (pairs + 7) / 8 * 8 * p.tiles;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  if (p.pieces > 1) {
-    const size_t all = size_t(units) * size_t(p.pieces) * size_t(p.tiles) * kBlock;
-    p.off_part = up(all * 8);
+  if (p.room) {
+    p.off_ml = up(size_t(B) * 8);
+    const size_t all = size_t(pairs) * size_t(p.tiles) * kBlock;
+    p.off_part = p.off_ml + up(all * 8);
     p.bytes = p.off_part + all * size_t(D) * 4;
   }
   return p;
@@ -382,7 +489,7 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
   a.per_seq = int(c.per_seq);
   a.cap = int(c.per_seq * c.S);
   a.most = int(r.most);
-  a.pieces = p.pieces;
+  a.room = p.room;
   a.tiles = int(p.tiles);
   a.rows = int(p.tiles) * kBlock;
   a.zero = r.scale == 0.f;
@@ -390,9 +497,13 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
   a.flip = r.scale < 0.f ? 0x80008000u : 0u;
   a.div = page_div(c.S);
   a.per_g = page_div(a.G);
-  if (p.pieces > 1) {
-    a.ml = static_cast<float*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.off_part);
+  a.per_pair = page_div(8 * p.tiles);
+  a.per_hkv = page_div(c.Hkv);
+  if (p.room) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.plan = reinterpret_cast<int32_t*>(w);
+    a.ml = reinterpret_cast<float*>(w + p.off_ml);
+    a.part = reinterpret_cast<float*>(w + p.off_part);
   }
   const uint32_t grid = uint32_t(p.grid);
   const hipError_t e = a.D <= 64    ? launch<4, 2, 8>(a, grid, s)
@@ -400,7 +511,7 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
                        : a.D <= 128 ? launch<8, 4, 16>(a, grid, s)
                        : a.D <= 192 ? launch<12, 6, 32>(a, grid, s)
                                     : launch<16, 8, 32>(a, grid, s);
-  if (e != hipSuccess || p.pieces == 1) return e;
+  if (e != hipSuccess || !p.room) return e;
   const int per = a.D <= 64 ? 16 : a.D <= 128 ? 32 : 64;
   const int64_t rows = r.T * r.Hq;
   tree_join_kernel<<<dim3(uint32_t((rows + kJoin / per - 1) / (kJoin / per))), kJoin, 0, s>>>(a, per);

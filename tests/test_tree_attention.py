@@ -405,7 +405,7 @@ def call(cache, **change):
 @pytest.mark.parametrize("fields,code", [
     (dict(k=None), 1), (dict(lengths=None), 1), (dict(table=None), 1), (dict(batch=-1), 1), (dict(pages=0), 1),
     (dict(k_slot=-64), 1), (dict(dim=60), 8), (dict(batch=65536), 8), (dict(page_size=1 << 30), 8), (dict(k=4104), 3),
-    (dict(v_head=4), 3),
+    (dict(v_head=4), 3), (dict(k_slot=1 << 26), 8), (dict(v_slot=1 << 26), 8),
 ])
 def test_cache_refusals(fields, code):
     assert call(cache_struct(**fields)) == code
