@@ -108,23 +108,23 @@ struct Reads {
   }
 };
 
-// Scores of 64 tokens of the key tile at `at` (bytes), before the scale.
-template <int NK, int ND, int C>
-__device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const half8 (&q)[NK], f32x16 (&s)[2]) {
-  half8 f[2][NK];
+// Scores of 32 NB tokens of the key tile at `at` (bytes), before the scale.
+template <int NB, int NK, int ND, int C>
+__device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const half8 (&q)[NK], f32x16 (&s)[NB]) {
+  half8 f[NB][NK];
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int x = 0; x < NK; ++x)  // rows 32 apart have their chunks in the same order
       f[b][x] = *reinterpret_cast<const __attribute__((address_space(3))) half8*>(a.base + a.k[x] +
                                                                                    (at + b * 32 * C * 16));
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < NB; ++b) {
     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][0], q[0], f32x16{}, 0, 0, 0);
 #pragma unroll
     for (int x = 1; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][x], q[x], s[b], 0, 0, 0);
   }
-  if (NK > 8) return;  // no registers for it
+  if (NB < 2 || NK > 8) return;  // nothing to overlap, or no registers for it
   // half of the fragments are on their way before the first product
   __builtin_amdgcn_sched_group_barrier(0x100, NK, 0);
 #pragma unroll
@@ -137,11 +137,11 @@ __device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const 
 
 // The weights of a tile's scores and the running maximum and sum; c > 0: scale
 // in units of log2.  The maximum follows when a row has outgrown it by kLazy.
-template <int ND>
-__device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], float c, half8 (&p)[4]) {
+template <int NB, int ND>
+__device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[NB], float c, half8 (&p)[2 * NB]) {
   float mx = s[0][0];
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
   mx = max_halves(mx);
@@ -158,7 +158,7 @@ __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], flo
   const float base = st.m == neg_inf() ? 0.f : kUp - st.m * c;  // nothing live so far: weights of 2^-inf
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
+  for (int x = 0; x < 2 * NB; ++x) {
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
@@ -172,12 +172,12 @@ __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[2], flo
   st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-// O^T += V^T P^T over the 64 tokens of the value tile at `at` (bytes).
-template <int NK, int ND, int C>
-__device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a, int at, const half8 (&p)[4]) {
-  half8 f[4][ND];
+// O^T += V^T P^T over the 16 NX tokens of the value tile at `at` (bytes).
+template <int NX, int NK, int ND, int C>
+__device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a, int at, const half8 (&p)[NX]) {
+  half8 f[NX][ND];
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
+  for (int x = 0; x < NX; ++x)
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
       u32x4 w;
@@ -192,13 +192,13 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
       f[x][d] = __builtin_bit_cast(half8, w);
     }
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
+  for (int x = 0; x < NX; ++x)
 #pragma unroll
     for (int d = 0; d < ND; ++d) st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[x][d], p[x], st.o[d], 0, 0, 0);
   if (ND > 4) return;
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * ND, 0);
 #pragma unroll
-  for (int x = 0; x < 3 * ND; ++x) {
+  for (int x = 0; x < (NX - 1) * ND; ++x) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
   }

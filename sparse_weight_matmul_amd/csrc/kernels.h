@@ -245,6 +245,8 @@ struct TreeCall {
 constexpr int kTreeMost = 64;
 struct TreePlan {
   int room = 0;        // pieces of all sequences at most; 0: every sequence is one
+  bool few = false;    // at most 32 query rows of a sequence and key-value head
+  bool order = false;  // whole sequences, the longest first
   int64_t tiles = 1;   // workgroups along the rows of a sequence and key-value head
   int64_t grid = 0;    // workgroups of the first launch
   size_t off_ml = 0, off_part = 0, bytes = 0;  // workspace

@@ -23,6 +23,9 @@ using namespace flash;
 
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
+// waves over few query rows, so that their tiles fill LDS
+constexpr int few_waves(int chunks) { return chunks == 32 ? 4 : 8; }
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
 constexpr int kMaxCut = 128;            // sequences whose lengths a wave holds, two a lane
 
 struct TreeArgs {
@@ -38,6 +41,7 @@ struct TreeArgs {
   int64_t table_b, mask_b;
   int32_t B, T, Hq, Hkv, G, D, S, pages, cap, per_seq, most;
   int32_t room;         // pieces of all sequences at most; 0: every sequence is one
+  int32_t order;        // whole sequences, the longest first
   int32_t tiles, rows;  // workgroups along a unit's rows; rows of a piece in the workspace
   float c;
   uint32_t flip;
@@ -50,6 +54,11 @@ __device__ __forceinline__ void drafted(const TreeArgs& a, int b, int* first, in
   const int s0 = min(max(a.starts[b], 0), a.T), s1 = min(max(a.starts[b + 1], 0), a.T);
   *first = s0;
   *n = min(max(s1 - s0, 0), a.most);
+}
+
+// Lane `from`'s value.
+__device__ __forceinline__ uint64_t pick(uint64_t v, int from) {
+  return uint64_t(uint32_t(__shfl(uint32_t(v >> 32), from))) << 32 | uint32_t(__shfl(uint32_t(v), from));
 }
 
 // Which drafted tokens the lane's one sees: bit j for token j.  Every lane
@@ -65,32 +74,36 @@ __device__ __forceinline__ uint64_t ancestors(const TreeArgs& a, int first, int 
 #pragma unroll
   for (int r = 0; r < 6; ++r) {
     const int from = max(up, 0);
-    const uint32_t lo = __shfl(uint32_t(sees), from), hi = __shfl(uint32_t(sees >> 32), from);
+    const uint64_t more = pick(sees, from);
     const int next = __shfl(up, from);
     if (up >= 0) {
-      sees |= uint64_t(hi) << 32 | lo;
+      sees |= more;
       up = next;
     }
   }
   return sees;
 }
 
-// The pieces that the sequences are cut into: `each` tiles of 64 tokens, the
-// fewest (two at least) with which they are a.room in all.  Lane l has sequences 2 l and
-// 2 l + 1, pieces first .. mid - 1 and mid .. last - 1.  A quotient that is
-// one off only moves the last piece's end.
+// Tokens of a sequence in units of kUnit, one at least where it has drafted ones.
+template <int kUnit>
+__device__ __forceinline__ uint32_t units_of(const TreeArgs& a, int b) {
+  if (b >= a.B) return 0;
+  int first, n;
+  drafted(a, b, &first, &n);
+  return n ? max((min(max(a.lengths[b], 0), a.cap) + kUnit - 1) / kUnit, 1) : 0;
+}
+
+// The pieces that the sequences are cut into: `each` units, the fewest (two at
+// least) with which they are a.room in all.  Lane l has sequences 2 l and 2 l +
+// 1, pieces first .. mid - 1 and mid .. last - 1.  A quotient that is one off
+// only moves the last piece's end.
 struct Cuts {
   uint32_t each;
   int first, mid, last;
 };
-__device__ __forceinline__ uint32_t tiles_of(const TreeArgs& a, int b) {
-  if (b >= a.B) return 0;
-  int first, n;
-  drafted(a, b, &first, &n);
-  return n ? max((min(max(a.lengths[b], 0), a.cap) + kTokens - 1) / kTokens, 1) : 0;
-}
+template <int kUnit>
 __device__ __forceinline__ Cuts cut(const TreeArgs& a, int lane) {
-  const uint32_t t0 = tiles_of(a, 2 * lane), t1 = tiles_of(a, 2 * lane + 1);
+  const uint32_t t0 = units_of<kUnit>(a, 2 * lane), t1 = units_of<kUnit>(a, 2 * lane + 1);
   const uint32_t total = wave_sum(t0 + t1), room = a.room;
   uint32_t c0, c1;
   auto count = [&](uint32_t q) {
@@ -121,151 +134,232 @@ __device__ __forceinline__ Cuts cut(const TreeArgs& a, int lane) {
   return r;
 }
 
-// One workgroup: 128 query rows (drafted token x query head of the group) of a
-// sequence and key-value head, over a piece of its tokens.  kUniform: the rows of
-// one load instruction are on one page, so that its address is scalar.
+// The sequence that comes i-th by length, the longest first.
+template <int kUnit>
+__device__ __forceinline__ int by_length(const TreeArgs& a, int lane, int i) {
+  // unique keys: units, then the lower sequence; those past the batch have none below them
+  auto key = [&](int b) { return b < a.B ? units_of<kUnit>(a, b) << 7 | uint32_t(127 - b) : 0u; };
+  const uint32_t k0 = key(2 * lane), k1 = key(2 * lane + 1);
+  int r0 = 0, r1 = 0;
+  for (int l = 0; l < (a.B + 1) / 2; ++l) {
+    const uint32_t x = __builtin_amdgcn_readlane(k0, l), z = __builtin_amdgcn_readlane(k1, l);
+    r0 += int(x > k0) + int(z > k0);
+    r1 += int(x > k1) + int(z > k1);
+  }
+  const uint64_t in0 = __builtin_amdgcn_ballot_w64(2 * lane < a.B && r0 == i);
+  const uint64_t in1 = __builtin_amdgcn_ballot_w64(2 * lane + 1 < a.B && r1 == i);
+  return in0 ? 2 * __builtin_ctzll(in0) : 2 * __builtin_ctzll(in1) + 1;
+}
+
+// What a workgroup does: tokens begin .. end - 1 of sequence b (n in all) and
+// key-value head hkv, for the query rows from m0 on of the sequence's `rows`.
+struct Work {
+  int b, hkv, m0, rows, first, drafts, n, begin, end;
+  int piece, count;  // which piece of all sequences' this is, and how many the sequence has
+};
+template <int kUnit, int kBlock>
+__device__ __forceinline__ bool find_work(const TreeArgs& a, int lane, int wave, Work* w) {
+  // Workgroups go round the eight XCDs: those that read the same tokens are
+  // eight apart, so that they share an L2.
+  const int group = page_index(a.per_pair, blockIdx.x), rest = blockIdx.x - group * 8 * a.tiles;
+  const int pair = group * 8 + (rest & 7);
+  w->m0 = (rest >> 3) * kBlock;
+  w->piece = page_index(a.per_hkv, pair);
+  w->hkv = pair - w->piece * a.Hkv;
+  if (w->piece >= (a.room > 0 ? a.room : a.B)) return false;
+  int b = w->piece, nth = 0;
+  w->count = 1;
+  uint32_t each = 0;
+  if (a.room > 0) {
+    const Cuts c = cut<kUnit>(a, lane);
+    if (blockIdx.x == 0 && wave == 0) {
+      if (2 * lane < a.B) {
+        a.plan[4 * lane] = c.first;
+        a.plan[4 * lane + 1] = c.mid - c.first;
+      }
+      if (2 * lane + 1 < a.B) {
+        a.plan[4 * lane + 2] = c.mid;
+        a.plan[4 * lane + 3] = c.last - c.mid;
+      }
+    }
+    const uint64_t in = __builtin_amdgcn_ballot_w64(w->piece >= c.first && w->piece < c.last);
+    if (in == 0) return false;  // more workgroups than pieces
+    const int l = __builtin_ctzll(in);
+    const int from = __builtin_amdgcn_readlane(c.first, l), mid = __builtin_amdgcn_readlane(c.mid, l);
+    const bool second = w->piece >= mid;
+    b = 2 * l + second;
+    nth = w->piece - (second ? mid : from);
+    w->count = second ? __builtin_amdgcn_readlane(c.last, l) - mid : mid - from;
+    each = __builtin_amdgcn_readfirstlane(c.each) * kUnit;
+  } else if (a.order) {
+    b = by_length<kUnit>(a, lane, w->piece);
+  }
+  w->b = b = __builtin_amdgcn_readfirstlane(b);
+  drafted(a, b, &w->first, &w->drafts);
+  w->first = __builtin_amdgcn_readfirstlane(w->first);
+  w->drafts = __builtin_amdgcn_readfirstlane(w->drafts);
+  w->rows = w->drafts * a.G;
+  w->n = __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), a.cap));
+  w->begin = __builtin_amdgcn_readfirstlane(int(min(int64_t(nth) * each, int64_t(w->n))));
+  w->end = __builtin_amdgcn_readfirstlane(
+      nth == w->count - 1 ? w->n : int(min(int64_t(nth + 1) * each, int64_t(w->n))));
+  return w->m0 < w->rows;
+}
+
+// A query row: token `token` of the drafted ones, query head `head`.
+struct Row {
+  int token, head;
+};
+__device__ __forceinline__ Row row_of(const TreeArgs& a, const Work& w, int m) {
+  Row r;
+  r.token = page_index(a.per_g, m);
+  r.head = w.hkv * a.G + m - r.token * a.G;
+  return r;
+}
+template <int NK>
+__device__ __forceinline__ void load_query(const TreeArgs& a, const Work& w, const Row& r, int h, half8 (&q)[NK]) {
+  const uint16_t* src = a.q + int64_t(w.first + r.token) * a.q_t + int64_t(r.head) * a.q_h;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    const int d = 16 * k + 8 * h;
+    u32x4 x = *reinterpret_cast<const u32x4*>(src + (d < a.D ? d : 0));
+    if (d >= a.D || a.zero) x = u32x4{0, 0, 0, 0};
+    q[k] = __builtin_bit_cast(half8, x ^ a.flip);
+  }
+}
+
+// The cache as one workgroup sees it.
+struct Source {
+  const int32_t* row;
+  const uint8_t* mask;
+  const uint16_t *k, *v;
+  int end;
+};
+__device__ __forceinline__ Source source_of(const TreeArgs& a, const Work& w) {
+  Source s;
+  s.row = a.table + int64_t(w.b) * a.table_b;
+  s.mask = a.mask ? a.mask + int64_t(w.b) * a.mask_b : nullptr;
+  s.k = a.k + int64_t(w.hkv) * a.k_h;
+  s.v = a.v + int64_t(w.hkv) * a.v_h;
+  s.end = w.end;
+  return s;
+}
+// The page of token t, always one of the pool; the top bit is set where the token is not live.
+constexpr int kDead = int(0x80000000u), kPage = 0x7fffffff;
+__device__ __forceinline__ int place(const TreeArgs& a, const Source& s, int t) {
+  if (t >= s.end) return kDead;
+  const int id = s.row[page_index(a.div, t)];
+  if (id < 0 || id >= a.pages) return kDead;
+  return s.mask && s.mask[t] == 0 ? id | kDead : id;
+}
+
+// Loads of 1 KiB, straight into LDS, of the rows r0 .. + 64 / C - 1 of the tile
+// from token t0 on; lane l of a wave holds the place of token t0 + l.  kUniform:
+// those rows are on one page, so that their address is scalar.  Value rows of
+// tokens that are not live become zeros, as their weight is.
+template <int C, bool kUniform>
+__device__ __forceinline__ void load_rows(const TreeArgs& a, const Source& s, int t0, int places, uint64_t live, bool all,
+                                          int r0, int lane, uint16_t* dk, uint16_t* dv) {
+  const int lr = lane / C, lc = lane % C, rw = r0 + lr;
+  const int kc = key_chunk<C>(rw, lc) * 8, vc = value_chunk<C>(rw, lc) * 8;
+  const uint32_t k_off = uint32_t(lr * int(a.k_s) + kc) * 2, v_off = uint32_t(lr * int(a.v_s) + vc) * 2;
+  const int page = (kUniform ? __builtin_amdgcn_readlane(places, r0) : __shfl(places, rw)) & kPage;
+  const int t = t0 + (kUniform ? r0 : rw), slot = t - page_index(a.div, t) * a.S - (kUniform ? 0 : lr);
+  const uint8_t* ks = reinterpret_cast<const uint8_t*>(s.k + page * a.k_p + slot * a.k_s) + k_off;
+  const uint8_t* vs = reinterpret_cast<const uint8_t*>(s.v + page * a.v_p + slot * a.v_s) + v_off;
+  if (all && a.D == C * 8) {
+    __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
+  } else {
+    const bool on = (live >> rw) & 1;
+    if (on && kc < a.D) __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
+    if (on && vc < a.D) __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
+    if (!on) *reinterpret_cast<u32x4*>(dv + lane * 8) = u32x4{0, 0, 0, 0};
+  }
+}
+
+// Scores of tokens that the lane's row does not see become -inf: those that
+// are not live, and drafted ones that are none of its ancestors.  own: tokens before
+// the drafted ones.
+template <int NB>
+__device__ __forceinline__ void hide(f32x16 (&s)[NB], uint64_t live, uint64_t sees, int t0, int own, int h) {
+  if (t0 + 32 * NB > own) {
+    const int rel = own - t0;  // drafted token j is token rel + j of the tile, rel < 64
+    uint64_t tree = rel >= 0 ? sees << rel : rel > -64 ? sees >> -rel : 0;
+    if (rel > 0) tree |= (uint64_t(1) << rel) - 1;
+    live &= tree;
+  }
+  live >>= 4 * h;
+#pragma unroll
+  for (int e = 0; e < NB; ++e)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!((uint32_t(live >> (32 * e)) >> (8 * (i >> 2) + (i & 3))) & 1)) s[e][i] = neg_inf();
+}
+
+// What clear_odd took out of the value row of drafted token t, for the rows that see it.
+template <int ND>
+__device__ __forceinline__ void add_odd(const TreeArgs& a, const Source& s, uint64_t sees, int t, int own, int h,
+                                        State<ND>& st) {
+  const int p = place(a, s, t);
+  if (p < 0 || !((sees >> (t - own)) & 1)) return;
+  const uint16_t* src = s.v + p * a.v_p + (t - page_index(a.div, t) * a.S) * a.v_s;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int e = 32 * d + 8 * (i >> 2) + 4 * h + (i & 3);
+      if (e >= a.D) continue;
+      const uint16_t x = src[e];
+      if ((x & 0x7c00) == 0x7c00) st.o[d][i] += float(__builtin_bit_cast(_Float16, x));
+    }
+}
+
+// Many query rows: 128 of them, 32 a wave, over tiles of 64 tokens that the
+// waves share, the next one on its way while one is worked on.
 template <int NK, int ND, int C, bool kUniform>
 __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs a) {
   constexpr int kTile = kTokens * C * 8;  // halves
-  constexpr int kLoads = C / kWaves;      // 1 KiB each, of a wave and tile
-  constexpr int kSpan = 64 / C;           // rows of one
   extern __shared__ uint16_t smem[];
   uint16_t* sk = smem;              // [2][kTile]
   uint16_t* sv = smem + 2 * kTile;  // [2][kTile]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
-  // Workgroups go round the eight XCDs: those that read the same tokens are
-  // eight apart, so that they share an L2.
-  const int group = page_index(a.per_pair, blockIdx.x), rest = blockIdx.x - group * 8 * a.tiles;
-  const int tile = rest >> 3, pair = group * 8 + (rest & 7);
-  const int piece = page_index(a.per_hkv, pair), hkv = pair - piece * a.Hkv;
-  if (piece >= (a.room > 0 ? a.room : a.B)) return;
-  int b = piece, nth = 0, count = 1;
-  uint32_t each = 0;
-  if (a.room > 0) {
-    const Cuts c = cut(a, lane);
-    if (blockIdx.x == 0 && wave == 0) {
-      if (2 * lane < a.B) a.plan[4 * lane] = c.first, a.plan[4 * lane + 1] = c.mid - c.first;
-      if (2 * lane + 1 < a.B) a.plan[4 * lane + 2] = c.mid, a.plan[4 * lane + 3] = c.last - c.mid;
-    }
-    const uint64_t in = __builtin_amdgcn_ballot_w64(piece >= c.first && piece < c.last);
-    if (in == 0) return;  // more workgroups than pieces
-    const int l = __builtin_ctzll(in);
-    const int mid = __builtin_amdgcn_readlane(c.mid, l);
-    const bool second = piece >= mid;
-    b = 2 * l + second;
-    nth = piece - (second ? mid : __builtin_amdgcn_readlane(c.first, l));
-    count = second ? __builtin_amdgcn_readlane(c.last, l) - mid : mid - __builtin_amdgcn_readlane(c.first, l);
-    each = __builtin_amdgcn_readfirstlane(c.each);
-  }
-  b = __builtin_amdgcn_readfirstlane(b);
-  int first, drafts;
-  drafted(a, b, &first, &drafts);
-  first = __builtin_amdgcn_readfirstlane(first);
-  drafts = __builtin_amdgcn_readfirstlane(drafts);
-  const int rows = drafts * a.G;
-  if (tile * kBlock >= rows) return;
-  const int n = __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), a.cap));
-  const int own = n - drafts;  // tokens before the drafted ones; negative where the length does not count them all
-  const int begin = __builtin_amdgcn_readfirstlane(min(int64_t(nth) * each * kTokens, int64_t(n)));
-  const int end = __builtin_amdgcn_readfirstlane(
-      nth == count - 1 ? n : min(int64_t(nth + 1) * each * kTokens, int64_t(n)));
-  const int32_t* row = a.table + int64_t(b) * a.table_b;
-  const uint8_t* mask = a.mask ? a.mask + int64_t(b) * a.mask_b : nullptr;
-  const uint16_t* kh = a.k + int64_t(hkv) * a.k_h;
-  const uint16_t* vh = a.v + int64_t(hkv) * a.v_h;
-
-  // the lane's query row: token i of the drafted ones, query head g of the group
-  const int m0 = tile * kBlock + wave * kRows;
-  const int mi = min(m0 + r, rows - 1);
-  const int qi = page_index(a.per_g, mi), qh = hkv * a.G + mi - qi * a.G;
-  const bool idle = m0 >= rows;
-  half8 q[NK];
-  {
-    const uint16_t* src = a.q + int64_t(first + qi) * a.q_t + int64_t(qh) * a.q_h;
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      const int d = 16 * k + 8 * h;
-      u32x4 w = *reinterpret_cast<const u32x4*>(src + (d < a.D ? d : 0));
-      if (d >= a.D || a.zero) w = u32x4{0, 0, 0, 0};
-      q[k] = __builtin_bit_cast(half8, w ^ a.flip);
-    }
-  }
-  uint64_t sees = ancestors(a, first, drafts, lane);
-  {
-    const uint32_t lo = __shfl(uint32_t(sees), qi), hi = __shfl(uint32_t(sees >> 32), qi);
-    sees = uint64_t(hi) << 32 | lo;
-  }
+  Work w;
+  if (!find_work<kTokens, kBlock>(a, lane, wave, &w)) return;
+  const Source src = source_of(a, w);
+  const int begin = w.begin, end = w.end;
+  const int own = w.n - w.drafts;  // negative where the length does not count all the drafted ones
+  const int m = w.m0 + wave * kRows + r;
+  const bool idle = w.m0 + wave * kRows >= w.rows;
 
   // Key dimensions that only pad the products: zeros, never loaded.
   if (a.D < 16 * NK) {
     for (int i = threadIdx.x; i < 2 * kTile / 8; i += 64 * kWaves)
       *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
+    __syncthreads();
   }
-
-  // The page of token t0 + lane, always one of the pool; the top bit is set
-  // where the token is not live.
-  constexpr int kDead = int(0x80000000u), kPage = 0x7fffffff;
-  auto place = [&](int t0) {
-    const int t = t0 + lane;
-    int page = kDead;
-    if (t < end) {
-      const int id = row[page_index(a.div, t)];
-      if (id >= 0 && id < a.pages) page = mask && mask[t] == 0 ? id | kDead : id;
-    }
-    return page;
-  };
-  // Of the wave's loads: the row of a tile and the lane's bytes in it, by the first row of each.
-  const int lr = lane / C, lc = lane % C;
-  uint32_t k_off[kLoads], v_off[kLoads];
-  bool k_in[kLoads], v_in[kLoads];
+  auto load = [&](int t0, int places, int buf) {
+    const uint64_t live = __builtin_amdgcn_ballot_w64(places >= 0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int rw = (i * kWaves + wave) * kSpan + lr;
-    const int kc = key_chunk<C>(rw, lc) * 8, vc = value_chunk<C>(rw, lc) * 8;
-    k_in[i] = kc < a.D;
-    v_in[i] = vc < a.D;
-    k_off[i] = uint32_t(lr * int(a.k_s) + kc) * 2;
-    v_off[i] = uint32_t(lr * int(a.v_s) + vc) * 2;
-  }
-  // A tile into buffer buf; rows that are not live become zeros.
-  auto load = [&](int t0, int pages, int buf) {
-    const uint64_t live = __builtin_amdgcn_ballot_w64(pages >= 0);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r0 = (i * kWaves + wave) * kSpan, rw = r0 + lr;
-      uint16_t* dk = sk + buf * kTile + (i * kWaves + wave) * 512;
-      uint16_t* dv = sv + buf * kTile + (i * kWaves + wave) * 512;
-      const uint8_t *ks, *vs;
-      if (kUniform) {
-        const int page = __builtin_amdgcn_readlane(pages, r0) & kPage, t = t0 + r0, slot = t - page_index(a.div, t) * a.S;
-        ks = reinterpret_cast<const uint8_t*>(kh + page * a.k_p + slot * a.k_s) + k_off[i];
-        vs = reinterpret_cast<const uint8_t*>(vh + page * a.v_p + slot * a.v_s) + v_off[i];
-      } else {
-        const int page = __shfl(pages, rw) & kPage, t = t0 + rw, slot = t - page_index(a.div, t) * a.S;
-        ks = reinterpret_cast<const uint8_t*>(kh + page * a.k_p + (slot - lr) * a.k_s) + k_off[i];
-        vs = reinterpret_cast<const uint8_t*>(vh + page * a.v_p + (slot - lr) * a.v_s) + v_off[i];
-      }
-      if (~live == 0 && a.D == C * 8) {
-        __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
-      } else {
-        const bool on = (live >> rw) & 1;
-        if (on && k_in[i]) __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
-        if (on && v_in[i]) __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
-        if (!on) *reinterpret_cast<u32x4*>(dv + lane * 8) = u32x4{0, 0, 0, 0};
-      }
+    for (int i = 0; i < C / kWaves; ++i) {
+      const int at = i * kWaves + wave;
+      load_rows<C, kUniform>(a, src, t0, places, live, ~live == 0, at * (64 / C), lane, sk + buf * kTile + at * 512,
+                             sv + buf * kTile + at * 512);
     }
   };
+  int now = place(a, src, begin + lane), next = place(a, src, begin + kTokens + lane);
+  if (begin < end) load(begin, now, 0);
 
+  const Row mine = row_of(a, w, min(m, w.rows - 1));
+  half8 q[NK];
+  load_query(a, w, mine, h, q);
+  const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
   const Reads<NK, ND, C> at(smem, lane);
   State<ND> st;
   st.clear();
   bool odd = false;
-  int now = place(begin), next = place(begin + kTokens);
-  if (a.D < 16 * NK) __syncthreads();
-  if (begin < end) load(begin, now, 0);
   // One tile, in buffer `buf`.
   auto step = [&](int t0, auto constant) {
     constexpr int buf = decltype(constant)::value;
@@ -274,7 +368,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     wait_vm<0>();
     __syncthreads();
     if (t0 + kTokens < end) load(t0 + kTokens, now, buf ^ 1);
-    next = place(t0 + 2 * kTokens);
+    next = place(a, src, t0 + 2 * kTokens + lane);
     const bool drafts_here = t0 + kTokens > own;
     if (drafts_here) {
       // A drafted token's infinity or NaN must not reach rows that do not see
@@ -288,21 +382,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     if (idle) return;
     f32x16 s[2];
     scores(at, buf * kTile * 2, q, s);
-    if (drafts_here || ~live) {
-      uint64_t on = live;
-      if (drafts_here) {
-        const int rel = own - t0;  // drafted token j is token rel + j of the tile
-        uint64_t tree = rel >= 0 ? sees << rel : rel > -64 ? sees >> -rel : 0;  // rel < kTokens
-        if (rel > 0) tree |= (uint64_t(1) << rel) - 1;
-        on &= tree;
-      }
-      on >>= 4 * h;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!((uint32_t(on >> (32 * e)) >> (8 * (i >> 2) + (i & 3))) & 1)) s[e][i] = neg_inf();
-    }
+    if (drafts_here || ~live) hide(s, live, sees, t0, own, h);
     half8 p[4];
     weights(st, s, a.c, p);
     outputs(st, at, (2 + buf) * kTile * 2, p);
@@ -313,24 +393,11 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
   }
   if (idle) return;
   const float l = sum_halves(st.l);
-  if (odd) {
-    for (int t = max(begin, own); t < end; ++t) {
-      const int page = row[page_index(a.div, t)], slot = t - page_index(a.div, t) * a.S;
-      if (!((sees >> (t - own)) & 1) || page < 0 || page >= a.pages || (mask && mask[t] == 0)) continue;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 32 * d + 8 * (i >> 2) + 4 * h + (i & 3);
-          if (e >= a.D) continue;
-          const uint16_t w = vh[page * a.v_p + slot * a.v_s + e];
-          if ((w & 0x7c00) == 0x7c00) st.o[d][i] += float(__builtin_bit_cast(_Float16, w));
-        }
-    }
-  }
-  if (m0 + r >= rows) return;
-  if (count > 1) {
-    const int64_t to = (int64_t(piece) * a.Hkv + hkv) * a.rows + m0 + r;
+  if (odd)
+    for (int t = max(begin, own); t < end; ++t) add_odd(a, src, sees, t, own, h, st);
+  if (m >= w.rows) return;
+  if (w.count > 1) {
+    const int64_t to = (int64_t(w.piece) * a.Hkv + w.hkv) * a.rows + m;
     if (h == 0) {
       a.ml[2 * to] = st.m * a.c;
       a.ml[2 * to + 1] = l;
@@ -347,7 +414,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = a.out + int64_t(first + qi) * a.o_t + int64_t(qh) * a.o_h;
+  uint16_t* dst = a.out + int64_t(w.first + mine.token) * a.o_t + int64_t(mine.head) * a.o_h;
 #pragma unroll
   for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -359,49 +426,196 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     }
 }
 
+// Few query rows, 32 at most: bound by the read of the cache.  Every wave has
+// tiles of its own, 32 tokens in LDS that no other wave looks at, so that there
+// is no barrier in the loop and as many bytes on their way as LDS holds; the
+// waves' sums are joined at the end.
+template <int NK, int ND, int C, int W, bool kUniform>
+__global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(TreeArgs a) {
+  constexpr int kTile = 32 * C * 8;  // halves
+  constexpr int kRow = 32 * ND + 4;  // floats, off the bank stride
+  extern __shared__ uint16_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  uint16_t* sk = smem + wave * 2 * kTile;
+  uint16_t* sv = sk + kTile;
+  Work w;
+  if (!find_work<32 * W, 32>(a, lane, wave, &w)) return;
+  const Source src = source_of(a, w);
+  const int end = w.end, own = w.n - w.drafts;
+  const int t_first = w.begin + 32 * wave;
+
+  if (a.D < 16 * NK) {
+    for (int i = lane; i < kTile / 8; i += 64) *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+  }
+  auto load = [&](int t0, int places) {
+    const uint64_t live = __builtin_amdgcn_ballot_w64(places >= 0);  // both halves of the wave hold the same
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i)
+      load_rows<C, kUniform>(a, src, t0, places, live, ~live == 0, i * (64 / C), lane, sk + i * 512, sv + i * 512);
+  };
+  int now = place(a, src, t_first + r), next = place(a, src, t_first + 32 * W + r);
+  if (t_first < end) load(t_first, now);
+
+  const Row mine = row_of(a, w, min(r, w.rows - 1));
+  half8 q[NK];
+  load_query(a, w, mine, h, q);
+  const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
+  const Reads<NK, ND, C> at(sk, lane);
+  State<ND> st;
+  st.clear();
+  bool odd = false;
+  for (int t0 = t_first; t0 < end; t0 += 32 * W) {
+    const uint64_t live = __builtin_amdgcn_ballot_w64(now >= 0) & 0xffffffffu;
+    now = next;
+    wait_vm<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    const bool drafts_here = t0 + 32 > own;
+    if (drafts_here) {
+      bool bad = false;
+      for (int i = lane; i < 32 * C; i += 64)
+        if (t0 + i / C >= own && value_chunk<C>(i / C, i % C) * 8 < a.D) bad |= clear_odd(sv + i * 8);
+      odd |= __builtin_amdgcn_ballot_w64(bad) != 0;
+    }
+    f32x16 s[1];
+    scores(at, 0, q, s);
+    if (drafts_here || live != 0xffffffffu) hide(s, live, sees, t0, own, h);
+    half8 p[2];
+    weights(st, s, a.c, p);
+    outputs(st, at, kTile * 2, p);
+    __builtin_amdgcn_sched_barrier(0);  // the tile has been read: the next one takes its place
+    if (t0 + 32 * W < end) load(t0 + 32 * W, now);
+    next = place(a, src, t0 + 64 * W + r);
+  }
+  if (odd)
+    for (int t = max(w.begin, own); t < end; ++t)
+      if ((t - w.begin) / 32 % W == wave) add_odd(a, src, sees, t, own, h, st);
+  const float l = sum_halves(st.l);
+
+  // The waves' sums: four dimensions of a row a thread.
+  __syncthreads();
+  float* sm_m = reinterpret_cast<float*>(smem);  // [W][32]
+  float* sm_l = sm_m + 32 * W;
+  float* sm_o = sm_l + 32 * W;  // [W][32][kRow]
+  if (h == 0) {
+    sm_m[32 * wave + r] = st.m * a.c;
+    sm_l[32 * wave + r] = l;
+  }
+  if (r < w.rows) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(sm_o + (32 * wave + r) * kRow + 32 * d + 2 * i + 4 * h) =
+            float4{st.o[d][i], st.o[d][i + 1], st.o[d][i + 2], st.o[d][i + 3]};
+  }
+  __syncthreads();
+  constexpr int kPer = 8 * ND;  // threads of a row
+  for (int i = threadIdx.x; i < w.rows * kPer; i += 64 * W) {
+    const int m = i / kPer, d = i % kPer * 4;
+    if (d >= a.D) continue;
+    float top = neg_inf();
+#pragma unroll
+    for (int x = 0; x < W; ++x) top = fmaxf(top, sm_m[32 * x + m]);
+    const float base = top == neg_inf() ? 0.f : top;
+    float sum = 0.f;
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < W; ++x) {
+      const float f = __builtin_amdgcn_exp2f(sm_m[32 * x + m] - base);
+      const float4 v = *reinterpret_cast<const float4*>(sm_o + (32 * x + m) * kRow + d);
+      sum += f * sm_l[32 * x + m];
+      o.x += f * v.x;
+      o.y += f * v.y;
+      o.z += f * v.z;
+      o.w += f * v.w;
+    }
+    if (w.count > 1) {
+      const int64_t to = (int64_t(w.piece) * a.Hkv + w.hkv) * a.rows + m;
+      if (d == 0) {
+        a.ml[2 * to] = top;
+        a.ml[2 * to + 1] = sum;
+      }
+      *reinterpret_cast<float4*>(a.part + to * a.D + d) = o;
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const Row it = row_of(a, w, m);
+      uint16_t* dst = a.out + int64_t(w.first + it.token) * a.o_t + int64_t(it.head) * a.o_h + d;
+      dst[0] = __builtin_bit_cast(uint16_t, _Float16(o.x * inv));
+      dst[1] = __builtin_bit_cast(uint16_t, _Float16(o.y * inv));
+      dst[2] = __builtin_bit_cast(uint16_t, _Float16(o.z * inv));
+      dst[3] = __builtin_bit_cast(uint16_t, _Float16(o.w * inv));
+    }
+  }
+}
+
 constexpr int kJoin = 256;
 
-// The pieces of a row added up, four dimensions a thread, `per` threads a row.
+// The pieces of a row added up by a wave: lane p has the maximum and the sum of
+// piece p, then `per` lanes take four dimensions each of a piece's outputs, all
+// groups of them another piece.  Everything that does not depend on the row's
+// place is requested at once.
 __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
-  const int tid = threadIdx.x;
-  const int64_t at = int64_t(blockIdx.x) * (kJoin / per) + tid / per;  // packed row and query head
-  const int d = tid % per * 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t at = int64_t(blockIdx.x) * (kJoin / 64) + (threadIdx.x >> 6);  // packed row and query head
   const int64_t t = at / a.Hq;
   const int qh = int(at - t * a.Hq);
-  if (t >= a.T || d >= a.D) return;
+  if (t >= a.T) return;
   // the row's sequence: the last that starts at or before it
-  int lo = 0, hi = a.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.starts[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+  const int s0 = 2 * lane < a.B ? a.starts[2 * lane] : 0x7fffffff;
+  const int s1 = 2 * lane + 1 < a.B ? a.starts[2 * lane + 1] : 0x7fffffff;
+  const uint64_t in0 = __builtin_amdgcn_ballot_w64(s0 <= t), in1 = __builtin_amdgcn_ballot_w64(s1 <= t);
+  if (!(in0 | in1)) return;
+  const int b = max(in0 ? 2 * (63 - __builtin_clzll(in0)) : -1, in1 ? 2 * (63 - __builtin_clzll(in1)) + 1 : -1);
   int first, drafts;
-  drafted(a, lo, &first, &drafts);
+  drafted(a, b, &first, &drafts);
+  const int from_piece = a.plan[2 * b], pieces = a.plan[2 * b + 1];
   const int i = int(t) - first;
-  if (i < 0 || i >= drafts) return;
-  const int pieces = a.plan[2 * lo + 1];
-  if (pieces < 2) return;  // written already
+  if (i < 0 || i >= drafts || pieces < 2) return;  // one piece: written already
   const int hkv = page_index(a.per_g, qh);
   const int64_t next = int64_t(a.Hkv) * a.rows;
-  const int64_t from = (int64_t(a.plan[2 * lo]) * a.Hkv + hkv) * a.rows + int64_t(i) * a.G + (qh - hkv * a.G);
+  const int64_t from = (int64_t(from_piece) * a.Hkv + hkv) * a.rows + int64_t(i) * a.G + (qh - hkv * a.G);
+  const float* ml = a.ml + 2 * from;
   float m = neg_inf();
-  for (int p = 0; p < pieces; ++p) m = fmaxf(m, a.ml[2 * (from + p * next)]);
+  for (int p = lane; p < pieces; p += 64) m = fmaxf(m, ml[2 * next * p]);
+  m = wave_max(m);
   const float base = m == neg_inf() ? 0.f : m;
   float l = 0.f;
+  for (int p = lane; p < pieces; p += 64) l += __builtin_amdgcn_exp2f(ml[2 * next * p] - base) * ml[2 * next * p + 1];
+  l = wave_sum(l);
+  const int d = lane % per * 4, part = lane / per, parts = 64 / per;
   float4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p < pieces; ++p) {
-    const int64_t x = from + p * next;
-    const float f = __builtin_amdgcn_exp2f(a.ml[2 * x] - base);
-    const float4 v = *reinterpret_cast<const float4*>(a.part + x * a.D + d);
-    l += f * a.ml[2 * x + 1];
-    o.x += f * v.x;
-    o.y += f * v.y;
-    o.z += f * v.z;
-    o.w += f * v.w;
+  if (d < a.D) {
+    const float* src = a.part + from * a.D + d;
+    constexpr int kUnroll = 8;
+    for (int p0 = part; p0 < pieces; p0 += kUnroll * parts) {
+      float4 v[kUnroll];
+      float f[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int p = min(p0 + u * parts, pieces - 1);
+        v[u] = *reinterpret_cast<const float4*>(src + p * next * a.D);
+        f[u] = p0 + u * parts < pieces ? __builtin_amdgcn_exp2f(ml[2 * next * p] - base) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (p0 + u * parts >= pieces) continue;
+        o.x += f[u] * v[u].x;
+        o.y += f[u] * v[u].y;
+        o.z += f[u] * v[u].z;
+        o.w += f[u] * v[u].w;
+      }
+    }
   }
+  for (int s = per; s < 64; s *= 2) {
+    o.x += __shfl_xor(o.x, s);
+    o.y += __shfl_xor(o.y, s);
+    o.z += __shfl_xor(o.z, s);
+    o.w += __shfl_xor(o.w, s);
+  }
+  if (part > 0 || d >= a.D) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* dst = a.out + t * a.o_t + int64_t(qh) * a.o_h + d;
   dst[0] = __builtin_bit_cast(uint16_t, _Float16(o.x * inv));
@@ -411,7 +625,16 @@ __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
 }
 
 template <int NK, int ND, int C, bool kUniform>
-hipError_t launch_as(const TreeArgs& a, uint32_t grid, hipStream_t s) {
+hipError_t launch_as(const TreeArgs& a, bool few, uint32_t grid, hipStream_t s) {
+  if (few) {
+    constexpr int W = few_waves(C);
+    constexpr int kLds = max_of(W * 2 * 32 * C * 16, W * 32 * 4 * (2 + 32 * ND + 4));
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_few_kernel<NK, ND, C, W, kUniform>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    tree_few_kernel<NK, ND, C, W, kUniform><<<grid, 64 * W, kLds, s>>>(a);
+    return hipGetLastError();
+  }
   constexpr int kLds = 4 * kTokens * C * 16;
   if (kLds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C, kUniform>),
@@ -423,32 +646,41 @@ hipError_t launch_as(const TreeArgs& a, uint32_t grid, hipStream_t s) {
 }
 
 template <int NK, int ND, int C>
-hipError_t launch(const TreeArgs& a, uint32_t grid, hipStream_t s) {
-  return a.S % (64 / C) == 0 ? launch_as<NK, ND, C, true>(a, grid, s) : launch_as<NK, ND, C, false>(a, grid, s);
+hipError_t launch(const TreeArgs& a, bool few, uint32_t grid, hipStream_t s) {
+  return a.S % (64 / C) == 0 ? launch_as<NK, ND, C, true>(a, few, grid, s)
+                             : launch_as<NK, ND, C, false>(a, few, grid, s);
 }
 
 }  // namespace
 
-// How the work is dealt: see the kernel.
+// How the work is dealt.
 TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, int64_t most, int num_cus) {
   TreePlan p;
   const int64_t rows = most * (Hq / Hkv);
-  p.tiles = std::max<int64_t>(1, (rows + kBlock - 1) / kBlock);
-  const int64_t units = Hkv * p.tiles;  // of a sequence
-  const int64_t steps = (cap + kTokens - 1) / kTokens;
-  const int64_t slots = (D <= 128 ? 2 : 1) * int64_t(num_cus);  // workgroups at a time
-  if (B >= 1 && B <= kMaxCut && steps > 2 && units * B <= 4 * slots) {
-    int64_t k = 1;
-    while (B > 1 && k < 4 && k * slots < 4 * B * units) ++k;
-    p.room = int(std::min<int64_t>(k * slots / units, (steps + 1) / 2 * B));
-    if (p.room <= B) p.room = 0;
+  p.few = rows <= kRows;
+  const int64_t block = p.few ? kRows : kBlock;
+  p.tiles = std::max<int64_t>(1, (rows + block - 1) / block);
+  const int64_t units = B * Hkv * p.tiles;
+  const int chunks = D <= 64 ? 8 : D <= 128 ? 16 : 32;
+  const int64_t unit = p.few ? 32 * few_waves(chunks) : kTokens;
+  const int64_t steps = (cap + unit - 1) / unit;
+  // workgroups at a time
+  const int64_t slots = num_cus * int64_t(p.few ? (chunks == 8 ? 2 : 1) : (chunks == 32 ? 1 : 2));
+  if (B >= 1 && B <= kMaxCut && steps > 2) {
+    if (units < 2 * slots) {
+      int64_t k = 1;
+      while (B > 1 && k < 4 && k * slots < 4 * units) ++k;
+      p.room = int(std::min<int64_t>(k * slots * B / units, (steps + 1) / 2 * B));
+      if (p.room <= B) p.room = 0;
+    }
+    p.order = p.room == 0 && B > 1 && units > slots;
   }
   const int64_t pairs = (p.room ? p.room : B) * Hkv;
   p.grid = (pairs + 7) / 8 * 8 * p.tiles;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   if (p.room) {
     p.off_ml = up(size_t(B) * 8);
-    const size_t all = size_t(pairs) * size_t(p.tiles) * kBlock;
+    const size_t all = size_t(pairs) * size_t(p.tiles * block);
     p.off_part = p.off_ml + up(all * 8);
     p.bytes = p.off_part + all * size_t(D) * 4;
   }
@@ -491,7 +723,8 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
   a.most = int(r.most);
   a.room = p.room;
   a.tiles = int(p.tiles);
-  a.rows = int(p.tiles) * kBlock;
+  a.rows = int(p.tiles) * (p.few ? kRows : kBlock);
+  a.order = p.order;
   a.zero = r.scale == 0.f;
   a.c = a.zero ? 1.f : std::abs(r.scale) * 1.44269504088896340736f;
   a.flip = r.scale < 0.f ? 0x80008000u : 0u;
@@ -506,15 +739,15 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
     a.part = reinterpret_cast<float*>(w + p.off_part);
   }
   const uint32_t grid = uint32_t(p.grid);
-  const hipError_t e = a.D <= 64    ? launch<4, 2, 8>(a, grid, s)
-                       : a.D <= 96  ? launch<6, 3, 16>(a, grid, s)
-                       : a.D <= 128 ? launch<8, 4, 16>(a, grid, s)
-                       : a.D <= 192 ? launch<12, 6, 32>(a, grid, s)
-                                    : launch<16, 8, 32>(a, grid, s);
+  const hipError_t e = a.D <= 64    ? launch<4, 2, 8>(a, p.few, grid, s)
+                       : a.D <= 96  ? launch<6, 3, 16>(a, p.few, grid, s)
+                       : a.D <= 128 ? launch<8, 4, 16>(a, p.few, grid, s)
+                       : a.D <= 192 ? launch<12, 6, 32>(a, p.few, grid, s)
+                                    : launch<16, 8, 32>(a, p.few, grid, s);
   if (e != hipSuccess || !p.room) return e;
   const int per = a.D <= 64 ? 16 : a.D <= 128 ? 32 : 64;
   const int64_t rows = r.T * r.Hq;
-  tree_join_kernel<<<dim3(uint32_t((rows + kJoin / per - 1) / (kJoin / per))), kJoin, 0, s>>>(a, per);
+  tree_join_kernel<<<dim3(uint32_t((rows + kJoin / 64 - 1) / (kJoin / 64))), kJoin, 0, s>>>(a, per);
   return hipGetLastError();
 }
 
