@@ -205,17 +205,36 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
   __builtin_amdgcn_sched_group_barrier(0x008, ND, 0);
 }
 
-// A wave's part of a tile, n loads of 1 KiB straight into LDS: 16 bytes at
-// `off` from `src` a lane, those from `bytes` on as zeros.
-__device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const uint32_t* off, int n, uint16_t* dst,
+// Loads of 16 bytes a lane straight into LDS, lane l's to `to` + 16 l.  In
+// assembly, so that the compiler does not wait for them before the next
+// transposing read, of another tile; who reads what they bring waits for it
+// himself (wait_vm).  They have no register for a result.  The counter that
+// the compiler's own waits look at runs in order, so that these only make them
+// longer.
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
+  return __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)(const_cast<uint16_t*>(p)))));
+}
+__device__ __forceinline__ void to_lds(const void* src, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(to) : "memory");
+}
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t to) {  // base: of the whole wave
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
+               : "memory");
+}
+
+// A wave's part of a tile, n such loads of 1 KiB: 16 bytes at `off` from `src` a
+// lane, those from `bytes` on as zeros.
+__device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const uint32_t* off, int n, uint32_t to,
                                           int step) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass does not know the resource type
-  const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(src), 0, bytes, 0x00020000);
+  const uint64_t base = reinterpret_cast<uint64_t>(src);
+  const u32x4 resource = {uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(base))),
+                          uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(base >> 32))) & 0xffffu,
+                          uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 #pragma unroll
   for (int i = 0; i < n; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + i * step), 16, off[i], 0, 0, 0);
-#endif
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[i]),
+                 "s"(resource), "s"(to + i * step)
+                 : "memory");
 }
 
 // Zeros for the infinities and NaN among eight halves in LDS; whether there were any.

@@ -64,8 +64,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
   constexpr int kTile = kTokens * C * 8;  // halves
   constexpr int kLoads = C / kWaves;      // 1 KiB each, of a wave and tile
   extern __shared__ uint16_t smem[];
-  uint16_t* sk = smem;              // [2][kTile]
-  uint16_t* sv = smem + 2 * kTile;  // [2][kTile]
+  uint16_t* sv = smem + 2 * kTile;  // two key tiles, then two value tiles
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int u = blockIdx.x / a.Hq;
@@ -105,12 +104,13 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
     k_off[i] = kc < a.D ? uint32_t(row * int(a.k_t) + kc) * 2 : 0x80000000u;
     v_off[i] = vc < a.D ? uint32_t(row * int(a.v_t) + vc) * 2 : 0x80000000u;
   }
+  const uint32_t to = lds_address(smem);
   auto load = [&](int t0, int buf) {
     const int left = min(n - t0, kTokens);
     load_tile(kh + int64_t(t0) * a.k_t, ((left - 1) * int(a.k_t) + a.D) * 2, k_off, kLoads,
-                      sk + buf * kTile + wave * 512, kWaves * 512);
+              to + (buf * kTile + wave * 512) * 2, kWaves * 1024);
     load_tile(vh + int64_t(t0) * a.v_t, ((left - 1) * int(a.v_t) + a.D) * 2, v_off, kLoads,
-                      sv + buf * kTile + wave * 512, kWaves * 512);
+              to + ((2 + buf) * kTile + wave * 512) * 2, kWaves * 1024);
   };
 
   // Bytes from the start of LDS: two key tiles, then two value tiles.

@@ -253,28 +253,60 @@ __device__ __forceinline__ int place(const TreeArgs& a, const Source& s, int t) 
   return s.mask && s.mask[t] == 0 ? id | kDead : id;
 }
 
-// Loads of 1 KiB, straight into LDS, of the rows r0 .. + 64 / C - 1 of the tile
-// from token t0 on; lane l of a wave holds the place of token t0 + l.  kUniform:
-// those rows are on one page, so that their address is scalar.  Value rows of
-// tokens that are not live become zeros, as their weight is.
-template <int C, bool kUniform>
-__device__ __forceinline__ void load_rows(const TreeArgs& a, const Source& s, int t0, int places, uint64_t live, bool all,
-                                          int r0, int lane, uint16_t* dk, uint16_t* dv) {
-  const int lr = lane / C, lc = lane % C, rw = r0 + lr;
-  const int kc = key_chunk<C>(rw, lc) * 8, vc = value_chunk<C>(rw, lc) * 8;
-  const uint32_t k_off = uint32_t(lr * int(a.k_s) + kc) * 2, v_off = uint32_t(lr * int(a.v_s) + vc) * 2;
-  const int page = (kUniform ? __builtin_amdgcn_readlane(places, r0) : __shfl(places, rw)) & kPage;
-  const int t = t0 + (kUniform ? r0 : rw), slot = t - page_index(a.div, t) * a.S - (kUniform ? 0 : lr);
-  const uint8_t* ks = reinterpret_cast<const uint8_t*>(s.k + page * a.k_p + slot * a.k_s) + k_off;
-  const uint8_t* vs = reinterpret_cast<const uint8_t*>(s.v + page * a.v_p + slot * a.v_s) + v_off;
-  if (all && a.D == C * 8) {
-    __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
-    __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
-  } else {
+// A tile's loads into LDS, straight, N of 1 KiB from the keys and as many from the
+// values: load i brings rows r0 + i step .. + 64 / C - 1 of the tile from token t0 on,
+// where lane l holds the place of token t0 + l.  Every lane finds the addresses of its
+// token's rows (a scalar calculation for every load, 50 instructions each, took
+// a third of the time); kUniform: the rows of a load are on one page, so that its
+// first row's address serves.  Value rows of tokens that are not live become
+// zeros, as their weight is.
+template <int C, int N, bool kUniform>
+__device__ __forceinline__ void load_tile(const TreeArgs& a, const Source& s, int t0, int places, int lane, int r0,
+                                          int step, uint16_t* dk, uint16_t* dv) {
+  const uint64_t live = __builtin_amdgcn_ballot_w64(places >= 0);
+  const int t = t0 + lane, slot = t - page_index(a.div, t) * a.S, page = places & kPage;
+  const uint64_t ka = reinterpret_cast<uint64_t>(s.k + page * a.k_p + slot * a.k_s);
+  const uint64_t va = reinterpret_cast<uint64_t>(s.v + page * a.v_p + slot * a.v_s);
+  const int lr = lane / C, lc = lane % C;
+  const uint32_t to_k = lds_address(dk), to_v = lds_address(dv);
+  auto offsets = [&](int i, uint32_t* k, uint32_t* v) {  // from the row's address, or that of the load's first row
+    const int rw = r0 + i * step + lr;
+    *k = key_chunk<C>(rw, lc) * 16 + (kUniform ? uint32_t(lr * int(a.k_s)) * 2 : 0);
+    *v = value_chunk<C>(rw, lc) * 16 + (kUniform ? uint32_t(lr * int(a.v_s)) * 2 : 0);
+  };
+  auto from = [&](uint64_t at, int i) -> uint64_t {
+    const int r = r0 + i * step;
+    if (kUniform)
+      return uint64_t(uint32_t(__builtin_amdgcn_readlane(int(at >> 32), r))) << 32 |
+             uint32_t(__builtin_amdgcn_readlane(int(at), r));
+    return pick(at, r + lr);
+  };
+  auto issue = [&](uint64_t at, uint32_t off, uint32_t to) {
+    if (kUniform)
+      to_lds(at, off, to);
+    else
+      to_lds(reinterpret_cast<const void*>(at + off), to);
+  };
+  if (~live == 0 && a.D == C * 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t k, v;
+      offsets(i, &k, &v);
+      issue(from(ka, i), k, to_k + i * step * C * 16);
+      issue(from(va, i), v, to_v + i * step * C * 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t k, v;
+    offsets(i, &k, &v);
+    const uint64_t ki = from(ka, i), vi = from(va, i);
+    const int rw = r0 + i * step + lr;
     const bool on = (live >> rw) & 1;
-    if (on && kc < a.D) __builtin_amdgcn_global_load_lds(ks, (lds_ptr)dk, 16, 0, 0);
-    if (on && vc < a.D) __builtin_amdgcn_global_load_lds(vs, (lds_ptr)dv, 16, 0, 0);
-    if (!on) *reinterpret_cast<u32x4*>(dv + lane * 8) = u32x4{0, 0, 0, 0};
+    if (on && key_chunk<C>(rw, lc) * 8 < a.D) issue(ki, k, to_k + i * step * C * 16);
+    if (on && value_chunk<C>(rw, lc) * 8 < a.D) issue(vi, v, to_v + i * step * C * 16);
+    if (!on) *reinterpret_cast<u32x4*>(dv + i * step * C * 8 + lane * 8) = u32x4{0, 0, 0, 0};
   }
 }
 
@@ -341,13 +373,9 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     __syncthreads();
   }
   auto load = [&](int t0, int places, int buf) {
-    const uint64_t live = __builtin_amdgcn_ballot_w64(places >= 0);
-#pragma unroll
-    for (int i = 0; i < C / kWaves; ++i) {
-      const int at = i * kWaves + wave;
-      load_rows<C, kUniform>(a, src, t0, places, live, ~live == 0, at * (64 / C), lane, sk + buf * kTile + at * 512,
-                             sv + buf * kTile + at * 512);
-    }
+    constexpr int kSpan = 64 / C;  // rows of a load
+    load_tile<C, C / kWaves, kUniform>(a, src, t0, places, lane, wave * kSpan, kWaves * kSpan,
+                                       sk + buf * kTile + wave * 512, sv + buf * kTile + wave * 512);
   };
   int now = place(a, src, begin + lane), next = place(a, src, begin + kTokens + lane);
   if (begin < end) load(begin, now, 0);
@@ -450,11 +478,8 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
     for (int i = lane; i < kTile / 8; i += 64) *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
-  auto load = [&](int t0, int places) {
-    const uint64_t live = __builtin_amdgcn_ballot_w64(places >= 0);  // both halves of the wave hold the same
-#pragma unroll
-    for (int i = 0; i < C / 2; ++i)
-      load_rows<C, kUniform>(a, src, t0, places, live, ~live == 0, i * (64 / C), lane, sk + i * 512, sv + i * 512);
+  auto load = [&](int t0, int places) {  // both halves of the wave hold the same places
+    load_tile<C, C / 2, kUniform>(a, src, t0, places, lane, 0, 64 / C, sk, sv);
   };
   int now = place(a, src, t_first + r), next = place(a, src, t_first + 32 * W + r);
   if (t_first < end) load(t_first, now);
