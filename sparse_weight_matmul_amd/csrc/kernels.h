@@ -246,6 +246,7 @@ constexpr int kTreeMost = 64;
 struct TreePlan {
   int room = 0;        // pieces of all sequences at most; 0: every sequence is one
   bool few = false;    // at most 32 query rows of a sequence and key-value head
+  bool wide = false;   // 256 query rows of them a workgroup
   bool order = false;  // whole sequences, the longest first
   int64_t tiles = 1;   // workgroups along the rows of a sequence and key-value head
   int64_t grid = 0;    // workgroups of the first launch

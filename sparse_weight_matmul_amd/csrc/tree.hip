@@ -21,8 +21,7 @@ namespace {
 
 using namespace flash;
 
-constexpr int kWaves = 4;
-constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
+constexpr int kBlock = 4 * kRows;  // query rows of a workgroup of four waves
 // waves over few query rows, so that their tiles fill LDS
 constexpr int few_waves(int chunks) { return chunks == 32 ? 4 : 8; }
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
@@ -246,11 +245,12 @@ __device__ __forceinline__ Source source_of(const TreeArgs& a, const Work& w) {
 }
 // The page of token t, always one of the pool; the top bit is set where the token is not live.
 constexpr int kDead = int(0x80000000u), kPage = 0x7fffffff;
+__device__ __forceinline__ int place_of(const TreeArgs& a, int id, bool on) {
+  return id < 0 || id >= a.pages ? kDead : on ? id : id | kDead;
+}
 __device__ __forceinline__ int place(const TreeArgs& a, const Source& s, int t) {
   if (t >= s.end) return kDead;
-  const int id = s.row[page_index(a.div, t)];
-  if (id < 0 || id >= a.pages) return kDead;
-  return s.mask && s.mask[t] == 0 ? id | kDead : id;
+  return place_of(a, s.row[page_index(a.div, t)], !s.mask || s.mask[t] != 0);
 }
 
 // A tile's loads into LDS, straight, N of 1 KiB from the keys and as many from the
@@ -281,33 +281,40 @@ __device__ __forceinline__ void load_tile(const TreeArgs& a, const Source& s, in
              uint32_t(__builtin_amdgcn_readlane(int(at), r));
     return pick(at, r + lr);
   };
-  auto issue = [&](uint64_t at, uint32_t off, uint32_t to) {
-    if (kUniform)
-      to_lds(at, off, to);
-    else
-      to_lds(reinterpret_cast<const void*>(at + off), to);
-  };
   if (~live == 0 && a.D == C * 8) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       uint32_t k, v;
       offsets(i, &k, &v);
-      issue(from(ka, i), k, to_k + i * step * C * 16);
-      issue(from(va, i), v, to_v + i * step * C * 16);
+      if (kUniform) {
+        to_lds(from(ka, i), k, to_k + i * step * C * 16);
+        to_lds(from(va, i), v, to_v + i * step * C * 16);
+      } else {
+        to_lds(from(ka, i) + k, to_k + i * step * C * 16);
+        to_lds(from(va, i) + v, to_v + i * step * C * 16);
+      }
     }
     return;
   }
+  // Keys of tokens that are not live may hold anything: their scores are not used.
+  bool none = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     uint32_t k, v;
     offsets(i, &k, &v);
-    const uint64_t ki = from(ka, i), vi = from(va, i);
     const int rw = r0 + i * step + lr;
     const bool on = (live >> rw) & 1;
-    if (on && key_chunk<C>(rw, lc) * 8 < a.D) issue(ki, k, to_k + i * step * C * 16);
-    if (on && value_chunk<C>(rw, lc) * 8 < a.D) issue(vi, v, to_v + i * step * C * 16);
+    to_lds_some(from(ka, i) + k, to_k + i * step * C * 16,
+                __builtin_amdgcn_ballot_w64(key_chunk<C>(rw, lc) * 8 < a.D));
+    const uint64_t v_on = __builtin_amdgcn_ballot_w64(on && value_chunk<C>(rw, lc) * 8 < a.D);
+    const uint64_t vi = from(va, i) + v;
+    if (v_on)
+      to_lds_some(vi, to_v + i * step * C * 16, v_on);
+    else
+      none = true;
     if (!on) *reinterpret_cast<u32x4*>(dv + i * step * C * 8 + lane * 8) = u32x4{0, 0, 0, 0};
   }
+  if (none) wait_vm<0>();  // fewer are on their way than those who count them think
 }
 
 // Scores of tokens that the lane's row does not see become -inf: those that
@@ -347,19 +354,23 @@ __device__ __forceinline__ void add_odd(const TreeArgs& a, const Source& s, uint
     }
 }
 
-// Many query rows: 128 of them, 32 a wave, over tiles of 64 tokens that the
-// waves share, the next one on its way while one is worked on.
-template <int NK, int ND, int C, bool kUniform>
-__global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs a) {
+// Many query rows, 32 a wave, over tiles of 64 tokens that the waves share:
+// kBufs of them in LDS, all but one on their way.  Table entries and mask bytes
+// come through LDS too, kAhead tiles ahead: a wave that waited for one in a
+// register would wait for every tile requested before it (2 x 131072 tokens: 822
+// us, 697 without reading the table at all).
+constexpr int kRing = 8;  // tiles whose entries LDS holds
+template <int NK, int ND, int C, int W, int kBufs, bool kUniform>
+__global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs a) {
   constexpr int kTile = kTokens * C * 8;  // halves
   extern __shared__ uint16_t smem[];
-  uint16_t* sk = smem;              // [2][kTile]
-  uint16_t* sv = smem + 2 * kTile;  // [2][kTile]
+  uint16_t* sk = smem;                  // [kBufs][kTile]
+  uint16_t* sv = smem + kBufs * kTile;  // [kBufs][kTile]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
   Work w;
-  if (!find_work<kTokens, kBlock>(a, lane, wave, &w)) return;
+  if (!find_work<kTokens, W * kRows>(a, lane, wave, &w)) return;
   const Source src = source_of(a, w);
   const int begin = w.begin, end = w.end;
   const int own = w.n - w.drafts;  // negative where the length does not count all the drafted ones
@@ -368,17 +379,43 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
 
   // Key dimensions that only pad the products: zeros, never loaded.
   if (a.D < 16 * NK) {
-    for (int i = threadIdx.x; i < 2 * kTile / 8; i += 64 * kWaves)
+    for (int i = threadIdx.x; i < kBufs * kTile / 8; i += 64 * W)
       *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
   auto load = [&](int t0, int places, int buf) {
     constexpr int kSpan = 64 / C;  // rows of a load
-    load_tile<C, C / kWaves, kUniform>(a, src, t0, places, lane, wave * kSpan, kWaves * kSpan,
-                                       sk + buf * kTile + wave * 512, sv + buf * kTile + wave * 512);
+    load_tile<C, C / W, kUniform>(a, src, t0, places, lane, wave * kSpan, W * kSpan,
+                                  sk + buf * kTile + wave * 512, sv + buf * kTile + wave * 512);
   };
-  int now = place(a, src, begin + lane), next = place(a, src, begin + kTokens + lane);
-  if (begin < end) load(begin, now, 0);
+  // Table entries and mask of a tile, 64 / W tokens a wave.
+  constexpr int kAhead = 2 * kBufs - 1, kShare = 64 / W;
+  const int32_t* ring = reinterpret_cast<const int32_t*>(smem + 2 * kBufs * kTile);  // [kRing][2][64]
+  const uint32_t ring_to = lds_address(smem + 2 * kBufs * kTile);
+  const bool masked = src.mask != nullptr;
+  auto request = [&](int t0) {  // past the end the last token's, so that there is always something to count
+    const int t = t0 + wave * kShare + lane;
+    const uint64_t on = __builtin_amdgcn_ballot_w64(lane < kShare);
+    const uint32_t to = ring_to + (uint32_t(t0 - begin) / kTokens % kRing * 2 * 64 + wave * kShare) * 4;
+    const int x = min(t, end - 1);
+    word_to_lds(src.row + page_index(a.div, x), to, on);
+    if (masked) byte_to_lds(src.mask + x, to + 64 * 4, on);
+  };
+  auto requested = [&](int t0) {
+    const int32_t* e = ring + uint32_t(t0 - begin) / kTokens % kRing * 2 * 64 + lane;
+    const int id = e[0], on = masked ? e[64] : 1;
+    return t0 + lane < end ? place_of(a, id, on != 0) : kDead;
+  };
+  // places of the tile at hand and of the kBufs - 1 after it
+  int places[kBufs];
+#pragma unroll
+  for (int i = 0; i < kBufs; ++i) places[i] = place(a, src, begin + i * kTokens + lane);
+#pragma unroll
+  for (int i = kBufs; i < kAhead; ++i)
+    if (begin < end) request(begin + i * kTokens);
+#pragma unroll
+  for (int i = 0; i < kBufs - 1; ++i)
+    if (begin + i * kTokens < end) load(begin + i * kTokens, places[i], i);
 
   const Row mine = row_of(a, w, min(m, w.rows - 1));
   half8 q[NK];
@@ -391,19 +428,28 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
   // One tile, in buffer `buf`.
   auto step = [&](int t0, auto constant) {
     constexpr int buf = decltype(constant)::value;
-    const uint64_t live = __builtin_amdgcn_ballot_w64(now >= 0);
-    now = next;
-    wait_vm<0>();
+    const uint64_t live = __builtin_amdgcn_ballot_w64(places[0] >= 0);
+    // what was requested after this tile may be on its way, as long as it is the same every time
+    constexpr int kTiles = (kBufs - 2) * 2 * (C / W);
+    if (kBufs == 2 || t0 + (kBufs - 2) * kTokens >= end)
+      wait_vm<0>();
+    else if (masked)
+      wait_vm<kTiles + 2 * (kBufs - 2)>();
+    else
+      wait_vm<kTiles + (kBufs - 2)>();
     __syncthreads();
-    if (t0 + kTokens < end) load(t0 + kTokens, now, buf ^ 1);
-    next = place(a, src, t0 + 2 * kTokens + lane);
+    request(t0 + kAhead * kTokens);
+    if (t0 + (kBufs - 1) * kTokens < end) load(t0 + (kBufs - 1) * kTokens, places[kBufs - 1], (buf + kBufs - 1) % kBufs);
+#pragma unroll
+    for (int i = 0; i + 1 < kBufs; ++i) places[i] = places[i + 1];
+    places[kBufs - 1] = requested(t0 + kBufs * kTokens);
     const bool drafts_here = t0 + kTokens > own;
     if (drafts_here) {
       // A drafted token's infinity or NaN must not reach rows that do not see
       // it (its weight there is zero): zeros in its place, added at the end.
       uint16_t* vt = sv + buf * kTile;
       bool bad = false;
-      for (int i = threadIdx.x; i < kTokens * C; i += 64 * kWaves)
+      for (int i = threadIdx.x; i < kTokens * C; i += 64 * W)
         if (t0 + i / C >= own && value_chunk<C>(i / C, i % C) * 8 < a.D) bad |= clear_odd(vt + i * 8);
       odd |= __syncthreads_or(bad);
     }
@@ -413,11 +459,16 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void tree_kernel(Tree
     if (drafts_here || ~live) hide(s, live, sees, t0, own, h);
     half8 p[4];
     weights(st, s, a.c, p);
-    outputs(st, at, (2 + buf) * kTile * 2, p);
+    outputs(st, at, (kBufs + buf) * kTile * 2, p);
   };
-  for (int t0 = begin; t0 < end; t0 += 2 * kTokens) {
+  if (kBufs > 2) wait_vm<0>();  // the first tiles are followed by fewer requests than later ones
+  for (int t0 = begin; t0 < end; t0 += kBufs * kTokens) {
     step(t0, std::integral_constant<int, 0>());
     if (t0 + kTokens < end) step(t0 + kTokens, std::integral_constant<int, 1>());
+    if constexpr (kBufs == 4) {
+      if (t0 + 2 * kTokens < end) step(t0 + 2 * kTokens, std::integral_constant<int, 2>());
+      if (t0 + 3 * kTokens < end) step(t0 + 3 * kTokens, std::integral_constant<int, 3>());
+    }
   }
   if (idle) return;
   const float l = sum_halves(st.l);
@@ -650,7 +701,7 @@ __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
 }
 
 template <int NK, int ND, int C, bool kUniform>
-hipError_t launch_as(const TreeArgs& a, bool few, uint32_t grid, hipStream_t s) {
+hipError_t launch_as(const TreeArgs& a, bool few, bool wide, uint32_t grid, hipStream_t s) {
   if (few) {
     constexpr int W = few_waves(C);
     constexpr int kLds = max_of(W * 2 * 32 * C * 16, W * 32 * 4 * (2 + 32 * ND + 4));
@@ -660,20 +711,31 @@ hipError_t launch_as(const TreeArgs& a, bool few, uint32_t grid, hipStream_t s) 
     tree_few_kernel<NK, ND, C, W, kUniform><<<grid, 64 * W, kLds, s>>>(a);
     return hipGetLastError();
   }
-  constexpr int kLds = 4 * kTokens * C * 16;
-  if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C, kUniform>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  constexpr int kEntries = kRing * 2 * 64 * 4;
+  constexpr int kTwo = 4 * kTokens * C * 16 + kEntries, kFour = 8 * kTokens * C * 16 + kEntries;
+  if constexpr (C == 16) {
+    if (wide) {
+      const hipError_t e =
+          hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C, 8, 4, kUniform>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, kFour);
+      if (e != hipSuccess) return e;
+      tree_kernel<NK, ND, C, 8, 4, kUniform><<<grid, 64 * 8, kFour, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  if (kTwo > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(tree_kernel<NK, ND, C, 4, 2, kUniform>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kTwo);
     if (e != hipSuccess) return e;
   }
-  tree_kernel<NK, ND, C, kUniform><<<grid, 64 * kWaves, kLds, s>>>(a);
+  tree_kernel<NK, ND, C, 4, 2, kUniform><<<grid, 64 * 4, kTwo, s>>>(a);
   return hipGetLastError();
 }
 
 template <int NK, int ND, int C>
-hipError_t launch(const TreeArgs& a, bool few, uint32_t grid, hipStream_t s) {
-  return a.S % (64 / C) == 0 ? launch_as<NK, ND, C, true>(a, few, grid, s)
-                             : launch_as<NK, ND, C, false>(a, few, grid, s);
+hipError_t launch(const TreeArgs& a, bool few, bool wide, uint32_t grid, hipStream_t s) {
+  return a.S % (64 / C) == 0 ? launch_as<NK, ND, C, true>(a, few, wide, grid, s)
+                             : launch_as<NK, ND, C, false>(a, few, wide, grid, s);
 }
 
 }  // namespace
@@ -683,14 +745,15 @@ TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, i
   TreePlan p;
   const int64_t rows = most * (Hq / Hkv);
   p.few = rows <= kRows;
-  const int64_t block = p.few ? kRows : kBlock;
+  const int chunks = D <= 64 ? 8 : D <= 128 ? 16 : 32;
+  p.wide = chunks == 16 && rows > kBlock;
+  const int64_t block = p.few ? kRows : p.wide ? 2 * kBlock : kBlock;
   p.tiles = std::max<int64_t>(1, (rows + block - 1) / block);
   const int64_t units = B * Hkv * p.tiles;
-  const int chunks = D <= 64 ? 8 : D <= 128 ? 16 : 32;
   const int64_t unit = p.few ? 32 * few_waves(chunks) : kTokens;
   const int64_t steps = (cap + unit - 1) / unit;
   // workgroups at a time
-  const int64_t slots = num_cus * int64_t(p.few ? (chunks == 8 ? 2 : 1) : (chunks == 32 ? 1 : 2));
+  const int64_t slots = num_cus * int64_t(p.few ? (chunks == 8 ? 2 : 1) : (chunks == 32 || p.wide ? 1 : 2));
   if (B >= 1 && B <= kMaxCut && steps > 2) {
     if (units < 2 * slots) {
       int64_t k = 1;
@@ -748,7 +811,7 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
   a.most = int(r.most);
   a.room = p.room;
   a.tiles = int(p.tiles);
-  a.rows = int(p.tiles) * (p.few ? kRows : kBlock);
+  a.rows = int(p.tiles) * (p.few ? kRows : p.wide ? 2 * kBlock : kBlock);
   a.order = p.order;
   a.zero = r.scale == 0.f;
   a.c = a.zero ? 1.f : std::abs(r.scale) * 1.44269504088896340736f;
@@ -764,11 +827,11 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
     a.part = reinterpret_cast<float*>(w + p.off_part);
   }
   const uint32_t grid = uint32_t(p.grid);
-  const hipError_t e = a.D <= 64    ? launch<4, 2, 8>(a, p.few, grid, s)
-                       : a.D <= 96  ? launch<6, 3, 16>(a, p.few, grid, s)
-                       : a.D <= 128 ? launch<8, 4, 16>(a, p.few, grid, s)
-                       : a.D <= 192 ? launch<12, 6, 32>(a, p.few, grid, s)
-                                    : launch<16, 8, 32>(a, p.few, grid, s);
+  const hipError_t e = a.D <= 64    ? launch<4, 2, 8>(a, p.few, p.wide, grid, s)
+                       : a.D <= 96  ? launch<6, 3, 16>(a, p.few, p.wide, grid, s)
+                       : a.D <= 128 ? launch<8, 4, 16>(a, p.few, p.wide, grid, s)
+                       : a.D <= 192 ? launch<12, 6, 32>(a, p.few, p.wide, grid, s)
+                                    : launch<16, 8, 32>(a, p.few, p.wide, grid, s);
   if (e != hipSuccess || !p.room) return e;
   const int per = a.D <= 64 ? 16 : a.D <= 128 ? 32 : 64;
   const int64_t rows = r.T * r.Hq;
