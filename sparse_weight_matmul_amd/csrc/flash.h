@@ -94,7 +94,8 @@ template <int NK, int ND, int C>
 struct Reads {
   lds_bytes base;
   uint32_t k[NK], v[2][ND];
-  __device__ __forceinline__ Reads(const uint16_t* lds, int lane) : base((lds_bytes)lds) {
+  // values: bytes from the first key tile to the first value tile
+  __device__ __forceinline__ Reads(const uint16_t* lds, int lane, int values) : base((lds_bytes)lds) {
     const int r = lane & 31, j = lane & 15, d16 = (lane >> 4) & 1, h = lane >> 5;
 #pragma unroll
     for (int x = 0; x < NK; ++x) k[x] = (r * C + key_chunk<C>(r, 2 * x + h)) * 16;
@@ -103,10 +104,29 @@ struct Reads {
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         const int row = 8 * e + 4 * h + (j >> 2);
-        v[e][d] = (row * C + value_chunk<C>(row, 4 * d + 2 * d16 + ((j & 3) >> 1))) * 16 + 8 * (j & 1);
+        v[e][d] = values + (row * C + value_chunk<C>(row, 4 * d + 2 * d16 + ((j & 3) >> 1))) * 16 + 8 * (j & 1);
       }
   }
 };
+
+// Key fragment x of 32 tokens at `at` (bytes), and value fragment d of 16.
+template <int NK, int ND, int C>
+__device__ __forceinline__ half8 read_keys(const Reads<NK, ND, C>& a, int at, int x) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) half8*>(a.base + a.k[x] + at);
+}
+template <int NK, int ND, int C>
+__device__ __forceinline__ half8 read_values(const Reads<NK, ND, C>& a, int at, int d) {
+  u32x4 w;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const s16x4 t =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(a.base + a.v[e][d] + at));
+    const u32x2 u = __builtin_bit_cast(u32x2, t);
+    w[2 * e] = u[0];
+    w[2 * e + 1] = u[1];
+  }
+  return __builtin_bit_cast(half8, w);
+}
 
 // Scores of 32 NB tokens of the key tile at `at` (bytes), before the scale.
 template <int NB, int NK, int ND, int C>
@@ -116,8 +136,7 @@ __device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const 
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int x = 0; x < NK; ++x)  // rows 32 apart have their chunks in the same order
-      f[b][x] = *reinterpret_cast<const __attribute__((address_space(3))) half8*>(a.base + a.k[x] +
-                                                                                   (at + b * 32 * C * 16));
+      f[b][x] = read_keys(a, at + b * 32 * C * 16, x);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[b][0], q[0], f32x16{}, 0, 0, 0);
@@ -139,12 +158,14 @@ __device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const 
 // in units of log2.  The maximum follows when a row has outgrown it by kLazy.
 template <int NB, int ND>
 __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[NB], float c, half8 (&p)[2 * NB]) {
-  float mx = s[0][0];
+  float most[4];  // four chains: one would wait for itself at every step
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int e = 0; e < 4; ++e) {
+    most[e] = s[0][e];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-  mx = max_halves(mx);
+    for (int i = e + 4; i < 16 * NB; i += 4) most[e] = fmaxf(most[e], s[i >> 4][i & 15]);
+  }
+  const float mx = max_halves(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
   if (__builtin_amdgcn_ballot_w64((mx - st.m) * c > kLazy)) {
     const float m = fmaxf(mx, st.m);
     const float f = m == st.m ? 1.f : __builtin_amdgcn_exp2f((st.m - m) * c);
@@ -179,18 +200,8 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
 #pragma unroll
   for (int x = 0; x < NX; ++x)
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // rows 16 apart have their chunks in the same order
-        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(a.base + a.v[e][d] + (at + x * 16 * C * 16)));
-        const u32x2 u = __builtin_bit_cast(u32x2, t);
-        w[2 * e] = u[0];
-        w[2 * e + 1] = u[1];
-      }
-      f[x][d] = __builtin_bit_cast(half8, w);
-    }
+    for (int d = 0; d < ND; ++d)  // rows 16 apart have their chunks in the same order
+      f[x][d] = read_values(a, at + x * 16 * C * 16, d);
 #pragma unroll
   for (int x = 0; x < NX; ++x)
 #pragma unroll
@@ -199,6 +210,50 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * ND, 0);
 #pragma unroll
   for (int x = 0; x < (NX - 1) * ND; ++x) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, ND, 0);
+}
+
+// The key fragments of a tile's first 32 tokens.
+template <int NK, int ND, int C>
+__device__ __forceinline__ void read_first(const Reads<NK, ND, C>& a, int at, half8 (&k)[NK]) {
+#pragma unroll
+  for (int x = 0; x < NK; ++x) k[x] = read_keys(a, at, x);
+}
+
+// Scores of the next 64 tokens (key tile at `at_k`, k: its first fragments) and
+// O^T += V^T P^T of the 64 before them (value tile at `at_v`), with every read on
+// its way several products ahead.
+template <int NK, int ND, int C>
+__device__ __forceinline__ void scores_and_outputs(State<ND>& st, const Reads<NK, ND, C>& a, int at_k, int at_v,
+                                                   const half8 (&k)[NK], const half8 (&q)[NK], f32x16 (&s)[2],
+                                                   const half8 (&p)[4]) {
+  static_assert(NK == 2 * ND);
+  half8 f[NK], v[4][ND];
+  read_first(a, at_k + 32 * C * 16, f);
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) v[x][d] = read_values(a, at_v + x * 16 * C * 16, d);
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b ? f[0] : k[0], q[0], f32x16{}, 0, 0, 0);
+#pragma unroll
+    for (int x = 1; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b ? f[x] : k[x], q[x], s[b], 0, 0, 0);
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[x][d], p[x], st.o[d], 0, 0, 0);
+#pragma unroll
+  for (int x = 0; x < 2 * NK; ++x) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+#pragma unroll
+  for (int x = 0; x < 3 * ND; ++x) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
   }

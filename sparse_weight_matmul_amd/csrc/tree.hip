@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
   half8 q[NK];
   load_query(a, w, mine, h, q);
   const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
-  const Reads<NK, ND, C> at(smem, lane);
+  const Reads<NK, ND, C> at(smem, lane, kBufs * kTile * 2);
   State<ND> st;
   st.clear();
   bool odd = false;
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
     if (drafts_here || ~live) hide(s, live, sees, t0, own, h);
     half8 p[4];
     weights(st, s, a.c, p);
-    outputs(st, at, (kBufs + buf) * kTile * 2, p);
+    outputs(st, at, buf * kTile * 2, p);
   };
   if (kBufs > 2) wait_vm<0>();  // the first tiles are followed by fewer requests than later ones
   for (int t0 = begin; t0 < end; t0 += kBufs * kTokens) {
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
   half8 q[NK];
   load_query(a, w, mine, h, q);
   const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
-  const Reads<NK, ND, C> at(sk, lane);
+  const Reads<NK, ND, C> at(sk, lane, kTile * 2);
   State<ND> st;
   st.clear();
   bool odd = false;
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
     if (drafts_here || live != 0xffffffffu) hide(s, live, sees, t0, own, h);
     half8 p[2];
     weights(st, s, a.c, p);
-    outputs(st, at, kTile * 2, p);
+    outputs(st, at, 0, p);
     __builtin_amdgcn_sched_barrier(0);  // the tile has been read: the next one takes its place
     if (t0 + 32 * W < end) load(t0 + 32 * W, now);
     next = place(a, src, t0 + 64 * W + r);
