@@ -643,8 +643,8 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
  *  0 <= starts[b] <= tokens (others are clamped to that); rows that belong to
  *  no sequence are neither read nor written.  Read by the kernel, so a captured
  *  graph follows them.
- *  Scores, maxima, sums and outputs are fp32; a weight is rounded to fp16 once
- *  before it meets its value row, out is rounded once.  A value that is not
+ *  Scores, sums and outputs are fp32; a weight is rounded to fp16 once before it
+ *  meets its value row, and counts so in the sum; out is rounded once.  A value that is not
  *  finite makes the outputs of its dimension an infinity or NaN in the rows
  *  that see its token, and in no other.
  *  Limits: dim a multiple of 8 up to 256, batch and q_heads at most 65535,
@@ -740,8 +740,8 @@ swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_tok
  *  workspace: DEVICE memory of at least swm_tree_attention_workspace_bytes
  *  bytes (0: NULL is fine), 16-byte aligned; calls that share it must be
  *  ordered on one stream.
- *  Scores, maxima, sums and outputs are fp32; a weight is rounded to fp16 once
- *  before it meets its value row, out is rounded once.
+ *  Scores, sums and outputs are fp32; a weight is rounded to fp16 once before it
+ *  meets its value row, and counts so in the sum; out is rounded once.
  *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
  *  heads, a scale that is not finite, negative sizes or strides, rows of out
  *  that share memory, mask_ld below the capacity, a workspace too small.

@@ -4,7 +4,7 @@
 //
 // Scores are formed transposed, S^T = K Q^T (A: 32 tokens, B: 32 query rows):
 // lane l of the result holds, for the one row l % 32, the tokens 8 (i / 4) + 4
-// (l / 32) + i % 4 of its registers i.  Maxima and sums are then per lane but
+// (l / 32) + i % 4 of its registers i.  Sums and maxima are then per lane but
 // for one exchange with lane l ^ 32, and the weights are the second product's
 // B operand as they stand, O^T = V^T P^T: step s of 16 tokens takes registers
 // 8 (s % 2) .. + 7 of score block s / 2, which are tokens 16 s + 8 (e / 4) + 4
@@ -32,13 +32,15 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 constexpr int kTokens = 64;  // of a tile
 constexpr int kRows = 32;    // query rows of a wave
 
-// The weights go into the second product as fp16, once rounded (2^-11 of each
-// weight, as large as the output's own rounding), times 2^kUp or up to 2^(kUp +
-// kLazy) where the running maximum is kLazy behind: 2^15 at most.  Weights down
-// to 2^-25 of the largest then keep their relative precision, and smaller ones
-// are off by 2^-36 of it at most.
-constexpr float kUp = 11.f;
-constexpr float kLazy = 4.f;
+// The weights e^(x - m) go into the second product as fp16, once rounded (2^-11
+// of each, as large as the output's own rounding), times 2^kUp.  The sum that
+// divides is that of the rounded weights, so that what they lose together
+// cancels.  m is the largest score when it was last looked for: a row's scores may
+// outgrow it by a factor of 2^(16 - kUp) before a weight leaves fp16's range,
+// which the sum shows, and only then is the largest looked for again (looking in
+// every tile took a quarter of its vector instructions).  Weights down to 2^-24
+// of the largest keep their relative precision; smaller ones are off by 2^-35 of it at most.
+constexpr float kUp = 10.f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -70,14 +72,16 @@ __device__ __forceinline__ float sum_halves(float v) {
   return a + b;
 }
 
-// A wave's running state for 32 rows: maximum (of the unscaled scores) and sum
-// per lane's row, the sum over the lane's own tokens only; O^T.
+// A wave's running state for 32 rows: m (of the unscaled scores), what it adds to
+// a score in units of log2 (infinity while there is none, so that the first tile
+// looks for it), the sum per lane's row over the lane's own tokens; O^T.
 template <int ND>
 struct State {
-  float m, l;
+  float m, base, l;
   f32x16 o[ND];
   __device__ __forceinline__ void clear() {
     m = neg_inf();
+    base = __builtin_inff();
     l = 0.f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
@@ -108,6 +112,27 @@ struct Reads {
       }
   }
 };
+
+// A query row's fragments, and what the scale's sign and a D that is no multiple
+// of 16 make of them: apart, so that nothing waits for the loads before it has to.
+template <int NK>
+__device__ __forceinline__ void load_query(const uint16_t* row, int D, int h, half8 (&q)[NK]) {
+#pragma unroll
+  for (int x = 0; x < NK; ++x) {
+    const int d = 16 * x + 8 * h;
+    q[x] = *reinterpret_cast<const half8*>(row + (d < D ? d : 0));
+  }
+}
+template <int NK>
+__device__ __forceinline__ void mend_query(int D, int h, bool zero, uint32_t flip, half8 (&q)[NK]) {
+  if (D == 16 * NK && !zero && !flip) return;
+#pragma unroll
+  for (int x = 0; x < NK; ++x) {
+    u32x4 w = __builtin_bit_cast(u32x4, q[x]);
+    if (16 * x + 8 * h >= D || zero) w = u32x4{0, 0, 0, 0};
+    q[x] = __builtin_bit_cast(half8, w ^ flip);
+  }
+}
 
 // Key fragment x of 32 tokens at `at` (bytes), and value fragment d of 16.
 template <int NK, int ND, int C>
@@ -154,20 +179,41 @@ __device__ __forceinline__ void scores(const Reads<NK, ND, C>& a, int at, const 
   __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
 }
 
-// The weights of a tile's scores and the running maximum and sum; c > 0: scale
-// in units of log2.  The maximum follows when a row has outgrown it by kLazy.
-template <int NB, int ND>
-__device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[NB], float c, half8 (&p)[2 * NB]) {
-  float most[4];  // four chains: one would wait for itself at every step
+// 2^(s c + base) as fp16, and their sum; c > 0: scale in units of log2.
+template <int NB>
+__device__ __forceinline__ float powers(const f32x16 (&s)[NB], float c, float base, half8 (&p)[2 * NB]) {
+  float sum[2 * NB];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    most[e] = s[0][e];
+  for (int x = 0; x < 2 * NB; ++x) {
+    u32x4 w;
+    sum[x] = 0.f;
 #pragma unroll
-    for (int i = e + 4; i < 16 * NB; i += 4) most[e] = fmaxf(most[e], s[i >> 4][i & 15]);
+    for (int e = 0; e < 8; e += 2) {
+      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e], c, base));
+      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e + 1], c, base));
+      const half2v h = __builtin_convertvector(f32x2{p0, p1}, half2v);
+      sum[x] = __builtin_amdgcn_fdot2(h, half2v{_Float16(1.f), _Float16(1.f)}, sum[x], false);
+      w[e >> 1] = __builtin_bit_cast(uint32_t, h);
+    }
+    p[x] = __builtin_bit_cast(half8, w);
   }
-  const float mx = max_halves(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
-  if (__builtin_amdgcn_ballot_w64((mx - st.m) * c > kLazy)) {
-    const float m = fmaxf(mx, st.m);
+#pragma unroll
+  for (int x = 1; x < 2 * NB; ++x) sum[0] += sum[x];
+  return sum[0];
+}
+
+// The weights of a tile's scores, and the running sum.  fresh: it is the first tile.
+template <int NB, int ND>
+__device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[NB], float c, bool fresh, half8 (&p)[2 * NB]) {
+  float sum = __builtin_inff();
+  if (!fresh) sum = powers(s, c, st.base, p);
+  if (__builtin_amdgcn_ballot_w64(!(sum < __builtin_inff()))) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+    const float m = fmaxf(max_halves(mx), st.m);
     const float f = m == st.m ? 1.f : __builtin_amdgcn_exp2f((st.m - m) * c);
     st.m = m;
     st.l *= f;
@@ -175,22 +221,12 @@ __device__ __forceinline__ void weights(State<ND>& st, const f32x16 (&s)[NB], fl
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) st.o[d][i] *= f;
+    const bool none = m == neg_inf();  // nothing live so far: weights of 2^-inf
+    const float base = none ? 0.f : kUp - m * c;
+    st.base = none ? __builtin_inff() : base;
+    sum = powers(s, c, base, p);
   }
-  const float base = st.m == neg_inf() ? 0.f : kUp - st.m * c;  // nothing live so far: weights of 2^-inf
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int x = 0; x < 2 * NB; ++x) {
-    u32x4 w;
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e], c, base));
-      const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e + 1], c, base));
-      sum[(e >> 1) & 3] += p0 + p1;
-      w[e >> 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{p0, p1}, half2v));
-    }
-    p[x] = __builtin_bit_cast(half8, w);
-  }
-  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  st.l += sum;
 }
 
 // O^T += V^T P^T over the 16 NX tokens of the value tile at `at` (bytes).
@@ -210,50 +246,6 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
   __builtin_amdgcn_sched_group_barrier(0x100, 2 * ND, 0);
 #pragma unroll
   for (int x = 0; x < (NX - 1) * ND; ++x) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, ND, 0);
-}
-
-// The key fragments of a tile's first 32 tokens.
-template <int NK, int ND, int C>
-__device__ __forceinline__ void read_first(const Reads<NK, ND, C>& a, int at, half8 (&k)[NK]) {
-#pragma unroll
-  for (int x = 0; x < NK; ++x) k[x] = read_keys(a, at, x);
-}
-
-// Scores of the next 64 tokens (key tile at `at_k`, k: its first fragments) and
-// O^T += V^T P^T of the 64 before them (value tile at `at_v`), with every read on
-// its way several products ahead.
-template <int NK, int ND, int C>
-__device__ __forceinline__ void scores_and_outputs(State<ND>& st, const Reads<NK, ND, C>& a, int at_k, int at_v,
-                                                   const half8 (&k)[NK], const half8 (&q)[NK], f32x16 (&s)[2],
-                                                   const half8 (&p)[4]) {
-  static_assert(NK == 2 * ND);
-  half8 f[NK], v[4][ND];
-  read_first(a, at_k + 32 * C * 16, f);
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-#pragma unroll
-    for (int d = 0; d < ND; ++d) v[x][d] = read_values(a, at_v + x * 16 * C * 16, d);
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b ? f[0] : k[0], q[0], f32x16{}, 0, 0, 0);
-#pragma unroll
-    for (int x = 1; x < NK; ++x) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b ? f[x] : k[x], q[x], s[b], 0, 0, 0);
-  }
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-#pragma unroll
-    for (int d = 0; d < ND; ++d) st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[x][d], p[x], st.o[d], 0, 0, 0);
-#pragma unroll
-  for (int x = 0; x < 2 * NK; ++x) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-#pragma unroll
-  for (int x = 0; x < 3 * ND; ++x) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
   }
@@ -317,6 +309,29 @@ __device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const 
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[i]),
                  "s"(resource), "s"(to + i * step)
                  : "memory");
+}
+
+// A row's output, O^T times `inv`, rounded; four dimensions a store where rows
+// are aligned to them.
+template <int ND>
+__device__ __forceinline__ void write_row(const State<ND>& st, float inv, uint16_t* dst, int D, int h) {
+  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 7) == 0;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int x = 32 * d + 2 * i + 4 * h;
+      const half2v lo = __builtin_convertvector(f32x2{st.o[d][i] * inv, st.o[d][i + 1] * inv}, half2v);
+      const half2v hi = __builtin_convertvector(f32x2{st.o[d][i + 2] * inv, st.o[d][i + 3] * inv}, half2v);
+      const u32x2 w = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+      if (D < 32 * ND && x >= D) continue;
+      if (wide) {
+        *reinterpret_cast<u32x2*>(dst + x) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[x + e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
 }
 
 // Zeros for the infinities and NaN among eight halves in LDS; whether there were any.

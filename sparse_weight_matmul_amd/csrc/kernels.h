@@ -210,7 +210,7 @@ struct PromptCall {
   bool causal = true;
 };
 int64_t prompt_grid(int64_t T, int64_t B, int64_t Hq);  // workgroups
-hipError_t launch_prompt(const PromptCall& r, hipStream_t s);
+hipError_t launch_prompt(const PromptCall& r, int num_cus, hipStream_t s);
 
 // Pages for what a step adds to each sequence, and back.
 struct ReserveCall {

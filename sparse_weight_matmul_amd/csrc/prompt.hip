@@ -1,8 +1,25 @@
 // Attention over whole prompts, packed one behind the other.
 //
-//   x_ij = scale * q_i . k_j ;  o_i = sum_j e^(x_ij - m_i) v_j / sum_j e^(x_ij - m_i),  m_i = max x_ij
+//   x_ij = scale * q_i . k_j ;  o_i = sum_j e^(x_ij - m_i) v_j / sum_j e^(x_ij - m_i)
 //
-// over the tokens j of the row's own sequence, j <= i if causal.
+// over the tokens j of the row's own sequence, j <= i if causal; m_i is any
+// number near the row's largest score (flash.h says which).
+//
+// Four D operations for every row and token it sees, against 4 D bytes a token and
+// head: bound by the matrix cores but for the shortest prompts.  A workgroup has
+// 128 rows of a head, 32 a wave, and goes once over the keys and values they see,
+// tile by tile through LDS, the next tile on its way meanwhile.  Key fragments are
+// read once per 32 rows, so that LDS reads (128 bytes a cycle and CU) take as long
+// as the products; together with the power limit that is what holds long prompts at
+// about 1.05 PFLOP/s: 1 x 16384 tokens, 32 heads on 8, 2030 us (with zeros for
+// inputs, which draw less power, 1480; a library's product of 8192^3 runs at 1.34
+// to 1.53 PFLOP/s with random inputs and at 2.2 with zeros).  Shorter ones pay 5 us
+// a workgroup for its first tile, which two or three workgroups to a CU
+// hide in part: 16 ragged x 2048, 32 heads 272 us (0.71 PFLOP/s).
+// Tried and slower: eight waves in two groups that take turns on the matrix cores
+// (2020 us, but 352 for the ragged batch), 64 rows a wave (half the LDS reads, but
+// the accumulators do not fit beside the rest without copies: 2490), all blocks of a
+// batch by their tokens (see find_block).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,6 +36,11 @@ using namespace flash;
 
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
+// Workgroups per CU from which tiles are small.  Measured with 32 heads of 128, us,
+// tiles of 64 / 32 tokens: 8 x 1024 tokens (9 a CU) 103 / 107, 64 x 100 (14) 88 /
+// 67, 1 x 16384 (16) 2038 / 2030, 16 ragged x 2048 (19) 280 / 272, 32 x 512 (20)
+// 171 / 165, 64 x 256 (24) 163 / 140, 1 x 512 (0.6) 17 / 20.
+constexpr int kMany = 12;
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -38,38 +60,49 @@ __device__ __forceinline__ void rows_of(const PromptArgs& a, int s, int* first, 
   *n = max(s1 - s0, 0);
 }
 
-// The block of query rows that comes at place u: block *j of sequence *s.
-// Long blocks go first where every sequence has a lane's register.
-template <int kBlock>
-__device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane, int* s, int* j) {
+// The block of query rows that comes at place u: sequence after sequence, of up
+// to 64 the longest first, so that short ones fill the end; a sequence's last
+// block first.  (All blocks by their tokens, whatever their sequence, is worse, 298
+// us for 281 at 16 ragged x 2048: the workgroups at work then read keys of so many
+// sequences that no L2 holds them.)
+struct Block {
+  int first, n, j;  // the sequence's rows, and which block of them
+};
+__device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane, Block* out) {
+  auto take = [&](int first, int n, int l, int j) {
+    out->first = __builtin_amdgcn_readlane(first, l);
+    out->n = __builtin_amdgcn_readlane(n, l);
+    out->j = j;
+    return true;
+  };
+  if (a.B > 1 && a.B <= 64) {
+    int first = 0, n = 0;
+    if (lane < a.B) rows_of(a, lane, &first, &n);
+    const int blocks = (n + kBlock - 1) / kBlock;
+    int before = 0;  // blocks of longer sequences, and of equal ones with a lower index
+    for (int l = 0; l < a.B; ++l) {
+      const int x = __builtin_amdgcn_readlane(blocks, l);
+      before += x > blocks || (x == blocks && l < lane) ? x : 0;
+    }
+    const uint64_t in = __builtin_amdgcn_ballot_w64(before <= u && u < before + blocks);
+    if (!in) return false;
+    const int l = __builtin_ctzll(in);
+    return take(first, n, l, __builtin_amdgcn_readlane(before + blocks, l) - 1 - u);
+  }
   int base = 0;
   for (int s0 = 0; s0 < a.B; s0 += 64) {
-    int first, n = 0;
+    int first = 0, n = 0;
     if (s0 + lane < a.B) rows_of(a, s0 + lane, &first, &n);
     const int blocks = (n + kBlock - 1) / kBlock;
     const int upto = base + int(scan_wave(uint32_t(blocks)));
     const uint64_t in = __builtin_amdgcn_ballot_w64(u < upto);
     if (in) {
       const int l = __builtin_ctzll(in);
-      *s = s0 + l;
-      *j = __builtin_amdgcn_readlane(upto, l) - 1 - u;  // the last block of a sequence first
-      return true;
+      return take(first, n, l, __builtin_amdgcn_readlane(upto, l) - 1 - u);
     }
     base = __builtin_amdgcn_readlane(upto, 63);
   }
   return false;
-}
-
-template <int NK>
-__device__ __forceinline__ void load_query(const PromptArgs& a, int row, int head, int h, half8 (&q)[NK]) {
-  const uint16_t* src = a.q + int64_t(row) * a.q_t + int64_t(head) * a.q_h;
-#pragma unroll
-  for (int x = 0; x < NK; ++x) {
-    const int d = 16 * x + 8 * h;
-    u32x4 w = *reinterpret_cast<const u32x4*>(src + (d < a.D ? d : 0));
-    if (d >= a.D || a.zero) w = u32x4{0, 0, 0, 0};
-    q[x] = __builtin_bit_cast(half8, w ^ a.flip);
-  }
 }
 
 // A row's output; what clear_odd took out of the value rows `from` .. `end` - 1
@@ -94,43 +127,32 @@ __device__ __forceinline__ void finish(const PromptArgs& a, State<ND>& st, const
     }
   }
   if (qi >= n) return;
-  uint16_t* dst = a.out + int64_t(first + qi) * a.o_t + int64_t(head) * a.o_h;
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int x = 32 * d + 2 * i + 4 * h;
-      if (x >= a.D) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dst[x + e] = __builtin_bit_cast(uint16_t, _Float16(st.o[d][i + e] * inv));
-    }
+  write_row(st, inv, a.out + int64_t(first + qi) * a.o_t + int64_t(head) * a.o_h, a.D, h);
 }
 
-template <int NK, int ND, int C, bool kCausal>
-__global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(PromptArgs a) {
-  constexpr int kTile = kTokens * C * 8;  // halves
-  constexpr int kLoads = C / kWaves;      // 1 KiB each, of a wave and tile
+// Tiles of 32 NB tokens.  With 64 tokens two workgroups share a CU, with 32 three,
+// whose waves fill more of each other's gaps, but each alone takes longer.
+template <int NK, int ND, int C, bool kCausal, int NB>
+__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void prompt_kernel(PromptArgs a) {
+  constexpr int kTokens = 32 * NB;
+  constexpr int kTile = kTokens * C * 8;        // halves
+  constexpr int kLoads = C * NB / 2 / kWaves;  // 1 KiB each, of a wave and tile
   extern __shared__ uint16_t smem[];
   uint16_t* sv = smem + 2 * kTile;  // two key tiles, then two value tiles
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int u = blockIdx.x / a.Hq;
   int head = blockIdx.x - u * a.Hq;
+  // workgroups go round the eight XCDs: neighbouring heads, which share keys, to one of them
   if (a.Hq % 8 == 0) head = (head & 7) * (a.Hq >> 3) + (head >> 3);
-  int seq, j;
-  if (!find_block<kBlock>(a, u, lane, &seq, &j)) return;
-  int first, n;
-  rows_of(a, seq, &first, &n);
-  first = __builtin_amdgcn_readfirstlane(first);
-  n = __builtin_amdgcn_readfirstlane(n);
+  Block block;
+  if (!find_block(a, u, lane, &block)) return;
+  const int first = block.first, n = block.n, j = block.j;
   const int q0 = j * kBlock + wave * kRows;  // the wave's first row
   const int end = kCausal ? min(n, (j + 1) * kBlock) : n;
   const int hkv = head / a.G;
   const int r = lane & 31, h = lane >> 5;
   const int qi = q0 + r;
-
-  half8 q[NK];
-  load_query<NK>(a, first + min(qi, n - 1), head, h, q);
 
   const uint16_t* kh = a.k + int64_t(first) * a.k_t + int64_t(hkv) * a.k_h;
   const uint16_t* vh = a.v + int64_t(first) * a.v_t + int64_t(hkv) * a.v_h;
@@ -143,7 +165,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
     v_off[i] = vc < a.D ? uint32_t(row * int(a.v_t) + vc) * 2 : 0x80000000u;
   }
   const uint32_t to = lds_address(smem);
-  auto load = [&](int t0, int buf) {
+  auto load = [&](int t0, int buf) {  // rows behind the sequence's end are zeros
     const int left = min(n - t0, kTokens);
     load_tile(kh + int64_t(t0) * a.k_t, ((left - 1) * int(a.k_t) + a.D) * 2, k_off, kLoads,
               to + (buf * kTile + wave * 512) * 2, kWaves * 1024);
@@ -151,7 +173,9 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
               to + ((2 + buf) * kTile + wave * 512) * 2, kWaves * 1024);
   };
 
-  // Bytes from the start of LDS: two key tiles, then two value tiles.
+  load(0, 0);
+  half8 q[NK];
+  load_query(a.q + int64_t(first + min(qi, n - 1)) * a.q_t + int64_t(head) * a.q_h, a.D, h, q);
   const Reads<NK, ND, C> at(smem, lane, 2 * kTile * 2);
   State<ND> st;
   st.clear();
@@ -162,6 +186,7 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
     wait_vm<0>();
     __syncthreads();
     if (t0 + kTokens < end) load(t0 + kTokens, buf ^ 1);
+    if (buf == 0 && t0 == 0) mend_query(a.D, h, a.zero, a.flip, q);
     if (kCausal && t0 + kTokens > j * kBlock) {
       // An infinity or NaN times a weight of zero would reach rows that do not
       // see its token: zeros in its place here, added to the rows that do at the end.
@@ -171,21 +196,20 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
       odd |= __syncthreads_or(bad);
     }
     if (kCausal && t0 > q0 + kRows - 1) return;
-    f32x16 s[2];
+    f32x16 s[NB];
     scores(at, buf * kTile * 2, q, s);
     if (t0 + kTokens > n || (kCausal && t0 + kTokens - 1 > q0)) {
       const int last = (kCausal ? min(qi, n - 1) : n - 1) - t0 - 4 * h;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (32 * b + 8 * (i >> 2) + (i & 3) > last) s[b][i] = neg_inf();
     }
-    half8 p[4];
-    weights(st, s, a.c, p);
+    half8 p[2 * NB];
+    weights(st, s, a.c, buf == 0 && t0 == 0, p);
     outputs(st, at, buf * kTile * 2, p);
   };
-  load(0, 0);
   for (int t0 = 0; t0 < end; t0 += 2 * kTokens) {
     step(t0, std::integral_constant<int, 0>());
     if (t0 + kTokens < end) step(t0 + kTokens, std::integral_constant<int, 1>());
@@ -193,208 +217,31 @@ __global__ __launch_bounds__(64 * kWaves, ND <= 4 ? 2 : 1) void prompt_kernel(Pr
   finish(a, st, vh, kCausal && odd, j * kBlock, end, qi, n, first, head, h);
 }
 
-// Long prompts: 256 rows, two groups of four waves that take turns on the matrix
-// cores.  While one group forms the scores of its next tile and the outputs of
-// the one before, the other turns its scores into weights; a barrier after each.
-// Tiles of keys and values go round four places in LDS each.
-constexpr int kWide = 8;
-constexpr int kLong = 512;
-constexpr int kWideBlock = kWide * kRows;
-
-__device__ __forceinline__ void turn() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-template <int NK, int ND, int C, bool kCausal>
-__global__ __launch_bounds__(64 * kWide, 2) void prompt_wide_kernel(PromptArgs a) {
-  constexpr int kTile = kTokens * C * 8;  // halves
-  constexpr int kLoads = C / kWide;       // 1 KiB each, of a wave and tile
-  extern __shared__ uint16_t smem[];      // four key tiles, four value tiles
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool late = wave >= kWide / 2;  // the group that begins a turn later
-  const int u = blockIdx.x / a.Hq;
-  int head = blockIdx.x - u * a.Hq;
-  if (a.Hq % 8 == 0) head = (head & 7) * (a.Hq >> 3) + (head >> 3);
-  int seq, j;
-  if (!find_block<kWideBlock>(a, u, lane, &seq, &j)) return;
-  int first, n;
-  rows_of(a, seq, &first, &n);
-  first = __builtin_amdgcn_readfirstlane(first);
-  n = __builtin_amdgcn_readfirstlane(n);
-  const int q0 = j * kWideBlock + wave * kRows;  // the wave's first row
-  const int end = kCausal ? min(n, (j + 1) * kWideBlock) : n;
-  const int tiles = (end + kTokens - 1) / kTokens;  // of the workgroup
-  const int mine = kCausal ? min(tiles, (q0 + kRows - 1) / kTokens + 1) : tiles;
-  const int hkv = head / a.G;
-  const int r = lane & 31, h = lane >> 5;
-  const int qi = q0 + r;
-  half8 q[NK];
-  load_query<NK>(a, first + min(qi, n - 1), head, h, q);
-
-  const uint16_t* kh = a.k + int64_t(first) * a.k_t + int64_t(hkv) * a.k_h;
-  const uint16_t* vh = a.v + int64_t(first) * a.v_t + int64_t(hkv) * a.v_h;
-  uint32_t k_off[kLoads], v_off[kLoads];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int at = (i * kWide + wave) * 64 + lane, row = at / C, c = at % C;
-    const int kc = key_chunk<C>(row, c) * 8, vc = value_chunk<C>(row, c) * 8;
-    k_off[i] = kc < a.D ? uint32_t(row * int(a.k_t) + kc) * 2 : 0x80000000u;
-    v_off[i] = vc < a.D ? uint32_t(row * int(a.v_t) + vc) * 2 : 0x80000000u;
-  }
-  const uint32_t to = lds_address(smem);
-  // tile i into place i % 4; rows behind the sequence's end are zeros
-  auto load_k = [&](int i, int place) {
-    const int t0 = i * kTokens, left = min(n - t0, kTokens);
-    load_tile(kh + int64_t(t0) * a.k_t, ((left - 1) * int(a.k_t) + a.D) * 2, k_off, kLoads,
-              to + (place * kTile + wave * 512) * 2, kWide * 1024);
-  };
-  auto load_v = [&](int i, int place) {
-    const int t0 = i * kTokens, left = min(n - t0, kTokens);
-    load_tile(vh + int64_t(t0) * a.v_t, ((left - 1) * int(a.v_t) + a.D) * 2, v_off, kLoads,
-              to + ((4 + place) * kTile + wave * 512) * 2, kWide * 1024);
-  };
-  // Value tile i is here as far as this wave loaded it.  In tiles that some rows
-  // see a part of, see prompt_kernel.
-  bool odd = false;
-  auto arrived = [&](int i, int place) {
-    if (!kCausal || i >= tiles || (i + 1) * kTokens <= j * kWideBlock) return;
-    uint16_t* vt = smem + (4 + place) * kTile;
-#pragma unroll
-    for (int x = 0; x < kLoads; ++x) odd |= clear_odd(vt + (x * kWide + wave) * 512 + lane * 8);
-  };
-
-  const Reads<NK, ND, C> at(smem, lane, 4 * kTile * 2);
-  State<ND> st;
-  st.clear();
-  f32x16 s[2];
-  half8 p[4], k[NK];
-  auto softmax = [&] {
-    weights(st, s, a.c, p);
-    asm volatile("" ::"v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "v"(st.l));  // here, not where they are used
-  };
-  auto hide = [&](int i) {  // what the rows do not see of tile i
-    const int t0 = i * kTokens;
-    if (t0 + kTokens > n || (kCausal && t0 + kTokens - 1 > q0)) {
-      const int last = (kCausal ? min(qi, n - 1) : n - 1) - t0 - 4 * h;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (32 * b + 8 * (e >> 2) + (e & 3) > last) s[b][e] = neg_inf();
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < tiles) load_k(i, i);
-    if (i < 3 && i < tiles) load_v(i, i);
-  }
-  if (tiles > 3)
-    wait_vm<6 * kLoads>();
-  else
-    wait_vm<0>();
-  turn();
-  scores(at, 0, q, s);
-  hide(0);
-  softmax();
-  wait_vm<0>();
-  arrived(0, 0);
-  arrived(1, 1);
-  turn();
-  if (late) turn();
-  // One tile: the products of tile i, then the weights of tile i + 1.  While every
-  // row sees all of the tiles up to i + 2 and there are four more of them:
-  int i = 0;
-  auto step = [&](auto constant) {
-    constexpr int x = decltype(constant)::value;  // i % 4
-    load_k(i + 4, x);
-    load_v(i + 3, (x + 3) % 4);
-    __builtin_amdgcn_s_setprio(1);
-    scores_and_outputs(st, at, (x + 1) % 4 * kTile * 2, x * kTile * 2, k, q, s, p);
-    __builtin_amdgcn_s_setprio(0);
-    turn();
-    read_first(at, (x + 2) % 4 * kTile * 2, k);  // for the products of the next turn but one
-    softmax();
-    // the late group reads keys i + 3 and values i + 2 a turn after the early one has
-    wait_vm<2 * kLoads>();
-    turn();
-    ++i;
-  };
-  const int whole = min((kCausal ? min(j * kWideBlock, n) : n) / kTokens - 2, tiles - 4);
-  if (whole >= 4) read_first(at, kTile * 2, k);
-  while (i + 4 <= whole) {
-    step(std::integral_constant<int, 0>());
-    step(std::integral_constant<int, 1>());
-    step(std::integral_constant<int, 2>());
-    step(std::integral_constant<int, 3>());
-  }
-#pragma clang loop unroll(disable)
-  for (; i < tiles; ++i) {
-    const int x = i & 3;
-    if (i + 4 < tiles) load_k(i + 4, x);
-    if (i + 3 < tiles) load_v(i + 3, (x + 3) & 3);
-    if (i + 1 < mine) {
-      read_first(at, ((x + 1) & 3) * kTile * 2, k);
-      scores_and_outputs(st, at, ((x + 1) & 3) * kTile * 2, x * kTile * 2, k, q, s, p);
-    } else if (i < mine)
-      outputs(st, at, x * kTile * 2, p);
-    turn();
-    if (i + 1 < mine) {
-      hide(i + 1);
-      softmax();
-    }
-    if (i + 4 < tiles)
-      wait_vm<2 * kLoads>();
-    else
-      wait_vm<0>();
-    arrived(i + 2, (x + 2) & 3);
-    turn();
-  }
-  if (!late) turn();
-  if (kCausal) odd = __syncthreads_or(odd);
-  finish(a, st, vh, odd, j * kWideBlock, end, qi, n, first, head, h);
-}
-
-template <int NK, int ND, int C, bool kCausal>
+template <int NK, int ND, int C, bool kCausal, int NB>
 hipError_t launch_as(const PromptArgs& a, uint32_t grid, hipStream_t s) {
-  constexpr int kLds = 4 * kTokens * C * 16;
+  constexpr int kLds = 4 * 32 * NB * C * 16;
   if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel<NK, ND, C, kCausal>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel<NK, ND, C, kCausal, NB>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  prompt_kernel<NK, ND, C, kCausal><<<grid, 64 * kWaves, kLds, s>>>(a);
-  return hipGetLastError();
-}
-
-template <int NK, int ND, int C, bool kCausal>
-hipError_t launch_wide(const PromptArgs& a, uint32_t grid, hipStream_t s) {
-  constexpr int kLds = 8 * kTokens * C * 16;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_wide_kernel<NK, ND, C, kCausal>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-  if (e != hipSuccess) return e;
-  prompt_wide_kernel<NK, ND, C, kCausal><<<grid, 64 * kWide, kLds, s>>>(a);
+  prompt_kernel<NK, ND, C, kCausal, NB><<<grid, 64 * kWaves, kLds, s>>>(a);
   return hipGetLastError();
 }
 
 template <int NK, int ND, int C>
-hipError_t launch(const PromptArgs& a, bool causal, uint32_t grid, hipStream_t s) {
-  if constexpr (C == 16) {
-    if (a.T / a.B >= kLong) {
-      const uint32_t blocks = uint32_t(a.T / kWideBlock + std::min(a.T, a.B)) * a.Hq;
-      return causal ? launch_wide<NK, ND, C, true>(a, blocks, s) : launch_wide<NK, ND, C, false>(a, blocks, s);
-    }
+hipError_t launch(const PromptArgs& a, bool causal, bool small, uint32_t grid, hipStream_t s) {
+  if constexpr (C == 16) {  // shorter rows leave room for three anyway, longer ones for one
+    if (small) return causal ? launch_as<NK, ND, C, true, 1>(a, grid, s) : launch_as<NK, ND, C, false, 1>(a, grid, s);
   }
-  return causal ? launch_as<NK, ND, C, true>(a, grid, s) : launch_as<NK, ND, C, false>(a, grid, s);
+  return causal ? launch_as<NK, ND, C, true, 2>(a, grid, s) : launch_as<NK, ND, C, false, 2>(a, grid, s);
 }
 
 }  // namespace
 
 int64_t prompt_grid(int64_t T, int64_t B, int64_t Hq) { return (T / kBlock + std::min(T, B)) * Hq; }
 
-hipError_t launch_prompt(const PromptCall& r, hipStream_t s) {
+hipError_t launch_prompt(const PromptCall& r, int num_cus, hipStream_t s) {
   PromptArgs a{};
   a.q = r.q;
   a.k = r.k;
@@ -418,11 +265,12 @@ hipError_t launch_prompt(const PromptCall& r, hipStream_t s) {
   a.c = a.zero ? 1.f : std::abs(r.scale) * 1.44269504088896340736f;
   a.flip = r.scale < 0.f ? 0x80008000u : 0u;
   const uint32_t grid = uint32_t(prompt_grid(r.T, r.B, r.Hq));
-  if (a.D <= 64) return launch<4, 2, 8>(a, r.causal, grid, s);
-  if (a.D <= 96) return launch<6, 3, 16>(a, r.causal, grid, s);
-  if (a.D <= 128) return launch<8, 4, 16>(a, r.causal, grid, s);
-  if (a.D <= 192) return launch<12, 6, 32>(a, r.causal, grid, s);
-  return launch<16, 8, 32>(a, r.causal, grid, s);
+  const bool small = int64_t(grid) >= kMany * num_cus;
+  if (a.D <= 64) return launch<4, 2, 8>(a, r.causal, small, grid, s);
+  if (a.D <= 96) return launch<6, 3, 16>(a, r.causal, small, grid, s);
+  if (a.D <= 128) return launch<8, 4, 16>(a, r.causal, small, grid, s);
+  if (a.D <= 192) return launch<12, 6, 32>(a, r.causal, small, grid, s);
+  return launch<16, 8, 32>(a, r.causal, small, grid, s);
 }
 
 }  // namespace swm

@@ -262,7 +262,9 @@ swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, 
   r.D = dim;
   r.scale = scale;
   r.causal = causal != 0;
-  SWM_HIP(swm::launch_prompt(r, static_cast<hipStream_t>(stream)));
+  int dev = 0;
+  SWM_HIP(hipGetDevice(&dev));
+  SWM_HIP(swm::launch_prompt(r, swm::num_cus(dev), static_cast<hipStream_t>(stream)));
   return SWM_OK;
 }
 

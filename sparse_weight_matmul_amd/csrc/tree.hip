@@ -63,13 +63,12 @@ __device__ __forceinline__ uint64_t pick(uint64_t v, int from) {
 // Which drafted tokens the lane's one sees: bit j for token j.  Every lane
 // starts with itself and its parent; each round adds what the farthest one seen
 // so far sees: 2, 4, .. generations.  A parent that is not before its child is none.
-__device__ __forceinline__ uint64_t ancestors(const TreeArgs& a, int first, int n, int lane) {
+__device__ __forceinline__ int parent_of(const TreeArgs& a, int first, int n, int lane) {
+  return lane < n ? a.parents ? a.parents[first + lane] : lane - 1 : -1;
+}
+__device__ __forceinline__ uint64_t ancestors(int up, int lane) {
   uint64_t sees = uint64_t(1) << lane;
-  int up = -1;
-  if (lane < n) {
-    up = a.parents ? a.parents[first + lane] : lane - 1;
-    if (up < 0 || up >= lane) up = -1;
-  }
+  if (up >= lane) up = -1;
 #pragma unroll
   for (int r = 0; r < 6; ++r) {
     const int from = max(up, 0);
@@ -83,13 +82,26 @@ __device__ __forceinline__ uint64_t ancestors(const TreeArgs& a, int first, int 
   return sees;
 }
 
+// What lane l holds of sequences 2 l and 2 l + 1: the packed rows of their drafted
+// tokens, how many they are, and their tokens (none of all that past the batch).
+struct Held {
+  int first[2], drafts[2], n[2];
+};
+__device__ __forceinline__ Held hold(const TreeArgs& a, int lane) {
+  Held x;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int b = min(2 * lane + e, a.B - 1);
+    drafted(a, b, &x.first[e], &x.drafts[e]);
+    x.n[e] = min(max(a.lengths[b], 0), a.cap);
+    if (2 * lane + e >= a.B) x.drafts[e] = x.n[e] = 0;
+  }
+  return x;
+}
 // Tokens of a sequence in units of kUnit, one at least where it has drafted ones.
 template <int kUnit>
-__device__ __forceinline__ uint32_t units_of(const TreeArgs& a, int b) {
-  if (b >= a.B) return 0;
-  int first, n;
-  drafted(a, b, &first, &n);
-  return n ? max((min(max(a.lengths[b], 0), a.cap) + kUnit - 1) / kUnit, 1) : 0;
+__device__ __forceinline__ uint32_t units_of(const Held& x, int e) {
+  return x.drafts[e] ? max((x.n[e] + kUnit - 1) / kUnit, 1) : 0;
 }
 
 // The pieces that the sequences are cut into: `each` units, the fewest (two at
@@ -101,8 +113,8 @@ struct Cuts {
   int first, mid, last;
 };
 template <int kUnit>
-__device__ __forceinline__ Cuts cut(const TreeArgs& a, int lane) {
-  const uint32_t t0 = units_of<kUnit>(a, 2 * lane), t1 = units_of<kUnit>(a, 2 * lane + 1);
+__device__ __forceinline__ Cuts cut(const TreeArgs& a, const Held& x) {
+  const uint32_t t0 = units_of<kUnit>(x, 0), t1 = units_of<kUnit>(x, 1);
   const uint32_t total = wave_sum(t0 + t1), room = a.room;
   uint32_t c0, c1;
   auto count = [&](uint32_t q) {
@@ -135,15 +147,18 @@ __device__ __forceinline__ Cuts cut(const TreeArgs& a, int lane) {
 
 // The sequence that comes i-th by length, the longest first.
 template <int kUnit>
-__device__ __forceinline__ int by_length(const TreeArgs& a, int lane, int i) {
+__device__ __forceinline__ int by_length(const TreeArgs& a, const Held& x, int lane, int i) {
   // unique keys: units, then the lower sequence; those past the batch have none below them
-  auto key = [&](int b) { return b < a.B ? units_of<kUnit>(a, b) << 7 | uint32_t(127 - b) : 0u; };
-  const uint32_t k0 = key(2 * lane), k1 = key(2 * lane + 1);
+  auto key = [&](int e) {
+    const int b = 2 * lane + e;
+    return b < a.B ? units_of<kUnit>(x, e) << 7 | uint32_t(127 - b) : 0u;
+  };
+  const uint32_t k0 = key(0), k1 = key(1);
   int r0 = 0, r1 = 0;
   for (int l = 0; l < (a.B + 1) / 2; ++l) {
-    const uint32_t x = __builtin_amdgcn_readlane(k0, l), z = __builtin_amdgcn_readlane(k1, l);
-    r0 += int(x > k0) + int(z > k0);
-    r1 += int(x > k1) + int(z > k1);
+    const uint32_t y = __builtin_amdgcn_readlane(k0, l), z = __builtin_amdgcn_readlane(k1, l);
+    r0 += int(y > k0) + int(z > k0);
+    r1 += int(y > k1) + int(z > k1);
   }
   const uint64_t in0 = __builtin_amdgcn_ballot_w64(2 * lane < a.B && r0 == i);
   const uint64_t in1 = __builtin_amdgcn_ballot_w64(2 * lane + 1 < a.B && r1 == i);
@@ -169,36 +184,45 @@ __device__ __forceinline__ bool find_work(const TreeArgs& a, int lane, int wave,
   int b = w->piece, nth = 0;
   w->count = 1;
   uint32_t each = 0;
-  if (a.room > 0) {
-    const Cuts c = cut<kUnit>(a, lane);
-    if (blockIdx.x == 0 && wave == 0) {
-      if (2 * lane < a.B) {
-        a.plan[4 * lane] = c.first;
-        a.plan[4 * lane + 1] = c.mid - c.first;
+  if (a.room > 0 || a.order) {
+    const Held x = hold(a, lane);
+    if (a.room > 0) {
+      const Cuts c = cut<kUnit>(a, x);
+      if (blockIdx.x == 0 && wave == 0) {
+        if (2 * lane < a.B) {
+          a.plan[4 * lane] = c.first;
+          a.plan[4 * lane + 1] = c.mid - c.first;
+        }
+        if (2 * lane + 1 < a.B) {
+          a.plan[4 * lane + 2] = c.mid;
+          a.plan[4 * lane + 3] = c.last - c.mid;
+        }
       }
-      if (2 * lane + 1 < a.B) {
-        a.plan[4 * lane + 2] = c.mid;
-        a.plan[4 * lane + 3] = c.last - c.mid;
-      }
+      const uint64_t in = __builtin_amdgcn_ballot_w64(w->piece >= c.first && w->piece < c.last);
+      if (in == 0) return false;  // more workgroups than pieces
+      const int l = __builtin_ctzll(in);
+      const int from = __builtin_amdgcn_readlane(c.first, l), mid = __builtin_amdgcn_readlane(c.mid, l);
+      const bool second = w->piece >= mid;
+      b = 2 * l + second;
+      nth = w->piece - (second ? mid : from);
+      w->count = second ? __builtin_amdgcn_readlane(c.last, l) - mid : mid - from;
+      each = __builtin_amdgcn_readfirstlane(c.each) * kUnit;
+    } else {
+      b = by_length<kUnit>(a, x, lane, w->piece);
     }
-    const uint64_t in = __builtin_amdgcn_ballot_w64(w->piece >= c.first && w->piece < c.last);
-    if (in == 0) return false;  // more workgroups than pieces
-    const int l = __builtin_ctzll(in);
-    const int from = __builtin_amdgcn_readlane(c.first, l), mid = __builtin_amdgcn_readlane(c.mid, l);
-    const bool second = w->piece >= mid;
-    b = 2 * l + second;
-    nth = w->piece - (second ? mid : from);
-    w->count = second ? __builtin_amdgcn_readlane(c.last, l) - mid : mid - from;
-    each = __builtin_amdgcn_readfirstlane(c.each) * kUnit;
-  } else if (a.order) {
-    b = by_length<kUnit>(a, lane, w->piece);
+    w->b = b = __builtin_amdgcn_readfirstlane(b);
+    const bool odd = b & 1;
+    w->first = __builtin_amdgcn_readlane(odd ? x.first[1] : x.first[0], b >> 1);
+    w->drafts = __builtin_amdgcn_readlane(odd ? x.drafts[1] : x.drafts[0], b >> 1);
+    w->n = __builtin_amdgcn_readlane(odd ? x.n[1] : x.n[0], b >> 1);
+  } else {
+    w->b = b = __builtin_amdgcn_readfirstlane(b);
+    drafted(a, b, &w->first, &w->drafts);
+    w->first = __builtin_amdgcn_readfirstlane(w->first);
+    w->drafts = __builtin_amdgcn_readfirstlane(w->drafts);
+    w->n = __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), a.cap));
   }
-  w->b = b = __builtin_amdgcn_readfirstlane(b);
-  drafted(a, b, &w->first, &w->drafts);
-  w->first = __builtin_amdgcn_readfirstlane(w->first);
-  w->drafts = __builtin_amdgcn_readfirstlane(w->drafts);
   w->rows = w->drafts * a.G;
-  w->n = __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), a.cap));
   w->begin = __builtin_amdgcn_readfirstlane(int(min(int64_t(nth) * each, int64_t(w->n))));
   w->end = __builtin_amdgcn_readfirstlane(
       nth == w->count - 1 ? w->n : int(min(int64_t(nth + 1) * each, int64_t(w->n))));
@@ -215,16 +239,8 @@ __device__ __forceinline__ Row row_of(const TreeArgs& a, const Work& w, int m) {
   r.head = w.hkv * a.G + m - r.token * a.G;
   return r;
 }
-template <int NK>
-__device__ __forceinline__ void load_query(const TreeArgs& a, const Work& w, const Row& r, int h, half8 (&q)[NK]) {
-  const uint16_t* src = a.q + int64_t(w.first + r.token) * a.q_t + int64_t(r.head) * a.q_h;
-#pragma unroll
-  for (int k = 0; k < NK; ++k) {
-    const int d = 16 * k + 8 * h;
-    u32x4 x = *reinterpret_cast<const u32x4*>(src + (d < a.D ? d : 0));
-    if (d >= a.D || a.zero) x = u32x4{0, 0, 0, 0};
-    q[k] = __builtin_bit_cast(half8, x ^ a.flip);
-  }
+__device__ __forceinline__ const uint16_t* query_of(const TreeArgs& a, const Work& w, const Row& r) {
+  return a.q + int64_t(w.first + r.token) * a.q_t + int64_t(r.head) * a.q_h;
 }
 
 // The cache as one workgroup sees it.
@@ -376,6 +392,11 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
   const int own = w.n - w.drafts;  // negative where the length does not count all the drafted ones
   const int m = w.m0 + wave * kRows + r;
   const bool idle = w.m0 + wave * kRows >= w.rows;
+  // requested before the tiles, which whoever waits for these would wait for too
+  const Row mine = row_of(a, w, min(m, w.rows - 1));
+  const int parent = parent_of(a, w.first, w.drafts, lane);
+  half8 q[NK];
+  load_query(query_of(a, w, mine), a.D, h, q);
 
   // Key dimensions that only pad the products: zeros, never loaded.
   if (a.D < 16 * NK) {
@@ -417,10 +438,8 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
   for (int i = 0; i < kBufs - 1; ++i)
     if (begin + i * kTokens < end) load(begin + i * kTokens, places[i], i);
 
-  const Row mine = row_of(a, w, min(m, w.rows - 1));
-  half8 q[NK];
-  load_query(a, w, mine, h, q);
-  const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
+  const uint64_t sees = pick(ancestors(parent, lane), mine.token);
+  mend_query(a.D, h, a.zero, a.flip, q);
   const Reads<NK, ND, C> at(smem, lane, kBufs * kTile * 2);
   State<ND> st;
   st.clear();
@@ -458,7 +477,7 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
     scores(at, buf * kTile * 2, q, s);
     if (drafts_here || ~live) hide(s, live, sees, t0, own, h);
     half8 p[4];
-    weights(st, s, a.c, p);
+    weights(st, s, a.c, buf == 0 && t0 == begin, p);
     outputs(st, at, buf * kTile * 2, p);
   };
   if (kBufs > 2) wait_vm<0>();  // the first tiles are followed by fewer requests than later ones
@@ -493,16 +512,20 @@ __global__ __launch_bounds__(64 * W, ND <= 4 ? 2 : 1) void tree_kernel(TreeArgs 
     return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = a.out + int64_t(w.first + mine.token) * a.o_t + int64_t(mine.head) * a.o_h;
+  write_row(st, inv, a.out + int64_t(w.first + mine.token) * a.o_t + int64_t(mine.head) * a.o_h, a.D, h);
+}
+
+// Four dimensions of an output row.
+__device__ __forceinline__ void write_four(uint16_t* dst, const float4& o, float inv) {
+  const half2v lo = __builtin_convertvector(f32x2{o.x * inv, o.y * inv}, half2v);
+  const half2v hi = __builtin_convertvector(f32x2{o.z * inv, o.w * inv}, half2v);
+  const u32x2 w = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+    *reinterpret_cast<u32x2*>(dst) = w;
+  } else {
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int e = 32 * d + 2 * i + 4 * h;
-      if (e >= a.D) continue;
-#pragma unroll
-      for (int f = 0; f < 4; ++f) dst[e + f] = __builtin_bit_cast(uint16_t, _Float16(st.o[d][i + f] * inv));
-    }
+    for (int e = 0; e < 4; ++e) dst[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+  }
 }
 
 // Few query rows, 32 at most: bound by the read of the cache.  Every wave has
@@ -524,6 +547,11 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
   const Source src = source_of(a, w);
   const int end = w.end, own = w.n - w.drafts;
   const int t_first = w.begin + 32 * wave;
+  // requested before the tiles, which whoever waits for these would wait for too
+  const Row mine = row_of(a, w, min(r, w.rows - 1));
+  const int parent = parent_of(a, w.first, w.drafts, lane);
+  half8 q[NK];
+  load_query(query_of(a, w, mine), a.D, h, q);
 
   if (a.D < 16 * NK) {
     for (int i = lane; i < kTile / 8; i += 64) *reinterpret_cast<u32x4*>(sk + i * 8) = u32x4{0, 0, 0, 0};
@@ -535,10 +563,8 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
   int now = place(a, src, t_first + r), next = place(a, src, t_first + 32 * W + r);
   if (t_first < end) load(t_first, now);
 
-  const Row mine = row_of(a, w, min(r, w.rows - 1));
-  half8 q[NK];
-  load_query(a, w, mine, h, q);
-  const uint64_t sees = pick(ancestors(a, w.first, w.drafts, lane), mine.token);
+  const uint64_t sees = pick(ancestors(parent, lane), mine.token);
+  mend_query(a.D, h, a.zero, a.flip, q);
   const Reads<NK, ND, C> at(sk, lane, kTile * 2);
   State<ND> st;
   st.clear();
@@ -559,7 +585,7 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
     scores(at, 0, q, s);
     if (drafts_here || live != 0xffffffffu) hide(s, live, sees, t0, own, h);
     half8 p[2];
-    weights(st, s, a.c, p);
+    weights(st, s, a.c, t0 == t_first, p);
     outputs(st, at, 0, p);
     __builtin_amdgcn_sched_barrier(0);  // the tile has been read: the next one takes its place
     if (t0 + 32 * W < end) load(t0 + 32 * W, now);
@@ -618,11 +644,7 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
     } else {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const Row it = row_of(a, w, m);
-      uint16_t* dst = a.out + int64_t(w.first + it.token) * a.o_t + int64_t(it.head) * a.o_h + d;
-      dst[0] = __builtin_bit_cast(uint16_t, _Float16(o.x * inv));
-      dst[1] = __builtin_bit_cast(uint16_t, _Float16(o.y * inv));
-      dst[2] = __builtin_bit_cast(uint16_t, _Float16(o.z * inv));
-      dst[3] = __builtin_bit_cast(uint16_t, _Float16(o.w * inv));
+      write_four(a.out + int64_t(w.first + it.token) * a.o_t + int64_t(it.head) * a.o_h + d, o, inv);
     }
   }
 }
@@ -693,11 +715,7 @@ __global__ __launch_bounds__(kJoin) void tree_join_kernel(TreeArgs a, int per) {
   }
   if (part > 0 || d >= a.D) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = a.out + t * a.o_t + int64_t(qh) * a.o_h + d;
-  dst[0] = __builtin_bit_cast(uint16_t, _Float16(o.x * inv));
-  dst[1] = __builtin_bit_cast(uint16_t, _Float16(o.y * inv));
-  dst[2] = __builtin_bit_cast(uint16_t, _Float16(o.z * inv));
-  dst[3] = __builtin_bit_cast(uint16_t, _Float16(o.w * inv));
+  write_four(a.out + t * a.o_t + int64_t(qh) * a.o_h + d, o, inv);
 }
 
 template <int NK, int ND, int C, bool kUniform>
@@ -754,7 +772,7 @@ TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, i
   const int64_t steps = (cap + unit - 1) / unit;
   // workgroups at a time
   const int64_t slots = num_cus * int64_t(p.few ? (chunks == 8 ? 2 : 1) : (chunks == 32 || p.wide ? 1 : 2));
-  if (B >= 1 && B <= kMaxCut && steps > 2) {
+  if (B >= 1 && B <= kMaxCut && steps > 4) {
     if (units < 2 * slots) {
       int64_t k = 1;
       while (B > 1 && k < 4 && k * slots < 4 * units) ++k;

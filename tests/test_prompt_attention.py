@@ -4,10 +4,13 @@ Tolerances follow from the arithmetic: products of fp16 values are exact in
 fp32, so a score is off by at most E = scale * D * 2^-24 * sum |q_d k_d| (the
 fp32 sum) plus 2^-22 |x| (scaling and the subtraction of the maximum).  A
 weight is then relatively off by at most 2 E plus 2^-19 (the exponential, the
-rescales and the sum), and by its one rounding to fp16, 2^-11, or 2^-36 of the
-largest where it is far below it; the output's sum over n tokens, sixteen at a
-time, adds n / 16 + 64 roundings of 2^-24, its own rounding 2^-11 of itself
-(2^-25 below the normal range).
+rescales and the sum).  Its one rounding to fp16, d_j = 2^-11 p_j at most, or
+2^-35 of the largest weight where it is far below it, is in the numerator and in
+the sum that divides: sum (p_j + d_j) v_j / sum (p_j + d_j) is off by sum d_j
+(v_j - o), to first order, so by at most 2^-11 (sum p |v| + |o|) and n 2^-34 max
+|v|.  The output's sum over n tokens, sixteen at a time, adds n / 16 + 64
+roundings of 2^-24, its own rounding 2^-11 of itself (2^-25 below the normal
+range).
 """
 import ctypes
 
@@ -33,7 +36,7 @@ def attend(q, K, V, scale, sees):
     n = sees.sum(1)[:, None]
     eps = 2 * err + 2.0**-19 + 2.0**-11 + (n / 16 + 64) * 2.0**-24
     out = p @ V
-    tol = eps * (p @ np.abs(V)) + 2.0**-36 * n * np.abs(V).max(initial=0) + 2.0**-11 * np.abs(out) + 2.0**-25
+    tol = eps * (p @ np.abs(V)) + 2.0**-34 * n * np.abs(V).max(initial=0) + 2.0**-10 * np.abs(out) + 2.0**-25
     return out, tol
 
 
