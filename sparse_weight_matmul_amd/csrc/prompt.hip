@@ -41,6 +41,11 @@ constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
 // 67, 1 x 16384 (16) 2038 / 2030, 16 ragged x 2048 (19) 280 / 272, 32 x 512 (20)
 // 171 / 165, 64 x 256 (24) 163 / 140, 1 x 512 (0.6) 17 / 20.
 constexpr int kMany = 12;
+// Mean length below which a wave has a block of 32 rows by itself, where there are
+// two workgroups per CU and more.  us, as blocks of 128 / so: 64 x 10 tokens, 160 heads of
+// 64 135 / 35, 32 heads of 128: 64 x 10 46 / 17, 64 x 32 49 / 25, 64 x 64 50 / 44,
+// 64 x 100 67 / 69; 8 x 40, 32 of 256 (1.2 a CU) 13.7 / 14.9.
+constexpr int kShort = 80;
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -68,6 +73,7 @@ __device__ __forceinline__ void rows_of(const PromptArgs& a, int s, int* first, 
 struct Block {
   int first, n, j;  // the sequence's rows, and which block of them
 };
+template <int kBlock>
 __device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane, Block* out) {
   auto take = [&](int first, int n, int l, int j) {
     out->first = __builtin_amdgcn_readlane(first, l);
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void pro
   // workgroups go round the eight XCDs: neighbouring heads, which share keys, to one of them
   if (a.Hq % 8 == 0) head = (head & 7) * (a.Hq >> 3) + (head >> 3);
   Block block;
-  if (!find_block(a, u, lane, &block)) return;
+  if (!find_block<kBlock>(a, u, lane, &block)) return;
   const int first = block.first, n = block.n, j = block.j;
   const int q0 = j * kBlock + wave * kRows;  // the wave's first row
   const int end = kCausal ? min(n, (j + 1) * kBlock) : n;
@@ -217,6 +223,73 @@ __global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void pro
   finish(a, st, vh, kCausal && odd, j * kBlock, end, qi, n, first, head, h);
 }
 
+// Short prompts: a wave has 32 rows of a head by itself, with a tile of 32 tokens
+// of its own, so that no wave is there for rows that a sequence does not have.
+template <int NK, int ND, int C, bool kCausal>
+__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : 2) void prompt_short_kernel(PromptArgs a) {
+  constexpr int kTile = kRows * C * 8;  // halves
+  constexpr int kLoads = C / 2;         // 1 KiB each, of a tile
+  extern __shared__ uint16_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t* sk = smem + wave * 2 * kTile;  // no other wave looks at these
+  uint16_t* sv = sk + kTile;
+  const int unit = blockIdx.x * kWaves + wave, u = unit / a.Hq, head = unit - u * a.Hq;
+  Block block;
+  if (!find_block<kRows>(a, u, lane, &block)) return;
+  const int first = block.first, n = block.n, q0 = block.j * kRows;
+  const int end = kCausal ? min(n, q0 + kRows) : n;
+  const int hkv = head / a.G;
+  const int r = lane & 31, h = lane >> 5, qi = q0 + r;
+  const uint16_t* kh = a.k + int64_t(first) * a.k_t + int64_t(hkv) * a.k_h;
+  const uint16_t* vh = a.v + int64_t(first) * a.v_t + int64_t(hkv) * a.v_h;
+  uint32_t k_off[kLoads], v_off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = i * 64 + lane, row = at / C, c = at % C;
+    const int kc = key_chunk<C>(row, c) * 8, vc = value_chunk<C>(row, c) * 8;
+    k_off[i] = kc < a.D ? uint32_t(row * int(a.k_t) + kc) * 2 : 0x80000000u;
+    v_off[i] = vc < a.D ? uint32_t(row * int(a.v_t) + vc) * 2 : 0x80000000u;
+  }
+  const uint32_t to = lds_address(sk);
+  auto load = [&](int t0) {
+    const int left = min(n - t0, kRows);
+    load_tile(kh + int64_t(t0) * a.k_t, ((left - 1) * int(a.k_t) + a.D) * 2, k_off, kLoads, to, 1024);
+    load_tile(vh + int64_t(t0) * a.v_t, ((left - 1) * int(a.v_t) + a.D) * 2, v_off, kLoads, to + kTile * 2, 1024);
+  };
+  load(0);
+  half8 q[NK];
+  load_query(a.q + int64_t(first + min(qi, n - 1)) * a.q_t + int64_t(head) * a.q_h, a.D, h, q);
+  const Reads<NK, ND, C> at(sk, lane, kTile * 2);
+  State<ND> st;
+  st.clear();
+  bool odd = false;
+  for (int t0 = 0; t0 < end; t0 += kRows) {
+    wait_vm<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 == 0) mend_query(a.D, h, a.zero, a.flip, q);
+    if (kCausal && t0 == q0) {  // see prompt_kernel
+      bool bad = false;
+      for (int i = lane; i < kRows * C; i += 64) bad |= clear_odd(sv + i * 8);
+      odd = __builtin_amdgcn_ballot_w64(bad) != 0;
+    }
+    f32x16 s[1];
+    scores(at, 0, q, s);
+    if (t0 + kRows > n || (kCausal && t0 == q0)) {
+      const int last = (kCausal ? min(qi, n - 1) : n - 1) - t0 - 4 * h;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * (i >> 2) + (i & 3) > last) s[0][i] = neg_inf();
+    }
+    half8 p[2];
+    weights(st, s, a.c, t0 == 0, p);
+    outputs(st, at, 0, p);
+    __builtin_amdgcn_sched_barrier(0);  // the tile has been read: the next one takes its place
+    if (t0 + kRows < end) load(t0 + kRows);
+  }
+  finish(a, st, vh, odd, q0, end, qi, n, first, head, h);
+}
+
 template <int NK, int ND, int C, bool kCausal, int NB>
 hipError_t launch_as(const PromptArgs& a, uint32_t grid, hipStream_t s) {
   constexpr int kLds = 4 * 32 * NB * C * 16;
@@ -229,10 +302,27 @@ hipError_t launch_as(const PromptArgs& a, uint32_t grid, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int NK, int ND, int C, bool kCausal>
+hipError_t launch_short(const PromptArgs& a, hipStream_t s) {
+  constexpr int kLds = kWaves * 2 * kRows * C * 16;
+  if (kLds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_short_kernel<NK, ND, C, kCausal>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t units = (a.T / kRows + std::min(a.T, a.B)) * int64_t(a.Hq);
+  const uint32_t grid = uint32_t((units + kWaves - 1) / kWaves);
+  prompt_short_kernel<NK, ND, C, kCausal><<<grid, 64 * kWaves, kLds, s>>>(a);
+  return hipGetLastError();
+}
+
 template <int NK, int ND, int C>
-hipError_t launch(const PromptArgs& a, bool causal, bool small, uint32_t grid, hipStream_t s) {
+hipError_t launch(const PromptArgs& a, bool causal, uint32_t grid, int num_cus, hipStream_t s) {
+  if (a.T / a.B < kShort && grid >= 2u * num_cus)
+    return causal ? launch_short<NK, ND, C, true>(a, s) : launch_short<NK, ND, C, false>(a, s);
   if constexpr (C == 16) {  // shorter rows leave room for three anyway, longer ones for one
-    if (small) return causal ? launch_as<NK, ND, C, true, 1>(a, grid, s) : launch_as<NK, ND, C, false, 1>(a, grid, s);
+    if (grid >= uint32_t(kMany) * num_cus)
+      return causal ? launch_as<NK, ND, C, true, 1>(a, grid, s) : launch_as<NK, ND, C, false, 1>(a, grid, s);
   }
   return causal ? launch_as<NK, ND, C, true, 2>(a, grid, s) : launch_as<NK, ND, C, false, 2>(a, grid, s);
 }
@@ -265,12 +355,11 @@ hipError_t launch_prompt(const PromptCall& r, int num_cus, hipStream_t s) {
   a.c = a.zero ? 1.f : std::abs(r.scale) * 1.44269504088896340736f;
   a.flip = r.scale < 0.f ? 0x80008000u : 0u;
   const uint32_t grid = uint32_t(prompt_grid(r.T, r.B, r.Hq));
-  const bool small = int64_t(grid) >= kMany * num_cus;
-  if (a.D <= 64) return launch<4, 2, 8>(a, r.causal, small, grid, s);
-  if (a.D <= 96) return launch<6, 3, 16>(a, r.causal, small, grid, s);
-  if (a.D <= 128) return launch<8, 4, 16>(a, r.causal, small, grid, s);
-  if (a.D <= 192) return launch<12, 6, 32>(a, r.causal, small, grid, s);
-  return launch<16, 8, 32>(a, r.causal, small, grid, s);
+  if (a.D <= 64) return launch<4, 2, 8>(a, r.causal, grid, num_cus, s);
+  if (a.D <= 96) return launch<6, 3, 16>(a, r.causal, grid, num_cus, s);
+  if (a.D <= 128) return launch<8, 4, 16>(a, r.causal, grid, num_cus, s);
+  if (a.D <= 192) return launch<12, 6, 32>(a, r.causal, grid, num_cus, s);
+  return launch<16, 8, 32>(a, r.causal, grid, num_cus, s);
 }
 
 }  // namespace swm

@@ -104,6 +104,12 @@ CASES = [
     (40, 8, 16, [65, 130], "stacked"),
     (8, 8, 64, [3] * 70 + [150] + [0] * 60 + [129, 1], "separate"),  # more sequences than lanes
     (1, 1, 128, [2100], "separate"),
+    (16, 4, 64, [9, 1, 0, 33, 70, 31, 32, 64] * 8, "stacked"),       # a wave a block
+    (24, 3, 128, [20] * 30 + [0, 100, 65], "head"),
+    (32, 32, 80, [1, 2, 40] * 20, "separate"),
+    (36, 4, 256, [17, 35, 5, 0] * 16, "separate"),
+    (48, 4, 128, [100] * 70, "separate"),                            # small tiles
+    (48, 4, 96, [90, 0, 300, 128, 129, 1] * 12, "stacked"),
     (8, 2, 128, [1111, 640], "separate"),
 ]
 
@@ -207,6 +213,23 @@ def test_what_is_not_finite_stays_with_its_readers(gpu_lib, D, bad, at):
     hit[at:300] = True
     out = swm.prompt_attention(dq, dk, dv, ints(starts)).double().cpu().numpy()
     assert np.array_equal(np.isnan(out), hit)
+
+
+@gpu
+@pytest.mark.parametrize("Hq,lengths,at", [(32, [40, 9] * 20, 25), (32, [40, 9] * 20, 39), (64, [150] * 30, 70),
+                                           (64, [150] * 30, 149)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_is_not_finite_in_large_batches(gpu_lib, Hq, lengths, at, D):
+    """The same where blocks are a wave's and where tiles are small."""
+    q, k, v, dq, dk, dv = make(sum(lengths), Hq, 2, D)
+    starts = bounds(lengths)
+    ref, tol, _ = reference(q, k, v, starts, D ** -0.5, True)
+    dv[int(starts[2]) + at, 1, 5] = float("nan")
+    hit = np.zeros(ref.shape, bool)
+    hit[starts[2] + at:starts[3], Hq // 2:, 5] = True
+    out = swm.prompt_attention(dq, dk, dv, ints(starts)).double().cpu().numpy()
+    assert np.array_equal(np.isnan(out), hit)
+    assert np.all(np.abs(out - ref)[~hit] <= tol[~hit])
 
 
 @gpu
