@@ -1,9 +1,10 @@
-"""Greedy decoding with one pruned decoder layer, every step between its
-products on the library's serving operators:
+"""A prompt, then greedy decoding with one pruned decoder layer, every step
+between its products on the library's serving operators:
 
-    q, k, v     spmm of the row-stacked projections; the new keys and values
-                go into the paged cache
-    attention   paged_attention, adding the attention weights up per cached row
+    q, k, v     spmm of the row-stacked projections; kv_append puts the new keys
+                and values into the paged cache
+    attention   prompt_attention over the prompt, then paged_attention, adding
+                the attention weights up per cached row
     o_proj      spmm_epilogue with the residual stream
     FFN         gate_up_silu, then spmm_epilogue with the residual stream
     cache       kv_evict once a sequence is `slack` tokens over its budget
@@ -15,7 +16,7 @@ position encoding.  The state on the host is the step number and the length of
 each sequence.
 
     python examples/pruned_decode.py [--hidden 4096 --ffn 11008 --heads 32
-        --kv-heads 32 --vocab 32000 --batch 4 --steps 64 --budget 32 ...]
+        --kv-heads 32 --vocab 32000 --batch 4 --prompt 16 --steps 64 --budget 32 ...]
 """
 from __future__ import annotations
 
@@ -71,29 +72,44 @@ class Session:
         self.positions = torch.zeros(slots, dtype=torch.int32, device="cuda")
         self.used, self.seen, self.page_size = 0, 0, page_size  # tokens in the cache, tokens so far
 
-    def append(self, k, v):
-        """One token of every sequence into the next slot."""
-        page, slot = self.table[:, self.used // self.page_size].long(), self.used % self.page_size
-        self.k[page, slot], self.v[page, slot] = k, v
-        self.weights[page, :, slot] = 0.0
-        self.positions[page, :, slot] = self.seen
-        self.used += 1
-        self.seen += 1
+    def append(self, k, v, n):
+        """The next n tokens of every sequence into their slots, with no attention weight yet."""
+        at = torch.arange(n, device="cuda")
+        page = self.table[:, (self.used + at) // self.page_size].long()
+        slots = page * self.page_size + (self.used + at) % self.page_size
+        positions = (self.seen + at).to(torch.int32).repeat(self.batch)
+        swm.kv_append(self.cache, k, v, slots.view(-1), weights=self.weights, positions=self.positions, at=positions)
+        self.used += n
+        self.seen += n
         self.lengths.fill_(self.used)
+
+    def prompt(self, tokens):
+        """Next tokens, their log probabilities and the entropies after prompts, (batch, n) tokens; the cache is empty."""
+        n = tokens.shape[1]
+        assert self.used == 0 and n < self.budget + self.slack
+        starts = torch.arange(0, self.batch * n + 1, n, dtype=torch.int32, device="cuda")
+        return self.forward(tokens.reshape(-1), n, lambda q, k, v: swm.prompt_attention(q, k, v, starts))
 
     def step(self, tokens):
         """Next tokens, their log probabilities and the entropies for a batch of tokens."""
+        return self.forward(tokens, 1, lambda q, k, v: swm.paged_attention(self.cache, q, weights=self.weights))
+
+    def forward(self, tokens, n, attend):
         y, f = self.layer, self.layer.fmt
+        rows = self.batch * n
         x = y.embed[tokens]
         qkv = swm.spmm(f["qkv"], norm(x))
         kv = y.kv_heads * y.dim
-        q = qkv[:, :y.hidden].view(self.batch, y.heads, y.dim)  # strided: the stacked product as it is
-        k, v = (qkv[:, i:i + kv].view(self.batch, y.kv_heads, y.dim) for i in (y.hidden, y.hidden + kv))
-        self.append(k, v)
-        a = swm.paged_attention(self.cache, q, weights=self.weights)
-        x = swm.spmm_epilogue(f["o"], a.view(self.batch, y.hidden), residual=x)
-        h = swm.gate_up_silu(f["gate"], f["up"], norm(x))
+        q = qkv[:, :y.hidden].view(rows, y.heads, y.dim)  # strided: the stacked product as it is
+        k, v = (qkv[:, i:i + kv].view(rows, y.kv_heads, y.dim) for i in (y.hidden, y.hidden + kv))
+        self.append(k, v, n)
+        a = attend(q, k, v)
+        x = swm.spmm_epilogue(f["o"], a.view(rows, y.hidden), residual=x)
+        need = swm.gate_up_silu_workspace_bytes(f["gate"], f["up"], rows)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        h = swm.gate_up_silu_ws(f["gate"], f["up"], norm(x), ws)
         swm.spmm_epilogue(f["down"], h, residual=x, Y=x)
+        x = x[n - 1::n].contiguous()  # the last token of every sequence
         if self.used == self.budget + self.slack:
             swm.kv_evict(self.cache, self.weights, self.positions, self.budget, self.recent)
             self.used = self.budget
@@ -105,12 +121,14 @@ class Session:
 def main(argv=None):
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     for name, value in (("hidden", 4096), ("ffn", 11008), ("heads", 32), ("kv-heads", 32), ("vocab", 32000),
-                        ("batch", 4), ("steps", 64), ("budget", 32), ("slack", 8), ("recent", 8), ("page-size", 16)):
+                        ("batch", 4), ("prompt", 16), ("steps", 64), ("budget", 32), ("slack", 8), ("recent", 8),
+                        ("page-size", 16)):
         p.add_argument("--" + name, type=int, default=value)
     a = p.parse_args(argv)
     s = Session(Layer(a.hidden, a.ffn, a.heads, a.kv_heads, a.vocab), a.batch, a.budget, a.slack, a.recent,
                 a.page_size)
-    tokens = torch.arange(a.batch, device="cuda")
+    tokens = torch.arange(a.batch * max(a.prompt, 1), device="cuda").view(a.batch, -1) % a.vocab
+    tokens, _, _ = s.prompt(tokens)
     s.step(tokens)  # the first call loads the kernels
     torch.cuda.synchronize()
     t, total = time.perf_counter(), torch.zeros(a.batch, device="cuda")

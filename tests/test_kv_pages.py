@@ -382,6 +382,30 @@ def test_a_prompt_drafts_and_an_eviction_on_one_cache(gpu_lib):
 
 
 @gpu
+def test_new_tensors_are_memory_of_the_stream(gpu_lib):
+    """What the calls allocate on a stream that is not the current one is no block that the current one just gave back."""
+    import torch
+    k = torch.randn((40, 16, 2, 64), device="cuda").half()
+    c = swm.PagedCache(k, k.clone(), ints(np.arange(40).reshape(1, 40)), ints([640]))
+    q, starts = torch.randn((30, 4, 64), device="cuda").half(), ints([0, 30])
+    free, count, n = ints(np.zeros(40)), ints([0]), ints([0])
+    for call in (lambda s: [swm.prompt_attention(q, q, q, starts, stream=s)],
+                 lambda s: [swm.tree_attention(c, q, starts, max_tokens=30, stream=s)],
+                 lambda s: list(swm.kv_reserve(c, n, free, count, 5, stream=s))):
+        want = call(None)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        given = [torch.empty_like(t) for t in want for _ in range(4)]
+        held = {t.data_ptr() for t in given}
+        del given
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        assert not held & {t.data_ptr() for t in got}
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
 def test_bindings_refuse(gpu_lib):
     import torch
     k = pool_of(4, 16, 2, 64)

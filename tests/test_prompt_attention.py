@@ -315,6 +315,35 @@ def test_no_tokens_and_no_sequences(gpu_lib):
 
 
 @gpu
+@pytest.mark.parametrize("n", [9, 40])
+def test_a_prompt_is_its_tokens_one_by_one(gpu_lib, n):
+    """The decoding example: a prompt at once, and the same tokens as steps of another session."""
+    import importlib.util
+    import os
+    import torch
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "pruned_decode.py")
+    spec = importlib.util.spec_from_file_location("pruned_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    y = m.Layer(hidden=256, ffn=520, heads=4, kv_heads=2, vocab=1003, seed=3)
+    a, b = (m.Session(y, batch=3, budget=60, slack=4, recent=4, page_size=8) for _ in range(2))
+    tokens = (torch.arange(3 * n, device="cuda") * 37 % 1003).view(3, n)
+    ids, logp, entropy = a.prompt(tokens)
+    for i in range(n):
+        ids_b, logp_b, entropy_b = b.step(tokens[:, i])
+    # both round every product's outputs to fp16; logits of rms 1 differ by 2^-7 at most, as against plain torch
+    assert float((entropy - entropy_b).abs().max()) < 2.0**-6 and float((logp - logp_b).abs().max()) < 2.0**-6
+    assert a.lengths.tolist() == b.lengths.tolist() == [n] * 3
+    t = torch.arange(n, device="cuda")
+    for x, z in ((a.k, b.k), (a.v, b.v), (a.positions.transpose(1, 2), b.positions.transpose(1, 2))):
+        x, z = (c[s.table[:, t // 8].long(), t % 8] for c, s in ((x, a), (z, b)))
+        assert float((x.float() - z.float()).abs().max()) < 2.0**-6
+    # and on from there: the next step reads the prompt's rows
+    (ids, logp, entropy), (ids_b, logp_b, entropy_b) = a.step(ids), b.step(ids)
+    assert float((entropy - entropy_b).abs().max()) < 2.0**-6 and float((logp - logp_b).abs().max()) < 2.0**-6
+
+
+@gpu
 def test_binding_refuses(gpu_lib):
     import torch
     q, k, v, dq, dk, dv = make(8, 4, 2, 64)
