@@ -746,7 +746,7 @@ swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_tok
  *  heads, a scale that is not finite, negative sizes or strides, rows of out
  *  that share memory, mask_ld below the capacity, a workspace too small.
  *  SWM_ERR_ALIGN: q or the workspace.  SWM_ERR_UNSUPPORTED: q_heads above
- *  65535, max_tokens above 64, tokens * q_heads of 2^26 and more, slot strides of
+ *  65535, max_tokens above 64, tokens * q_heads of 2^26 - 4 and more, slot strides of
  *  2^26 and more, or a grid beyond the device's.  Cache errors as above.  One or two launches, asynchronous on
  *  stream, bitwise reproducible. */
 swm_status swm_tree_attention(const swm_kv_cache* cache, const void* q, int64_t q_token, int64_t q_head,

@@ -95,18 +95,33 @@ __device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane,
     const int l = __builtin_ctzll(in);
     return take(first, n, l, __builtin_amdgcn_readlane(before + blocks, l) - 1 - u);
   }
-  int base = 0;
-  for (int s0 = 0; s0 < a.B; s0 += 64) {
+  // Every lane adds up a 64th of the sequences, whose bounds are requested one
+  // behind the other, then the wave goes through the one part that has place u.
+  const int per = (a.B + 63) / 64, own = min(lane * per, a.B), next = min(own + per, a.B);
+  int sum = 0, from = own < a.B ? min(max(a.starts[own], 0), a.T) : 0;
+#pragma unroll 8
+  for (int s = own; s < next; ++s) {
+    const int to = min(max(a.starts[s + 1], 0), a.T);
+    sum += (max(to - from, 0) + kBlock - 1) / kBlock;
+    from = to;
+  }
+  const int upto = int(scan_wave(uint32_t(sum)));
+  const uint64_t part = __builtin_amdgcn_ballot_w64(u < upto);
+  if (!part) return false;
+  const int l = __builtin_ctzll(part);
+  int base = __builtin_amdgcn_readlane(upto - sum, l);
+  const int end = __builtin_amdgcn_readlane(next, l);
+  for (int s0 = __builtin_amdgcn_readlane(own, l); s0 < end; s0 += 64) {
     int first = 0, n = 0;
-    if (s0 + lane < a.B) rows_of(a, s0 + lane, &first, &n);
+    if (s0 + lane < end) rows_of(a, s0 + lane, &first, &n);
     const int blocks = (n + kBlock - 1) / kBlock;
-    const int upto = base + int(scan_wave(uint32_t(blocks)));
-    const uint64_t in = __builtin_amdgcn_ballot_w64(u < upto);
+    const int last = base + int(scan_wave(uint32_t(blocks)));
+    const uint64_t in = __builtin_amdgcn_ballot_w64(u < last);
     if (in) {
-      const int l = __builtin_ctzll(in);
-      return take(first, n, l, __builtin_amdgcn_readlane(upto, l) - 1 - u);
+      const int i = __builtin_ctzll(in);
+      return take(first, n, i, __builtin_amdgcn_readlane(last, i) - 1 - u);
     }
-    base = __builtin_amdgcn_readlane(upto, 63);
+    base = __builtin_amdgcn_readlane(last, 63);
   }
   return false;
 }

@@ -372,8 +372,8 @@ swm_status swm_tree_attention(const swm_kv_cache* c, const void* q, int64_t q_to
   int dev = 0;
   SWM_HIP(hipGetDevice(&dev));
   const swm::TreePlan p = swm::plan_tree(c->batch, q_heads, c->heads, c->dim, cap, max_tokens, swm::num_cus(dev));
-  // either launch: at most 2^24 - 1 workgroups of 256 threads
-  if (p.grid >= (int64_t(1) << 24) || tokens * q_heads >= (int64_t(1) << 26)) return SWM_ERR_UNSUPPORTED;
+  // at most 2^23 - 1 workgroups of 512 threads, 2^24 - 1 of 256 in the second launch
+  if (p.grid >= (int64_t(1) << 23) || tokens * q_heads >= (int64_t(1) << 26) - 4) return SWM_ERR_UNSUPPORTED;
   if (p.bytes > 0) {
     if (!workspace || ws_bytes < p.bytes) return SWM_ERR_INVALID_ARG;
     if (misaligned(workspace)) return SWM_ERR_ALIGN;

@@ -98,7 +98,8 @@ __device__ __forceinline__ Held hold(const TreeArgs& a, int lane) {
   }
   return x;
 }
-// Tokens of a sequence in units of kUnit, one at least where it has drafted ones.
+// Tokens of a sequence in units of kUnit (64 or more), one at least where it has
+// drafted ones: below 2^25, so that 128 of them add up in 32 bits.
 template <int kUnit>
 __device__ __forceinline__ uint32_t units_of(const Held& x, int e) {
   return x.drafts[e] ? max((x.n[e] + kUnit - 1) / kUnit, 1) : 0;

@@ -108,6 +108,7 @@ CASES = [
     (24, 3, 128, [20] * 30 + [0, 100, 65], "head"),
     (32, 32, 80, [1, 2, 40] * 20, "separate"),
     (36, 4, 256, [17, 35, 5, 0] * 16, "separate"),
+    (2, 1, 64, [(7 * b) % 5 for b in range(3000)] + [140], "separate"),
     (48, 4, 128, [100] * 70, "separate"),                            # small tiles
     (48, 4, 96, [90, 0, 300, 128, 129, 1] * 12, "stacked"),
     (8, 2, 128, [1111, 640], "separate"),

@@ -271,7 +271,7 @@ def test_strided_operands_stream_and_scale(gpu_lib):
 
 
 @gpu
-@pytest.mark.parametrize("Hq,Hkv,drafts", [(4, 2, [20, 8]), (16, 1, [64, 33])])
+@pytest.mark.parametrize("Hq,Hkv,drafts", [(4, 2, [20, 8]), (16, 1, [64, 33]), (2, 1, [8, 15])])
 def test_graph_follows_everything_in_device_memory(gpu_lib, Hq, Hkv, drafts):
     import torch
     lengths = [3000, 2500]
@@ -332,6 +332,30 @@ def test_offsets_past_32_bits(gpu_lib):
     hk, hv = (np.stack([rows[p][i] for p in rows]) for i in range(2))
     ref, tol, _ = reference(q, hk, hv, np.vectorize(small.get)(table), n, [0, 5, 14], None, D ** -0.5)
     check(out, ref, tol)
+
+
+@gpu
+@pytest.mark.parametrize("Hq", [2, 16, 64])  # few query rows, many, more than 128
+def test_lengths_next_to_2_31(gpu_lib, Hq):
+    """One page of a thousand million slots and a table of two: the tokens that count are the last ones."""
+    import torch
+    S, D, t = (1 << 30) - 40000, 8, 9
+    n = 2 * S - 5
+    k = torch.zeros((1, S, 1, D), dtype=torch.float16, device="cuda")
+    r = np.random.default_rng(3)
+    hk = r.standard_normal((2, 300, D)).astype(np.float16)
+    k[0, S - 305:S - 5, 0] = torch.from_numpy(hk[0]).cuda()
+    v = torch.zeros_like(k)
+    v[0, S - 305:S - 5, 0] = torch.from_numpy(hk[1]).cuda()
+    mask = torch.zeros((1, 2 * S), dtype=torch.bool, device="cuda")
+    mask[0, n - 300:] = True  # of the second time that the page comes
+    c = swm.PagedCache(k, v, ints([[0, 0]]), ints([n]))
+    q = r.standard_normal((t, Hq, D)).astype(np.float16)
+    out = swm.tree_attention(c, torch.from_numpy(q).cuda(), ints([0, t]), max_tokens=t, mask=mask)
+    sees = np.tril(np.ones((t, 300), bool), 300 - t)
+    for h in range(Hq):
+        ref, tol = attend(q[:, h], hk[0], hk[1], D ** -0.5, sees)
+        check(out[:, h], ref, tol)
 
 
 @gpu
