@@ -1,6 +1,6 @@
 // Pieces of an attention with many query rows, on v_mfma_f32_32x32x16_f16: a
-// wave takes 32 query rows and 64 tokens at a time, from key and value tiles in
-// LDS.
+// wave takes 32 query rows and 32 or 64 tokens at a time, from key and value tiles
+// in LDS.
 //
 // Scores are formed transposed, S^T = K Q^T (A: 32 tokens, B: 32 query rows):
 // lane l of the result holds, for the one row l % 32, the tokens 8 (i / 4) + 4

@@ -281,6 +281,7 @@ __global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : 2) void prompt_short_kern
   bool odd = false;
   for (int t0 = 0; t0 < end; t0 += kRows) {
     wait_vm<0>();
+    asm volatile("" ::: "memory");  // no barrier follows: reads of the tile stay below
     __builtin_amdgcn_sched_barrier(0);
     if (t0 == 0) mend_query(a.D, h, a.zero, a.flip, q);
     if (kCausal && t0 == q0) {  // see prompt_kernel

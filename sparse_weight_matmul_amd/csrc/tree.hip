@@ -582,6 +582,7 @@ __global__ __launch_bounds__(64 * W, C == 8 ? 4 : W / 4) void tree_few_kernel(Tr
     const uint64_t live = __builtin_amdgcn_ballot_w64(now >= 0) & 0xffffffffu;
     now = next;
     wait_vm<0>();
+    asm volatile("" ::: "memory");  // no barrier follows: reads of the tile stay below
     __builtin_amdgcn_sched_barrier(0);
     const bool drafts_here = t0 + 32 > own;
     if (drafts_here) {
@@ -770,8 +771,8 @@ hipError_t launch(const TreeArgs& a, bool few, bool wide, uint32_t grid, hipStre
 // How the work is dealt.  The lengths are in device memory, so the host decides by
 // the capacity alone whether sequences are cut and into how many pieces at most; the
 // kernel sizes them.  Up to twice as many units as workgroups at a time and more
-// than four steps: cut (1 x 1024 tokens, 32 heads, four steps: 16 us whole, 18 as
-// two pieces and a join); of several sequences into up to four pieces a place, so
+// than four steps: cut (1 x 1024 tokens, 32 heads, four steps: 19.7 us whole, 21.3
+// as two pieces and a join); of several sequences into up to four pieces a place, so
 // that unlike lengths even out.  More units: whole sequences, the longest first (16
 // ragged x 4096, 32 heads 103 us; cut, with the tiles shared, 134).
 // 256 rows a workgroup rather than 128 where there are more than 128: 648 us for 664
