@@ -684,10 +684,10 @@ swm_status swm_prompt_attention(const void* q, int64_t q_token, int64_t q_head, 
  *  in the page, -1 where a sequence was not granted its tokens, where the table
  *  names no page and from starts[batch] on.
  *  granted: DEVICE int32, batch: by how much each length changed.
- *  SWM_ERR_INVALID_ARG: null pointers, negative sizes, table rows that share
- *  memory, outputs at an input's address or each other's.  SWM_ERR_SHAPE:
- *  free_size below pages.  SWM_ERR_UNSUPPORTED: free_size or tokens of 2^31 -
- *  65536 and more.  Cache errors as above.  No workspace; one or two launches,
+ *  SWM_ERR_INVALID_ARG: null pointers, negative sizes, memory that rows of the
+ *  table or two of the arguments (table and lengths among them) share, in whole
+ *  or in part.  SWM_ERR_SHAPE: free_size below pages.  SWM_ERR_UNSUPPORTED:
+ *  free_size or tokens of 2^31 - 65536 and more.  Cache errors as above.  No workspace; one or two launches,
  *  asynchronous on stream; whole numbers, so bitwise reproducible. */
 swm_status swm_kv_reserve(const swm_kv_cache* cache, const int32_t* counts, int32_t* free_pages, int64_t free_size,
                           int32_t* free_count, int64_t tokens, int32_t* starts, int64_t* slots, int32_t* granted,

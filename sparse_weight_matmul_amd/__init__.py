@@ -944,7 +944,7 @@ def kv_reserve(cache: PagedCache, counts, free, free_count, tokens: int, starts=
     tokens: the sum of the positive counts.  Returns starts (B + 1,) int32, where
     each sequence's added tokens begin among all, slots (tokens,) int64, the
     slot of each of them in the pool (-1: not granted) and granted (B,) int32, by
-    how much each length changed."""
+    how much each length changed.  No two of the tensors may share memory."""
     import torch
     lib = load()
     device, B, tokens = cache.device, cache.batch, int(tokens)

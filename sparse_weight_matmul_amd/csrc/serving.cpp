@@ -2,6 +2,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <iterator>
 
 #include "host_util.h"
 #include "kernels.h"
@@ -75,6 +76,29 @@ bool cache_rows_overlap(const swm_kv_cache* c) {
          rows_overlap(c->dim, c->pages, c->v_page, c->heads, c->v_head) ||
          rows_overlap(c->dim, c->page_size, c->k_slot, c->heads, c->k_head) ||
          rows_overlap(c->dim, c->page_size, c->v_slot, c->heads, c->v_head);
+}
+
+// Memory of an argument: rows of `bytes`, `step` bytes apart.
+struct Span {
+  uintptr_t at;
+  int64_t rows, bytes, step;
+};
+template <typename T>
+Span span_of(const T* p, int64_t rows, int64_t len, int64_t ld) {
+  return {reinterpret_cast<uintptr_t>(p), len > 0 ? rows : 0, len * int64_t(sizeof(T)), ld * int64_t(sizeof(T))};
+}
+template <typename T>
+Span span_of(const T* p, int64_t n) {
+  return span_of(p, n > 0, n, n);
+}
+
+// Whether two have a byte in common; b is one row.
+bool spans_meet(const Span& a, const Span& b) {
+  if (a.rows < 1 || b.rows < 1) return false;
+  const int64_t from = int64_t(b.at - a.at), to = from + b.bytes;  // in bytes from a's first
+  // the first row of a that ends behind b's start
+  int64_t r = from < a.bytes ? 0 : a.step > 0 ? (from - a.bytes) / a.step + 1 : a.rows;
+  return r < a.rows && r * a.step < to;
 }
 
 bool heads_fit(const swm_kv_cache* c, int64_t q_heads) {
@@ -279,11 +303,15 @@ swm_status swm_kv_reserve(const swm_kv_cache* c, const int32_t* counts, int32_t*
   if (!starts || !free_count || (!free_pages && free_size > 0) || (!slots && tokens > 0)) return SWM_ERR_INVALID_ARG;
   if (c->batch > 0 && (!counts || !granted)) return SWM_ERR_INVALID_ARG;
   if (free_size < c->pages) return SWM_ERR_SHAPE;
-  // what is written is nobody else's
   if (c->batch > 1 && c->table_ld < c->pages_per_seq) return SWM_ERR_INVALID_ARG;
-  if (c->batch > 0 && (granted == counts || granted == c->lengths || counts == c->lengths || starts == c->lengths ||
-                       starts == counts || starts == granted))
-    return SWM_ERR_INVALID_ARG;
+  // What is written is nobody else's; of these only counts is not.
+  const Span spans[] = {span_of(c->table, c->batch, c->pages_per_seq, c->table_ld), span_of(c->lengths, c->batch),
+                        span_of(counts, c->batch),    span_of(free_pages, free_size),
+                        span_of(free_count, 1),       span_of(starts, c->batch + 1),
+                        span_of(slots, tokens),       span_of(granted, c->batch)};
+  for (const Span* a = spans; a != std::end(spans); ++a)
+    for (const Span* b = a + 1; b != std::end(spans); ++b)
+      if (spans_meet(*a, *b)) return SWM_ERR_INVALID_ARG;
   swm_log("kv_reserve B=%lld capacity=%lld: %lld tokens, %lld free pages at most", (long long)c->batch,
           (long long)(c->pages_per_seq * c->page_size), (long long)tokens, (long long)free_size);
   swm::ReserveCall r;

@@ -475,6 +475,69 @@ def test_reserve_refusals(change, code):
     assert swm.load().swm_kv_reserve(None, *a.values()) == 1
 
 
+# (address, bytes) of every argument's memory: two sequences, rows of three pages and an entry between them,
+# eight free pages, three added tokens
+SPANS = dict(table=(4096, 28), lengths=(8192, 8), counts=(12288, 8), free=(16384, 32), free_count=(20480, 4),
+             starts=(24576, 12), slots=(32768, 24), granted=(28672, 8))
+
+
+def reserve_at(tokens=3, **at):
+    """Status of a call with some arguments at other addresses."""
+    a = {name: at.get(name, SPANS[name][0]) for name in SPANS}
+    cache = cache_struct(table=a["table"], lengths=a["lengths"], table_ld=4, pages_per_seq=3)
+    return swm.load().swm_kv_reserve(ctypes.addressof(cache), a["counts"], a["free"], 8, a["free_count"], tokens,
+                                     a["starts"], a["slots"], a["granted"], None)
+
+
+@pytest.mark.parametrize("one", SPANS)
+@pytest.mark.parametrize("two", SPANS)
+def test_reserve_refuses_memory_that_is_shared(one, two):
+    """All but counts is written: no two of the arguments may have an entry in common, in whole or in part."""
+    if one == two:
+        return
+    at, n = SPANS[one]
+    assert reserve_at(**{two: at}) == 1                              # the same address
+    assert reserve_at(**{two: at + n - 4}) == 1                      # from its last entry on
+    assert reserve_at(**{two: at + 4 - SPANS[two][1]}) == 1          # up to its first entry
+
+
+def test_reserve_refuses_entries_of_any_table_row():
+    for one in SPANS:
+        if one != "table":
+            assert reserve_at(**{one: 4096 + 16 + 8}) == 1           # the second sequence's last page
+
+
+@pytest.mark.gpu
+def test_reserve_between_the_rows_of_a_table(gpu_lib):
+    """Arguments side by side in one buffer share nothing, the number of free pages in a column that the table's
+    rows leave out among them."""
+    import torch
+    y = torch.zeros(64, dtype=torch.int32, device="cuda")
+    table, lengths, counts, free, starts, granted = (y[:8].view(2, 4)[:, :3], y[8:10], y[10:12], y[12:20], y[20:23],
+                                                     y[23:25])
+    table.fill_(-1)
+    count = y[3:4]
+    count.fill_(8)
+    counts.copy_(ints([17, 1]))
+    free.copy_(ints(range(8)))
+    slots = torch.zeros(18, dtype=torch.int64, device="cuda")
+    k = pool_of(8, 16)
+    c = swm.PagedCache(k, k, table, lengths)
+    swm.kv_reserve(c, counts, free, count, 18, starts=starts, slots=slots, granted=granted)
+    assert table.tolist() == [[7, 6, -1], [5, -1, -1]] and lengths.tolist() == [17, 1] and count.tolist() == [5]
+    assert starts.tolist() == [0, 17, 18] and granted.tolist() == [17, 1]
+    assert slots.tolist() == list(range(7 * 16, 8 * 16)) + [6 * 16, 5 * 16]
+    counts.fill_(0)
+    swm.kv_reserve(c, counts, free, count, 0, starts=starts, slots=slots[:0], granted=granted)
+    assert granted.tolist() == [0, 0] and lengths.tolist() == [17, 1]
+    for bad in (dict(starts=starts, granted=starts[:2]), dict(starts=starts, granted=starts[1:]),
+                dict(starts=free[5:]), dict(granted=table[0, :2])):
+        with pytest.raises(swm.SwmError, match="INVALID"):
+            swm.kv_reserve(c, counts, free, count, 0, **bad)
+    with pytest.raises(swm.SwmError, match="INVALID"):
+        swm.kv_reserve(c, counts, free, free[7:], 0)
+
+
 @pytest.mark.parametrize("fields,code", [
     (dict(batch=-1), 1), (dict(table=None), 1), (dict(lengths=None), 1), (dict(table_ld=3), 1), (dict(pages=0), 1),
     (dict(dim=60), 8), (dict(page_size=1 << 30), 8), (dict(k=4104), 3),
