@@ -604,6 +604,8 @@ def _workspace(workspace, need, device, stream):
         if not need:
             return None, None, 0
         workspace = _empty((need,), torch.uint8, device, stream)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a CUDA tensor")
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -671,7 +673,8 @@ class PagedCache:
 
     def _per_slot(self, t, name, dtype):
         """(pointer, page stride, head stride) of an array with one entry per cached row, (pages, heads, page_size)."""
-        if not t.is_cuda or t.device != self.device or t.dtype is not dtype:
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != self.device or t.dtype is not dtype:
             raise TypeError(f"{name} must be a {dtype} tensor on {self.device}")
         if t.shape != self._slots:
             raise ValueError(f"{name} must be (pages, heads, page_size)")
@@ -686,7 +689,8 @@ def _mask(cache, mask):
     import torch
     if mask is None:
         return None, 0
-    if not mask.is_cuda or mask.dtype not in (torch.bool, torch.uint8) or mask.dim() != 2:
+    if (not isinstance(mask, torch.Tensor) or not mask.is_cuda or mask.dtype not in (torch.bool, torch.uint8)
+            or mask.dim() != 2):
         raise TypeError("mask must be a 2-D bool or uint8 CUDA tensor")
     B = cache.batch
     if mask.shape[0] != B or mask.shape[1] < cache.capacity or mask.device != cache.device:
@@ -905,7 +909,7 @@ def tree_attention(cache: PagedCache, q, starts, parents=None, max_tokens: Optio
         raise ValueError(f"starts must have {cache.batch + 1} entries")
     pp = None
     if parents is not None:
-        if parents.dtype is not torch.int32 or parents.device != device:
+        if not isinstance(parents, torch.Tensor) or parents.dtype is not torch.int32 or parents.device != device:
             raise TypeError(f"parents must be an int32 tensor on {device}")
         if parents.shape != (T,) or not parents.is_contiguous():
             raise ValueError(f"parents must be contiguous, ({T},)")

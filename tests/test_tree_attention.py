@@ -412,6 +412,32 @@ def test_binding_refuses(gpu_lib):
         swm.tree_attention(c, dev["q"], s, max_tokens=6, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
 
 
+@gpu
+@pytest.mark.parametrize("bad", [[1, 2], 3, np.zeros((2, 64), np.int32)])
+def test_what_is_no_tensor_is_a_type_error(gpu_lib, bad):
+    q, k, v, table, parents, dev = make(4, 2, 64, 16, [20, 30], [4, 6])
+    c = cache_of(dev)
+    for name in ("parents", "mask", "out", "workspace"):
+        with pytest.raises(TypeError):
+            swm.tree_attention(c, dev["q"], dev["starts"], **{name: bad})
+    with pytest.raises(TypeError):
+        swm.tree_attention(c, dev["q"], bad)
+    with pytest.raises(TypeError):
+        swm.tree_attention(c, bad, dev["starts"])
+    for name in ("mask", "weights", "workspace"):
+        with pytest.raises(TypeError):
+            swm.paged_attention(c, dev["q"][:2], **{name: bad})
+    import torch
+    slots, at = torch.zeros(2, dtype=torch.int64, device="cuda"), ints([0, 1])
+    rows = dev["q"][:2, :2]
+    for kw in (dict(weights=bad), dict(positions=bad, at=at), dict(positions=ints(np.zeros((dev["k"].shape[0], 2, 16))),
+                                                                   at=bad)):
+        with pytest.raises(TypeError):
+            swm.kv_append(c, rows, rows, slots, **kw)
+    with pytest.raises(TypeError):
+        swm.kv_append(c, rows, rows, bad)
+
+
 def cache_struct(**kw):
     f = dict(k=4096, v=4096, table=4096, lengths=4096, k_page=1024, k_slot=64, k_head=64, v_page=1024, v_slot=64,
              v_head=64, table_ld=4, pages=8, page_size=16, heads=1, dim=64, batch=2, pages_per_seq=4)
