@@ -257,42 +257,43 @@ __device__ __forceinline__ void outputs(State<ND>& st, const Reads<NK, ND, C>& a
 // transposing read, of another tile; who reads what they bring waits for it
 // himself (wait_vm).  They have no register for a result.  The counter that
 // the compiler's own waits look at runs in order, so that these only make them
-// longer.
+// longer.  Their place in LDS is an operand in m0, which the compiler writes
+// itself: a statement that wrote it would have to name it, and m0 cannot be named
+// as clobbered.
 __device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
   return __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>((lds_ptr)(const_cast<uint16_t*>(p)))));
 }
 __device__ __forceinline__ void to_lds(uint64_t at, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "s"(to) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at), "{m0}"(to) : "memory");
 }
 __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t to) {  // base: of the whole wave
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to)
-               : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(to) : "memory");
 }
-// The same for the lanes of `on` alone, and counted also where there are none: a
-// branch round it would change how many are on their way.
+// The same for the lanes of `on` alone, one at least, so that it is always counted:
+// a branch round it would change how many are on their way.
 __device__ __forceinline__ void to_lds_some(uint64_t at, uint32_t to, uint64_t on) {
   uint64_t all;
   asm volatile(
-      "s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, %0"
+      "s_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
-      : "v"(at), "s"(to), "s"(on)
+      : "v"(at), "{m0}"(to), "s"(on)
       : "memory", "scc");
 }
 // A word, or a byte as a word, of each lane of `on`: lane l's to `to` + 4 l.
 __device__ __forceinline__ void word_to_lds(const void* at, uint32_t to, uint64_t on) {
   uint64_t all;
   asm volatile(
-      "s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_dword %1, off\n\ts_mov_b64 exec, %0"
+      "s_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_dword %1, off\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
-      : "v"(at), "s"(to), "s"(on)
+      : "v"(at), "{m0}"(to), "s"(on)
       : "memory", "scc");
 }
 __device__ __forceinline__ void byte_to_lds(const void* at, uint32_t to, uint64_t on) {
   uint64_t all;
   asm volatile(
-      "s_mov_b32 m0, %2\n\ts_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, off\n\ts_mov_b64 exec, %0"
+      "s_and_saveexec_b64 %0, %3\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, off\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
-      : "v"(at), "s"(to), "s"(on)
+      : "v"(at), "{m0}"(to), "s"(on)
       : "memory", "scc");
 }
 
@@ -306,8 +307,8 @@ __device__ __forceinline__ void load_tile(const uint16_t* src, int bytes, const 
                           uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 #pragma unroll
   for (int i = 0; i < n; ++i)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[i]),
-                 "s"(resource), "s"(to + i * step)
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off[i]), "s"(resource),
+                 "{m0}"(to + i * step)
                  : "memory");
 }
 

@@ -26,6 +26,23 @@ def _declared_functions():
     return sorted(set(re.findall(r"\b(swm_[a-z_]+)\s*\(", text)))
 
 
+def test_inline_assembly_writes_no_register_behind_the_compilers_back():
+    """m0 cannot be named as clobbered: where a statement needs it, it is an operand and no instruction's result."""
+    csrc = os.path.join(os.path.dirname(swm.LIB_PATH), "csrc")
+    seen = 0
+    for name in sorted(os.listdir(csrc)):
+        text = open(os.path.join(csrc, name)).read()
+        for statement in re.findall(r"\basm(?:\s+volatile)?\s*\(.*?\);", text, flags=re.S):
+            code = "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', statement.split(":")[0]))
+            for line in code.replace("\\t", "").split("\\n"):
+                written = line.split(",")[0].split()[1:]
+                assert written != ["m0"], (name, line)
+                seen += "_load_" in line and "lds" in line
+                assert "scc" in statement or not re.match(r"s_(and|or|bcnt|add|lshl\d_add)", line), (name, line)
+                assert "vcc" not in written or '"vcc"' in statement, (name, line)
+    assert seen >= 5  # the loads into LDS, which read m0
+
+
 def test_library_exports_every_declared_symbol():
     lib = swm.load()
     names = _declared_functions()
