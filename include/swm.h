@@ -706,8 +706,8 @@ swm_status swm_kv_reserve(const swm_kv_cache* cache, const int32_t* counts, int3
  *  The cache's table and lengths are not looked at.
  *  SWM_ERR_INVALID_ARG: null pointers, negative sizes or strides, rows of the
  *  pools or entries of weights or positions that share memory.
- *  SWM_ERR_ALIGN: k or v.  SWM_ERR_UNSUPPORTED: 2^34 halves of keys or more.
- *  Cache errors as above.  No workspace; one launch, asynchronous on stream. */
+ *  SWM_ERR_ALIGN: k or v.  SWM_ERR_UNSUPPORTED: tokens of 2^31 - 65536 and more,
+ *  tokens * heads * dim of 2^37 - 2^13 and more.  Cache errors as above.  No workspace; one launch, asynchronous on stream. */
 swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_token, int64_t k_head, const void* v,
                          int64_t v_token, int64_t v_head, int64_t tokens, const int64_t* slots, float* weights,
                          int64_t w_page, int64_t w_head, int32_t* positions, int64_t p_page, int64_t p_head,

@@ -281,6 +281,25 @@ def test_append_past_32_bits(gpu_lib):
 
 
 @gpu
+def test_append_next_to_its_limit(gpu_lib):
+    """Almost 2^37 halves of keys, as many as a call takes, of which the last token alone has a slot; with a token
+    more they are refused."""
+    import torch
+    H, D, T = 65535, 256, 8192
+    assert T * H * D < 2**37 - 2**13 <= (T + 1) * H * D
+    row = torch.randn((1, H, D), device="cuda").half()
+    k, v = (torch.zeros((2, 1, H, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    c = swm.PagedCache(k, v, ints([[0]]), ints([0]))
+    slots = torch.full((T + 1,), -1, dtype=torch.int64, device="cuda")
+    slots[T - 1] = 1
+    swm.kv_append(c, row.expand(T, H, D), (-row).expand(T, H, D), slots[:T])
+    assert torch.equal(k[1, 0], row[0]) and torch.equal(v[1, 0], -row[0])
+    assert not bool(k[0].any()) and not bool(v[0].any())
+    with pytest.raises(swm.SwmError, match="UNSUPPORTED"):
+        swm.kv_append(c, row.expand(T + 1, H, D), row.expand(T + 1, H, D), slots)
+
+
+@gpu
 def test_append_on_a_stream_and_in_a_graph(gpu_lib):
     import torch
     pools = [torch.zeros((9, 16, 2, 64), dtype=torch.float16, device="cuda") for _ in range(2)]
