@@ -358,6 +358,95 @@ def test_lengths_next_to_2_31(gpu_lib, Hq):
         check(out[:, h], ref, tol)
 
 
+def against_shared_heads(G, Hkv, D, S, lengths, drafts, masked, pieces=None):
+    """Many key-value heads over one head's rows, so that there is work for the whole device and one head to check
+    against 64 bits; the others have to be equal to it.  pieces: of a sequence at most, None: sequences are whole."""
+    import torch
+    q, k, v, table, parents, dev = make(G, 1, D, S, lengths, drafts)
+    cap = table.shape[1] * S
+    r = np.random.default_rng(11)
+    mask = dmask = None
+    if masked:
+        mask = r.random((len(lengths), cap)) < 0.8
+        for b, n in enumerate(lengths):
+            mask[b, n // 3:n // 3 + 200] = False  # whole tiles, whole loads, and the ends of both
+            mask[b, n // 2:n // 2 + 24] = False
+            table[b, n // 2 // S + 3] = -1 if b % 2 else k.shape[0]
+            t = np.arange(n)[~mask[b, :n]]
+            page = table[b][t // S]
+            on = (page >= 0) & (page < k.shape[0])
+            k[page[on], t[on] % S], v[page[on], t[on] % S] = np.nan, np.inf
+        for name, x in (("k", k), ("v", v), ("table", table), ("mask", mask)):
+            dev[name] = torch.from_numpy(x).cuda()
+        dmask = dev["mask"]
+    c = swm.PagedCache(*(dev[x].expand(-1, -1, Hkv, -1) for x in "kv"), dev["table"], dev["lengths"])
+    most = max(drafts)
+    # the workspace holds D + 2 words for every piece, key-value head and row, rows up to the next 256
+    room = c.tree_workspace_bytes(G * Hkv, most) // (4 * (D + 2) * Hkv * -(-G * most // 256) * 256)
+    assert room == (pieces or 0) * len(lengths)
+    out = torch.full((sum(drafts), G * Hkv, D), 7.0, dtype=torch.float16, device="cuda")
+    swm.tree_attention(c, dev["q"].repeat(1, Hkv, 1), dev["starts"], dev["parents"], max_tokens=most, mask=dmask,
+                       out=out)
+    ref, tol, rows = reference(q, k, v, table, lengths, bounds(drafts), parents, D ** -0.5, mask)
+    assert rows.all()
+    out = out.view(-1, Hkv, G, D)
+    check(out[:, 0], ref, tol)
+    assert torch.equal(out, out[:, :1].expand_as(out))
+
+
+@gpu
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("G,Hkv,D,S,lengths,drafts,pieces", [
+    (3, 256, 128, 16, [1700, 901], [43, 43], None),        # a workgroup's whole sequence, 14 to 26 tiles of 64
+    (3, 256, 80, 16, [1500, 1023], [64, 50], None),
+    (5, 128, 96, 5, [1301, 1100, 1000], [60, 40, 64], None),  # rows of a load on several pages
+    (3, 256, 128, 5, [64 * 14 + 1, 64 * 20], [43, 50], None),
+    (4, 512, 72, 4, [2000], [64], None),
+    (9, 64, 128, 16, [16 * 900], [20], 4),                 # pieces of 3600 tokens
+    (3, 64, 104, 3, [9001], [43], 4),
+])
+def test_more_than_128_rows_over_many_tiles(gpu_lib, G, Hkv, D, S, lengths, drafts, pieces, masked):
+    """Tiles come into places that were read before, entries of the table into places that were used: twice and more."""
+    assert 64 < D <= 128 and G * max(drafts) > 128 and min(lengths) // (pieces or 1) >= 13 * 64
+    against_shared_heads(G, Hkv, D, S, lengths, drafts, masked, pieces)
+
+
+def unlike(B, most, drafts):
+    """Lengths and drafted tokens of a batch: long, short, equal ones, empty ones, some with nothing drafted."""
+    n = [(most, 700, 300, 300, 64, 17, 1, 0)[b % 8] + (b % 3 if b % 8 < 3 else 0) for b in range(B)]
+    if B > 2:
+        n[1], n[2] = most, most
+    t = [0 if b % 5 == 3 else 1 + b % drafts for b in range(B)]
+    t[0] = drafts
+    return n, t
+
+
+@gpu
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("G,Hkv,D,S,B,drafts", [
+    (1, 32, 128, 16, 17, 8),    # up to 32 rows
+    (2, 16, 128, 5, 33, 16),
+    (1, 4, 128, 16, 128, 8),
+    (4, 8, 64, 16, 128, 8),
+    (1, 256, 200, 16, 2, 20),
+    (2, 8, 128, 16, 128, 31),   # up to 128
+    (3, 32, 64, 8, 33, 40),
+    (1, 512, 256, 16, 3, 40),
+    (4, 4, 128, 16, 128, 40),   # more
+    (5, 33, 96, 5, 31, 64),
+])
+def test_whole_sequences_by_their_lengths(gpu_lib, G, Hkv, D, S, B, drafts, masked):
+    """More workgroups than places, sequences of unlike lengths: each is done once, whatever the order."""
+    lengths, t = unlike(B, 1500, drafts)
+    against_shared_heads(G, Hkv, D, S, lengths, t, masked)
+
+
+@gpu
+def test_equal_lengths_by_their_order(gpu_lib):
+    against_shared_heads(1, 8, 128, 16, [1100] * 128, [2] * 128, False)
+    against_shared_heads(1, 32, 128, 16, [0] * 16 + [1100], [2] * 17, False)
+
+
 @gpu
 def test_nothing_to_do(gpu_lib):
     import torch
