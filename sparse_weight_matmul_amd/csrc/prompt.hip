@@ -19,7 +19,7 @@
 // Tried and slower: eight waves in two groups that take turns on the matrix cores
 // (2020 us, but 352 for the ragged batch), 64 rows a wave (half the LDS reads, but
 // the accumulators do not fit beside the rest without copies: 2490), all blocks of a
-// batch by their tokens (see find_block).
+// batch by their tokens (see pick_of_few).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,6 +27,7 @@
 
 #include "flash.h"
 #include "kernels.h"
+#include "paging.h"
 #include "wave.h"
 
 namespace swm {
@@ -43,9 +44,14 @@ constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
 constexpr int kMany = 12;
 // Mean length below which a wave has a block of 32 rows by itself, where there are
 // two workgroups per CU and more.  us, as blocks of 128 / so: 64 x 10 tokens, 160 heads of
-// 64 135 / 35, 32 heads of 128: 64 x 10 46 / 17, 64 x 32 49 / 25, 64 x 64 50 / 44,
-// 64 x 100 67 / 69; 8 x 40, 32 of 256 (1.2 a CU) 13.7 / 14.9.
+// 64 103 / 27, 32 heads of 128: 64 x 10 37 / 13, 64 x 32 42 / 22, 64 x 64 42 / 39,
+// 64 x 100 61 / 63; 8 x 40, 32 of 256 (1.2 a CU) 13.5 / 14.6.
 constexpr int kShort = 80;
+// Tokens up to which a sequence of such a batch is dealt out so.  32 heads of 128, us,
+// by 32 rows / by 128: 255 empty places and 1 x 512 23 / 21, 1 x 1024 41 / 33, 1 x 2048
+// 82 / 60, 1 x 16384 2990 / 2260 (2130 in a batch of its own, whose tiles leave room for
+// three workgroups on a CU); 60 x 5 and 4 x 300 25 / 28, 200 x 5 and 30 x 300 120 / 133.
+constexpr int kLong = 512;
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -56,6 +62,7 @@ struct PromptArgs {
   float c;        // |scale| log2(e), or 1 where the scale is 0
   uint32_t flip;  // sign bits that turn q where the scale is negative
   bool zero;      // the scale is 0
+  PageDiv per_hq;
 };
 
 // The sequence's part of the packed rows, whatever `starts` holds.
@@ -65,46 +72,54 @@ __device__ __forceinline__ void rows_of(const PromptArgs& a, int s, int* first, 
   *n = max(s1 - s0, 0);
 }
 
+struct Block {
+  int first, n, j;  // the sequence's rows, and which block of them
+};
+// Block j of the sequence that lane l holds; false for one that it does not have.
+template <int kBlock>
+__device__ __forceinline__ bool take(int first, int n, int l, int j, Block* out) {
+  out->first = __builtin_amdgcn_readlane(first, l);
+  out->n = __builtin_amdgcn_readlane(n, l);
+  out->j = j;
+  return j >= 0 && j < (out->n + kBlock - 1) / kBlock;
+}
+
 // The block of query rows that comes at place u: sequence after sequence, of up
 // to 64 the longest first, so that short ones fill the end; a sequence's last
 // block first.  (All blocks by their tokens, whatever their sequence, is worse, 298
 // us for 281 at 16 ragged x 2048: the workgroups at work then read keys of so many
-// sequences that no L2 holds them.)
-struct Block {
-  int first, n, j;  // the sequence's rows, and which block of them
-};
+// sequences that no L2 holds them.)  Of up to 64 sequences lane l holds number l,
+// its rows and how many blocks of it count.
 template <int kBlock>
-__device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane, Block* out) {
-  auto take = [&](int first, int n, int l, int j) {
-    out->first = __builtin_amdgcn_readlane(first, l);
-    out->n = __builtin_amdgcn_readlane(n, l);
-    out->j = j;
-    return true;
-  };
-  if (a.B > 1 && a.B <= 64) {
-    int first = 0, n = 0;
-    if (lane < a.B) rows_of(a, lane, &first, &n);
-    const int blocks = (n + kBlock - 1) / kBlock;
-    int before = 0;  // blocks of longer sequences, and of equal ones with a lower index
-    for (int l = 0; l < a.B; ++l) {
-      const int x = __builtin_amdgcn_readlane(blocks, l);
-      before += x > blocks || (x == blocks && l < lane) ? x : 0;
-    }
-    const uint64_t in = __builtin_amdgcn_ballot_w64(before <= u && u < before + blocks);
-    if (!in) return false;
-    const int l = __builtin_ctzll(in);
-    return take(first, n, l, __builtin_amdgcn_readlane(before + blocks, l) - 1 - u);
+__device__ __forceinline__ bool pick_of_few(const PromptArgs& a, int u, int lane, int first, int n, int blocks,
+                                            Block* out) {
+  int before = 0;  // blocks of longer sequences, and of equal ones with a lower index
+  for (int l = 0; l < a.B; ++l) {
+    const int x = __builtin_amdgcn_readlane(blocks, l);
+    before += x + int(l < lane) > blocks ? x : 0;
   }
-  // Every lane adds up a 64th of the sequences, whose bounds are requested one
-  // behind the other, then the wave goes through the one part that has place u.
+  const uint64_t in = __builtin_amdgcn_ballot_w64(before <= u && u < before + blocks);
+  if (!in) return false;
+  const int l = __builtin_ctzll(in);
+  return take<kBlock>(first, n, l, __builtin_amdgcn_readlane(before + blocks, l) - 1 - u, out);
+}
+
+// Of more, every lane has added up a 64th, whose bounds are requested one behind
+// the other, then the wave goes through the one part that has place u.
+template <typename F>
+__device__ __forceinline__ void each_of_part(const PromptArgs& a, int lane, F f) {
   const int per = (a.B + 63) / 64, own = min(lane * per, a.B), next = min(own + per, a.B);
-  int sum = 0, from = own < a.B ? min(max(a.starts[own], 0), a.T) : 0;
+  int from = own < a.B ? min(max(a.starts[own], 0), a.T) : 0;
 #pragma unroll 8
   for (int s = own; s < next; ++s) {
     const int to = min(max(a.starts[s + 1], 0), a.T);
-    sum += (max(to - from, 0) + kBlock - 1) / kBlock;
+    f(max(to - from, 0));
     from = to;
   }
+}
+template <int kBlock, typename F>
+__device__ __forceinline__ bool pick_of_many(const PromptArgs& a, int u, int lane, int sum, F blocks_of, Block* out) {
+  const int per = (a.B + 63) / 64, own = min(lane * per, a.B), next = min(own + per, a.B);
   const int upto = int(scan_wave(uint32_t(sum)));
   const uint64_t part = __builtin_amdgcn_ballot_w64(u < upto);
   if (!part) return false;
@@ -114,16 +129,89 @@ __device__ __forceinline__ bool find_block(const PromptArgs& a, int u, int lane,
   for (int s0 = __builtin_amdgcn_readlane(own, l); s0 < end; s0 += 64) {
     int first = 0, n = 0;
     if (s0 + lane < end) rows_of(a, s0 + lane, &first, &n);
-    const int blocks = (n + kBlock - 1) / kBlock;
-    const int last = base + int(scan_wave(uint32_t(blocks)));
+    const int last = base + int(scan_wave(uint32_t(blocks_of(n))));
     const uint64_t in = __builtin_amdgcn_ballot_w64(u < last);
     if (in) {
       const int i = __builtin_ctzll(in);
-      return take(first, n, i, __builtin_amdgcn_readlane(last, i) - 1 - u);
+      return take<kBlock>(first, n, i, __builtin_amdgcn_readlane(last, i) - 1 - u, out);
     }
     base = __builtin_amdgcn_readlane(last, 63);
   }
   return false;
+}
+
+__device__ __forceinline__ bool held_by_lanes(const PromptArgs& a) { return a.B > 1 && a.B <= 64; }
+
+// Blocks of 128 rows, a workgroup each.
+__device__ __forceinline__ bool find_wide(const PromptArgs& a, int u, int lane, Block* out) {
+  auto blocks_of = [](int n) { return (n + kBlock - 1) / kBlock; };
+  if (held_by_lanes(a)) {
+    int first = 0, n = 0;
+    if (lane < a.B) rows_of(a, lane, &first, &n);
+    return pick_of_few<kBlock>(a, u, lane, first, n, blocks_of(n), out);
+  }
+  int sum = 0;
+  each_of_part(a, lane, [&](int n) { sum += blocks_of(n); });
+  return pick_of_many<kBlock>(a, u, lane, sum, blocks_of, out);
+}
+
+// Where prompts are short in the mean: blocks of 32 rows, a wave each, but of sequences
+// of more than kLong tokens, which the mean hides among short and empty ones; those
+// keep their blocks of 128 rows, which come first.  Without such sequences the place is
+// the wave's own, known before the bounds come.  With the code for both, more than 64
+// sequences take 1 to 3% longer than with that for 32 rows alone (1024 x 10 tokens 137
+// us for 132).
+struct Place {
+  int u, head;
+  bool wide;  // a workgroup's block of 128 rows
+};
+__device__ __forceinline__ bool find_mixed(const PromptArgs& a, int lane, int wave, Place* p, Block* out) {
+  auto small_at = [&](int before) {  // behind so many workgroups of wide ones
+    const int i = (int(blockIdx.x) - before) * kWaves + wave, u = page_index(a.per_hq, i);
+    return Place{u, i - u * a.Hq, false};
+  };
+  auto place = [&](int blocks) {  // by the number of wide ones; a grid has less than 2^24 workgroups
+    const int before = int(min(uint32_t(blocks), (1u << 24) / a.Hq + 1)) * a.Hq;
+    if (int(blockIdx.x) >= before) return small_at(before);
+    const int u = page_index(a.per_hq, blockIdx.x);
+    return Place{u, int(blockIdx.x) - u * a.Hq, true};
+  };
+  auto all = [](int n) { return (n + kRows - 1) / kRows; };
+  auto wide = [](int n) { return n > kLong ? (n + kBlock - 1) / kBlock : 0; };
+  auto small = [&](int n) { return n > kLong ? 0 : all(n); };
+  *p = small_at(0);
+  if (held_by_lanes(a)) {
+    int first = 0, n = 0;
+    if (lane < a.B) rows_of(a, lane, &first, &n);
+    if (__builtin_amdgcn_ballot_w64(n > kLong)) {
+      *p = place(int(wave_sum(uint32_t(wide(n)))));
+      if (p->wide) return pick_of_few<kBlock>(a, p->u, lane, first, n, wide(n), out);
+    }
+    return pick_of_few<kRows>(a, p->u, lane, first, n, small(n), out);
+  }
+  int sum = 0, longest = 0;
+  each_of_part(a, lane, [&](int n) {
+    sum += all(n);
+    longest = max(longest, n);
+  });
+  if (__builtin_amdgcn_ballot_w64(longest > kLong)) {
+    int blocks = 0;
+    sum = 0;
+    each_of_part(a, lane, [&](int n) {
+      blocks += wide(n);
+      sum += small(n);
+    });
+    *p = place(int(wave_sum(uint32_t(blocks))));
+    if (p->wide) return pick_of_many<kBlock>(a, p->u, lane, blocks, wide, out);
+    return pick_of_many<kRows>(a, p->u, lane, sum, small, out);
+  }
+  return pick_of_many<kRows>(a, p->u, lane, sum, all, out);
+}
+
+// The head of workgroup `i` of those over one block of rows: they go round the eight
+// XCDs, and neighbouring heads, which share keys, to one of them.
+__device__ __forceinline__ int head_of(const PromptArgs& a, int i) {
+  return a.Hq % 8 == 0 ? (i & 7) * (a.Hq >> 3) + (i >> 3) : i;
 }
 
 // A row's output; what clear_odd took out of the value rows `from` .. `end` - 1
@@ -134,14 +222,16 @@ __device__ __forceinline__ void finish(const PromptArgs& a, State<ND>& st, const
   const float l = sum_halves(st.l);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (odd) {
+    int D = a.D;
     for (int t = from; t < end; ++t) {
+      asm volatile("" : "+s"(D));  // its comparisons stay here: before the loop they would take 64 pairs of registers
       if (t > qi) continue;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int x = 32 * d + 8 * (i >> 2) + 4 * h + (i & 3);
-          if (x >= a.D) continue;
+          if (x >= D) continue;
           const uint16_t w = vh[int64_t(t) * a.v_t + x];
           if ((w & 0x7c00) == 0x7c00) st.o[d][i] += float(__builtin_bit_cast(_Float16, w));
         }
@@ -151,23 +241,15 @@ __device__ __forceinline__ void finish(const PromptArgs& a, State<ND>& st, const
   write_row(st, inv, a.out + int64_t(first + qi) * a.o_t + int64_t(head) * a.o_h, a.D, h);
 }
 
-// Tiles of 32 NB tokens.  With 64 tokens two workgroups share a CU, with 32 three,
-// whose waves fill more of each other's gaps, but each alone takes longer.
+// A workgroup's block of 128 rows, over tiles of 32 NB tokens.
 template <int NK, int ND, int C, bool kCausal, int NB>
-__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void prompt_kernel(PromptArgs a) {
+__device__ __forceinline__ void wide_block(const PromptArgs& a, const Block& block, int head, uint16_t* smem) {
   constexpr int kTokens = 32 * NB;
   constexpr int kTile = kTokens * C * 8;        // halves
   constexpr int kLoads = C * NB / 2 / kWaves;  // 1 KiB each, of a wave and tile
-  extern __shared__ uint16_t smem[];
   uint16_t* sv = smem + 2 * kTile;  // two key tiles, then two value tiles
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int u = blockIdx.x / a.Hq;
-  int head = blockIdx.x - u * a.Hq;
-  // workgroups go round the eight XCDs: neighbouring heads, which share keys, to one of them
-  if (a.Hq % 8 == 0) head = (head & 7) * (a.Hq >> 3) + (head >> 3);
-  Block block;
-  if (!find_block<kBlock>(a, u, lane, &block)) return;
   const int first = block.first, n = block.n, j = block.j;
   const int q0 = j * kBlock + wave * kRows;  // the wave's first row
   const int end = kCausal ? min(n, (j + 1) * kBlock) : n;
@@ -238,20 +320,27 @@ __global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void pro
   finish(a, st, vh, kCausal && odd, j * kBlock, end, qi, n, first, head, h);
 }
 
+// With tiles of 64 tokens two workgroups share a CU, with 32 three, whose waves
+// fill more of each other's gaps, but each alone takes longer.
+template <int NK, int ND, int C, bool kCausal, int NB>
+__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : NB == 1 ? 3 : 2) void prompt_kernel(PromptArgs a) {
+  extern __shared__ uint16_t smem[];
+  const int u = page_index(a.per_hq, blockIdx.x);
+  Block block;
+  if (!find_wide(a, u, threadIdx.x & 63, &block)) return;
+  wide_block<NK, ND, C, kCausal, NB>(a, block, head_of(a, blockIdx.x - u * a.Hq), smem);
+}
+
 // Short prompts: a wave has 32 rows of a head by itself, with a tile of 32 tokens
 // of its own, so that no wave is there for rows that a sequence does not have.
 template <int NK, int ND, int C, bool kCausal>
-__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : 2) void prompt_short_kernel(PromptArgs a) {
+__device__ __forceinline__ void small_block(const PromptArgs& a, const Block& block, int head, uint16_t* smem) {
   constexpr int kTile = kRows * C * 8;  // halves
   constexpr int kLoads = C / 2;         // 1 KiB each, of a tile
-  extern __shared__ uint16_t smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint16_t* sk = smem + wave * 2 * kTile;  // no other wave looks at these
   uint16_t* sv = sk + kTile;
-  const int unit = blockIdx.x * kWaves + wave, u = unit / a.Hq, head = unit - u * a.Hq;
-  Block block;
-  if (!find_block<kRows>(a, u, lane, &block)) return;
   const int first = block.first, n = block.n, q0 = block.j * kRows;
   const int end = kCausal ? min(n, q0 + kRows) : n;
   const int hkv = head / a.G;
@@ -306,6 +395,19 @@ __global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : 2) void prompt_short_kern
   finish(a, st, vh, odd, q0, end, qi, n, first, head, h);
 }
 
+// Both, a workgroup of one kind or the other.
+template <int NK, int ND, int C, bool kCausal>
+__global__ __launch_bounds__(64 * kWaves, ND > 4 ? 1 : 2) void prompt_mixed_kernel(PromptArgs a) {
+  extern __shared__ uint16_t smem[];
+  Place p;
+  Block block;
+  if (!find_mixed(a, threadIdx.x & 63, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), &p, &block)) return;
+  if (p.wide)
+    wide_block<NK, ND, C, kCausal, 1>(a, block, head_of(a, p.head), smem);
+  else
+    small_block<NK, ND, C, kCausal>(a, block, p.head, smem);
+}
+
 template <int NK, int ND, int C, bool kCausal, int NB>
 hipError_t launch_as(const PromptArgs& a, uint32_t grid, hipStream_t s) {
   constexpr int kLds = 4 * 32 * NB * C * 16;
@@ -319,23 +421,26 @@ hipError_t launch_as(const PromptArgs& a, uint32_t grid, hipStream_t s) {
 }
 
 template <int NK, int ND, int C, bool kCausal>
-hipError_t launch_short(const PromptArgs& a, hipStream_t s) {
-  constexpr int kLds = kWaves * 2 * kRows * C * 16;
+hipError_t launch_mixed(const PromptArgs& a, hipStream_t s) {
+  constexpr int kLds = kWaves * 2 * kRows * C * 16;  // of the small blocks, more than the wide ones use
   if (kLds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_short_kernel<NK, ND, C, kCausal>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(prompt_mixed_kernel<NK, ND, C, kCausal>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
-  const int64_t units = (a.T / kRows + std::min(a.T, a.B)) * int64_t(a.Hq);
-  const uint32_t grid = uint32_t((units + kWaves - 1) / kWaves);
-  prompt_short_kernel<NK, ND, C, kCausal><<<grid, 64 * kWaves, kLds, s>>>(a);
+  // Of m sequences with tokens up to x are long: T / 128 + x workgroups for whole blocks and long ends, a quarter
+  // of one for a short end.
+  const int64_t m = std::min(a.T, a.B), x = std::min<int64_t>(m, a.T / (kLong + 1));
+  const int64_t quarters = a.T / kRows + 1 + 4 * x + (m - x);  // of a workgroup, for each head
+  const uint32_t grid = uint32_t((quarters * a.Hq + kWaves - 1) / kWaves);
+  prompt_mixed_kernel<NK, ND, C, kCausal><<<grid, 64 * kWaves, kLds, s>>>(a);
   return hipGetLastError();
 }
 
 template <int NK, int ND, int C>
 hipError_t launch(const PromptArgs& a, bool causal, uint32_t grid, int num_cus, hipStream_t s) {
   if (a.T / a.B < kShort && grid >= 2u * num_cus)
-    return causal ? launch_short<NK, ND, C, true>(a, s) : launch_short<NK, ND, C, false>(a, s);
+    return causal ? launch_mixed<NK, ND, C, true>(a, s) : launch_mixed<NK, ND, C, false>(a, s);
   if constexpr (C == 16) {  // shorter rows leave room for three anyway, longer ones for one
     if (grid >= uint32_t(kMany) * num_cus)
       return causal ? launch_as<NK, ND, C, true, 1>(a, grid, s) : launch_as<NK, ND, C, false, 1>(a, grid, s);
@@ -369,6 +474,7 @@ hipError_t launch_prompt(const PromptCall& r, int num_cus, hipStream_t s) {
   a.D = int(r.D);
   a.zero = r.scale == 0.f;
   a.c = a.zero ? 1.f : std::abs(r.scale) * 1.44269504088896340736f;
+  a.per_hq = page_div(r.Hq);
   a.flip = r.scale < 0.f ? 0x80008000u : 0u;
   const uint32_t grid = uint32_t(prompt_grid(r.T, r.B, r.Hq));
   if (a.D <= 64) return launch<4, 2, 8>(a, r.causal, grid, num_cus, s);

@@ -216,6 +216,56 @@ def test_what_is_not_finite_stays_with_its_readers(gpu_lib, D, bad, at):
     assert np.array_equal(np.isnan(out), hit)
 
 
+LONG = [
+    # Hq, Hkv, D, lengths: short in the mean, some far above it
+    (8, 2, 128, [1] * 30 + [513] + [0] * 30 + [512, 9]),
+    (12, 4, 64, [3, 0, 700, 1, 641, 640, 40] + [2] * 57),
+    (8, 1, 256, [0] * 63 + [1500]),
+    (9, 3, 80, [1300] + [0, 1] * 40),                          # more sequences than lanes
+    (4, 4, 128, [5] * 100 + [2049] + [31, 33, 0] * 60 + [514]),
+    (2, 1, 96, [0] * 700 + [513, 511, 1025] + [1, 0, 64] * 100 + [1100]),
+    (4, 2, 40, [(7 * b) % 5 for b in range(3000)] + [900, 140, 600]),
+    (16, 16, 192, [10] * 60 + [600]),
+]
+
+
+@gpu
+@pytest.mark.parametrize("Hq,Hkv,D,lengths", LONG)
+@pytest.mark.parametrize("causal", [True, False])
+def test_long_prompts_among_short_and_empty_ones(gpu_lib, Hq, Hkv, D, lengths, causal):
+    """Short ones are dealt out by 32 rows, long ones by 128, in one call: each row is done once."""
+    import torch
+    T = sum(lengths) + 2
+    assert T // len(lengths) < 80 and (T // 128 + min(T, len(lengths))) * Hq >= 512
+    q, k, v, dq, dk, dv = make(T, Hq, Hkv, D, "stacked")
+    starts = bounds(lengths, 1)
+    out = torch.full((T, Hq, D), 7.0, dtype=torch.float16, device="cuda")
+    swm.prompt_attention(dq, dk, dv, ints(starts), causal=causal, out=out)
+    ref, tol, rows = reference(q, k, v, starts, D ** -0.5, causal)
+    check(out[torch.from_numpy(rows).cuda()], ref[rows], tol[rows])
+    assert bool((out[0] == 7.0).all()) and bool((out[T - 1] == 7.0).all())
+    n, at = max(lengths), int(starts[int(np.argmax(lengths))])
+    dv[at + n - 70, 0, 1] = float("inf")  # of the long one, seen by its last rows or by all of it
+    out = swm.prompt_attention(dq, dk, dv, ints(starts), causal=causal).double().cpu().numpy()
+    hit = np.zeros((T, Hq, D), bool)
+    hit[at + n - 70 if causal else at:at + n, :Hq // Hkv, 1] = True
+    assert np.array_equal(~np.isfinite(out[rows]), hit[rows])
+    assert np.all((np.abs(out - ref) <= tol)[rows[:, None, None] & ~hit])
+
+
+@gpu
+def test_starts_that_fall_among_many(gpu_lib):
+    """Bounds that are not in order: rows of a sequence may be another's too, and nothing else is read or written."""
+    import torch
+    q, k, v, dq, dk, dv = make(900, 8, 2, 64)
+    starts = np.array(([0, 700, 100] * 40) + [900], np.int32)  # 40 of 700 tokens, 39 of none, one of 800
+    out = torch.full_like(dq, 3.0)
+    swm.prompt_attention(dq, dk, dv, ints(starts), out=out)
+    ref, tol, _ = reference(q, k, v, [0, 700], 0.125, True)
+    check(out[:100], ref[:100], tol[:100])
+    assert bool(torch.isfinite(out).all())
+
+
 @gpu
 @pytest.mark.parametrize("Hq,lengths,at", [(32, [40, 9] * 20, 25), (32, [40, 9] * 20, 39), (64, [150] * 30, 70),
                                            (64, [150] * 30, 149)])
