@@ -36,7 +36,7 @@ struct ReserveArgs {
   int32_t *free_pages, *free_count, *starts, *granted;
   int64_t* slots;
   int64_t table_b, tokens;
-  int32_t B, S, pages, per_seq, cap, room;  // room: entries of free_pages
+  int32_t B, S, pages, cap, room;  // room: entries of free_pages
   PageDiv div;
 };
 
@@ -337,7 +337,6 @@ hipError_t launch_reserve(const KvView& c, const ReserveCall& r, hipStream_t s) 
   a.B = int(c.B);
   a.S = int(c.S);
   a.pages = int(c.pages);
-  a.per_seq = int(c.per_seq);
   a.cap = int(c.per_seq * c.S);
   a.room = int(r.free_size);
   a.div = page_div(c.S);

@@ -46,7 +46,7 @@ struct TreeArgs {
   int64_t q_t, q_h, o_t, o_h;
   int64_t k_p, k_s, k_h, v_p, v_s, v_h;
   int64_t table_b, mask_b;
-  int32_t B, T, Hq, Hkv, G, D, S, pages, cap, per_seq, most;
+  int32_t B, T, Hq, Hkv, G, D, S, pages, cap, most;
   int32_t room;         // pieces of all sequences at most; 0: every sequence is one
   int32_t order;        // whole sequences, the longest first
   int32_t tiles, rows;  // workgroups along a unit's rows; rows of a piece in the workspace
@@ -842,7 +842,6 @@ hipError_t launch_tree(const KvView& c, const TreeCall& r, const TreePlan& p, vo
   a.D = int(c.D);
   a.S = int(c.S);
   a.pages = int(c.pages);
-  a.per_seq = int(c.per_seq);
   a.cap = int(c.per_seq * c.S);
   a.most = int(r.most);
   a.room = p.room;
