@@ -4,7 +4,8 @@ between its products on the library's serving operators:
     q, k, v     spmm of the row-stacked projections; kv_append puts the new keys
                 and values into the paged cache
     attention   prompt_attention over the prompt, then paged_attention, adding
-                the attention weights up per cached row
+                a step's attention weights up per cached row; a prompt adds
+                none, so its rows are ranked by the steps behind it alone
     o_proj      spmm_epilogue with the residual stream
     FFN         gate_up_silu, then spmm_epilogue with the residual stream
     cache       kv_evict once a sequence is `slack` tokens over its budget
@@ -84,9 +85,11 @@ class Session:
         self.lengths.fill_(self.used)
 
     def prompt(self, tokens):
-        """Next tokens, their log probabilities and the entropies after prompts, (batch, n) tokens; the cache is empty."""
+        """Next tokens, their log probabilities and the entropies after prompts, (batch, n) tokens, n below
+        budget + slack; the cache is empty."""
         n = tokens.shape[1]
-        assert self.used == 0 and n < self.budget + self.slack
+        if self.used or not 0 < n < self.budget + self.slack:
+            raise ValueError(f"a prompt begins a session and has 1 to {self.budget + self.slack - 1} tokens")
         starts = torch.arange(0, self.batch * n + 1, n, dtype=torch.int32, device="cuda")
         return self.forward(tokens.reshape(-1), n, lambda q, k, v: swm.prompt_attention(q, k, v, starts))
 

@@ -647,6 +647,9 @@ swm_status swm_token_logprobs(const void* logits, int32_t fp32, int64_t N, int64
  *  meets its value row, and counts so in the sum; out is rounded once.  A value that is not
  *  finite makes the outputs of its dimension an infinity or NaN in the rows
  *  that see its token, and in no other.
+ *  Weights are not added up: the rows of a prompt that swm_kv_append brings into
+ *  a cache begin at weight 0, and what swm_kv_evict ranks them by is what later
+ *  calls of swm_paged_attention add.
  *  Limits: dim a multiple of 8 up to 256, batch and q_heads at most 65535,
  *  tokens below 2^31 - 65536, k_token and v_token below 2^23, and (tokens / 128 +
  *  batch) * q_heads below 2^24 (SWM_ERR_UNSUPPORTED).
@@ -742,6 +745,8 @@ swm_status swm_kv_append(const swm_kv_cache* cache, const void* k, int64_t k_tok
  *  ordered on one stream.
  *  Scores, sums and outputs are fp32; a weight is rounded to fp16 once before it
  *  meets its value row, and counts so in the sum; out is rounded once.
+ *  (swm_paged_attention keeps more of a weight's bits: of a single token it is the
+ *  nearer one.)  No weights are added up.
  *  SWM_ERR_INVALID_ARG: null pointers, q_heads not a positive multiple of
  *  heads, a scale that is not finite, negative sizes or strides, rows of out
  *  that share memory, mask_ld below the capacity, a workspace too small.

@@ -858,7 +858,8 @@ def prompt_attention(q, k, v, starts, scale: Optional[float] = None, causal: boo
     D of 8 up to 256; scale defaults to D ** -0.5; any strides that are
     multiples of 8 (views of a stacked product's rows, head-major tensors).
     starts: (B + 1,) int32 on the device.  Rows that belong to no sequence are
-    not written."""
+    not written.  Unlike paged_attention it adds up no weights: a prompt's rows
+    in a cache are ranked by what later tokens give them."""
     import torch
     lib = load()
     qp, device = _heads(q, "q"), q.device

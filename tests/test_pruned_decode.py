@@ -93,3 +93,26 @@ def test_command_line(gpu_lib, capsys):
     load().main(["--hidden", "256", "--ffn", "512", "--heads", "4", "--kv-heads", "4", "--vocab", "500", "--batch", "3",
                  "--steps", "30", "--budget", "16", "--slack", "4"])
     assert "30 steps of 3 sequences" in capsys.readouterr().out
+
+
+def test_a_prompts_rows_are_ranked_by_the_steps_behind_it(gpu_lib):
+    """A prompt adds no attention weights; a step adds one for every query head, over all the tokens it sees."""
+    import torch
+    m = load()
+    y = m.Layer(hidden=256, ffn=520, heads=4, kv_heads=2, vocab=1003, seed=3)
+    s = m.Session(y, batch=3, budget=20, slack=4, recent=4, page_size=8)
+    s.weights.fill_(9.0)
+    tokens = (torch.arange(3 * 11, device="cuda") * 37 % 1003).view(3, 11)
+    ids, _, _ = s.prompt(tokens)
+    held = lambda n: s.weights.transpose(1, 2)[s.table[:, torch.arange(n, device="cuda") // 8].long(),
+                                               torch.arange(n, device="cuda") % 8]  # (sequence, token, head)
+    assert bool((held(11) == 0).all())
+    s.step(ids)
+    w = held(12)
+    # each of a step's twelve weights is off by 2^-19 of itself, as in test_prompt_attention, their sum by 2^-18
+    assert bool((w > 0).all()) and float((w.sum(1) - 2).abs().max()) < 2 * 2.0**-18
+    with pytest.raises(ValueError):
+        s.prompt(tokens)
+    for n in (0, 24):
+        with pytest.raises(ValueError):
+            m.Session(y, batch=3, budget=20, slack=4, recent=4, page_size=8).prompt(tokens[:, :1].expand(3, n))
