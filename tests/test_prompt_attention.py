@@ -355,6 +355,25 @@ def test_offsets_past_32_bits(gpu_lib):
 
 
 @gpu
+@pytest.mark.parametrize("Hq", [1, 3])
+def test_as_many_sequences_as_there_may_be(gpu_lib, Hq):
+    """65535 of them, of one token and none, two of three tokens and one of 600 at the end."""
+    import torch
+    n = np.arange(65535) % 2
+    n[[5, 40000]], n[-1] = 3, 600
+    T, starts = int(n.sum()), bounds(n)
+    q, k, v, dq, dk, dv = make(T, Hq, 1, 8)
+    out = swm.prompt_attention(dq, dk, dv, ints(starts))
+    one = np.repeat(n == 1, n)
+    assert np.array_equal(out.cpu().numpy()[one], np.broadcast_to(v, q.shape)[one])
+    for b in (5, 40000, 65534):
+        ref, tol, _ = reference(*(x[starts[b]:starts[b + 1]] for x in (q, k, v)), [0, n[b]], 8 ** -0.5, True)
+        check(out[starts[b]:starts[b + 1]], ref, tol)
+    with pytest.raises(swm.SwmError, match="UNSUPPORTED"):
+        swm.prompt_attention(dq, dk, dv, ints(np.zeros(65537)))
+
+
+@gpu
 def test_no_tokens_and_no_sequences(gpu_lib):
     import torch
     q, k, v, dq, dk, dv = make(5, 2, 1, 64)

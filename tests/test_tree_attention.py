@@ -448,6 +448,34 @@ def test_equal_lengths_by_their_order(gpu_lib):
 
 
 @gpu
+def test_as_many_sequences_as_there_may_be(gpu_lib):
+    """65535 of one or two tokens on a page each, of which every other one drafts its last."""
+    import torch
+    B, D = 65535, 8
+    r = np.random.default_rng(6)
+    k, v = (r.standard_normal((B, 2, 1, D)).astype(np.float16) for _ in range(2))
+    q = r.standard_normal(((B + 1) // 2, 2, D)).astype(np.float16)
+    n = 1 + np.arange(B) // 2 % 2
+    starts = bounds(np.arange(B) % 2 == 0)
+    c = swm.PagedCache(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), ints(np.arange(B)[::-1].reshape(B, 1).copy()),
+                       ints(n))
+    out = swm.tree_attention(c, torch.from_numpy(q).cuda(), ints(starts), max_tokens=1)
+    at, page = np.arange(0, B, 2), B - 1 - np.arange(0, B, 2)
+    one = n[at] == 1
+    assert np.array_equal(out.cpu().numpy()[one], np.broadcast_to(v[page[one], :1, 0], (int(one.sum()), 2, D)))
+    x = np.einsum("bhd,btd->bht", q[~one].astype(np.float64), k[page[~one], :, 0].astype(np.float64)) * D ** -0.5
+    p = np.exp(x - x.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    V = v[page[~one], :, 0].astype(np.float64)
+    want = np.einsum("bht,btd->bhd", p, V)
+    # as derived in test_prompt_attention, sum |q_d k_d| below 40 here: a score's error is below 2^-17, twice, and the
+    # roundings of the weights and the sums
+    tol = (2.0**-16 + 2.0**-19 + 2.0**-11 + 2.0**-17) * np.einsum("bht,btd->bhd", p, np.abs(V)) + \
+        2.0**-10 * np.abs(want) + 2.0**-25
+    check(out[torch.from_numpy(~one).cuda()], want, tol)
+
+
+@gpu
 def test_nothing_to_do(gpu_lib):
     import torch
     q, k, v, table, parents, dev = make(4, 2, 64, 16, [40, 30], [4, 4])
