@@ -90,7 +90,7 @@ __device__ __forceinline__ Three scan_three(int x, int y, int z, uint32_t (*part
       all[f] = __builtin_amdgcn_readlane(sums, first + kParts - 1);
       before[f] = wave ? __builtin_amdgcn_readlane(sums, first + (wave ? wave - 1 : 0)) : 0;
     }
-    r.upto[e] = (int64_t(before[1]) + v[2 * e + 1] << 16) + before[0] + v[2 * e];
+    r.upto[e] = ((int64_t(before[1]) + v[2 * e + 1]) << 16) + before[0] + v[2 * e];
     r.all[e] = (int64_t(all[1]) << 16) + all[0];
   }
   return r;

@@ -11,15 +11,17 @@
 // tile by tile through LDS, the next tile on its way meanwhile.  Key fragments are
 // read once per 32 rows, so that LDS reads (128 bytes a cycle and CU) take as long
 // as the products; together with the power limit that is what holds long prompts at
-// about 1.05 PFLOP/s: 1 x 16384 tokens, 32 heads on 8, 2030 us (with zeros for
-// inputs, which draw less power, 1480; a library's product of 8192^3 runs at 1.34
-// to 1.53 PFLOP/s with random inputs and at 2.2 with zeros).  Shorter ones pay 5 us
+// about 1.05 PFLOP/s: 1 x 16384 tokens, 32 heads on 8, 2055 to 2135 us by the card (with
+// zeros for inputs, which draw less power, 1480; a library's product of 8192^3 runs at
+// 1.34 to 1.53 PFLOP/s with random inputs and at 2.2 with zeros).  Shorter ones pay 5 us
 // a workgroup for its first tile, which two or three workgroups to a CU
-// hide in part: 16 ragged x 2048, 32 heads 272 us (0.71 PFLOP/s).
-// Tried and slower: eight waves in two groups that take turns on the matrix cores
-// (2020 us, but 352 for the ragged batch), 64 rows a wave (half the LDS reads, but
-// the accumulators do not fit beside the rest without copies: 2490), all blocks of a
-// batch by their tokens (see pick_of_few).
+// hide in part: 16 ragged x 2048, 32 heads 268 to 280 us (0.7 PFLOP/s).  Rows above 128
+// halves leave room for one workgroup on a CU: 1 x 4096 tokens, 32 heads on 8, of 64
+// 94 us (0.73 PFLOP/s), of 128 159 (0.87), of 192 353 (0.58), of 256 420 (0.66).
+// Tried: eight waves in two groups that take turns on the matrix cores (1 x 16384 1 to
+// 4% faster, but 352 us for 280 for the ragged batch), 64 rows a wave (half the LDS
+// reads, but the accumulators do not fit beside the rest without copies: 2490), all blocks
+// of a batch by their tokens (see pick_of_few).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -38,9 +40,9 @@ using namespace flash;
 constexpr int kWaves = 4;
 constexpr int kBlock = kWaves * kRows;  // query rows of a workgroup
 // Workgroups per CU from which tiles are small.  Measured with 32 heads of 128, us,
-// tiles of 64 / 32 tokens: 8 x 1024 tokens (9 a CU) 103 / 107, 64 x 100 (14) 88 /
-// 67, 1 x 16384 (16) 2038 / 2030, 16 ragged x 2048 (19) 280 / 272, 32 x 512 (20)
-// 171 / 165, 64 x 256 (24) 163 / 140, 1 x 512 (0.6) 17 / 20.
+// tiles of 64 / 32 tokens: 8 x 1024 tokens (9 a CU) 121 / 129, 64 x 100 (14) 81 /
+// 64, 1 x 16384 (16) 2079 / 2081, 16 ragged x 2048 (19) 292 / 279, 32 x 512 (20)
+// 179 / 174, 64 x 256 (24) 167 / 153, 1 x 512 (0.6) 17.5 / 20.6.
 constexpr int kMany = 12;
 // Mean length below which a wave has a block of 32 rows by itself, where there are
 // two workgroups per CU and more.  us, as blocks of 128 / so: 64 x 10 tokens, 160 heads of

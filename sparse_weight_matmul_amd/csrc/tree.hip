@@ -11,8 +11,14 @@
 // ragged x 4096 tokens, 8 drafted: 528 MB in 103 us, 5.1 TB/s; a wave waits for
 // its tile and nothing else, so 128 KiB of a CU's LDS are on their way), hundreds by
 // the matrix cores (2 x 131072, 64 drafted, eight heads to a group: 550 GFLOP in
-// 595 us, and 12 for the join).  Which of the two kernels runs goes by the rows
-// that max_tokens allows.
+// 590 to 620 us, and 12 for the join).  Which of the two kernels runs goes by the
+// rows that max_tokens allows.  16 x 4096 tokens, 32 heads on 8: 32 rows 72 us (3.8
+// TB/s), 36 rows 64, 64 rows 68, 96 rows 74, 128 rows 79.  Rows above 128 halves leave
+// room for one workgroup of four waves on a CU: 16 x 4096, 8 drafted, 32 heads of 192
+// 312 us (5.2 TB/s), of 256 379 (5.7); 2 x 32768, 32 drafted, 32 heads of 256 on 8 152
+// (0.45 PFLOP/s).  Registers spill where these instances for rows above 192 halves
+// have no more (16 to 24 of a lane), and 6 or 8 in those for few query rows of up to 64
+// halves, which keep four waves on a SIMD: 16 ragged x 4096, 32 heads of 64 82 us (3.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -771,11 +777,11 @@ hipError_t launch(const TreeArgs& a, bool few, bool wide, uint32_t grid, hipStre
 // How the work is dealt.  The lengths are in device memory, so the host decides by
 // the capacity alone whether sequences are cut and into how many pieces at most; the
 // kernel sizes them.  Up to twice as many units as workgroups at a time and more
-// than four steps: cut (1 x 1024 tokens, 32 heads, four steps: 19.7 us whole, 21.3
+// than four steps: cut (1 x 1024 tokens, 32 heads, four steps: 18.6 us whole, 20.4
 // as two pieces and a join); of several sequences into up to four pieces a place, so
 // that unlike lengths even out.  More units: whole sequences, the longest first (16
 // ragged x 4096, 32 heads 103 us; cut, with the tiles shared, 134).
-// 256 rows a workgroup rather than 128 where there are more than 128: 648 us for 664
+// 256 rows a workgroup rather than 128 where there are more than 128: 606 us for 642
 // at 2 x 131072.
 TreePlan plan_tree(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap, int64_t most, int num_cus) {
   TreePlan p;
