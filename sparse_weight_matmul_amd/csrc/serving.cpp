@@ -97,7 +97,7 @@ bool spans_meet(const Span& a, const Span& b) {
   if (a.rows < 1 || b.rows < 1) return false;
   const int64_t from = int64_t(b.at - a.at), to = from + b.bytes;  // in bytes from a's first
   // the first row of a that ends behind b's start
-  int64_t r = from < a.bytes ? 0 : a.step > 0 ? (from - a.bytes) / a.step + 1 : a.rows;
+  const int64_t r = from < a.bytes ? 0 : a.rows > 1 ? (from - a.bytes) / a.step + 1 : a.rows;
   return r < a.rows && r * a.step < to;
 }
 

@@ -116,6 +116,15 @@ def test_reserve_is_its_definition(gpu_lib, lengths, counts, S, per, spare):
 
 
 @gpu
+def test_dropped_drafts_give_back_the_pages_they_leave(gpu_lib):
+    """One page here: 76 -> 71, 21 -> 2 and 36 -> 34 tokens keep 5 of 5, 1 of 2 and 3 of 3."""
+    table, free, count, P = state([76, 21, 36], 12, 16, 20)
+    left = table[1, 1]
+    c, got = run_both(table, [76, 21, 36], [-5, -19, -2], free, count, P, 16)
+    assert free[20] == left and (table >= 0).sum(1).tolist() == [5, 1, 3] and got[2].tolist() == [-5, -19, -2]
+
+
+@gpu
 def test_many_steps_keep_every_page(gpu_lib):
     """Random growth and shrinkage: after every step each page has one owner."""
     import torch
